@@ -415,6 +415,86 @@ tp_status tp_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* qa,
                       int64_t ldb, const float* scale_b, void* C, int64_t ldc,
                       tp_stream stream);
 
+/* ------------------------------------------- FP8 with a scale per block --
+ * Block-scaled E4M3: every 128 consecutive columns of a row (TP_FP8_ROW), or
+ * every 128×128 block (TP_FP8_BLOCK), of a matrix [rows, cols] share one
+ * fp32 scale.  A quantized matrix is
+ *   codes  q[r·ldq + c], one byte each; ldq ≥ cols and a multiple of 16, the
+ *          base 16-byte aligned (bytes between cols and ldq are neither
+ *          written nor read);
+ *   scales s[b·lds + r] (TP_FP8_ROW) or s[b·lds + r/128] (TP_FP8_BLOCK) for
+ *          column block b = c/128: ⌈cols/128⌉ rows of scales, lds ≥ rows or
+ *          ⌈rows/128⌉.
+ * The last block of an axis may be short.  With amax the largest magnitude
+ * of a block, in fp32 (every operation rounded once):
+ *   r = 448 / amax,  s = amax / 448,  q = E4M3 code of x·r (nearest even),
+ * and the element's value is q·s; amax = 0 gives s = 1, an amax below 2^-100
+ * counts as 2^-100.  A NaN keeps its place (code 0x7F or 0xFF) and does not
+ * enter amax; an infinity makes its block's scale infinite, so that the
+ * whole block reads as NaN.
+ * (The per-tensor tp_quantize_fp8 stores the factor r as its scale; here the
+ * scale is what a code is multiplied by.)
+ * Sizes: 1 ≤ rows, cols ≤ 2^30, at most 2^31 − 1 tiles of 128×128. */
+typedef enum { TP_FP8_ROW = 0, TP_FP8_BLOCK = 1 } tp_fp8_group;
+
+/* Codes of x (TP_F32 or TP_BF16, [rows, cols], row stride ldx ≥ cols) in q
+ * and s, and of its transpose [cols, rows] in qt and st (for TP_FP8_ROW with
+ * groups of 128 rows of x, for TP_FP8_BLOCK the same codes and scales); q or
+ * qt may be NULL (then s or st is not touched), not both.  x is read once. */
+tp_status tp_quantize_fp8_block(int32_t dtype, int32_t group, int64_t rows,
+                                int64_t cols, const void* x, int64_t ldx,
+                                void* q, int64_t ldq, float* s, int64_t lds,
+                                void* qt, int64_t ldqt, float* st,
+                                int64_t ldst, tp_stream stream);
+
+/* SwiGLU into codes (TP_FP8_ROW).  gu is [G | U], bf16 [T, 2·f] with row
+ * stride ldgu ≥ 2·f: gate columns [0, f), up columns [f, 2·f), what X·W1ᵀ
+ * gives.  Forward: A = SiLU(G) ⊙ U, [T, f].  Backward: from dA (bf16
+ * [T, f], row stride ldda ≥ f) the gradient [dG | dU], [T, 2·f]:
+ *   dG = dA ⊙ U ⊙ σ(G)·(1 + G·(1 − σ(G))),  dU = dA ⊙ G·σ(G).
+ * Values are computed in fp32 and rounded once, to E4M3.  q, s: the rows'
+ * codes (the next product's operand); qt, st: the transpose's (the weight
+ * gradient's operand); either pair may be NULL, not both. */
+tp_status tp_swiglu_fp8_fwd(int64_t T, int64_t f, const void* gu,
+                            int64_t ldgu, void* q, int64_t ldq, float* s,
+                            int64_t lds, void* qt, int64_t ldqt, float* st,
+                            int64_t ldst, tp_stream stream);
+tp_status tp_swiglu_fp8_bwd(int64_t T, int64_t f, const void* dA,
+                            int64_t ldda, const void* gu, int64_t ldgu,
+                            void* q, int64_t ldq, float* s, int64_t lds,
+                            void* qt, int64_t ldqt, float* st, int64_t ldst,
+                            tp_stream stream);
+
+/* Residual addition and RMSNorm into codes (TP_FP8_ROW); x, r, x1, y [T, h]
+ * and γ [h] bf16, dense, 1 ≤ h ≤ 16384:
+ *   x1 = x + r (rounded to bf16),  rstd_t = 1/sqrt(mean_j x1_tj² + ε),
+ *   y = x1·rstd·γ (fp32), its codes in q and s.
+ * r NULL: x1 = x.  x1 NULL (only where r is): not written; it may be x or r
+ * itself.  y (bf16, may be NULL): the norm's output for a backward that
+ * needs it.  The backward is tp_rmsnorm_bwd on x1 and rstd (dres: the
+ * gradient that reaches x1 past the norm); x and r share its dx. */
+tp_status tp_add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps,
+                                 const void* x, const void* r,
+                                 const void* gamma, void* x1, void* y,
+                                 float* rstd, void* q, int64_t ldq, float* s,
+                                 int64_t lds, tp_stream stream);
+
+/* C[M, N] = Σ_b Σ_{k in block b} (qa·sa)[m, k]·(qb·sb)[n, k] over the blocks
+ * b of 128 along K: A [M, K] and B [N, K] block-scaled E4M3, each with the
+ * scales of its own tp_fp8_group; products within a block accumulate in fp32
+ * on the tensor cores, the blocks' sums times sa·sb in fp32 in order of b.
+ * C: out_dtype TP_BF16 or TP_F32, row stride ldc ≥ N.  With X the input, W
+ * [out, in] the weight in TP_FP8_BLOCK and dY the output's gradient:
+ *   Y  = X·Wᵀ       A = X (rows),            B = W;
+ *   dX = dY·W       A = dY (rows),           B = Wᵀ (qt, st of W);
+ *   dW = dYᵀ·X      A = dYᵀ (qt, st of dY),  B = Xᵀ (qt, st of X). */
+tp_status tp_gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void* qa,
+                            int64_t lda, const float* sa, int64_t ldsa,
+                            int32_t a_group, const void* qb, int64_t ldb,
+                            const float* sb, int64_t ldsb, int32_t b_group,
+                            int32_t out_dtype, void* C, int64_t ldc,
+                            tp_stream stream);
+
 /* ------------------------------------------------------------ profiling --
  * Per-kernel-family device time for roofline reporting.  While enabled,
  * every kernel the library launches is bracketed by two CUDA events recorded

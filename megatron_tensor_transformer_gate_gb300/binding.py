@@ -17,6 +17,7 @@ F32, BF16, FP8 = 0, 1, 2
 GELU, SWIGLU = 0, 1
 FUSED, MATERIALISED, OVERLAP, SP = 0, 1, 2, 3
 SCOPE_MLP, SCOPE_ATTN, SCOPE_LAYER = 0, 1, 2
+FP8_ROW, FP8_BLOCK = 0, 1
 
 STATUS = {0: "TP_OK", 1: "TP_ERR_NULL", 2: "TP_ERR_SHAPE", 3: "TP_ERR_DTYPE",
           4: "TP_ERR_WORKSPACE", 5: "TP_ERR_UNSUPPORTED", 6: "TP_ERR_CUDA",
@@ -126,6 +127,17 @@ SIGNATURES = {
     "tp_quantize_fp8": (_I32, [_I64, _P, _P, _P, _P, _P]),
     "tp_gemm_fp8": (_I32, [_I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P,
                            _I64, _P]),
+    "tp_quantize_fp8_block": (_I32, [_I32, _I32, _I64, _I64, _P, _I64] +
+                              [_P, _I64, _P, _I64] * 2 + [_P]),
+    "tp_swiglu_fp8_fwd": (_I32, [_I64, _I64, _P, _I64] +
+                          [_P, _I64, _P, _I64] * 2 + [_P]),
+    "tp_swiglu_fp8_bwd": (_I32, [_I64, _I64, _P, _I64, _P, _I64] +
+                          [_P, _I64, _P, _I64] * 2 + [_P]),
+    "tp_add_rmsnorm_fp8_fwd": (_I32, [_I64, _I64, _F, _P, _P, _P, _P, _P, _P,
+                                      _P, _I64, _P, _I64, _P]),
+    "tp_gemm_fp8_block": (_I32, [_I64, _I64, _I64] +
+                          [_P, _I64, _P, _I64, _I32] * 2 +
+                          [_I32, _P, _I64, _P]),
     "tp_mlp_flops": (_I32, [_MP, _U64P, _U64P]),
     "tp_attn_flops": (_I32, [_AP, _U64P, _U64P]),
     "tp_gemm": (_I32, [_I32, _I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _I32,
@@ -223,6 +235,193 @@ def gemm_fp8(qa, scale_a, qb, scale_b, C, stream=None):
                             ptr(qb), qb.stride(0), ptr(scale_b), ptr(C),
                             C.stride(0), stream_handle(stream)),
           "tp_gemm_fp8")
+
+
+# ------------------------------------------------ FP8 with a scale per block --
+# A block-scaled matrix is a pair (q, s): codes q [rows, cols] (float8_e4m3fn
+# or uint8, unit column stride, rows 16-byte aligned) and fp32 scales s with
+# one row for each 128 columns, [⌈cols/128⌉, rows] (a scale for each row) or
+# [⌈cols/128⌉, ⌈rows/128⌉] (one for each 128×128 block).
+def fp8_block_empty(rows, cols, group=FP8_ROW, device="cuda"):
+    """Room for a block-scaled [rows, cols] matrix: (q, s)."""
+    import torch
+    q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.float8_e4m3fn,
+                    device=device)[:, :cols]
+    s = torch.empty(((cols + 127) // 128,
+                     rows if group == FP8_ROW else (rows + 127) // 128),
+                    dtype=torch.float32, device=device)
+    return q, s
+
+
+def _matrix(t, what):
+    """(rows, cols, row stride) of a device matrix with unit column stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{what}: a matrix, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols != 1:
+        raise ValueError(f"{what}: columns must be adjacent, strides {(ld, unit)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: not on a GPU")
+    return rows, cols, ld if rows > 1 else max(ld, cols)
+
+
+def _bf16(t, what, shape=None):
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: bfloat16, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what}: shape {shape}, got {tuple(t.shape)}")
+
+
+def _fp8_pair(q, s, what, shape=None):
+    """(rows, cols, q, ldq, s, lds, group) of a block-scaled matrix."""
+    import torch
+    rows, cols, ldq = _matrix(q, what)
+    if q.dtype != torch.float8_e4m3fn and q.dtype != torch.uint8:
+        raise TypeError(f"{what}: E4M3 codes, got {q.dtype}")
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{what}: shape {shape}, got {(rows, cols)}")
+    if rows == 1:
+        ldq = (max(ldq, cols) + 15) // 16 * 16
+    sb, sr, lds = _matrix(s, what + " scales")
+    if s.dtype != torch.float32:
+        raise TypeError(f"{what} scales: float32, got {s.dtype}")
+    if sb == (cols + 127) // 128 and sr == rows:
+        group = FP8_ROW
+    elif sb == (cols + 127) // 128 and sr == (rows + 127) // 128:
+        group = FP8_BLOCK
+    else:
+        raise ValueError(f"{what} scales: {(sb, sr)} for codes {(rows, cols)}")
+    if s.device != q.device:
+        raise ValueError(f"{what}: codes and scales on different devices")
+    return rows, cols, q.data_ptr(), ldq, s.data_ptr(), lds, group
+
+
+def _fp8_outs(rows, cols, q, s, qt, st):
+    """The eight output arguments and the group of a quantizing call."""
+    args, groups = [], []
+    for codes, scales, what, shape in ((q, s, "q", (rows, cols)),
+                                       (qt, st, "qt", (cols, rows))):
+        if codes is None:
+            args += [None, 0, None, 0]
+            continue
+        if scales is None:
+            raise ValueError(f"{what}: codes without scales")
+        _, _, p, ld, ps, lds, g = _fp8_pair(codes, scales, what, shape)
+        args += [p, ld, ps, lds]
+        # one row: 1×128 groups and 128×128 blocks have the same layout
+        groups.append((g, shape[0] == 1))
+    if not groups:
+        raise ValueError("neither q nor qt given")
+    sure = {g for g, either in groups if not either} or {FP8_ROW}
+    if len(sure) > 1:
+        raise ValueError("q and qt have scales of different groups")
+    return args, sure.pop()
+
+
+def _same_device(first, *others):
+    import torch
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def quantize_fp8_block(x, q=None, s=None, qt=None, st=None, stream=None):
+    """Block-scaled E4M3 codes of x (bf16 or fp32 [rows, cols]) into (q, s),
+    of its transpose into (qt, st); the scales' shape says whether a scale
+    belongs to 128 elements of a row or to a 128×128 block."""
+    rows, cols, ld = _matrix(x, "x")
+    outs, group = _fp8_outs(rows, cols, q, s, qt, st)
+    _same_device(x, q, s, qt, st)
+    check(lib().tp_quantize_fp8_block(dtype_code(x), group, rows, cols,
+                                      x.data_ptr(), ld, *outs,
+                                      stream_handle(stream)),
+          "tp_quantize_fp8_block")
+
+
+def _row_group(group, what):
+    if group != FP8_ROW:
+        raise ValueError(f"{what} writes a scale for each row")
+
+
+def swiglu_fp8_fwd(gu, q=None, s=None, qt=None, st=None, stream=None):
+    """Codes of SiLU(G)⊙U ([T, f]) into (q, s), of its transpose into
+    (qt, st); gu is [G | U], bf16 [T, 2f]."""
+    T, f2, ld = _matrix(gu, "gu")
+    _bf16(gu, "gu")
+    if f2 % 2:
+        raise ValueError(f"gu: an even number of columns, got {f2}")
+    outs, group = _fp8_outs(T, f2 // 2, q, s, qt, st)
+    _row_group(group, "swiglu_fp8_fwd")
+    _same_device(gu, q, s, qt, st)
+    check(lib().tp_swiglu_fp8_fwd(T, f2 // 2, gu.data_ptr(), ld, *outs,
+                                  stream_handle(stream)), "tp_swiglu_fp8_fwd")
+
+
+def swiglu_fp8_bwd(dA, gu, q=None, s=None, qt=None, st=None, stream=None):
+    """Codes of [dG | dU] ([T, 2f]) into (q, s), of its transpose into
+    (qt, st), from dA (bf16 [T, f]) and the forward's gu."""
+    T, f2, ld = _matrix(gu, "gu")
+    _bf16(gu, "gu")
+    _, _, ldda = _matrix(dA, "dA")
+    _bf16(dA, "dA", (T, f2 // 2))
+    if f2 % 2:
+        raise ValueError(f"gu: an even number of columns, got {f2}")
+    outs, group = _fp8_outs(T, f2, q, s, qt, st)
+    _row_group(group, "swiglu_fp8_bwd")
+    _same_device(gu, dA, q, s, qt, st)
+    check(lib().tp_swiglu_fp8_bwd(T, f2 // 2, dA.data_ptr(), ldda,
+                                  gu.data_ptr(), ld, *outs,
+                                  stream_handle(stream)), "tp_swiglu_fp8_bwd")
+
+
+def add_rmsnorm_fp8_fwd(x, r, gamma, x1, q, s, rstd, y=None, eps=1e-5,
+                        stream=None):
+    """x1 = x + r (r None: x1 is x and may be None), the codes of
+    RMSNorm(x1)·γ into (q, s), rstd [T] fp32, and y (bf16, optional); x1 may
+    be x or r."""
+    import torch
+    T, h, _ = _matrix(x, "x")
+    _bf16(gamma, "gamma", (h,))
+    for t, what in ((x, "x"), (r, "r"), (x1, "x1"), (y, "y")):
+        if t is not None:
+            _bf16(t, what, (T, h))
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: dense rows")
+    if r is not None and x1 is None:
+        raise ValueError("x1: where the sum with r goes")
+    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (T,) or \
+            not rstd.is_contiguous() or not gamma.is_contiguous():
+        raise ValueError("rstd: dense float32 [T]; gamma: dense")
+    _, _, pq, ldq, ps, lds, group = _fp8_pair(q, s, "q", (T, h))
+    if T > 1:
+        _row_group(group, "add_rmsnorm_fp8_fwd")
+    _same_device(x, r, gamma, x1, q, s, rstd, y)
+    check(lib().tp_add_rmsnorm_fp8_fwd(T, h, eps, x.data_ptr(), ptr(r),
+                                       gamma.data_ptr(), ptr(x1), ptr(y),
+                                       rstd.data_ptr(), pq, ldq, ps, lds,
+                                       stream_handle(stream)),
+          "tp_add_rmsnorm_fp8_fwd")
+
+
+def gemm_fp8_block(qa, sa, qb, sb, C, stream=None):
+    """C[M, N] (bf16 or fp32) = A·Bᵀ of the block-scaled A = (qa, sa) [M, K]
+    and B = (qb, sb) [N, K]."""
+    M, K, pa, lda, psa, ldsa, ga = _fp8_pair(qa, sa, "qa")
+    N, _, pb, ldb, psb, ldsb, gb = _fp8_pair(qb, sb, "qb", (qb.shape[0], K))
+    m, n, ldc = _matrix(C, "C")
+    if m != M or n != N:
+        raise ValueError(f"C: shape {(M, N)}, got {(m, n)}")
+    _same_device(C, qa, qb)
+    check(lib().tp_gemm_fp8_block(M, N, K, pa, lda, psa, ldsa, ga, pb, ldb,
+                                  psb, ldsb, gb, dtype_code(C), C.data_ptr(),
+                                  ldc, stream_handle(stream)),
+          "tp_gemm_fp8_block")
 
 
 def act_memory(b, s, h, h_ffn, n_q, n_kv, d, n, dtype=BF16, act=SWIGLU,

@@ -12,6 +12,7 @@
 #include "attention.h"
 #include "common.cuh"
 #include "elementwise.h"
+#include "fp8_block.h"
 #include "gemm.h"
 #include "profile.h"
 
@@ -1154,6 +1155,178 @@ extern "C" tp_status tp_gemm_fp8(int64_t M, int64_t N, int64_t K,
     g.epi.scale_a = scale_a;
     g.epi.scale_b = scale_b;
     return cuda_status(run_gemm(g, stream));
+  });
+}
+
+// --------------------------------------------- FP8 with a scale per block --
+namespace {
+
+constexpr int64_t kMaxDim = 1 << 30;
+
+bool aligned4(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
+// One quantized operand [rows, cols]: pitches, alignment, scale rows.
+tp_status check_fp8_operand(int64_t rows, int64_t cols, int32_t group,
+                            const void* q, int64_t ldq, const float* s,
+                            int64_t lds) {
+  if (q == nullptr || s == nullptr) return TP_ERR_NULL;
+  if (ldq < cols || ldq % 16 || ldq > ((int64_t)1 << 39)) return TP_ERR_SHAPE;
+  if (lds < (group == TP_FP8_ROW ? rows : (rows + 127) / 128))
+    return TP_ERR_SHAPE;
+  if (!aligned16(q) || !aligned4(s)) return TP_ERR_ARG;
+  return TP_OK;
+}
+
+// The outputs of a quantizing call on a [rows, cols] matrix.
+tp_status check_fp8_out(int64_t rows, int64_t cols, int32_t group,
+                        const Fp8BlockOut& o) {
+  if (rows < 1 || cols < 1 || rows > kMaxDim || cols > kMaxDim)
+    return TP_ERR_SHAPE;
+  if (((rows + 127) / 128) * ((cols + 127) / 128) > INT32_MAX)
+    return TP_ERR_SHAPE;
+  if (o.q == nullptr && o.qt == nullptr) return TP_ERR_NULL;
+  if (o.q != nullptr) {
+    const tp_status st =
+        check_fp8_operand(rows, cols, group, o.q, o.ldq, o.s, o.lds);
+    if (st != TP_OK) return st;
+  }
+  if (o.qt != nullptr)
+    return check_fp8_operand(cols, rows, group, o.qt, o.ldqt, o.st, o.ldst);
+  return TP_OK;
+}
+
+Fp8BlockOut fp8_out(void* q, int64_t ldq, float* s, int64_t lds, void* qt,
+                    int64_t ldqt, float* st, int64_t ldst) {
+  Fp8BlockOut o;
+  o.q = static_cast<uint8_t*>(q);
+  o.ldq = ldq;
+  o.s = s;
+  o.lds = lds;
+  o.qt = static_cast<uint8_t*>(qt);
+  o.ldqt = ldqt;
+  o.st = st;
+  o.ldst = ldst;
+  return o;
+}
+
+}  // namespace
+
+extern "C" tp_status tp_quantize_fp8_block(
+    int32_t dtype, int32_t group, int64_t rows, int64_t cols, const void* x,
+    int64_t ldx, void* q, int64_t ldq, float* s, int64_t lds, void* qt,
+    int64_t ldqt, float* st, int64_t ldst, tp_stream stream) {
+  return guarded([&]() -> tp_status {
+    if (dtype != TP_F32 && dtype != TP_BF16) return TP_ERR_DTYPE;
+    if (group != TP_FP8_ROW && group != TP_FP8_BLOCK) return TP_ERR_DTYPE;
+    if (x == nullptr) return TP_ERR_NULL;
+    const Fp8BlockOut o = fp8_out(q, ldq, s, lds, qt, ldqt, st, ldst);
+    const tp_status rc = check_fp8_out(rows, cols, group, o);
+    if (rc != TP_OK) return rc;
+    if (ldx < cols) return TP_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(x) % elem_size(dtype)) return TP_ERR_ARG;
+    return cuda_status(
+        quantize_fp8_block(dtype, group, rows, cols, x, ldx, o, stream));
+  });
+}
+
+extern "C" tp_status tp_swiglu_fp8_fwd(int64_t T, int64_t f, const void* gu,
+                                       int64_t ldgu, void* q, int64_t ldq,
+                                       float* s, int64_t lds, void* qt,
+                                       int64_t ldqt, float* st, int64_t ldst,
+                                       tp_stream stream) {
+  return guarded([&]() -> tp_status {
+    if (gu == nullptr) return TP_ERR_NULL;
+    const Fp8BlockOut o = fp8_out(q, ldq, s, lds, qt, ldqt, st, ldst);
+    const tp_status rc = check_fp8_out(T, f, TP_FP8_ROW, o);
+    if (rc != TP_OK) return rc;
+    if (ldgu < 2 * f) return TP_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(gu) & 1u) return TP_ERR_ARG;
+    return cuda_status(swiglu_fp8_fwd(T, f, gu, ldgu, o, stream));
+  });
+}
+
+extern "C" tp_status tp_swiglu_fp8_bwd(int64_t T, int64_t f, const void* dA,
+                                       int64_t ldda, const void* gu,
+                                       int64_t ldgu, void* q, int64_t ldq,
+                                       float* s, int64_t lds, void* qt,
+                                       int64_t ldqt, float* st, int64_t ldst,
+                                       tp_stream stream) {
+  return guarded([&]() -> tp_status {
+    if (dA == nullptr || gu == nullptr) return TP_ERR_NULL;
+    if (f < 1 || f > kMaxDim) return TP_ERR_SHAPE;
+    const Fp8BlockOut o = fp8_out(q, ldq, s, lds, qt, ldqt, st, ldst);
+    const tp_status rc = check_fp8_out(T, 2 * f, TP_FP8_ROW, o);
+    if (rc != TP_OK) return rc;
+    if (ldgu < 2 * f || ldda < f) return TP_ERR_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(gu) & 1u) ||
+        (reinterpret_cast<uintptr_t>(dA) & 1u))
+      return TP_ERR_ARG;
+    return cuda_status(swiglu_fp8_bwd(T, f, dA, ldda, gu, ldgu, o, stream));
+  });
+}
+
+extern "C" tp_status tp_add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps,
+                                            const void* x, const void* r,
+                                            const void* gamma, void* x1,
+                                            void* y, float* rstd, void* q,
+                                            int64_t ldq, float* s,
+                                            int64_t lds, tp_stream stream) {
+  return guarded([&]() -> tp_status {
+    if (!x || !gamma || !rstd) return TP_ERR_NULL;
+    if (r != nullptr && x1 == nullptr) return TP_ERR_NULL;
+    if (T < 1 || T > kMaxDim || h < 1 || h > 16384) return TP_ERR_SHAPE;
+    const tp_status rc = check_fp8_operand(T, h, TP_FP8_ROW, q, ldq, s, lds);
+    if (rc != TP_OK) return rc;
+    for (const void* p : {x, r, gamma, (const void*)x1, (const void*)y})
+      if (reinterpret_cast<uintptr_t>(p) & 1u) return TP_ERR_ARG;
+    if (!aligned4(rstd)) return TP_ERR_ARG;
+    return cuda_status(add_rmsnorm_fp8_fwd(T, h, eps, x, r, gamma, x1, y,
+                                           rstd, static_cast<uint8_t*>(q),
+                                           ldq, s, lds, stream));
+  });
+}
+
+extern "C" tp_status tp_gemm_fp8_block(
+    int64_t M, int64_t N, int64_t K, const void* qa, int64_t lda,
+    const float* sa, int64_t ldsa, int32_t a_group, const void* qb,
+    int64_t ldb, const float* sb, int64_t ldsb, int32_t b_group,
+    int32_t out_dtype, void* C, int64_t ldc, tp_stream stream) {
+  return guarded([&]() -> tp_status {
+    if (out_dtype != TP_BF16 && out_dtype != TP_F32) return TP_ERR_DTYPE;
+    if ((a_group != TP_FP8_ROW && a_group != TP_FP8_BLOCK) ||
+        (b_group != TP_FP8_ROW && b_group != TP_FP8_BLOCK))
+      return TP_ERR_DTYPE;
+    if (C == nullptr) return TP_ERR_NULL;
+    if (M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+      return TP_ERR_SHAPE;
+    tp_status rc = check_fp8_operand(M, K, a_group, qa, lda, sa, ldsa);
+    if (rc == TP_OK)
+      rc = check_fp8_operand(N, K, b_group, qb, ldb, sb, ldsb);
+    if (rc != TP_OK) return rc;
+    if (((M + 127) / 128) * ((N + 127) / 128) > INT32_MAX || ldc < N)
+      return TP_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(C) % elem_size(out_dtype))
+      return TP_ERR_ARG;
+    GemmFp8Block g;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.qa = static_cast<const uint8_t*>(qa);
+    g.qb = static_cast<const uint8_t*>(qb);
+    g.lda = lda;
+    g.ldb = ldb;
+    g.sa = sa;
+    g.sb = sb;
+    g.ldsa = ldsa;
+    g.ldsb = ldsb;
+    g.a_group = a_group;
+    g.b_group = b_group;
+    g.out_f32 = out_dtype == TP_F32;
+    g.c = C;
+    g.ldc = ldc;
+    return cuda_status(gemm_fp8_block(g, stream, device_status_ptr()));
   });
 }
 

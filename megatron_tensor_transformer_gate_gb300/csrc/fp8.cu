@@ -11,19 +11,17 @@
 // atomicMax of the float's bits per block: non-negative floats order like
 // their bit patterns) and the conversion, which also writes the scale.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include <algorithm>
 
 #include "common.cuh"
 #include "elementwise.h"
+#include "fp8.cuh"
 #include "gemm.h"
 #include "profile.h"
 
 namespace tp {
 namespace {
-
-constexpr float kE4M3Max = 448.0f;
 
 __global__ void __launch_bounds__(256)
     amax_kernel(const uint4* __restrict__ x, int64_t nvec,
@@ -49,14 +47,6 @@ __global__ void __launch_bounds__(256)
     for (int i = 1; i < (int)(blockDim.x >> 5); ++i) b = fmaxf(b, red[i]);
     atomicMax(amax_bits, __float_as_uint(b));
   }
-}
-
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  const __nv_fp8x2_storage_t lo =
-      __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t hi =
-      __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
 __global__ void __launch_bounds__(256)
