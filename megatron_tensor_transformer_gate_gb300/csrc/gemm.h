@@ -98,6 +98,11 @@ bool encode_tmap_3d_f16(CUtensorMap* m, const void* base, uint64_t d0,
                         uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
                         uint32_t b0, uint32_t b1, uint32_t b2);
 
+// The same for E4M3 codes (8-bit elements).
+bool encode_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t d0,
+                       uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+                       uint32_t b0, uint32_t b1, uint32_t b2);
+
 // Number of SMs of the current device.
 int device_sm_count();
 // Host counter of launched kernels (tp_launch_count).

@@ -594,6 +594,13 @@ bool encode_tmap_3d_f16(CUtensorMap* m, const void* base, uint64_t d0,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t d0,
+                       uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+                       uint32_t b0, uint32_t b1, uint32_t b2) {
+  return get_encode() && encode_3d(m, base, d0, d1, d2, s1, s2, b0, b1, b2,
+                                   CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
 int launch_gemm_tc(const GemmProblem& pr, void* stream, unsigned* status) {
   if (!get_encode()) return cudaErrorNotSupported;
   const GemmEpilogue& e = pr.epi;

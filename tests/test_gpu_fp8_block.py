@@ -293,7 +293,8 @@ PRODUCTS = [(1, 1, 1), (1, 16, 16), (1, 129, 130), (1, 1000, 4096),
             (2, 256, 128), (5, 300, 77), (16, 136, 1000), (17, 520, 2100),
             (48, 384, 1376), (64, 256, 640), (65, 130, 260), (128, 128, 384),
             (129, 257, 513), (200, 1024, 512), (256, 256, 128),
-            (300, 520, 208), (513, 384, 4096), (700, 260, 1100)]
+            (300, 520, 208), (513, 384, 4096), (700, 260, 1100),
+            (2600, 2400, 300)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
