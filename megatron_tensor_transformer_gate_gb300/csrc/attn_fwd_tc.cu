@@ -151,26 +151,6 @@ __device__ __forceinline__ void st_row(uint8_t* half_tile, int r,
         make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
 }
 
-// 16 TMEM lanes × 64 columns (eight 8-column units) into 32 registers: in
-// unit u a thread holds lanes base + lane/4 (r[4u], r[4u+1]) and base + 8 +
-// lane/4 (r[4u+2], r[4u+3]), columns 8u + 2·(lane % 4) and the next one.
-__device__ __forceinline__ void tmem_ld16x256b_x8(uint32_t taddr,
-                                                  uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
-        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-        "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
 // Four 8×8 b16 matrices stored transposed: register j of a lane holds
 // elements (lane/4, 2·(lane % 4)) and (lane/4, 2·(lane % 4) + 1) of matrix j;
 // lane 8j + i gives the address of stored row i of matrix j, which receives

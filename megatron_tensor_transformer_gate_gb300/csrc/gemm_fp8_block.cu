@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp8_block.h"
@@ -46,18 +47,18 @@ struct Params {
 
 // ==================================================================== wide ==
 constexpr int BN = 256;
-constexpr int BNH = BN / 2;                    // B rows held by each CTA
-constexpr int STAGES = 6;
-constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-constexpr int TMEM_COLS = 512;
+constexpr int BNH = BN / 2;                    // B rows loaded by each CTA
+constexpr int STAGES = 4;
+constexpr int STAGE_BYTES = 3 * TILE_BYTES;    // 128 rows of A, 256 of B
+constexpr int TMEM_COLS = 512;                 // two halves × two K blocks × 128
 constexpr int WIDE_THREADS = 384;
-// Scales reach the epilogue through shared memory by asynchronous copies
-// SLOTS − 1 K blocks ahead, each warp's apart: 32 row scales and up to 128
-// column scales a block.  (Loads into registers that are handed on from block
-// to block stall on the hand-over: 480 instead of ... µs.)
-constexpr int SLOTS = 4;   // a power of two
-constexpr int WIDE_SCALES = 8 * SLOTS * (32 + BNH);   // floats
-constexpr int WIDE_SMEM = STAGES * STAGE_BYTES + WIDE_SCALES * 4 + 1024 + 256;
+// Scales of the tile's 128 rows and of its columns (two blocks', or 256) for
+// one K block; staged this many blocks deep.
+constexpr int SLOT = BM + BN;                  // floats
+constexpr int SLOTS = 8;
+constexpr int STAGING = 2048;                  // bytes an epilogue warp
+constexpr int WIDE_SMEM = STAGES * STAGE_BYTES + SLOTS * SLOT * 4 +
+                          8 * STAGING + 1024 + 256;
 
 __device__ __forceinline__ void decode_tile(const Params& p, int t, int& mt,
                                             int& nt) {
@@ -70,27 +71,231 @@ __device__ __forceinline__ void decode_tile(const Params& p, int t, int& mt,
   nt = rr / gm;
 }
 
-// The K blocks of this CTA's tiles in order.
-struct Cursor {
-  int t, kb, mt, nt;
-  __device__ void start(const Params& p, int cid) {
-    t = cid;
-    kb = 0;
-    if (t < p.total_tiles) decode_tile(p, t, mt, nt);
+// 16 TMEM lanes × 32 columns: the layout of tmem_ld16x256b_x8, four units.
+__device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr,
+                                                  uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(taddr));
+}
+
+// One output tile's part of an epilogue warp: 32 rows × 128 columns.
+//
+// RowAcc: a scale for each row (sa) times one for the columns.  A thread has
+// one row and all 128 columns, so one multiplier serves them all.
+struct RowAcc {
+  static constexpr int CHUNKS = 4;      // of 32 columns
+  using Chunk = uint32_t[32];
+  uint64_t acc[64];
+  uint64_t s2;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) acc[i] = 0;
   }
-  __device__ void next(const Params& p, int ncl) {
-    if (++kb == p.kblocks) {
-      kb = 0;
-      t += ncl;
-      if (t < p.total_tiles) decode_tile(p, t, mt, nt);
+  __device__ __forceinline__ static void load(uint32_t taddr, int c,
+                                              Chunk& r) {
+    tmem_ld32(taddr + 32 * c, r);
+  }
+  __device__ __forceinline__ static void wait(Chunk& r) { tmem_ld_wait(r); }
+  __device__ __forceinline__ void scales(const float* rows, const float* cols,
+                                         int half, int lane) {
+    const uint32_t s = __float_as_uint(rows[lane] * cols[half]);
+    s2 = pack_f32x2(s, s);
+  }
+  __device__ __forceinline__ void columns(const float*, int, int) {}
+  __device__ __forceinline__ void add(const Chunk& r, int c) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      fma_f32x2(acc[c * 16 + i], pack_f32x2(r[2 * i], r[2 * i + 1]), s2);
+  }
+  // Stores go through 2 KB of shared memory, 64 bytes of each row at a time
+  // (16-byte piece k of row r at k ^ (r / 2 mod 4)): a warp's store then
+  // writes 64 bytes in each of eight rows instead of 16 in each of 32.
+  template <int OUT_F32>
+  __device__ __forceinline__ void store(const Params& p, uint4* stage, int m0,
+                                        int n0, int lane) const {
+    const bool whole = p.vec && n0 + BNH <= p.N;
+    constexpr int W = OUT_F32 ? 16 : 32;   // columns in 64 bytes
+    constexpr int ES = OUT_F32 ? 4 : 2;
+    if (whole) {
+#pragma unroll
+      for (int c = 0; c < BNH / W; ++c) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (OUT_F32) {
+              const float2 x = unpack_f32x2(acc[c * 8 + k * 2 + (j >> 1)]);
+              w[j] = __float_as_uint(j & 1 ? x.y : x.x);
+            } else {
+              const float2 x = unpack_f32x2(acc[c * 16 + k * 4 + j]);
+              w[j] = pack_bf16x2(x.x, x.y);
+            }
+          }
+          stage[lane * 4 + (k ^ ((lane >> 1) & 3))] =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + (lane >> 2), k = lane & 3;
+          if (m0 + r < p.M)
+            *reinterpret_cast<uint4*>(
+                static_cast<uint8_t*>(p.c) +
+                ((int64_t)(m0 + r) * p.ldc + n0 + c * W) * ES + k * 16) =
+                stage[r * 4 + (k ^ ((r >> 1) & 3))];
+        }
+      }
+    } else if (m0 + lane < p.M) {
+      const int64_t at = (int64_t)(m0 + lane) * p.ldc + n0;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        const float2 x = unpack_f32x2(acc[i]);
+        if (n0 + 2 * i < p.N) put<OUT_F32>(p.c, at + 2 * i, x.x);
+        if (n0 + 2 * i + 1 < p.N) put<OUT_F32>(p.c, at + 2 * i + 1, x.y);
+      }
     }
+  }
+  template <int OUT_F32>
+  __device__ __forceinline__ static void put(void* c, int64_t at, float v) {
+    if (OUT_F32)
+      static_cast<float*>(c)[at] = v;
+    else
+      static_cast<__nv_bfloat16*>(c)[at] = __float2bfloat16_rn(v);
   }
 };
 
-// Warp 0: TMA producer.  Warp 1: MMA issue (leader) and TMEM.  Warps 4–11:
-// epilogue, warp w on TMEM lanes 32·(w mod 4) and on 128 of the 256 columns.
+// GridAcc: a scale for each row and each column.  Chunks of 16 rows × 32
+// columns in which a thread has rows lane/4 and lane/4 + 8 and in each unit of
+// eight columns 2·(lane mod 4) and the next: four rows and 32 columns in all,
+// so that a column pair's scales, read once from shared memory, serve four
+// products.  Chunk c: rows 16·(c mod 2), columns 32·(c / 2).
+struct GridAcc {
+  static constexpr int CHUNKS = 8;
+  using Chunk = uint32_t[16];
+  uint64_t acc[64];   // [chunk][unit][row]
+  uint64_t s2[4], w2[4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) acc[i] = 0;
+  }
+  __device__ __forceinline__ static void load(uint32_t taddr, int c,
+                                              Chunk& r) {
+    tmem_ld16x256b_x4(
+        taddr + (static_cast<uint32_t>(16 * (c & 1)) << 16) + 32 * (c >> 1), r);
+  }
+  __device__ __forceinline__ static void wait(Chunk& r) { tmem_ld_wait16(r); }
+  __device__ __forceinline__ void scales(const float* rows, const float*, int,
+                                         int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t s = __float_as_uint(rows[(lane >> 2) + 8 * j]);
+      s2[j] = pack_f32x2(s, s);
+    }
+  }
+  // cols: the half's 128 scales, column 16g + 8u + 2q + e at 16g + 4q + 2u + e
+  __device__ __forceinline__ void columns(const float* cols, int c, int lane) {
+    if (c & 1) return;
+#pragma unroll
+    for (int u = 0; u < 4; u += 2) {
+      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(
+          cols + 32 * (c >> 1) + 8 * u + (lane & 3) * 4);
+      w2[u] = w.x;
+      w2[u + 1] = w.y;
+    }
+  }
+  __device__ __forceinline__ void add(const Chunk& r, int c) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        fma_f32x2(acc[c * 8 + u * 2 + i],
+                  pack_f32x2(r[4 * u + 2 * i], r[4 * u + 2 * i + 1]),
+                  mul_f32x2(s2[(c & 1) * 2 + i], w2[u]));
+  }
+  // The four lanes of a row exchange what makes 16 bytes in each: 64 bytes of
+  // a row a store.
+  template <int OUT_F32>
+  __device__ __forceinline__ void store(const Params& p, uint4*, int m0,
+                                        int n0, int lane) const {
+    const int q = lane & 3;
+    const bool whole = p.vec && n0 + BNH <= p.N;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = m0 + 16 * (c & 1) + 8 * i + (lane >> 2);
+        const int nc = n0 + 32 * (c >> 1);
+        const int64_t at = (int64_t)m * p.ldc + nc;
+        if (!whole) {
+          if (m >= p.M) continue;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float2 x = unpack_f32x2(acc[c * 8 + u * 2 + i]);
+            const int n = 8 * u + 2 * q;
+            if (nc + n < p.N) RowAcc::put<OUT_F32>(p.c, at + n, x.x);
+            if (nc + n + 1 < p.N) RowAcc::put<OUT_F32>(p.c, at + n + 1, x.y);
+          }
+        } else if (OUT_F32) {
+#pragma unroll
+          for (int u = 0; u < 4; u += 2) {
+            // even lanes: four columns of unit u, odd lanes: of unit u + 1
+            const float2 x = unpack_f32x2(acc[c * 8 + u * 2 + i]);
+            const float2 y = unpack_f32x2(acc[c * 8 + u * 2 + 2 + i]);
+            const bool odd = q & 1;
+            const float sx = __shfl_xor_sync(0xffffffffu, odd ? x.x : y.x, 1);
+            const float sy = __shfl_xor_sync(0xffffffffu, odd ? x.y : y.y, 1);
+            if (m < p.M)
+              *reinterpret_cast<float4*>(static_cast<float*>(p.c) + at +
+                                         8 * (u + (q & 1)) + 4 * (q >> 1)) =
+                  odd ? make_float4(sx, sy, y.x, y.y)
+                      : make_float4(x.x, x.y, sx, sy);
+          }
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = unpack_f32x2(acc[c * 8 + j * 2 + i]);
+            w[j] = pack_bf16x2(x.x, x.y);
+          }
+          // 4×4 transpose over the row's lanes: lane q gets unit q
+          const bool o1 = q & 1, o2 = q & 2;
+          uint32_t a = __shfl_xor_sync(0xffffffffu, o1 ? w[0] : w[1], 1);
+          uint32_t b = __shfl_xor_sync(0xffffffffu, o1 ? w[2] : w[3], 1);
+          if (o1) w[0] = a, w[2] = b; else w[1] = a, w[3] = b;
+          a = __shfl_xor_sync(0xffffffffu, o2 ? w[0] : w[2], 2);
+          b = __shfl_xor_sync(0xffffffffu, o2 ? w[1] : w[3], 2);
+          if (o2) w[0] = a, w[1] = b; else w[2] = a, w[3] = b;
+          if (m < p.M)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.c) + at +
+                                      8 * q) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+  }
+};
+
+// Two CTAs, each with 128 rows of a 256×256 tile; every CTA loads its A rows
+// and half of B, the half into both (multicast).  The MMAs are the CTA's own
+// (cta_group::1), so that handing a TMEM buffer over and back stays inside
+// the SM.  Roles:
+//   warp 0      TMA producer, a ring of four K blocks;
+//   warps 1, 2  MMA issue, 128 of the tile's columns each, two TMEM buffers
+//               a half (one thread's waits, MMAs and commits for a K block
+//               take longer beside eight busy epilogue warps than its MMAs);
+//   warp 3      the scales, by asynchronous copies up to six K blocks ahead;
+//               its arrival joins the MMAs' commit on the epilogue's barrier;
+//   warps 4–11  epilogue, warp w on TMEM lanes 32·(w mod 4) of half (w − 4)/4.
 // The epilogue's 128 sums a thread need more than the 168 registers that 384
-// threads can have, so the first warpgroup hands some over (128·88 + 256·208
+// threads can have, so the first warpgroup hands some over (128·56 + 256·224
 // = 384·168).
 template <int B_ROW, int OUT_F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
@@ -100,37 +305,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smA = smem;
   uint8_t* smB = smem + STAGES * TILE_BYTES;
-  float* scales = reinterpret_cast<float*>(smB + STAGES * TILE_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(scales + WIDE_SCALES);
+  float* scales = reinterpret_cast<float*>(smB + STAGES * 2 * TILE_BYTES);
+  uint8_t* staging = reinterpret_cast<uint8_t*>(scales + SLOTS * SLOT);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * STAGING);
   uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* tfull = empty + STAGES;    // [half][buffer]
+  uint64_t* tempty = tfull + 4;
+  uint64_t* drain = tempty + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank() & 1u;
-  const bool leader = rank == 0;
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  const int64_t blocks =
+      (int64_t)((p.total_tiles - cid + ncl - 1) / ncl) * p.kblocks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 4);    // both halves' MMAs of both CTAs
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * 8);   // a lane of each epilogue warp, both CTAs
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&tfull[b], 2);    // the MMAs and the scales
+      mbar_init(&tempty[b], 4);   // a lane of each of the half's warps
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.ma);
     tma_prefetch_desc(&p.mb);
   }
-  if (warp == 1) tmem_alloc_pair(tmem_slot, TMEM_COLS);
+  if (warp == 1) tmem_alloc(tmem_slot, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // barriers of both CTAs initialised before any remote use
@@ -138,10 +346,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer --
-      const uint32_t full0 = cluster_addr(full, 0);   // the leader's full[0]
       uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
       bool ok = true;
       for (int t = cid; ok && t < p.total_tiles; t += ncl) {
@@ -154,14 +361,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
             ok = false;
             break;
           }
-          if (leader) {
-            mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
-            armed |= 1u << stage;
-            armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-          }
-          const uint32_t fb = full0 + stage * 8;
-          tma_load_3d_pair(smA + stage * TILE_BYTES, &p.ma, fb, kb * BK, 0, m0);
-          tma_load_3d_pair(smB + stage * TILE_BYTES, &p.mb, fb, kb * BK, 0, n0);
+          mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+          armed |= 1u << stage;
+          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+          tma_load_3d(smA + stage * TILE_BYTES, &p.ma, &full[stage], kb * BK, 0,
+                      m0);
+          // this CTA's half of B, into both
+          tma_load_3d_multicast(smB + (2 * stage + rank) * TILE_BYTES, &p.mb,
+                                &full[stage], kb * BK, 0, n0, 3);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -169,8 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
         }
       }
       if (ok) {
-        // the leader's last commits land on this CTA's empty barriers before
-        // the CTA may exit
+        // both CTAs' last commits land on this CTA's empty barriers before it
+        // may exit
         for (int i = 0; i < STAGES; ++i) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, 42))
             break;
@@ -180,188 +387,177 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
           }
         }
       }
-      if (*abort_flag && leader) {
+      if (*abort_flag) {
         // let every copy counted on this CTA's barriers land
         volatile int no_abort = 0;
         for (int s = 0; s < STAGES; ++s)
           if (armed & (1u << s))
             mbar_wait(&full[s], (armed_par >> s) & 1u, &no_abort, nullptr, 0);
       }
-    } else if (warp == 1 && leader && lane == 0) {
+    } else if ((warp == 1 || warp == 2) && lane == 0) {
       // -------------------------------------------------------- MMA issue --
-      constexpr uint32_t IDESC = idesc_e4m3_f32(2 * BM, BN);
-      uint32_t stage = 0, phase = 0;
-      bool ok = true;
-      int it = 0;   // K blocks so far: TMEM buffer it & 1
-      for (int t = cid; ok && t < p.total_tiles; t += ncl) {
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const int buf = it & 1;
-          if (!mbar_wait(&tempty[buf], ((it >> 1) & 1) ^ 1, abort_flag,
-                         p.status, 43) ||
-              !mbar_wait(&full[stage], phase, abort_flag, p.status, 44)) {
+      constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BNH);
+      const int half = warp - 1;
+      const uint64_t ad0 = smem_desc_sw128(smem_u32(smA), 16, 1024);
+      const uint64_t bd0 =
+          smem_desc_sw128(smem_u32(smB + half * TILE_BYTES), 16, 1024);
+      uint32_t stage = 0, phase = 0, buf = 0, tphase = 1;
+      for (int64_t it = 0; it < blocks; ++it) {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, 43) ||
+            !mbar_wait(&tempty[2 * half + buf], tphase, abort_flag, p.status,
+                       44))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + (2 * half + buf) * BNH;
+        const uint64_t ad = ad0 + stage * (TILE_BYTES >> 4);
+        const uint64_t bd = bd0 + stage * (2 * TILE_BYTES >> 4);
+        tc_mma_f8(d, ad, bd, IDESC, 0);
+        tc_mma_f8(d, ad + 2, bd + 2, IDESC, 1);
+        tc_mma_f8(d, ad + 4, bd + 4, IDESC, 1);
+        tc_mma_f8(d, ad + 6, bd + 6, IDESC, 1);
+        tc_commit(&tfull[2 * half + buf]);
+        tc_commit_multicast(&empty[stage], 3);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+        tphase ^= buf;
+        buf ^= 1;
+      }
+      if (*abort_flag) {
+        volatile int no_abort = 0;
+        tc_commit(&drain[half]);
+        mbar_wait(&drain[half], 0, &no_abort, nullptr, 0);
+      }
+    } else if (warp == 3) {
+      // ----------------------------------------------------------- scales --
+      constexpr int AHEAD = 4;
+      int ft = cid, fk = 0, fslot = 0;
+      int m0 = 0, n0 = 0;
+      auto fetch = [&]() {
+        if (ft < p.total_tiles) {
+          if (fk == 0) {
+            int mt, nt;
+            decode_tile(p, ft, mt, nt);
+            m0 = mt * 2 * BM + (int)rank * BM;
+            n0 = nt * BN;
+          }
+          float* rows = scales + fslot * SLOT;
+          float* cols = rows + BM;
+          const float* pa = p.sa + fk * p.ldsa;
+          const float* pb = p.sb + fk * p.ldsb;
+#pragma unroll
+          for (int j = 0; j < BM / 32; ++j) {
+            const int m = m0 + 32 * j + lane;
+            const bool in = m < p.M;
+            cp_async4(rows + 32 * j + lane,
+                      pa + (in ? (p.a_row ? m : m / BM) : 0), in);
+          }
+          if (B_ROW) {
+            // column 16g + 8u + 2q + e is kept at 16g + 4q + 2u + e
+            const int at = (lane & 16) + ((lane >> 1) & 3) * 4 +
+                           ((lane >> 3) & 1) * 2 + (lane & 1);
+#pragma unroll
+            for (int j = 0; j < BN / 32; ++j) {
+              const int n = n0 + 32 * j + lane;
+              const bool in = n < p.N;
+              cp_async4(cols + 32 * j + at, pb + (in ? n : 0), in);
+            }
+          } else if (lane < 2) {
+            const int n = n0 + BNH * lane;
+            const bool in = n < p.N;
+            cp_async4(cols + lane, pb + (in ? n / BM : 0), in);
+          }
+          if (++fk == p.kblocks) {
+            fk = 0;
+            ft += ncl;
+          }
+        }
+        cp_async_commit();
+        fslot = (fslot + 1) & (SLOTS - 1);
+      };
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) fetch();
+      for (int64_t it = 0; it < blocks; ++it) {
+        const int buf = it & 1;
+        // Block it − 2 complete on both halves: this block's phase is open,
+        // and block it − 4, whose slot the next copies go to, has been read
+        // (the MMAs of it − 2 waited for its buffers).
+        if (it >= 2) {
+          const uint32_t par = ((it - 2) >> 1) & 1;
+          if (!mbar_wait_warp(&tfull[buf], par, abort_flag, p.status, 46) ||
+              !mbar_wait_warp(&tfull[2 + buf], par, abort_flag, p.status, 47))
+            break;
+        }
+        fetch();
+        cp_async_wait<AHEAD>();
+        __syncwarp();
+        if (lane < 2) mbar_arrive(&tfull[2 * lane + buf]);
+      }
+      cp_async_wait<0>();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ------------------------------------------------------------ epilogue --
+    using Acc = typename std::conditional<B_ROW != 0, GridAcc, RowAcc>::type;
+    const int quarter = warp & 3;          // TMEM lanes this warp may read
+    const int half = (warp - 4) >> 2;      // its 128 of the 256 columns
+    uint4* stage = reinterpret_cast<uint4*>(staging + (warp - 4) * STAGING);
+    const uint32_t taddr0 = tmem_base +
+                            (static_cast<uint32_t>(quarter * 32) << 16) +
+                            2 * half * BNH;
+    uint64_t* tf = tfull + 2 * half;
+    uint64_t* te = tempty + 2 * half;
+    int64_t it = 0;
+    bool ok = true, ready = false;
+    typename Acc::Chunk r[2];   // a chunk being added, the next on its way
+    for (int t = cid; ok && t < p.total_tiles; t += ncl) {
+      Acc a;
+      a.clear();
+      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+        const int buf = it & 1;
+        const uint32_t taddr = taddr0 + buf * BNH;
+        if (!ready) {
+          if (!mbar_wait_warp(&tf[buf], (it >> 1) & 1, abort_flag, p.status,
+                              45)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smA + stage * TILE_BYTES);
-          const uint32_t b0 = smem_u32(smB + stage * TILE_BYTES);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f8_pair(tmem_base + buf * BN,
-                           smem_desc_sw128(a0 + kk * 32, 16, 1024),
-                           smem_desc_sw128(b0 + kk * 32, 16, 1024), IDESC,
-                           kk != 0);
-          tc_commit_pair(&empty[stage], 3);
-          tc_commit_pair(&tfull[buf], 3);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+          Acc::load(taddr, 0, r[0]);
         }
-      }
-      if (*abort_flag) {
-        volatile int no_abort = 0;
-        tc_commit_pair(drain, 1);
-        mbar_wait(drain, 0, &no_abort, nullptr, 0);
-      }
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    // ------------------------------------------------------------ epilogue --
-    const int quarter = warp & 3;          // TMEM lanes this warp may read
-    const int half = (warp - 4) >> 2;      // its 128 of the 256 columns
-    const int row = (int)rank * BM + quarter * 32 + lane;   // in the pair tile
-    float* myrows = scales + (warp - 4) * SLOTS * (32 + BNH);  // [SLOTS][32]
-    float* mycols = myrows + SLOTS * 32;                       // [SLOTS][BNH]
-    const uint32_t tempty0 = cluster_addr(tempty, 0);   // the leader's
-    const uint32_t taddr0 =
-        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * BNH;
-
-    // one group of copies per K block: the lane's row scale, and the column
-    // block's scale (lane 0) or four columns' (B_ROW)
-    Cursor ahead;
-    ahead.start(p, cid);
-    int slot_in = 0;
-    auto fetch = [&]() {
-      if (ahead.t < p.total_tiles) {
-        const int m = ahead.mt * 2 * BM + row;
-        const int n = ahead.nt * BN + half * BNH;
-        const float* pa = p.sa + ahead.kb * p.ldsa;
-        const float* pb = p.sb + ahead.kb * p.ldsb;
-        cp_async4(myrows + slot_in * 32 + lane,
-                  pa + (m < p.M ? (p.a_row ? m : m / BM) : 0), m < p.M);
-        if (B_ROW) {
+        const float* rows = scales + (it & (SLOTS - 1)) * SLOT;
+        a.scales(rows + quarter * 32, rows + BM, half, lane);
+        const float* cols = rows + BM + half * BNH;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int nj = n + 32 * j + lane;
-            cp_async4(mycols + slot_in * BNH + 32 * j + lane,
-                      pb + (nj < p.N ? nj : 0), nj < p.N);
-          }
-        } else if (lane == 0) {
-          cp_async4(mycols + slot_in * BNH, pb + (n < p.N ? n / BM : 0),
-                    n < p.N);
-        }
-        ahead.next(p, ncl);
-      }
-      cp_async_commit();
-      slot_in = (slot_in + 1) & (SLOTS - 1);
-    };
-#pragma unroll
-    for (int i = 0; i < SLOTS - 1; ++i) fetch();
-
-    int it = 0;
-    bool ok = true;
-    for (int t = cid; ok && t < p.total_tiles; t += ncl) {
-      uint64_t acc[BNH / 2];
-#pragma unroll
-      for (int i = 0; i < BNH / 2; ++i) acc[i] = 0;
-      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-        const int buf = it & 1;
-        cp_async_wait<SLOTS - 2>();   // this block's group is complete
-        __syncwarp();   // for every lane's, and the last block's are read
-        const float a0 = myrows[(it & (SLOTS - 1)) * 32 + lane];
-        const float* cs = mycols + (it & (SLOTS - 1)) * BNH;
-        fetch();
-        if (!mbar_wait_warp(&tfull[buf], (it >> 1) & 1, abort_flag, p.status,
-                            45)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sb = __float_as_uint(B_ROW ? a0 : a0 * cs[0]);
-        const uint64_t s2 = pack_f32x2(sb, sb);
-        const uint32_t taddr = taddr0 + buf * BN;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(taddr + c * 32, r);
-          tmem_ld_wait(r);
-          if (c == 3) {   // the buffer is read: the MMAs may have it back
+        for (int c = 0; c < Acc::CHUNKS; ++c) {
+          Acc::wait(r[c & 1]);
+          a.columns(cols, c, lane);
+          if (c + 1 < Acc::CHUNKS) {
+            Acc::load(taddr, c + 1, r[(c + 1) & 1]);
+          } else {
+            // the buffer is read: the MMAs may have it back
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            uint64_t x0 = s2, x1 = s2;
-            if (B_ROW) {
-              const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(
-                  cs + c * 32 + 2 * i);
-              x0 = mul_f32x2(s2, w.x);
-              x1 = mul_f32x2(s2, w.y);
+            if (lane == 0) mbar_arrive_relaxed(&te[buf]);
+            // the next block's first chunk, if it is there already
+            ready = mbar_test_warp(&tf[buf ^ 1], ((it + 1) >> 1) & 1);
+            if (ready) {
+              tc_fence_after();
+              Acc::load(taddr0 + (buf ^ 1) * BNH, 0, r[0]);
             }
-            fma_f32x2(acc[c * 16 + i], pack_f32x2(r[2 * i], r[2 * i + 1]), x0);
-            fma_f32x2(acc[c * 16 + i + 1],
-                      pack_f32x2(r[2 * i + 2], r[2 * i + 3]), x1);
           }
+          a.add(r[c & 1], c);
         }
       }
       if (!ok) break;
       int mt, nt;
       decode_tile(p, t, mt, nt);
-      const int m = mt * 2 * BM + row;
       const int n0 = nt * BN + half * BNH;
-      if (m < p.M && n0 < p.N) {
-        const int valid = min(BNH, p.N - n0);
-        if (OUT_F32) {
-          float* dst = static_cast<float*>(p.c) + (int64_t)m * p.ldc + n0;
-#pragma unroll
-          for (int i = 0; i < BNH / 2; i += 2) {
-            const float2 x = unpack_f32x2(acc[i]), y = unpack_f32x2(acc[i + 1]);
-            if (p.vec && 2 * i + 4 <= valid) {
-              *reinterpret_cast<float4*>(dst + 2 * i) =
-                  make_float4(x.x, x.y, y.x, y.y);
-            } else {
-              if (2 * i < valid) dst[2 * i] = x.x;
-              if (2 * i + 1 < valid) dst[2 * i + 1] = x.y;
-              if (2 * i + 2 < valid) dst[2 * i + 2] = y.x;
-              if (2 * i + 3 < valid) dst[2 * i + 3] = y.y;
-            }
-          }
-        } else {
-          __nv_bfloat16* dst =
-              static_cast<__nv_bfloat16*>(p.c) + (int64_t)m * p.ldc + n0;
-#pragma unroll
-          for (int i = 0; i < BNH / 2; i += 4) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 x = unpack_f32x2(acc[i + j]);
-              w[j] = pack_bf16x2(x.x, x.y);
-            }
-            if (p.vec && 2 * i + 8 <= valid) {
-              *reinterpret_cast<uint4*>(dst + 2 * i) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (2 * i + j < valid)
-                  reinterpret_cast<uint16_t*>(dst)[2 * i + j] =
-                      (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-            }
-          }
-        }
-      }
+      if (n0 < p.N)
+        a.template store<OUT_F32>(p, stage,
+                                  mt * 2 * BM + (int)rank * BM + quarter * 32,
+                                  n0, lane);
     }
   }
 
@@ -369,11 +565,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   __syncthreads();
   cluster_sync();   // neither CTA leaves while the pair still uses it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
 // ================================================================== narrow ==
 constexpr int NARROW_THREADS = 192;
+// Scales reach the epilogue by asynchronous copies NSLOTS − 1 K blocks ahead,
+// each warp's apart.
+constexpr int NSLOTS = 4;   // a power of two
 
 // BN rows of A against 128 rows of B; shared memory for two CTAs on an SM.
 template <int BNT>
@@ -383,7 +582,7 @@ struct Narrow {
   static constexpr int STAGES = BNT <= 16 ? 6 : BNT <= 32 ? 5 : BNT <= 64 ? 4 : 3;
   static constexpr int BUFS = BNT <= 64 ? 4 : 2;
   static constexpr int COLS = BUFS * BNT;    // TMEM: 64, 128, 256, 256
-  static constexpr int SCALES = 4 * SLOTS * (32 + BNT);   // floats
+  static constexpr int SCALES = 4 * NSLOTS * (32 + BNT);   // floats
   static constexpr int SMEM = STAGES * STAGE + SCALES * 4 + 1024 + 256;
 };
 
@@ -511,11 +710,11 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
     }
   } else {
     const int r = r0 + ctid;
-    float* myrows = scales + (warp - 2) * SLOTS * (32 + BNT);   // [SLOTS][32]
-    float* mycols = myrows + SLOTS * 32;                        // [SLOTS][BNT]
+    float* myrows = scales + (warp - 2) * NSLOTS * (32 + BNT);   // [NSLOTS][32]
+    float* mycols = myrows + NSLOTS * 32;                        // [NSLOTS][BNT]
     auto fetch = [&](int kb) {
       if (kb < kb1) {
-        const int slot = (kb - kb0) & (SLOTS - 1);
+        const int slot = (kb - kb0) & (NSLOTS - 1);
         const float* pr = p.sr + kb * p.ldsr;
         const float* pt = p.st + kb * p.ldst;
         cp_async4(myrows + slot * 32 + lane,
@@ -531,17 +730,17 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < SLOTS - 1; ++i) fetch(kb0 + i);
+    for (int i = 0; i < NSLOTS - 1; ++i) fetch(kb0 + i);
     const uint32_t taddr0 =
         tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     int it = 0;
     for (int kb = kb0; kb < kb1; ++kb, ++it) {
       const int buf = it % L::BUFS;
-      cp_async_wait<SLOTS - 2>();   // this block's group is complete
+      cp_async_wait<NSLOTS - 2>();   // this block's group is complete
       __syncwarp();   // for every lane's, and the last block's are read
-      const float a0 = myrows[(it & (SLOTS - 1)) * 32 + lane];
-      const float* cs = mycols + (it & (SLOTS - 1)) * BNT;
-      fetch(kb + SLOTS - 1);
+      const float a0 = myrows[(it & (NSLOTS - 1)) * 32 + lane];
+      const float* cs = mycols + (it & (NSLOTS - 1)) * BNT;
+      fetch(kb + NSLOTS - 1);
       if (!mbar_wait_warp(&tfull[buf], (it / L::BUFS) & 1, abort_flag,
                           p.status, 54))
         break;
