@@ -205,12 +205,11 @@ struct GridAcc {
   __device__ __forceinline__ void columns(const float* cols, int c, int lane) {
     if (c & 1) return;
 #pragma unroll
-    for (int u = 0; u < 4; u += 2) {
-      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(
-          cols + 32 * (c >> 1) + 8 * u + (lane & 3) * 4);
-      w2[u] = w.x;
-      w2[u + 1] = w.y;
-    }
+    for (int u = 0; u < 4; u += 2)   // in order: hoisted loads cost spills
+      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                   : "=l"(w2[u]), "=l"(w2[u + 1])
+                   : "r"(smem_u32(cols + 32 * (c >> 1) + 8 * u +
+                                  (lane & 3) * 4)));
   }
   __device__ __forceinline__ void add(const Chunk& r, int c) {
 #pragma unroll
