@@ -10,6 +10,8 @@ raises.
 import ctypes
 import os
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtp.so")
 
@@ -190,14 +192,19 @@ def ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def raw_stream(stream, dev):
+    """The stream's handle, the current one of device ``dev`` if None (read
+    without making a torch.cuda.Stream, which costs as much as a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def stream_handle(stream=None):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(raw_stream(stream, torch.cuda.current_device()))
 
 
 def dtype_code(t):
-    import torch
     if t.dtype == torch.float32:
         return F32
     if t.dtype == torch.bfloat16:
@@ -244,7 +251,6 @@ def gemm_fp8(qa, scale_a, qb, scale_b, C, stream=None):
 # [⌈cols/128⌉, ⌈rows/128⌉] (one for each 128×128 block).
 def fp8_block_empty(rows, cols, group=FP8_ROW, device="cuda"):
     """Room for a block-scaled [rows, cols] matrix: (q, s)."""
-    import torch
     q = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.float8_e4m3fn,
                     device=device)[:, :cols]
     s = torch.empty(((cols + 127) // 128,
@@ -253,94 +259,126 @@ def fp8_block_empty(rows, cols, group=FP8_ROW, device="cuda"):
     return q, s
 
 
-def _matrix(t, what):
-    """(rows, cols, row stride) of a device matrix with unit column stride."""
+# The checks of a call run before every launch and are on the path of a
+# generated token, where the launch itself takes about 3 µs: each is one
+# expression over attributes read once, and only a failed one looks for words.
+def _shape(t):
+    return tuple(t.shape)
+
+
+def _refuse_matrix(t, what):
     if t.dim() != 2:
-        raise ValueError(f"{what}: a matrix, got {tuple(t.shape)}")
+        raise ValueError(f"{what}: a matrix, got {_shape(t)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: not on a GPU")
+    raise ValueError(f"{what}: columns must be adjacent, strides {t.stride()}")
+
+
+def _matrix(t, what):
+    """(rows, cols, row stride, device) of a matrix on the current device with
+    adjacent columns."""
+    dev = t.get_device()
+    if t.dim() != 2 or dev < 0:
+        _refuse_matrix(t, what)
     rows, cols = t.shape
     ld, unit = t.stride()
     if unit != 1 and cols != 1:
-        raise ValueError(f"{what}: columns must be adjacent, strides {(ld, unit)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: not on a GPU")
-    return rows, cols, ld if rows > 1 else max(ld, cols)
+        _refuse_matrix(t, what)
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} is on cuda:{dev}, the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()}")
+    return rows, cols, ld if rows > 1 else cols, dev
 
 
-def _bf16(t, what, shape=None):
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{what}: bfloat16, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what}: shape {shape}, got {tuple(t.shape)}")
+def _refuse_dense(t, what, dtype, shape, dev):
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype}, got {t.dtype}")
+    if _shape(t) != shape:
+        raise ValueError(f"{what}: shape {shape}, got {_shape(t)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, not cuda:{dev}")
+    raise ValueError(f"{what}: dense rows, strides {t.stride()}")
 
 
-def _fp8_pair(q, s, what, shape=None):
-    """(rows, cols, q, ldq, s, lds, group) of a block-scaled matrix."""
-    import torch
-    rows, cols, ldq = _matrix(q, what)
-    if q.dtype != torch.float8_e4m3fn and q.dtype != torch.uint8:
+def _dense(t, what, dtype, shape, dev):
+    """Address of a dense tensor of this type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
+            not t.is_contiguous():
+        _refuse_dense(t, what, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _refuse_pair(q, s, what, rows, cols, dev):
+    if s is None:
+        raise ValueError(f"{what}: codes without scales")
+    if q.dtype not in _CODE_TYPES:
         raise TypeError(f"{what}: E4M3 codes, got {q.dtype}")
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{what}: shape {shape}, got {(rows, cols)}")
-    if rows == 1:
-        ldq = (max(ldq, cols) + 15) // 16 * 16
-    sb, sr, lds = _matrix(s, what + " scales")
     if s.dtype != torch.float32:
         raise TypeError(f"{what} scales: float32, got {s.dtype}")
-    if sb == (cols + 127) // 128 and sr == rows:
-        group = FP8_ROW
-    elif sb == (cols + 127) // 128 and sr == (rows + 127) // 128:
-        group = FP8_BLOCK
-    else:
-        raise ValueError(f"{what} scales: {(sb, sr)} for codes {(rows, cols)}")
-    if s.device != q.device:
-        raise ValueError(f"{what}: codes and scales on different devices")
-    return rows, cols, q.data_ptr(), ldq, s.data_ptr(), lds, group
+    if _shape(q) != (rows, cols):
+        raise ValueError(f"{what}: shape {(rows, cols)}, got {_shape(q)}")
+    for t, w in ((q, what), (s, what + " scales")):
+        if t.get_device() != dev:
+            raise ValueError(f"{w}: on {t.device}, not cuda:{dev}")
+        if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+            _refuse_matrix(t, w)
+    raise ValueError(f"{what} scales: {_shape(s)} for codes {(rows, cols)}")
 
 
-def _fp8_outs(rows, cols, q, s, qt, st):
+_CODE_TYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _fp8_pair(q, s, what, rows, cols, dev):
+    """(address, ldq, address of the scales, lds, group) of a block-scaled
+    matrix of this shape on this device."""
+    kb, rb = (cols + 127) >> 7, (rows + 127) >> 7
+    if s is None or q.shape != (rows, cols) or q.dtype not in _CODE_TYPES or \
+            s.dtype is not torch.float32 or q.get_device() != dev or \
+            s.get_device() != dev or s.dim() != 2:
+        _refuse_pair(q, s, what, rows, cols, dev)
+    ld, unit = q.stride()
+    lds, sunit = s.stride()
+    sb, sr = s.shape
+    if (unit != 1 and cols != 1) or (sunit != 1 and sr != 1) or sb != kb or \
+            (sr != rows and sr != rb):
+        _refuse_pair(q, s, what, rows, cols, dev)
+    # a single row's stride is free: what the kernels ask for
+    if rows == 1:
+        ld = (cols + 15) & ~15
+    return (q.data_ptr(), ld, s.data_ptr(), lds if sb > 1 else sr,
+            FP8_ROW if sr == rows else FP8_BLOCK)
+
+
+_NO_PAIR = (None, 0, None, 0)
+
+
+def _fp8_outs(rows, cols, dev, q, s, qt, st):
     """The eight output arguments and the group of a quantizing call."""
-    args, groups = [], []
-    for codes, scales, what, shape in ((q, s, "q", (rows, cols)),
-                                       (qt, st, "qt", (cols, rows))):
-        if codes is None:
-            args += [None, 0, None, 0]
-            continue
-        if scales is None:
-            raise ValueError(f"{what}: codes without scales")
-        _, _, p, ld, ps, lds, g = _fp8_pair(codes, scales, what, shape)
-        args += [p, ld, ps, lds]
-        # one row: 1×128 groups and 128×128 blocks have the same layout
-        groups.append((g, shape[0] == 1))
-    if not groups:
-        raise ValueError("neither q nor qt given")
-    sure = {g for g, either in groups if not either} or {FP8_ROW}
-    if len(sure) > 1:
+    if qt is None:
+        if q is None:
+            raise ValueError("neither q nor qt given")
+        a = _fp8_pair(q, s, "q", rows, cols, dev)
+        return a[:4] + _NO_PAIR, a[4]
+    b = _fp8_pair(qt, st, "qt", cols, rows, dev)
+    if q is None:
+        return _NO_PAIR + b[:4], b[4]
+    a = _fp8_pair(q, s, "q", rows, cols, dev)
+    # of a single row, 1×128 groups and 128×128 blocks have one layout
+    ga, gb = a[4] if rows > 1 else b[4], b[4] if cols > 1 else a[4]
+    if ga != gb:
         raise ValueError("q and qt have scales of different groups")
-    return args, sure.pop()
-
-
-def _same_device(first, *others):
-    import torch
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    return a[:4] + b[:4], ga
 
 
 def quantize_fp8_block(x, q=None, s=None, qt=None, st=None, stream=None):
     """Block-scaled E4M3 codes of x (bf16 or fp32 [rows, cols]) into (q, s),
     of its transpose into (qt, st); the scales' shape says whether a scale
     belongs to 128 elements of a row or to a 128×128 block."""
-    rows, cols, ld = _matrix(x, "x")
-    outs, group = _fp8_outs(rows, cols, q, s, qt, st)
-    _same_device(x, q, s, qt, st)
+    rows, cols, ld, dev = _matrix(x, "x")
+    outs, group = _fp8_outs(rows, cols, dev, q, s, qt, st)
     check(lib().tp_quantize_fp8_block(dtype_code(x), group, rows, cols,
                                       x.data_ptr(), ld, *outs,
-                                      stream_handle(stream)),
+                                      raw_stream(stream, dev)),
           "tp_quantize_fp8_block")
 
 
@@ -349,35 +387,42 @@ def _row_group(group, what):
         raise ValueError(f"{what} writes a scale for each row")
 
 
+def _gate_up(gu):
+    T, f2, ld, dev = _matrix(gu, "gu")
+    if gu.dtype is not torch.bfloat16:
+        raise TypeError(f"gu: bfloat16, got {gu.dtype}")
+    if f2 % 2:
+        raise ValueError(f"gu: an even number of columns, got {f2}")
+    return T, f2 // 2, ld, dev
+
+
 def swiglu_fp8_fwd(gu, q=None, s=None, qt=None, st=None, stream=None):
     """Codes of SiLU(G)⊙U ([T, f]) into (q, s), of its transpose into
     (qt, st); gu is [G | U], bf16 [T, 2f]."""
-    T, f2, ld = _matrix(gu, "gu")
-    _bf16(gu, "gu")
-    if f2 % 2:
-        raise ValueError(f"gu: an even number of columns, got {f2}")
-    outs, group = _fp8_outs(T, f2 // 2, q, s, qt, st)
-    _row_group(group, "swiglu_fp8_fwd")
-    _same_device(gu, q, s, qt, st)
-    check(lib().tp_swiglu_fp8_fwd(T, f2 // 2, gu.data_ptr(), ld, *outs,
-                                  stream_handle(stream)), "tp_swiglu_fp8_fwd")
+    T, f, ld, dev = _gate_up(gu)
+    outs, group = _fp8_outs(T, f, dev, q, s, qt, st)
+    if group != FP8_ROW and T > 1:
+        _row_group(group, "swiglu_fp8_fwd")
+    check(lib().tp_swiglu_fp8_fwd(T, f, gu.data_ptr(), ld, *outs,
+                                  raw_stream(stream, dev)),
+          "tp_swiglu_fp8_fwd")
 
 
 def swiglu_fp8_bwd(dA, gu, q=None, s=None, qt=None, st=None, stream=None):
     """Codes of [dG | dU] ([T, 2f]) into (q, s), of its transpose into
     (qt, st), from dA (bf16 [T, f]) and the forward's gu."""
-    T, f2, ld = _matrix(gu, "gu")
-    _bf16(gu, "gu")
-    _, _, ldda = _matrix(dA, "dA")
-    _bf16(dA, "dA", (T, f2 // 2))
-    if f2 % 2:
-        raise ValueError(f"gu: an even number of columns, got {f2}")
-    outs, group = _fp8_outs(T, f2, q, s, qt, st)
-    _row_group(group, "swiglu_fp8_bwd")
-    _same_device(gu, dA, q, s, qt, st)
-    check(lib().tp_swiglu_fp8_bwd(T, f2 // 2, dA.data_ptr(), ldda,
-                                  gu.data_ptr(), ld, *outs,
-                                  stream_handle(stream)), "tp_swiglu_fp8_bwd")
+    T, f, ld, dev = _gate_up(gu)
+    rows, cols, ldda, _ = _matrix(dA, "dA")
+    if dA.dtype is not torch.bfloat16:
+        raise TypeError(f"dA: bfloat16, got {dA.dtype}")
+    if rows != T or cols != f:
+        raise ValueError(f"dA: shape {(T, f)}, got {(rows, cols)}")
+    outs, group = _fp8_outs(T, 2 * f, dev, q, s, qt, st)
+    if group != FP8_ROW and T > 1:
+        _row_group(group, "swiglu_fp8_bwd")
+    check(lib().tp_swiglu_fp8_bwd(T, f, dA.data_ptr(), ldda, gu.data_ptr(),
+                                  ld, *outs, raw_stream(stream, dev)),
+          "tp_swiglu_fp8_bwd")
 
 
 def add_rmsnorm_fp8_fwd(x, r, gamma, x1, q, s, rstd, y=None, eps=1e-5,
@@ -385,42 +430,34 @@ def add_rmsnorm_fp8_fwd(x, r, gamma, x1, q, s, rstd, y=None, eps=1e-5,
     """x1 = x + r (r None: x1 is x and may be None), the codes of
     RMSNorm(x1)·γ into (q, s), rstd [T] fp32, and y (bf16, optional); x1 may
     be x or r."""
-    import torch
-    T, h, _ = _matrix(x, "x")
-    _bf16(gamma, "gamma", (h,))
-    for t, what in ((x, "x"), (r, "r"), (x1, "x1"), (y, "y")):
-        if t is not None:
-            _bf16(t, what, (T, h))
-            if not t.is_contiguous():
-                raise ValueError(f"{what}: dense rows")
-    if r is not None and x1 is None:
+    T, h, _, dev = _matrix(x, "x")
+    bf16, shape = torch.bfloat16, (T, h)
+    px = _dense(x, "x", bf16, shape, dev)
+    pr = None if r is None else _dense(r, "r", bf16, shape, dev)
+    p1 = None if x1 is None else _dense(x1, "x1", bf16, shape, dev)
+    py = None if y is None else _dense(y, "y", bf16, shape, dev)
+    pg = _dense(gamma, "gamma", bf16, (h,), dev)
+    prs = _dense(rstd, "rstd", torch.float32, (T,), dev)
+    if p1 is None and pr is not None:
         raise ValueError("x1: where the sum with r goes")
-    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (T,) or \
-            not rstd.is_contiguous() or not gamma.is_contiguous():
-        raise ValueError("rstd: dense float32 [T]; gamma: dense")
-    _, _, pq, ldq, ps, lds, group = _fp8_pair(q, s, "q", (T, h))
-    if T > 1:
+    pq, ldq, ps, lds, group = _fp8_pair(q, s, "q", T, h, dev)
+    if group != FP8_ROW and T > 1:
         _row_group(group, "add_rmsnorm_fp8_fwd")
-    _same_device(x, r, gamma, x1, q, s, rstd, y)
-    check(lib().tp_add_rmsnorm_fp8_fwd(T, h, eps, x.data_ptr(), ptr(r),
-                                       gamma.data_ptr(), ptr(x1), ptr(y),
-                                       rstd.data_ptr(), pq, ldq, ps, lds,
-                                       stream_handle(stream)),
+    check(lib().tp_add_rmsnorm_fp8_fwd(T, h, eps, px, pr, pg, p1, py, prs, pq,
+                                       ldq, ps, lds, raw_stream(stream, dev)),
           "tp_add_rmsnorm_fp8_fwd")
 
 
 def gemm_fp8_block(qa, sa, qb, sb, C, stream=None):
     """C[M, N] (bf16 or fp32) = A·Bᵀ of the block-scaled A = (qa, sa) [M, K]
     and B = (qb, sb) [N, K]."""
-    M, K, pa, lda, psa, ldsa, ga = _fp8_pair(qa, sa, "qa")
-    N, _, pb, ldb, psb, ldsb, gb = _fp8_pair(qb, sb, "qb", (qb.shape[0], K))
-    m, n, ldc = _matrix(C, "C")
-    if m != M or n != N:
-        raise ValueError(f"C: shape {(M, N)}, got {(m, n)}")
-    _same_device(C, qa, qb)
+    M, N, ldc, dev = _matrix(C, "C")
+    K = qa.shape[-1]
+    pa, lda, psa, ldsa, ga = _fp8_pair(qa, sa, "qa", M, K, dev)
+    pb, ldb, psb, ldsb, gb = _fp8_pair(qb, sb, "qb", N, K, dev)
     check(lib().tp_gemm_fp8_block(M, N, K, pa, lda, psa, ldsa, ga, pb, ldb,
                                   psb, ldsb, gb, dtype_code(C), C.data_ptr(),
-                                  ldc, stream_handle(stream)),
+                                  ldc, raw_stream(stream, dev)),
           "tp_gemm_fp8_block")
 
 

@@ -1284,7 +1284,8 @@ extern "C" tp_status tp_add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps,
     if (!aligned4(rstd)) return TP_ERR_ARG;
     return cuda_status(add_rmsnorm_fp8_fwd(T, h, eps, x, r, gamma, x1, y,
                                            rstd, static_cast<uint8_t*>(q),
-                                           ldq, s, lds, stream));
+                                           ldq, s, lds, device_status_ptr(),
+                                           stream));
   });
 }
 

@@ -155,6 +155,17 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst,
       : "memory");
 }
 
+// Bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
+// from global memory into this CTA's shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_g2s(void* dst, const void* src,
+                                         uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 4-byte asynchronous copy to shared memory, zero where !in (nothing is read
 // then); commit closes a group, wait<n> returns when at most the n newest
 // groups of this thread are open.

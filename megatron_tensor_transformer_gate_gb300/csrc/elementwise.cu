@@ -463,17 +463,6 @@ __global__ void __launch_bounds__(512, 1)
                         dgacc + j * V);
 }
 
-// Bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
-// from global memory into this CTA's shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_g2s(void* dst, const void* src,
-                                         uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // rmsnorm_bwd_kernel<T, NV, true> for rows whose n shard partials fit in
 // shared memory: one thread copies the n partial rows of the next row into
 // shared memory by bulk copies (the bytes in flight are the copy engine's,

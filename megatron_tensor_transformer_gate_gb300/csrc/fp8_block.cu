@@ -35,10 +35,33 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* v) {
   v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
   v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
 }
-// Eight elements; those at and beyond `valid` are 0 and not read.
-__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int valid,
-                                       bool vec) {
-  if (vec && valid >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
+// 16 bytes in pieces of W that are W-aligned.
+template <int W>
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 u;
+  if constexpr (W == 16) {
+    u = __ldg(static_cast<const uint4*>(p));
+  } else if constexpr (W == 8) {
+    const uint2 a = __ldg(static_cast<const uint2*>(p)),
+                b = __ldg(static_cast<const uint2*>(p) + 1);
+    u = make_uint4(a.x, a.y, b.x, b.y);
+  } else if constexpr (W == 4) {
+    const uint32_t* w = static_cast<const uint32_t*>(p);
+    u = make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+  } else {
+    const uint16_t* h = static_cast<const uint16_t*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = (uint32_t)__ldg(h + 2 * j) | ((uint32_t)__ldg(h + 2 * j + 1) << 16);
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return u;
+}
+// Eight bf16; those at and beyond `valid` are 0 and not read.
+template <int W>
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int valid) {
+  if (valid >= 8) return load16<W>(p);
   uint32_t w[4] = {0, 0, 0, 0};
   const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
@@ -46,35 +69,53 @@ __device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int valid,
     if (j < valid) w[j >> 1] |= (uint32_t)h[j] << (16 * (j & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+template <int W>
+__device__ __forceinline__ void save8(__nv_bfloat16* p, const uint4& u,
+                                      int valid) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if (W == 16 && valid >= 8) {
+    *reinterpret_cast<uint4*>(p) = u;
+  } else if (W == 8 && valid >= 8) {
+    reinterpret_cast<uint2*>(p)[0] = make_uint2(u.x, u.y);
+    reinterpret_cast<uint2*>(p)[1] = make_uint2(u.z, u.w);
+  } else if (W == 4 && valid >= 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(p)[j] = w[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < valid)
+        reinterpret_cast<uint16_t*>(p)[j] =
+            (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+  }
+}
 
-// A source: raw() loads eight columns of a row (columns at and beyond `cols`
+// A source: raw() loads eight columns of a row (W: the bytes that its rows'
+// starts and pitch are multiples of, at most 16) (columns at and beyond `cols`
 // give 0), value() makes them fp32.
+template <int W>
 struct CopyBf16 {
   static constexpr int RAW = 1, R = 8, BATCH = 8, CTAS = 4;
   const __nv_bfloat16* x;
   int64_t ld;
-  bool vec;
   __device__ __forceinline__ void raw(int64_t r, int64_t c, int64_t cols,
                                       uint4* u) const {
-    u[0] = load8(x + r * ld + c, (int)(cols - c < 8 ? cols - c : 8), vec);
-  }
-  __device__ __forceinline__ void value(const uint4* u, int64_t, float* v) const {
-    unpack8(u[0], v);
+    u[0] = load8<W>(x + r * ld + c, (int)(cols - c < 8 ? cols - c : 8));
   }
   __device__ int64_t col_tile(int64_t j, int64_t) const { return j; }
 };
 
+template <int W>
 struct CopyF32 {
   static constexpr int RAW = 2, R = 4, BATCH = 4, CTAS = 2;
   const float* x;
   int64_t ld;
-  bool vec;
   __device__ __forceinline__ void raw(int64_t r, int64_t c, int64_t cols,
                                       uint4* u) const {
     const float* p = x + r * ld + c;
-    if (vec && cols - c >= 8) {
-      u[0] = __ldg(reinterpret_cast<const uint4*>(p));
-      u[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    if (cols - c >= 8) {
+      u[0] = load16<W>(p);
+      u[1] = load16<W>(p + 4);
     } else {
       uint32_t w[8];
 #pragma unroll
@@ -100,7 +141,7 @@ __device__ __forceinline__ float sigmoid_approx(float x) {
 }
 
 // A = SiLU(G)·U.
-template <bool VEC>   // 16-byte loads: f a multiple of 8, rows aligned
+template <int W>
 struct SwigluSource {
   static constexpr int RAW = 2, R = 4, BATCH = 4, CTAS = 2;
   const __nv_bfloat16* gu;
@@ -109,8 +150,8 @@ struct SwigluSource {
                                       uint4* u) const {
     const int valid = (int)(cols - c < 8 ? cols - c : 8);
     const __nv_bfloat16* p = gu + r * ld + c;
-    u[0] = load8(p, VEC ? 8 : valid, VEC);
-    u[1] = load8(p + f, VEC ? 8 : valid, VEC);
+    u[0] = load8<W>(p, W == 16 ? 8 : valid);   // W = 16: f a multiple of 8
+    u[1] = load8<W>(p + f, W == 16 ? 8 : valid);
   }
   __device__ __forceinline__ void value(const uint4* x, int64_t, float* v) const {
     float g[8], u[8];
@@ -125,7 +166,7 @@ struct SwigluSource {
 // [dG | dU]: dG = dA·U·s·(1 + G·(1 − s)), dU = dA·G·s with s = σ(G).  The
 // multiplier of the up side is read for dG alone; which side a column is on
 // may change inside eight columns when f is not a multiple of 8.
-template <bool VEC>
+template <bool VEC>   // 16-byte loads: f a multiple of 8, rows aligned
 struct SwigluBwdSource {
   static constexpr int RAW = 3, R = 4, BATCH = 2, CTAS = 2;
   const __nv_bfloat16 *da, *gu;
@@ -224,11 +265,12 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   memcpy(&a, &x, 4);
   return a;
 }
-template <>
-struct Held<CopyBf16> {
+template <int W>
+struct Held<CopyBf16<W>> {
+  static constexpr int R = 8;
   uint4 u[8];
-  __device__ __forceinline__ void take(const CopyBf16&, int i, const uint4* x,
-                                       int64_t) {
+  __device__ __forceinline__ void take(const CopyBf16<W>&, int i,
+                                       const uint4* x, int64_t) {
     u[i] = x[0];
   }
   __device__ __forceinline__ void row(int i, float* o) const { unpack8(u[i], o); }
@@ -277,38 +319,29 @@ __device__ __forceinline__ uint2 codes8(const float* v, float f) {
   return c;
 }
 
-// A row's codes leave as 16 lanes × 8 bytes; a column's largest magnitude
-// takes one shuffle and one pass through shared memory; R rows of a column
-// pack into one R-byte shared-memory store of the transposed tile, whose rows
-// then leave the same way.
-template <typename SRC, int GROUP>
-__global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
-    quantize_tile_kernel(const SRC src, int64_t rows, int64_t cols,
-                         int64_t col_tiles, const Fp8BlockOut o) {
-  constexpr int R = SRC::R, WARPS = 64 / R;
-  __shared__ __align__(16) float cmax[WARPS][TILE];
-  __shared__ __align__(16) uint8_t tile_t[TILE * TILE];
+// Scratch of a CTA: the warps' column maxima, the transposed codes.
+template <int R>
+struct TileScratch {
+  __align__(16) float cmax[64 / R][TILE];
+  __align__(16) uint8_t t[TILE * TILE];
+};
+
+// The codes and scales of tile (rt, ct).  A row's codes leave as 16 lanes × 8
+// bytes; a column's largest magnitude takes one shuffle and one pass through
+// shared memory; R rows of a column pack into one R-byte shared-memory store
+// of the transposed tile, whose rows then leave the same way.
+template <int GROUP, typename H>
+__device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
+                                          int64_t rows, int64_t cols,
+                                          int64_t rt, int64_t ct,
+                                          TileScratch<H::R>& sm) {
+  constexpr int R = H::R, WARPS = 64 / R;
+  float(&cmax)[WARPS][TILE] = sm.cmax;
+  uint8_t* tile_t = sm.t;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = lane >> 4, l = lane & 15;
-  const int64_t rt = blockIdx.x / col_tiles;
-  const int64_t ct = src.col_tile(blockIdx.x - rt * col_tiles, col_tiles);
   const int64_t r0 = rt * TILE + (warp * 2 + half) * R;
   const int64_t c0 = ct * TILE + l * 8;
-
-  Held<SRC> h;
-#pragma unroll
-  for (int b = 0; b < R; b += SRC::BATCH) {
-    uint4 u[SRC::BATCH][SRC::RAW];
-#pragma unroll
-    for (int i = 0; i < SRC::BATCH; ++i) {
-#pragma unroll
-      for (int k = 0; k < SRC::RAW; ++k) u[i][k] = make_uint4(0, 0, 0, 0);
-      if (r0 + b + i < rows && c0 < cols) src.raw(r0 + b + i, c0, cols, u[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < SRC::BATCH; ++i) h.take(src, b + i, u[i], c0);
-  }
-
   float colr[8];   // the factor of each of this thread's columns
   float rowr[R];   // and of each of its rows
   if (GROUP == kFp8Row) {
@@ -418,7 +451,89 @@ __global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
   }
 }
 
-template <typename SRC>
+template <typename SRC, int GROUP>
+__global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
+    quantize_tile_kernel(const SRC src, int64_t rows, int64_t cols,
+                         int64_t col_tiles, const Fp8BlockOut o) {
+  constexpr int R = SRC::R;
+  __shared__ TileScratch<R> sm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t rt = blockIdx.x / col_tiles;
+  const int64_t ct = src.col_tile(blockIdx.x - rt * col_tiles, col_tiles);
+  const int64_t r0 = rt * TILE + (warp * 2 + (lane >> 4)) * R;
+  const int64_t c0 = ct * TILE + (lane & 15) * 8;
+
+  Held<SRC> h;
+#pragma unroll
+  for (int b = 0; b < R; b += SRC::BATCH) {
+    uint4 u[SRC::BATCH][SRC::RAW];
+#pragma unroll
+    for (int i = 0; i < SRC::BATCH; ++i) {
+#pragma unroll
+      for (int k = 0; k < SRC::RAW; ++k) u[i][k] = make_uint4(0, 0, 0, 0);
+      if (r0 + b + i < rows && c0 < cols) src.raw(r0 + b + i, c0, cols, u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < SRC::BATCH; ++i) h.take(src, b + i, u[i], c0);
+  }
+  emit_tile<GROUP>(h, o, rows, cols, rt, ct, sm);
+}
+
+// The SwiGLU backward where dG's and dU's tiles line up (f a multiple of 128):
+// one CTA makes both from one read of dA, G and U and one σ; dU waits in
+// shared memory, each thread's in its own slots, while dG leaves.
+struct Fp32Rows {
+  static constexpr int R = 4;
+};
+constexpr int PAIR_SMEM = 128 * 128 * 4;
+__global__ void __launch_bounds__(512, 2)
+    swiglu_bwd_pair_kernel(const SwigluBwdSource<true> src, int64_t rows,
+                           int64_t pairs, const Fp8BlockOut o) {
+  extern __shared__ float4 kept[];   // [row][half of eight][thread]
+  __shared__ TileScratch<4> sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t rt = blockIdx.x / pairs, ct = blockIdx.x - rt * pairs;
+  const int64_t r0 = rt * TILE + (warp * 2 + (lane >> 4)) * 4;
+  const int64_t c0 = ct * TILE + (lane & 15) * 8;
+  Held<Fp32Rows> h;
+#pragma unroll
+  for (int b = 0; b < 4; b += 2) {
+    uint4 x[2][3];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) x[i][k] = make_uint4(0, 0, 0, 0);
+      if (r0 + b + i < rows) src.raw(r0 + b + i, c0, 2 * src.f, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float a[8], g[8], u[8];
+      unpack8(x[i][0], a);
+      unpack8(x[i][1], g);
+      unpack8(x[i][2], u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = sigmoid_approx(g[j]);
+        h.v[b + i][j] = a[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
+        u[j] = a[j] * g[j] * s;
+      }
+      kept[((b + i) * 2) * 512 + tid] = make_float4(u[0], u[1], u[2], u[3]);
+      kept[((b + i) * 2 + 1) * 512 + tid] = make_float4(u[4], u[5], u[6], u[7]);
+    }
+  }
+  emit_tile<kFp8Row>(h, o, rows, 2 * src.f, rt, ct, sm);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 a = kept[(i * 2) * 512 + tid], b = kept[(i * 2 + 1) * 512 + tid];
+    h.v[i][0] = a.x; h.v[i][1] = a.y; h.v[i][2] = a.z; h.v[i][3] = a.w;
+    h.v[i][4] = b.x; h.v[i][5] = b.y; h.v[i][6] = b.z; h.v[i][7] = b.w;
+  }
+  __syncthreads();   // the scratch is read
+  emit_tile<kFp8Row>(h, o, rows, 2 * src.f, rt, pairs + ct, sm);
+}
+
+// BLOCKS: whether the source is also quantized in 128×128 blocks.
+template <bool BLOCKS, typename SRC>
 int launch_tiles(const SRC& src, int group, int64_t rows, int64_t cols,
                  const Fp8BlockOut& o, double bytes, cudaStream_t s) {
   const int64_t ct = (cols + TILE - 1) / TILE, rt = (rows + TILE - 1) / TILE;
@@ -426,10 +541,10 @@ int launch_tiles(const SRC& src, int group, int64_t rows, int64_t cols,
   const unsigned grid = (unsigned)(ct * rt);
   {
     ProfScope ps(s, KF_QUANT, 0.0, bytes);
-    if (group == kFp8Row)
+    if (!BLOCKS || group == kFp8Row)
       quantize_tile_kernel<SRC, kFp8Row>
           <<<grid, 2048 / SRC::R, 0, s>>>(src, rows, cols, ct, o);
-    else
+    else if constexpr (BLOCKS)
       quantize_tile_kernel<SRC, kFp8Block>
           <<<grid, 2048 / SRC::R, 0, s>>>(src, rows, cols, ct, o);
   }
@@ -437,8 +552,11 @@ int launch_tiles(const SRC& src, int group, int64_t rows, int64_t cols,
   return cudaGetLastError();
 }
 
-bool vec_rows(const void* p, int64_t ld, int elem) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * elem) % 16 == 0;
+// The largest power of two, at most 16, that the address and the byte pitch
+// are multiples of (a null address is a multiple of any).
+int width(const void* p, int64_t pitch) {
+  const uint64_t m = reinterpret_cast<uintptr_t>(p) | (uint64_t)pitch | 16u;
+  return (int)(m & -m);
 }
 
 double out_bytes(const Fp8BlockOut& o, int64_t rows, int64_t cols) {
@@ -446,111 +564,282 @@ double out_bytes(const Fp8BlockOut& o, int64_t rows, int64_t cols) {
 }
 
 // ----------------------------------------------------- residual + RMSNorm --
-// One CTA per row, which stays in registers: V vectors of eight columns a
-// thread, 16 neighbouring threads hold one group of 128.  γ is read before the
-// row's sum is known, so that its latency is not paid after the barrier.
-template <int THREADS, int V, int CTAS, bool VEC>
-__global__ void __launch_bounds__(THREADS, CTAS)
-    add_rmsnorm_fp8_kernel(const __nv_bfloat16* x, const __nv_bfloat16* r,
-                           const __nv_bfloat16* __restrict__ gamma,
-                           __nv_bfloat16* x1, __nv_bfloat16* y,
-                           float* __restrict__ rstd, uint8_t* q, int64_t ldq,
-                           float* s, int64_t lds, int h, float eps) {
-  __shared__ float red[THREADS / 32];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
+struct NormArgs {
   // x1 may be x or r: no read-only loads, and each element is read before it
   // is written, by the same thread
-  auto load = [&](const __nv_bfloat16* p, int c) -> uint4 {
-    if (VEC) return *reinterpret_cast<const uint4*>(p + c);
-    uint32_t w[4] = {0, 0, 0, 0};
+  const __nv_bfloat16 *x, *r, *gamma;
+  __nv_bfloat16 *x1, *y;
+  float* rstd;
+  uint8_t* q;
+  int64_t ldq;
+  float* s;
+  int64_t lds;
+  int64_t rows;
+  int h;
+  float eps;
+  unsigned* status;
+};
+
+// u + ur rounded to bf16 (the stored stream is what is normed), and its sum
+// of squares.
+__device__ __forceinline__ float add_squares(uint4& u, const uint4& ur,
+                                             bool add) {
+  float a[8];
+  if (add) {
+    float b[8];
+    unpack8(u, a);
+    unpack8(ur, b);
+    u.x = pack_bf16x2(a[0] + b[0], a[1] + b[1]);
+    u.y = pack_bf16x2(a[2] + b[2], a[3] + b[3]);
+    u.z = pack_bf16x2(a[4] + b[4], a[5] + b[5]);
+    u.w = pack_bf16x2(a[6] + b[6], a[7] + b[7]);
+  }
+  unpack8(u, a);
+  float ss = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < h)
-        w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[c + j]
-                     << (16 * (j & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  };
-  auto save = [&](__nv_bfloat16* p, int c, const uint4& u) {
-    if (VEC) {
-      *reinterpret_cast<uint4*>(p + c) = u;
-    } else {
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  for (int j = 0; j < 8; ++j) ss += a[j] * a[j];
+  return ss;
+}
+
+// Eight columns of a normed row: codes, the scale of the 16 lanes' 128
+// columns, y.  All lanes of a half-warp call it; valid ≤ 0 writes nothing.
+template <int W>
+__device__ __forceinline__ void emit_norm(const NormArgs& p, int64_t row,
+                                          int c, int valid, const uint4& u,
+                                          const uint4& g, float rs) {
+  float v[8], gm[8];
+  unpack8(u, v);
+  unpack8(g, gm);
+  float m = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < h)
-          reinterpret_cast<uint16_t*>(p)[c + j] =
-              (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-    }
-  };
+  for (int j = 0; j < 8; ++j) {
+    v[j] = v[j] * rs * gm[j];
+    m = fmaxf(m, fabsf(v[j]));
+  }
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1)
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (valid <= 0) return;
+  store8(p.q + row * p.ldq + c, codes8(v, block_factor(m)), valid);
+  if ((threadIdx.x & 15) == 0) p.s[(c >> 7) * p.lds + row] = block_scale(m);
+  if (p.y != nullptr)
+    save8<W>(p.y + row * p.h + c,
+             make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                        pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])),
+             valid);
+}
+
+template <int W>
+__device__ __forceinline__ uint4 load8_plain(const __nv_bfloat16* p,
+                                             int valid) {
+  if (W == 16 && valid >= 8) return *reinterpret_cast<const uint4*>(p);
+  if (W == 8 && valid >= 8) {
+    const uint2 a = reinterpret_cast<const uint2*>(p)[0],
+                b = reinterpret_cast<const uint2*>(p)[1];
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < valid)
+      w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[j]
+                   << (16 * (j & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// THREADS threads a row, which stays in their registers (V vectors of eight
+// columns each, 16 neighbouring threads hold one group of 128); a warp per
+// row (eight rows a CTA) up to 1024 columns, else a CTA per row.  γ is read
+// before the row's sum is known, so that its latency is not paid after it.
+template <int THREADS, int V, int CTAS, int W>
+__global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
+    add_rmsnorm_fp8_kernel(const NormArgs p) {
+  constexpr bool WARP = THREADS == 32;
+  __shared__ float red[THREADS / 32];
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row =
+      WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && row >= p.rows) return;
+  const int h = p.h;
+  const __nv_bfloat16* x = p.x + row * h;
+  const __nv_bfloat16* r = p.r + row * h;
   uint4 u[V], ur[V], g[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = (k * THREADS + tid) * 8;
     u[k] = ur[k] = make_uint4(0, 0, 0, 0);
     if (c < h) {
-      u[k] = load(x + row * h, c);
-      if (r != nullptr) ur[k] = load(r + row * h, c);
+      u[k] = load8_plain<W>(x + c, h - c);
+      if (p.r != nullptr) ur[k] = load8_plain<W>(r + c, h - c);
     }
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = (k * THREADS + tid) * 8;
     g[k] = make_uint4(0, 0, 0, 0);
-    if (c < h) g[k] = load8(gamma + c, h - c < 8 ? h - c : 8, VEC);
+    if (c < h) g[k] = load8<W>(p.gamma + c, h - c);
   }
   float ss = 0.0f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = (k * THREADS + tid) * 8;
-    if (r != nullptr) {   // the stored stream is what is normed
-      float a[8], b[8];
-      unpack8(u[k], a);
-      unpack8(ur[k], b);
-      u[k].x = pack_bf16x2(a[0] + b[0], a[1] + b[1]);
-      u[k].y = pack_bf16x2(a[2] + b[2], a[3] + b[3]);
-      u[k].z = pack_bf16x2(a[4] + b[4], a[5] + b[5]);
-      u[k].w = pack_bf16x2(a[6] + b[6], a[7] + b[7]);
-    }
-    if (x1 != nullptr && c < h) save(x1 + row * h, c, u[k]);
-    float a[8];
-    unpack8(u[k], a);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss += a[j] * a[j];
+    ss += add_squares(u[k], ur[k], p.r != nullptr);
+    if (p.x1 != nullptr && c < h) save8<W>(p.x1 + row * h + c, u[k], h - c);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-  if ((tid & 31) == 0) red[tid >> 5] = ss;
-  __syncthreads();
-  float tot = 0.0f;
+  if (!WARP) {
+    if ((tid & 31) == 0) red[tid >> 5] = ss;
+    __syncthreads();
+    ss = 0.0f;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) tot += red[w];
-  const float rs = rsqrtf(tot / (float)h + eps);
-  if (tid == 0) rstd[row] = rs;
+    for (int w = 0; w < THREADS / 32; ++w) ss += red[w];
+  }
+  const float rs = rsqrtf(ss / (float)h + p.eps);
+  if (tid == 0) p.rstd[row] = rs;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = (k * THREADS + tid) * 8;
-    float v[8], gm[8];
-    unpack8(u[k], v);
-    unpack8(g[k], gm);
-    float m = 0.0f;
+    emit_norm<W>(p, row, c, h - c, u[k], g[k], rs);
+  }
+}
+
+// Many rows of 16-byte aligned vectors: a CTA works through every gridDim-th
+// row, thread 0 copying x and r of the rows to come into a ring of STAGES
+// stages (bulk copies), so that loads are in flight all the time and γ is
+// read once.  Waits are bounded; the block agrees on every outcome.
+template <int V, int CTAS, int STAGES>
+__global__ void __launch_bounds__(512, CTAS)
+    add_rmsnorm_fp8_staged_kernel(const NormArgs p) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ uint64_t full[STAGES];
+  __shared__ float red[2][16];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, h = p.h;
+  const int nin = p.r != nullptr ? 2 : 1;
+  const uint32_t row_bytes = (uint32_t)h * 2;
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  auto issue = [&](int64_t row, int sg) {
+    uint8_t* d = ring + (size_t)sg * nin * row_bytes;
+    mbar_arrive_expect_tx(&full[sg], nin * row_bytes);
+    bulk_g2s(d, p.x + row * h, row_bytes, &full[sg]);
+    if (nin == 2) bulk_g2s(d + row_bytes, p.r + row * h, row_bytes, &full[sg]);
+  };
+  const int64_t step = gridDim.x;
+  if (tid == 0)
+    for (int i = 0; i < STAGES; ++i)
+      if (blockIdx.x + i * step < p.rows) issue(blockIdx.x + i * step, i);
+  uint4 g[V];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = v[j] * rs * gm[j];
-      m = fmaxf(m, fabsf(v[j]));
+  for (int k = 0; k < V; ++k) {
+    const int c = (k * 512 + tid) * 8;
+    g[k] = c < h ? load16<16>(p.gamma + c) : make_uint4(0, 0, 0, 0);
+  }
+  int sg = 0;
+  uint32_t par = 0;
+  int64_t row = blockIdx.x;
+  bool odd = false;
+  for (; row < p.rows; row += step) {
+    const bool got = mbar_wait(&full[sg], par,
+                               reinterpret_cast<volatile int*>(&abort_flag),
+                               p.status, 61);
+    if (!__syncthreads_and(got)) break;
+    const uint8_t* in = ring + (size_t)sg * nin * row_bytes;
+    uint4 u[V];
+    float ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = (k * 512 + tid) * 8;
+      u[k] = make_uint4(0, 0, 0, 0);
+      uint4 ur = u[k];
+      if (c < h) {
+        u[k] = *reinterpret_cast<const uint4*>(in + c * 2);
+        if (nin == 2)
+          ur = *reinterpret_cast<const uint4*>(in + row_bytes + c * 2);
+      }
+      ss += add_squares(u[k], ur, nin == 2);
+      if (p.x1 != nullptr && c < h)
+        *reinterpret_cast<uint4*>(p.x1 + row * h + c) = u[k];
     }
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1)
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (c < h) {
-      store8(q + row * ldq + c, codes8(v, block_factor(m)), VEC ? 8 : h - c);
-      if ((tid & 15) == 0) s[(c >> 7) * lds + row] = block_scale(m);
-      if (y != nullptr)
-        save(y + row * h, c,
-             make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                        pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+    for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    if ((tid & 31) == 0) red[odd][tid >> 5] = ss;
+    __syncthreads();   // the sums are there, the stage is read
+    if (tid == 0 && row + STAGES * step < p.rows) issue(row + STAGES * step, sg);
+    ss = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) ss += red[odd][w];
+    odd = !odd;
+    const float rs = rsqrtf(ss / (float)h + p.eps);
+    if (tid == 0) p.rstd[row] = rs;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = (k * 512 + tid) * 8;
+      emit_norm<16>(p, row, c, h - c, u[k], g[k], rs);
+    }
+    if (++sg == STAGES) {
+      sg = 0;
+      par ^= 1;
     }
   }
+  if (row < p.rows && tid == 0) {
+    // gave up: let the copies in flight land before the block exits
+    volatile int no_abort = 0;
+    for (int i = 0; i < STAGES && row + i * step < p.rows; ++i) {
+      mbar_wait(&full[sg], par, &no_abort, nullptr, 0);
+      if (++sg == STAGES) {
+        sg = 0;
+        par ^= 1;
+      }
+    }
+  }
+}
+
+template <int V, int CTAS, int STAGES>
+int launch_norm_staged(const NormArgs& p, cudaStream_t s) {
+  static bool done[64];
+  auto kernel = add_rmsnorm_fp8_staged_kernel<V, CTAS, STAGES>;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !done[dev]) {
+    // V vectors of 16 bytes for 512 threads, x and r
+    err = cudaFuncSetAttribute(kernel,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               STAGES * 2 * V * 512 * 16);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) done[dev] = true;
+  }
+  const size_t smem = (size_t)STAGES * (p.r != nullptr ? 2 : 1) * p.h * 2;
+  const int64_t grid =
+      std::min<int64_t>(p.rows, (int64_t)device_sm_count() * CTAS);
+  kernel<<<(unsigned)grid, 512, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int W>
+int launch_norm(const NormArgs& p, cudaStream_t s) {
+  const unsigned T = (unsigned)p.rows;
+  if (p.h <= 256)
+    add_rmsnorm_fp8_kernel<32, 1, 4, W><<<(T + 7) / 8, 256, 0, s>>>(p);
+  else if (p.h <= 512)
+    add_rmsnorm_fp8_kernel<32, 2, 4, W><<<(T + 7) / 8, 256, 0, s>>>(p);
+  else if (p.h <= 1024)
+    add_rmsnorm_fp8_kernel<32, 4, 3, W><<<(T + 7) / 8, 256, 0, s>>>(p);
+  else if (p.h <= 2048)
+    add_rmsnorm_fp8_kernel<256, 1, 4, W><<<T, 256, 0, s>>>(p);
+  else if (p.h <= 4096)
+    add_rmsnorm_fp8_kernel<512, 1, 2, W><<<T, 512, 0, s>>>(p);
+  else if (p.h <= 8192)
+    add_rmsnorm_fp8_kernel<512, 2, 2, W><<<T, 512, 0, s>>>(p);
+  else
+    add_rmsnorm_fp8_kernel<1024, 2, 1, W><<<T, 1024, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -559,15 +848,24 @@ int quantize_fp8_block(int dtype, int group, int64_t rows, int64_t cols,
                        const void* x, int64_t ldx, const Fp8BlockOut& o,
                        void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int es = dtype == 0 ? 4 : 2;
+  const double bytes = (double)es * rows * cols + out_bytes(o, rows, cols);
+  auto go = [&](const auto& src) {
+    return launch_tiles<true>(src, group, rows, cols, o, bytes, s);
+  };
+  const int w = width(x, ldx * es);
   if (dtype == 0) {
-    const CopyF32 src{static_cast<const float*>(x), ldx, vec_rows(x, ldx, 4)};
-    return launch_tiles(src, group, rows, cols, o,
-                        4.0 * rows * cols + out_bytes(o, rows, cols), s);
+    const auto* p = static_cast<const float*>(x);
+    if (w == 16) return go(CopyF32<16>{p, ldx});
+    return go(CopyF32<4>{p, ldx});
   }
-  const CopyBf16 src{static_cast<const __nv_bfloat16*>(x), ldx,
-                     vec_rows(x, ldx, 2)};
-  return launch_tiles(src, group, rows, cols, o,
-                      2.0 * rows * cols + out_bytes(o, rows, cols), s);
+  const auto* p = static_cast<const __nv_bfloat16*>(x);
+  switch (w) {
+    case 16: return go(CopyBf16<16>{p, ldx});
+    case 8: return go(CopyBf16<8>{p, ldx});
+    case 4: return go(CopyBf16<4>{p, ldx});
+    default: return go(CopyBf16<2>{p, ldx});
+  }
 }
 
 int swiglu_fp8_fwd(int64_t T, int64_t f, const void* gu, int64_t ldgu,
@@ -575,11 +873,15 @@ int swiglu_fp8_fwd(int64_t T, int64_t f, const void* gu, int64_t ldgu,
   const auto* x = static_cast<const __nv_bfloat16*>(gu);
   const double bytes = 4.0 * T * f + out_bytes(o, T, f);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (vec_rows(gu, ldgu, 2) && f % 8 == 0)
-    return launch_tiles(SwigluSource<true>{x, ldgu, f}, kFp8Row, T, f, o, bytes,
-                        s);
-  return launch_tiles(SwigluSource<false>{x, ldgu, f}, kFp8Row, T, f, o, bytes,
-                      s);
+  auto go = [&](const auto& src) {
+    return launch_tiles<false>(src, kFp8Row, T, f, o, bytes, s);
+  };
+  switch (std::min(width(gu, ldgu * 2), width(nullptr, f * 2))) {
+    case 16: return go(SwigluSource<16>{x, ldgu, f});
+    case 8: return go(SwigluSource<8>{x, ldgu, f});
+    case 4: return go(SwigluSource<4>{x, ldgu, f});
+    default: return go(SwigluSource<2>{x, ldgu, f});
+  }
 }
 
 int swiglu_fp8_bwd(int64_t T, int64_t f, const void* da, int64_t ldda,
@@ -589,53 +891,69 @@ int swiglu_fp8_bwd(int64_t T, int64_t f, const void* da, int64_t ldda,
   const auto* x = static_cast<const __nv_bfloat16*>(gu);
   const double bytes = 6.0 * T * f + out_bytes(o, T, 2 * f);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (vec_rows(gu, ldgu, 2) && vec_rows(da, ldda, 2) && f % 8 == 0)
-    return launch_tiles(SwigluBwdSource<true>{a, x, ldda, ldgu, f}, kFp8Row, T,
-                        2 * f, o, bytes, s);
-  return launch_tiles(SwigluBwdSource<false>{a, x, ldda, ldgu, f}, kFp8Row, T,
-                      2 * f, o, bytes, s);
+  if (width(gu, ldgu * 2) < 16 || width(da, ldda * 2) < 16 || f % 8)
+    return launch_tiles<false>(SwigluBwdSource<false>{a, x, ldda, ldgu, f},
+                               kFp8Row, T, 2 * f, o, bytes, s);
+  const SwigluBwdSource<true> src{a, x, ldda, ldgu, f};
+  if (f % TILE)
+    return launch_tiles<false>(src, kFp8Row, T, 2 * f, o, bytes, s);
+  static bool done[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !done[dev]) {
+    err = cudaFuncSetAttribute(swiglu_bwd_pair_kernel,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               PAIR_SMEM);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) done[dev] = true;
+  }
+  const int64_t pairs = f / TILE, rt = (T + TILE - 1) / TILE;
+  {
+    ProfScope ps(s, KF_QUANT, 0.0, bytes);
+    swiglu_bwd_pair_kernel<<<(unsigned)(pairs * rt), 512, PAIR_SMEM, s>>>(
+        src, T, pairs, o);
+  }
+  count_launch();
+  return cudaGetLastError();
 }
 
 int add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps, const void* x,
                         const void* r, const void* gamma, void* x1, void* y,
                         float* rstd, uint8_t* q, int64_t ldq, float* s,
-                        int64_t lds, void* stream) {
+                        int64_t lds, unsigned* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto bf = [](const void* p) { return static_cast<const __nv_bfloat16*>(p); };
-  auto al = [](const void* p) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;   // null counts
-  };
-  const bool vec =
-      h % 8 == 0 && al(x) && al(r) && al(gamma) && al(x1) && al(y);
-  auto* o1 = static_cast<__nv_bfloat16*>(x1);
-  auto* oy = static_cast<__nv_bfloat16*>(y);
+  const NormArgs p{bf(x), bf(r), bf(gamma), static_cast<__nv_bfloat16*>(x1),
+                   static_cast<__nv_bfloat16*>(y), rstd, q, ldq, s, lds, T,
+                   (int)h, eps, status};
+  int w = width(gamma, h * 2);
+  for (const void* a : {x, r, (const void*)x1, (const void*)y})
+    w = std::min(w, width(a, 0));
+  int err;
   {
     ProfScope ps(st, KF_NORM, 4.0 * T * h,
                  (2.0 + 2.0 * (r != nullptr) + 2.0 * (x1 != nullptr) +
                   2.0 * (y != nullptr) + 1.0) * T * h);
-    auto go = [&](auto vec_kernel, auto any_kernel, int threads) {
-      auto k = vec ? vec_kernel : any_kernel;
-      k<<<(unsigned)T, threads, 0, st>>>(bf(x), bf(r), bf(gamma), o1, oy, rstd,
-                                         q, ldq, s, lds, (int)h, eps);
-    };
-    if (h <= 1024)
-      go(add_rmsnorm_fp8_kernel<128, 1, 12, true>,
-         add_rmsnorm_fp8_kernel<128, 1, 8, false>, 128);
-    else if (h <= 2048)
-      go(add_rmsnorm_fp8_kernel<256, 1, 6, true>,
-         add_rmsnorm_fp8_kernel<256, 1, 4, false>, 256);
-    else if (h <= 4096)
-      go(add_rmsnorm_fp8_kernel<512, 1, 3, true>,
-         add_rmsnorm_fp8_kernel<512, 1, 2, false>, 512);
-    else if (h <= 8192)
-      go(add_rmsnorm_fp8_kernel<512, 2, 3, true>,
-         add_rmsnorm_fp8_kernel<512, 2, 2, false>, 512);
-    else
-      go(add_rmsnorm_fp8_kernel<1024, 2, 1, true>,
-         add_rmsnorm_fp8_kernel<1024, 2, 1, false>, 1024);
+    // The ring pays where a CTA has several rows to run ahead on.
+    const bool many = T >= 4 * (int64_t)device_sm_count();
+    if (w == 16 && h > 1024 && many) {
+      if (h <= 4096)
+        err = launch_norm_staged<1, 3, 4>(p, st);
+      else if (h <= 8192)
+        err = launch_norm_staged<2, 2, 3>(p, st);
+      else
+        err = launch_norm_staged<4, 1, 3>(p, st);
+    } else if (w == 16) {
+      err = launch_norm<16>(p, st);
+    } else if (w == 8) {
+      err = launch_norm<8>(p, st);
+    } else {
+      err = launch_norm<2>(p, st);
+    }
   }
   count_launch();
-  return cudaGetLastError();
+  return err;
 }
 
 }  // namespace tp

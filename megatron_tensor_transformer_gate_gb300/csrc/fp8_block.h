@@ -43,7 +43,7 @@ int swiglu_fp8_bwd(int64_t T, int64_t f, const void* da, int64_t ldda,
 int add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps, const void* x,
                         const void* r, const void* gamma, void* x1, void* y,
                         float* rstd, uint8_t* q, int64_t ldq, float* s,
-                        int64_t lds, void* stream);
+                        int64_t lds, unsigned* status, void* stream);
 
 // gemm_fp8_block.cu: C[M, N] = Σ over K blocks sa·sb·Σ_k qa·qb.
 struct GemmFp8Block {

@@ -189,14 +189,87 @@ def test_gemm_refusals(tp):
 
 def test_binding_refuses_what_the_c_call_cannot_see(tp):
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    q, s = tp.fp8_block_empty(4, 256, device="cpu")
     with pytest.raises(ValueError, match="not on a GPU"):
-        tp.quantize_fp8_block(x, *tp.fp8_block_empty(4, 256, device="cpu"))
-    with pytest.raises(ValueError, match="columns"):
-        tp._matrix(x.t(), "x")
-    q, s = tp.fp8_block_empty(200, 300, tp.FP8_BLOCK, device="cpu")
-    assert q.shape == (200, 300) and q.stride() == (304, 1)
-    assert s.shape == (3, 2)
-    with pytest.raises(TypeError, match="bfloat16"):
-        tp._bf16(x.float(), "x")
-    with pytest.raises(ValueError, match="shape"):
-        tp._bf16(x, "x", (4, 255))
+        tp.quantize_fp8_block(x, q, s)
+    with pytest.raises(ValueError, match="a matrix"):
+        tp.quantize_fp8_block(x[0], q, s)
+    w, ws = tp.fp8_block_empty(200, 300, tp.FP8_BLOCK, device="cpu")
+    assert w.shape == (200, 300) and w.stride() == (304, 1)
+    assert ws.shape == (3, 2)
+
+
+class OnDevice:
+    """A CPU tensor that says it is on device 0: the binding's checks read
+    nothing of its storage."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def get_device(self):
+        return 0
+
+    is_cuda = True
+
+    def __getattr__(self, k):
+        return getattr(self.t, k)
+
+
+def test_binding_checks_types_shapes_strides_and_devices(tp, monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+
+    def on(*shape, dtype=torch.bfloat16):
+        return OnDevice(torch.zeros(*shape, dtype=dtype))
+
+    def pair(rows, cols, group=0):
+        return tuple(OnDevice(t) for t in
+                     tp.fp8_block_empty(rows, cols, group, device="cpu"))
+
+    q, s = pair(4, 256)
+    assert tp._fp8_pair(q, s, "q", 4, 256, 0)[1::2] == (256, 4)
+    assert tp._fp8_pair(*pair(200, 300, 1), "q", 200, 300, 0)[3:] == (2, 1)
+    # a single row: any stride, the two groups are one
+    one = OnDevice(torch.zeros(3, 40, dtype=torch.uint8)[1:2, :33])
+    assert tp._fp8_pair(one, pair(1, 33)[1], "q", 1, 33, 0)[1] == 48
+    for args, kind, words in (
+            ((q, s, "q", 4, 255, 0), ValueError, "shape"),
+            ((q, None, "q", 4, 256, 0), ValueError, "without scales"),
+            ((on(4, 256), s, "q", 4, 256, 0), TypeError, "E4M3"),
+            ((q, on(2, 4), "q", 4, 256, 0), TypeError, "float32"),
+            ((q, on(3, 4, dtype=torch.float32), "q", 4, 256, 0), ValueError,
+             "scales"),
+            ((q, on(2, 3, dtype=torch.float32), "q", 4, 256, 0), ValueError,
+             "scales"),
+            ((q, s, "q", 4, 256, 1), ValueError, "not cuda:1"),
+            ((OnDevice(torch.zeros(256, 4, dtype=torch.uint8).t()), s, "q", 4,
+              256, 0), ValueError, "adjacent")):
+        with pytest.raises(kind, match=words):
+            tp._fp8_pair(*args)
+    with pytest.raises(ValueError, match="adjacent"):
+        tp._matrix(OnDevice(torch.zeros(6, 4).t()), "x")
+    with pytest.raises(ValueError, match="different groups"):
+        tp._fp8_outs(200, 300, 0, *pair(200, 300, 0), *pair(300, 200, 1))
+    with pytest.raises(ValueError, match="neither"):
+        tp._fp8_outs(200, 300, 0, None, None, None, None)
+    with pytest.raises(ValueError, match="a scale for each row"):
+        tp.swiglu_fp8_fwd(on(200, 600), *pair(200, 300, 1))
+    with pytest.raises(ValueError, match="even"):
+        tp.swiglu_fp8_fwd(on(4, 601), *pair(4, 300))
+    with pytest.raises(ValueError, match="dA"):
+        tp.swiglu_fp8_bwd(on(4, 299), on(4, 600), *pair(4, 600))
+    x, g, rs = on(4, 256), on(256), on(4, dtype=torch.float32)
+    for kw, kind, words in (
+            (dict(x1=None), ValueError, "x1"),
+            (dict(gamma=on(255)), ValueError, "gamma"),
+            (dict(rstd=on(5, dtype=torch.float32)), ValueError, "rstd"),
+            (dict(r=on(4, 256, dtype=torch.float32)), TypeError, "r: "),
+            (dict(y=OnDevice(torch.zeros(4, 512, dtype=torch.bfloat16)
+                             [:, ::2])), ValueError, "dense")):
+        a = dict(x=x, r=x, gamma=g, x1=x, q=q, s=s, rstd=rs)
+        a.update(kw)
+        with pytest.raises(kind, match=words):
+            tp.add_rmsnorm_fp8_fwd(**a)
+    with pytest.raises(ValueError, match="qb: shape"):
+        tp.gemm_fp8_block(q, s, *pair(8, 255), on(4, 8))
+    with pytest.raises(ValueError, match="qa: shape"):
+        tp.gemm_fp8_block(q, s, *pair(8, 256), on(5, 8))

@@ -173,7 +173,7 @@ def close_codes(q, s, v, slack, what, mag=None):
 
 @pytest.mark.parametrize("T,f", [(1, 1), (1, 28), (1, 1376), (3, 130),
                                  (128, 128), (130, 264), (300, 77),
-                                 (257, 344)])
+                                 (257, 344), (130, 256), (257, 384)])
 def test_swiglu_forward_and_backward(tp, T, f):
     gu = activation(T, 2 * f, T + f)
     gu[0, 0] = 120.0                          # σ = 1 and σ = 0 to the last bit
@@ -209,9 +209,13 @@ def test_swiglu_rows_of_a_wider_buffer(tp):
     close_codes(q, s, ob.swiglu(f64(gu)), 2.0 ** -16, "A")
 
 
-@pytest.mark.parametrize("T", [1, 5])
-@pytest.mark.parametrize("h", [1, 7, 128, 130, 520, 1000, 2048, 2056, 4100,
-                               8192, 16384])
+NORMS = [(T, h) for T in (1, 5) for h in (1, 7, 128, 130, 520, 1000, 1024,
+                                          2048, 2056, 4100, 8192, 16384)]
+# enough rows for each CTA to go round its ring of rows
+NORMS += [(2500, 1032), (1900, 4096), (700, 4100), (1300, 8192), (700, 16384)]
+
+
+@pytest.mark.parametrize("T,h", NORMS)
 def test_add_rmsnorm(tp, T, h):
     x, r = activation(T, h, h), activation(T, h, h + 1) * 0.5
     gamma = (1.0 + 0.02 * torch.randn(h, generator=torch.Generator(
@@ -240,9 +244,10 @@ def test_add_rmsnorm(tp, T, h):
     assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8))
 
 
+@pytest.mark.parametrize("T", [9, 2500])
 @pytest.mark.parametrize("into", ["x", "r"])
-def test_add_rmsnorm_in_place(tp, into):
-    T, h = 9, 1032
+def test_add_rmsnorm_in_place(tp, into, T):
+    h = 1032
     x, r = activation(T, h, 1), activation(T, h, 2)
     gamma = torch.ones(h, dtype=torch.bfloat16, device="cuda")
     rstd = torch.empty(T, dtype=torch.float32, device="cuda")
