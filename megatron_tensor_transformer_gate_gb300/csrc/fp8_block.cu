@@ -158,7 +158,8 @@ struct SwigluSource {
     unpack8(x[0], g);
     unpack8(x[1], u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = g[j] * sigmoid_approx(g[j]) * u[j];
+    for (int j = 0; j < 8; ++j)
+      v[j] = __fdividef(g[j], 1.0f + __expf(-g[j])) * u[j];
   }
   __device__ int64_t col_tile(int64_t j, int64_t) const { return j; }
 };
@@ -319,10 +320,45 @@ __device__ __forceinline__ uint2 codes8(const float* v, float f) {
   return c;
 }
 
+// An IEEE division is a dozen instructions, so lanes share them: of the lanes
+// that know a block's amax some get its factor (want_scale false), the others
+// its scale, from the same division.
+__device__ __forceinline__ float factor_or_scale(float amax, bool want_scale) {
+  const float a = fmaxf(amax, kBlockAmaxFloor);
+  const float x = __fdiv_rn(want_scale ? a : kE4M3Max,
+                            want_scale ? kE4M3Max : a);
+  return want_scale && amax == 0.0f ? 1.0f : x;
+}
+
+// Maxima of R rows over the 16 lanes of a half-warp, row l mod R in lane l:
+// halving exchanges (R − 1 shuffles) instead of one reduction a row.
+template <int R>
+__device__ __forceinline__ float rows_max(float (&m)[R], int l) {
+  const bool b0 = l & 1, b1 = l & 2, b2 = l & 4;
+  float x[R / 2];
+#pragma unroll
+  for (int j = 0; j < R / 2; ++j)
+    x[j] = fmaxf(b0 ? m[2 * j + 1] : m[2 * j],
+                 __shfl_xor_sync(0xffffffffu, b0 ? m[2 * j] : m[2 * j + 1], 1));
+  float y[R / 4];
+#pragma unroll
+  for (int j = 0; j < R / 4; ++j)
+    y[j] = fmaxf(b1 ? x[2 * j + 1] : x[2 * j],
+                 __shfl_xor_sync(0xffffffffu, b1 ? x[2 * j] : x[2 * j + 1], 2));
+  float z;
+  if constexpr (R == 8)
+    z = fmaxf(b2 ? y[1] : y[0],
+              __shfl_xor_sync(0xffffffffu, b2 ? y[0] : y[1], 4));
+  else
+    z = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], 4));
+  return fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
+}
+
 // Scratch of a CTA: the warps' column maxima, the transposed codes.
 template <int R>
 struct TileScratch {
   __align__(16) float cmax[64 / R][TILE];
+  __align__(16) float colf[TILE];
   __align__(16) uint8_t t[TILE * TILE];
 };
 
@@ -346,15 +382,16 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
   float rowr[R];   // and of each of its rows
   if (GROUP == kFp8Row) {
     if (o.q != nullptr) {
+      float m[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float m = h.row_max(i);
+      for (int i = 0; i < R; ++i) m[i] = h.row_max(i);
+      // lanes 0 to 7 get the factors, 8 to 15 the scales, of row l mod R
+      const float x = factor_or_scale(rows_max<R>(m, l), l & 8);
+      if (l >= 8 && l < 8 + R && r0 + l - 8 < rows)
+        o.s[ct * o.lds + r0 + l - 8] = x;
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1)
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        rowr[i] = block_factor(m);
-        if (l == 0 && r0 + i < rows) o.s[ct * o.lds + r0 + i] = block_scale(m);
-      }
+      for (int i = 0; i < R; ++i)
+        rowr[i] = __shfl_sync(0xffffffffu, x, (lane & 16) | i);
     }
     if (o.qt != nullptr) {
       float cm[8];
@@ -368,16 +405,19 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
         d[1] = make_float4(cm[4], cm[5], cm[6], cm[7]);
       }
       __syncthreads();
-      if (tid < TILE) {   // a column each: its factor, and its scale
-        float m = cmax[0][tid];
+      if (tid < 2 * TILE) {   // a column each: its factor, its scale
+        const int c = tid & (TILE - 1);
+        float m = cmax[0][c];
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w) m = fmaxf(m, cmax[w][tid]);
-        const int64_t c = ct * TILE + tid;
-        if (c < cols) o.st[rt * o.ldst + c] = block_scale(m);
-        cmax[0][tid] = block_factor(m);   // read by this thread alone so far
+        for (int w = 1; w < WARPS; ++w) m = fmaxf(m, cmax[w][c]);
+        const float x = factor_or_scale(m, tid >= TILE);
+        if (tid < TILE)
+          sm.colf[c] = x;
+        else if (ct * TILE + c < cols)
+          o.st[rt * o.ldst + ct * TILE + c] = x;
       }
       __syncthreads();
-      const float4* d = reinterpret_cast<const float4*>(&cmax[0][l * 8]);
+      const float4* d = reinterpret_cast<const float4*>(&sm.colf[l * 8]);
       const float4 x = d[0], y = d[1];
       colr[0] = x.x; colr[1] = x.y; colr[2] = x.z; colr[3] = x.w;
       colr[4] = y.x; colr[5] = y.y; colr[6] = y.z; colr[7] = y.w;
@@ -619,9 +659,13 @@ __device__ __forceinline__ void emit_norm(const NormArgs& p, int64_t row,
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1)
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  // the half-warp's lane 8 gets the scale, lane 0 the factor of all
+  const int lane = threadIdx.x & 31;
+  const float x = factor_or_scale(m, lane & 8);
+  const float f = __shfl_sync(0xffffffffu, x, lane & 16);
+  if ((lane & 15) == 8 && c - 64 < p.h) p.s[(c >> 7) * p.lds + row] = x;
   if (valid <= 0) return;
-  store8(p.q + row * p.ldq + c, codes8(v, block_factor(m)), valid);
-  if ((threadIdx.x & 15) == 0) p.s[(c >> 7) * p.lds + row] = block_scale(m);
+  store8(p.q + row * p.ldq + c, codes8(v, f), valid);
   if (p.y != nullptr)
     save8<W>(p.y + row * p.h + c,
              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
@@ -649,7 +693,7 @@ __device__ __forceinline__ uint4 load8_plain(const __nv_bfloat16* p,
 
 // THREADS threads a row, which stays in their registers (V vectors of eight
 // columns each, 16 neighbouring threads hold one group of 128); a warp per
-// row (eight rows a CTA) up to 1024 columns, else a CTA per row.  γ is read
+// row (eight rows a CTA) up to 512 columns, else a CTA per row.  γ is read
 // before the row's sum is known, so that its latency is not paid after it.
 template <int THREADS, int V, int CTAS, int W>
 __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
@@ -708,12 +752,12 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
 // row, thread 0 copying x and r of the rows to come into a ring of STAGES
 // stages (bulk copies), so that loads are in flight all the time and γ is
 // read once.  Waits are bounded; the block agrees on every outcome.
-template <int V, int CTAS, int STAGES>
-__global__ void __launch_bounds__(512, CTAS)
+template <int THREADS, int V, int CTAS, int STAGES>
+__global__ void __launch_bounds__(THREADS, CTAS)
     add_rmsnorm_fp8_staged_kernel(const NormArgs p) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ uint64_t full[STAGES];
-  __shared__ float red[2][16];
+  __shared__ float red[2][THREADS / 32];
   __shared__ int abort_flag;
   const int tid = threadIdx.x, h = p.h;
   const int nin = p.r != nullptr ? 2 : 1;
@@ -737,7 +781,7 @@ __global__ void __launch_bounds__(512, CTAS)
   uint4 g[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = (k * 512 + tid) * 8;
+    const int c = (k * THREADS + tid) * 8;
     g[k] = c < h ? load16<16>(p.gamma + c) : make_uint4(0, 0, 0, 0);
   }
   int sg = 0;
@@ -754,7 +798,7 @@ __global__ void __launch_bounds__(512, CTAS)
     float ss = 0.0f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = (k * 512 + tid) * 8;
+      const int c = (k * THREADS + tid) * 8;
       u[k] = make_uint4(0, 0, 0, 0);
       uint4 ur = u[k];
       if (c < h) {
@@ -773,13 +817,13 @@ __global__ void __launch_bounds__(512, CTAS)
     if (tid == 0 && row + STAGES * step < p.rows) issue(row + STAGES * step, sg);
     ss = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) ss += red[odd][w];
+    for (int w = 0; w < THREADS / 32; ++w) ss += red[odd][w];
     odd = !odd;
     const float rs = rsqrtf(ss / (float)h + p.eps);
     if (tid == 0) p.rstd[row] = rs;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = (k * 512 + tid) * 8;
+      const int c = (k * THREADS + tid) * 8;
       emit_norm<16>(p, row, c, h - c, u[k], g[k], rs);
     }
     if (++sg == STAGES) {
@@ -800,25 +844,25 @@ __global__ void __launch_bounds__(512, CTAS)
   }
 }
 
-template <int V, int CTAS, int STAGES>
+template <int THREADS, int V, int CTAS, int STAGES>
 int launch_norm_staged(const NormArgs& p, cudaStream_t s) {
   static bool done[64];
-  auto kernel = add_rmsnorm_fp8_staged_kernel<V, CTAS, STAGES>;
+  auto kernel = add_rmsnorm_fp8_staged_kernel<THREADS, V, CTAS, STAGES>;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 64 || !done[dev]) {
-    // V vectors of 16 bytes for 512 threads, x and r
+    // V vectors of 16 bytes a thread, x and r
     err = cudaFuncSetAttribute(kernel,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               STAGES * 2 * V * 512 * 16);
+                               STAGES * 2 * V * THREADS * 16);
     if (err != cudaSuccess) return err;
     if (dev < 64) done[dev] = true;
   }
   const size_t smem = (size_t)STAGES * (p.r != nullptr ? 2 : 1) * p.h * 2;
   const int64_t grid =
       std::min<int64_t>(p.rows, (int64_t)device_sm_count() * CTAS);
-  kernel<<<(unsigned)grid, 512, smem, s>>>(p);
+  kernel<<<(unsigned)grid, THREADS, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -830,7 +874,7 @@ int launch_norm(const NormArgs& p, cudaStream_t s) {
   else if (p.h <= 512)
     add_rmsnorm_fp8_kernel<32, 2, 4, W><<<(T + 7) / 8, 256, 0, s>>>(p);
   else if (p.h <= 1024)
-    add_rmsnorm_fp8_kernel<32, 4, 3, W><<<(T + 7) / 8, 256, 0, s>>>(p);
+    add_rmsnorm_fp8_kernel<128, 1, 8, W><<<T, 128, 0, s>>>(p);
   else if (p.h <= 2048)
     add_rmsnorm_fp8_kernel<256, 1, 4, W><<<T, 256, 0, s>>>(p);
   else if (p.h <= 4096)
@@ -937,13 +981,17 @@ int add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps, const void* x,
                   2.0 * (y != nullptr) + 1.0) * T * h);
     // The ring pays where a CTA has several rows to run ahead on.
     const bool many = T >= 4 * (int64_t)device_sm_count();
-    if (w == 16 && h > 1024 && many) {
-      if (h <= 4096)
-        err = launch_norm_staged<1, 3, 4>(p, st);
+    if (w == 16 && h > 512 && many) {
+      if (h <= 1024)
+        err = launch_norm_staged<128, 1, 12, 4>(p, st);
+      else if (h <= 2048)
+        err = launch_norm_staged<256, 1, 6, 4>(p, st);
+      else if (h <= 4096)
+        err = launch_norm_staged<256, 2, 4, 3>(p, st);
       else if (h <= 8192)
-        err = launch_norm_staged<2, 2, 3>(p, st);
+        err = launch_norm_staged<512, 2, 2, 3>(p, st);
       else
-        err = launch_norm_staged<4, 1, 3>(p, st);
+        err = launch_norm_staged<512, 4, 1, 3>(p, st);
     } else if (w == 16) {
       err = launch_norm<16>(p, st);
     } else if (w == 8) {
