@@ -491,6 +491,51 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
   }
 }
 
+// Row scales alone (no transpose): a half-warp takes R rows of one group of 128
+// columns, nothing passes through shared memory, and a single row spreads over
+// as many half-warps as it has groups.
+template <typename SRC>
+__global__ void __launch_bounds__(256, 4)
+    quantize_rows_kernel(const SRC src, int64_t rows, int64_t cols,
+                         int64_t col_tiles, const Fp8BlockOut o) {
+  constexpr int R = SRC::R;
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const int64_t hw = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t rt = hw / col_tiles;
+  const int64_t ct = src.col_tile(hw - rt * col_tiles, col_tiles);
+  const int64_t r0 = rt * R, c0 = ct * TILE + l * 8;   // r0 ≥ rows: no work
+  Held<SRC> h;
+#pragma unroll
+  for (int b = 0; b < R; b += SRC::BATCH) {
+    uint4 u[SRC::BATCH][SRC::RAW];
+#pragma unroll
+    for (int i = 0; i < SRC::BATCH; ++i) {
+#pragma unroll
+      for (int k = 0; k < SRC::RAW; ++k) u[i][k] = make_uint4(0, 0, 0, 0);
+      if (r0 + b + i < rows && c0 < cols) src.raw(r0 + b + i, c0, cols, u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < SRC::BATCH; ++i) h.take(src, b + i, u[i], c0);
+  }
+  float m[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) m[i] = h.row_max(i);
+  // lanes 0 to 7 get the factors, 8 to 15 the scales, of row l mod R
+  const float x = factor_or_scale(rows_max<R>(m, l), l & 8);
+  if (l >= 8 && l < 8 + R && r0 + l - 8 < rows)
+    o.s[ct * o.lds + r0 + l - 8] = x;
+  const int valid = (int)(cols - c0 < 8 ? cols - c0 : 8);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const float f = __shfl_sync(0xffffffffu, x, (lane & 16) | i);
+    if (r0 + i < rows && valid > 0) {
+      float v[8];
+      h.row(i, v);
+      store8(o.q + (r0 + i) * o.ldq + c0, codes8(v, f), valid);
+    }
+  }
+}
+
 template <typename SRC, int GROUP>
 __global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
     quantize_tile_kernel(const SRC src, int64_t rows, int64_t cols,
@@ -581,7 +626,11 @@ int launch_tiles(const SRC& src, int group, int64_t rows, int64_t cols,
   const unsigned grid = (unsigned)(ct * rt);
   {
     ProfScope ps(s, KF_QUANT, 0.0, bytes);
-    if (!BLOCKS || group == kFp8Row)
+    if (o.qt == nullptr && group == kFp8Row) {
+      const int64_t half_warps = ct * ((rows + SRC::R - 1) / SRC::R);
+      quantize_rows_kernel<SRC><<<(unsigned)((half_warps + 15) / 16), 256, 0,
+                                  s>>>(src, rows, cols, ct, o);
+    } else if (!BLOCKS || group == kFp8Row)
       quantize_tile_kernel<SRC, kFp8Row>
           <<<grid, 2048 / SRC::R, 0, s>>>(src, rows, cols, ct, o);
     else if constexpr (BLOCKS)
@@ -939,7 +988,8 @@ int swiglu_fp8_bwd(int64_t T, int64_t f, const void* da, int64_t ldda,
     return launch_tiles<false>(SwigluBwdSource<false>{a, x, ldda, ldgu, f},
                                kFp8Row, T, 2 * f, o, bytes, s);
   const SwigluBwdSource<true> src{a, x, ldda, ldgu, f};
-  if (f % TILE)
+  // a few rows: spread over half-warps instead (1 x 28672: 2.8 us)
+  if (f % TILE || (o.qt == nullptr && T < 64))
     return launch_tiles<false>(src, kFp8Row, T, 2 * f, o, bytes, s);
   static bool done[64];
   int dev = 0;

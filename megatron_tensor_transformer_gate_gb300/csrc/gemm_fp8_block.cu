@@ -568,39 +568,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
 }
 
 // ================================================================== narrow ==
-constexpr int NARROW_THREADS = 192;
-// Scales reach the epilogue by asynchronous copies NSLOTS − 1 K blocks ahead,
-// each warp's apart.
-constexpr int NSLOTS = 4;   // a power of two
-
-// BN rows of A against 128 rows of B; shared memory for two CTAs on an SM.
+// BNT rows of A against 128 rows of B.  Up to 64 rows two CTAs share an SM
+// (four epilogue warps of 32 × BNT); 128 rows take eight epilogue warps of
+// 32 × 64 and the SM's shared memory for themselves.
+constexpr int NSLOTS = 4;   // scales kept, K blocks; a power of two
 template <int BNT>
 struct Narrow {
+  static constexpr int EWARPS = BNT <= 64 ? 4 : 8;
+  static constexpr int THREADS = 64 + 32 * EWARPS;
+  static constexpr int CTAS = BNT <= 64 ? 2 : 1;
+  static constexpr int NC = BNT <= 64 ? BNT : 64;      // columns of a warp
+  static constexpr int UNITS = NC <= 16 ? 2 : 4;       // of 8 columns a chunk
+  static constexpr int CHUNKS = 2 * NC / (8 * UNITS);  // 16 rows × 8·UNITS
   static constexpr int T_BYTES = BNT * BK;
   static constexpr int STAGE = TILE_BYTES + T_BYTES;
-  static constexpr int STAGES = BNT <= 16 ? 6 : BNT <= 32 ? 5 : BNT <= 64 ? 4 : 3;
-  static constexpr int BUFS = BNT <= 64 ? 4 : 2;
-  static constexpr int COLS = BUFS * BNT;    // TMEM: 64, 128, 256, 256
-  static constexpr int SCALES = 4 * NSLOTS * (32 + BNT);   // floats
+  static constexpr int STAGES = BNT <= 16 ? 6 : BNT <= 32 ? 5 : BNT <= 64 ? 4 : 6;
+  static constexpr int BUFS = 4;
+  static constexpr int COLS = BUFS * BNT;    // TMEM: 64, 128, 256, 512
+  static constexpr int SCALES = EWARPS * NSLOTS * (32 + NC);   // floats
   static constexpr int SMEM = STAGES * STAGE + SCALES * 4 + 1024 + 256;
 };
 
 struct NarrowParams {
-  CUtensorMap mr, mt;      // the 128-row side, the BN-row side
+  CUtensorMap mr, mt;      // the 128-row side (B), the BNT-row side (A)
   const float *sr, *st;
   int64_t ldsr, ldst;
   int r_row, t_row;
   int R, T, kblocks;
   int t_tiles, split;
   void* c;
-  int64_t cr, ct;          // element strides of C along R and T
+  int64_t ldc;
   unsigned* status;
 };
 
-// Warp 0: TMA producer.  Warp 1: MMA issue and TMEM.  Warps 2–5: epilogue, a
-// row of the 128 each thread.
+// 16 TMEM lanes × 16 columns (two units).
+__device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t taddr,
+                                                  uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]),
+                 "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+}
+
+// Warp 0: TMA producer.  Warp 1: MMA issue and TMEM.  The others: epilogue, in
+// the layout of GridAcc (four rows and a quarter of the columns a thread).
 template <int BNT, int OUT_F32>
-__global__ void __launch_bounds__(NARROW_THREADS, 2)
+__global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
     gemm_fp8_block_narrow(const __grid_constant__ NarrowParams p) {
   using L = Narrow<BNT>;
   extern __shared__ uint8_t smem_raw[];
@@ -632,13 +652,11 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
     }
     for (int b = 0; b < L::BUFS; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4);
+      mbar_init(&tempty[b], L::EWARPS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&p.mr);
-    tma_prefetch_desc(&p.mt);
   }
   if (warp == 1) tmem_alloc(tmem_slot, L::COLS);
   tc_fence_before();
@@ -646,10 +664,12 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  float acc[BNT];
+  // epilogue warps: rows 32·(warp mod 4), columns NC·((warp − 2) / 4)
+  const int quarter = warp & 3;
+  const int colw = warp >= 2 ? (warp - 2) / 4 * L::NC : 0;
+  uint64_t acc[L::NC / 2];   // [chunk][unit][row]
 #pragma unroll
-  for (int i = 0; i < BNT; ++i) acc[i] = 0.0f;
-  const int ctid = (warp & 3) * 32 + lane;
+  for (int i = 0; i < L::NC / 2; ++i) acc[i] = 0;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -679,145 +699,193 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BNT);
-      uint32_t stage = 0, phase = 0;
-      int it = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int buf = it % L::BUFS;
-        if (!mbar_wait(&tempty[buf], ((it / L::BUFS) & 1) ^ 1, abort_flag,
-                       p.status, 52) ||
-            !mbar_wait(&full[stage], phase, abort_flag, p.status, 53))
+      const uint64_t rd0 = smem_desc_sw128(smem_u32(smR), 16, 1024);
+      const uint64_t td0 = smem_desc_sw128(smem_u32(smT), 16, 1024);
+      uint32_t stage = 0, phase = 0, buf = 0, tphase = 1;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, 52) ||
+            !mbar_wait(&tempty[buf], tphase, abort_flag, p.status, 53))
           break;
         tc_fence_after();
-        const uint32_t a0 = smem_u32(smR + stage * TILE_BYTES);
-        const uint32_t b0 = smem_u32(smT + stage * L::T_BYTES);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f8(tmem_base + buf * BNT,
-                    smem_desc_sw128(a0 + kk * 32, 16, 1024),
-                    smem_desc_sw128(b0 + kk * 32, 16, 1024), IDESC, kk != 0);
-        tc_commit(&empty[stage]);
+        const uint32_t d = tmem_base + buf * BNT;
+        const uint64_t rd = rd0 + stage * (TILE_BYTES >> 4);
+        const uint64_t td = td0 + stage * (L::T_BYTES >> 4);
+        tc_mma_f8(d, rd, td, IDESC, 0);
+        tc_mma_f8(d, rd + 2, td + 2, IDESC, 1);
+        tc_mma_f8(d, rd + 4, td + 4, IDESC, 1);
+        tc_mma_f8(d, rd + 6, td + 6, IDESC, 1);
         tc_commit(&tfull[buf]);
+        tc_commit(&empty[stage]);
         if (++stage == L::STAGES) {
           stage = 0;
           phase ^= 1;
         }
+        if (++buf == L::BUFS) {
+          buf = 0;
+          tphase ^= 1;
+        }
       }
-      // every commit lands before the barriers' memory is used again
+      // every commit lands before the ring's memory is used again
       volatile int no_abort = 0;
       tc_commit(drain);
       mbar_wait(drain, 0, &no_abort, nullptr, 0);
     }
   } else {
-    const int r = r0 + ctid;
-    float* myrows = scales + (warp - 2) * NSLOTS * (32 + BNT);   // [NSLOTS][32]
-    float* mycols = myrows + NSLOTS * 32;                        // [NSLOTS][BNT]
-    auto fetch = [&](int kb) {
-      if (kb < kb1) {
-        const int slot = (kb - kb0) & (NSLOTS - 1);
-        const float* pr = p.sr + kb * p.ldsr;
-        const float* pt = p.st + kb * p.ldst;
-        cp_async4(myrows + slot * 32 + lane,
-                  pr + (r < p.R ? (p.r_row ? r : r / BM) : 0), r < p.R);
+    // scales by asynchronous copies NSLOTS − 1 K blocks ahead, each warp's
+    // apart: 32 rows, NC columns (column 16g + 8u + 2q + e kept at
+    // 16g + 4q + 2u + e, so that a thread reads its four of 16 at once)
+    float* myrows = scales + (warp - 2) * NSLOTS * (32 + L::NC);
+    float* mycols = myrows + NSLOTS * 32;
+    const int r = r0 + quarter * 32 + lane;
+    const int at = (lane & 16) + ((lane >> 1) & 3) * 4 + ((lane >> 3) & 1) * 2 +
+                   (lane & 1);
+    const float* pr = p.sr + kb0 * p.ldsr +
+                      (r < p.R ? (p.r_row ? r : r / BM) : 0);
+    const float* pt = p.st + kb0 * p.ldst;
+    int fkb = kb0, fslot = 0;
+    auto fetch = [&]() {
+      if (fkb < kb1) {
+        cp_async4(myrows + fslot * 32 + lane, pr, r < p.R);
 #pragma unroll
-        for (int j = 0; j < (BNT + 31) / 32; ++j) {
-          const int t = t0 + 32 * j + lane;
-          if (32 * j + lane < BNT)
-            cp_async4(mycols + slot * BNT + 32 * j + lane,
+        for (int j = 0; j < (L::NC + 31) / 32; ++j) {
+          const int t = t0 + colw + 32 * j + lane;
+          if (32 * j + lane < L::NC)
+            cp_async4(mycols + fslot * L::NC + 32 * j + at,
                       pt + (t < p.T ? (p.t_row ? t : t / BM) : 0), t < p.T);
         }
+        pr += p.ldsr;
+        pt += p.ldst;
+        ++fkb;
+        fslot = (fslot + 1) & (NSLOTS - 1);
       }
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < NSLOTS - 1; ++i) fetch(kb0 + i);
+    for (int i = 0; i < NSLOTS - 1; ++i) fetch();
     const uint32_t taddr0 =
-        tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    int it = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-      const int buf = it % L::BUFS;
+        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + colw;
+    constexpr int W = 8 * L::UNITS;   // columns of a chunk
+    auto load = [&](int buf, int c, uint32_t (&x)[4 * L::UNITS]) {
+      const uint32_t ta = taddr0 + buf * BNT + W * (c >> 1) +
+                          (static_cast<uint32_t>(16 * (c & 1)) << 16);
+      if constexpr (L::UNITS == 2)
+        tmem_ld16x256b_x2(ta, x);
+      else
+        tmem_ld16x256b_x4(ta, x);
+    };
+    auto wait = [&](uint32_t (&x)[4 * L::UNITS]) {
+      if constexpr (L::UNITS == 2)
+        tmem_ld_wait8(x);
+      else
+        tmem_ld_wait16(x);
+    };
+    int buf = 0, slot = 0;
+    uint32_t par = 0;
+    uint32_t x[2][4 * L::UNITS];
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait_warp(&tfull[buf], par, abort_flag, p.status, 54)) break;
+      tc_fence_after();
+      load(buf, 0, x[0]);
       cp_async_wait<NSLOTS - 2>();   // this block's group is complete
       __syncwarp();   // for every lane's, and the last block's are read
-      const float a0 = myrows[(it & (NSLOTS - 1)) * 32 + lane];
-      const float* cs = mycols + (it & (NSLOTS - 1)) * BNT;
-      fetch(kb + NSLOTS - 1);
-      if (!mbar_wait_warp(&tfull[buf], (it / L::BUFS) & 1, abort_flag,
-                          p.status, 54))
-        break;
-      tc_fence_after();
+      const float* rs = myrows + slot * 32 + (lane >> 2);
+      const float* cs = mycols + slot * L::NC;
+      uint64_t s2[4], w2[L::UNITS];
 #pragma unroll
-      for (int c = 0; c < BNT / 16; ++c) {
-        uint32_t v[16];
-        tmem_ld16(taddr0 + buf * BNT + c * 16, v);
-        tmem_ld_wait16(v);
-        if (c == BNT / 16 - 1) {
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t v = __float_as_uint(rs[8 * j]);
+        s2[j] = pack_f32x2(v, v);
+      }
+#pragma unroll
+      for (int c = 0; c < L::CHUNKS; ++c) {
+        if ((c & 1) == 0) {
+#pragma unroll
+          for (int u = 0; u < L::UNITS; u += 2)
+            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                         : "=l"(w2[u]), "=l"(w2[u + 1])
+                         : "r"(smem_u32(cs + W * (c >> 1) + 8 * u +
+                                        (lane & 3) * 4)));
+        }
+        wait(x[c & 1]);
+        if (c + 1 < L::CHUNKS) {
+          load(buf, c + 1, x[(c + 1) & 1]);
+        } else {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[buf]);
+          if (lane == 0) mbar_arrive_relaxed(&tempty[buf]);
+          fetch();
         }
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 w = *reinterpret_cast<const float4*>(cs + c * 16 + i);
-          float* d = acc + c * 16 + i;
-          d[0] = fmaf(__uint_as_float(v[i]), a0 * w.x, d[0]);
-          d[1] = fmaf(__uint_as_float(v[i + 1]), a0 * w.y, d[1]);
-          d[2] = fmaf(__uint_as_float(v[i + 2]), a0 * w.z, d[2]);
-          d[3] = fmaf(__uint_as_float(v[i + 3]), a0 * w.w, d[3]);
-        }
+        for (int u = 0; u < L::UNITS; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            fma_f32x2(acc[(c * L::UNITS + u) * 2 + i],
+                      pack_f32x2(x[c & 1][4 * u + 2 * i],
+                                 x[c & 1][4 * u + 2 * i + 1]),
+                      mul_f32x2(s2[(c & 1) * 2 + i], w2[u]));
+      }
+      slot = (slot + 1) & (NSLOTS - 1);
+      if (++buf == L::BUFS) {
+        buf = 0;
+        par ^= 1;
       }
     }
+    cp_async_wait<0>();
   }
 
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();   // copies, MMAs and TMEM reads of this CTA are done
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, L::COLS);
 
-  auto store = [&](int r, int t, float v) {
-    const int64_t at = r * p.cr + t * p.ct;
-    if (OUT_F32)
-      static_cast<float*>(p.c)[at] = v;
-    else
-      static_cast<__nv_bfloat16*>(p.c)[at] = __float2bfloat16_rn(v);
-  };
-  if (p.split == 1) {
-    if (warp >= 2 && r0 + ctid < p.R) {
-#pragma unroll
-      for (int i = 0; i < BNT; ++i)
-        if (t0 + i < p.T) store(r0 + ctid, t0 + i, acc[i]);
-    }
-    return;
-  }
-  // The cluster's parts: rank j adds up columns [j·w, (j + 1)·w) of the tile;
-  // every CTA hands it its own through j's shared memory, [rank][column][row]
-  // over the operand ring, which is free once every CTA's copies and MMAs are
-  // done (the barrier).
+  // The cluster's parts: rank j adds up columns [j·w, (j + 1)·w) of the tile in
+  // rank order; every CTA hands it its own through j's shared memory, [rank]
+  // [column][row] over the operand ring, which is free once every CTA is here.
   const int w = (BNT + p.split - 1) / p.split;
-  cluster_sync();
+  if (p.split > 1) cluster_sync();
   if (warp >= 2) {
     const uint32_t mine = smem_u32(smem);
 #pragma unroll
-    for (int i = 0; i < BNT; ++i) {
-      const int j = i / w;
-      if (t0 + i < p.T) {
-        uint32_t dst;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(dst)
-                     : "r"(mine), "r"(j));
-        dst += ((uint32_t)(part * w + i - j * w) * BM + ctid) * 4;
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(acc[i])
-                     : "memory");
+    for (int c = 0; c < L::CHUNKS; ++c)
+#pragma unroll
+      for (int u = 0; u < L::UNITS; ++u) {
+        const int col = colw + 8 * L::UNITS * (c >> 1) + 8 * u + 2 * (lane & 3);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (t0 + col + e >= p.T) continue;
+          const int j = (col + e) / w;
+          uint32_t dst = mine;
+          if (p.split > 1)
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(dst)
+                         : "r"(mine), "r"(j));
+          dst += ((uint32_t)(part * w + col + e - j * w) * BM + quarter * 32 +
+                  16 * (c & 1) + (lane >> 2)) * 4;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 v = unpack_f32x2(acc[(c * L::UNITS + u) * 2 + i]);
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 32 * i),
+                         "f"(e ? v.y : v.x)
+                         : "memory");
+          }
+        }
       }
-    }
   }
-  cluster_sync();
-  if (warp >= 2 && r0 + ctid < p.R) {
+  if (p.split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (warp >= 2) {
     const float* in = reinterpret_cast<const float*>(smem);
-    for (int i = 0; i < w; ++i) {
-      const int col = part * w + i;
-      if (col >= BNT || t0 + col >= p.T) break;
-      float v = 0.0f;
-      for (int k = 0; k < p.split; ++k) v += in[(k * w + i) * BM + ctid];
-      store(r0 + ctid, t0 + col, v);
+    const int row = quarter * 32 + lane;
+    if (r0 + row < p.R) {
+      for (int i = (warp - 2) / 4; i < w; i += L::EWARPS / 4) {
+        const int col = part * w + i;
+        if (col >= BNT || t0 + col >= p.T) break;
+        float v = 0.0f;
+        for (int k = 0; k < p.split; ++k) v += in[(k * w + i) * BM + row];
+        RowAcc::put<OUT_F32>(p.c, (int64_t)(t0 + col) * p.ldc + r0 + row, v);
+      }
     }
   }
 }
@@ -881,7 +949,7 @@ int launch_narrow(const NarrowParams& prm, unsigned grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(NARROW_THREADS);
+  cfg.blockDim = dim3(Narrow<BNT>::THREADS);
   cfg.dynamicSmemBytes = Narrow<BNT>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute at;
@@ -942,8 +1010,7 @@ int narrow(const GemmFp8Block& g, cudaStream_t s, unsigned* status, int bn,
   p.t_tiles = (int)((g.M + bn - 1) / bn);
   p.split = split;
   p.c = g.c;
-  p.cr = 1;
-  p.ct = g.ldc;
+  p.ldc = g.ldc;
   p.status = status;
   const int64_t grid =
       (g.N + BM - 1) / BM * (int64_t)p.t_tiles * split;
