@@ -571,21 +571,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
 // BNT rows of A against 128 rows of B.  Up to 64 rows two CTAs share an SM
 // (four epilogue warps of 32 × BNT); 128 rows take eight epilogue warps of
 // 32 × 64 and the SM's shared memory for themselves.
-constexpr int NSLOTS = 4;   // scales kept, K blocks; a power of two
+constexpr int NSLOTS = 16;   // K blocks of scales kept; a power of two
+constexpr int NAHEAD = 8;    // and loaded ahead of the epilogue
 template <int BNT>
 struct Narrow {
   static constexpr int EWARPS = BNT <= 64 ? 4 : 8;
-  static constexpr int THREADS = 64 + 32 * EWARPS;
+  static constexpr int THREADS = 96 + 32 * EWARPS;
   static constexpr int CTAS = BNT <= 64 ? 2 : 1;
   static constexpr int NC = BNT <= 64 ? BNT : 64;      // columns of a warp
   static constexpr int UNITS = NC <= 16 ? 2 : 4;       // of 8 columns a chunk
   static constexpr int CHUNKS = 2 * NC / (8 * UNITS);  // 16 rows × 8·UNITS
   static constexpr int T_BYTES = BNT * BK;
   static constexpr int STAGE = TILE_BYTES + T_BYTES;
-  static constexpr int STAGES = BNT <= 16 ? 6 : BNT <= 32 ? 5 : BNT <= 64 ? 4 : 6;
+  static constexpr int STAGES = BNT <= 32 ? 5 : BNT <= 64 ? 4 : 6;
   static constexpr int BUFS = 4;
   static constexpr int COLS = BUFS * BNT;    // TMEM: 64, 128, 256, 512
-  static constexpr int SCALES = EWARPS * NSLOTS * (32 + NC);   // floats
+  static constexpr int SLOT = BM + BNT;                        // floats
+  static constexpr int SCALES = NSLOTS * SLOT;
   static constexpr int SMEM = STAGES * STAGE + SCALES * 4 + 1024 + 256;
 };
 
@@ -617,8 +619,10 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
                  "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
 }
 
-// Warp 0: TMA producer.  Warp 1: MMA issue and TMEM.  The others: epilogue, in
-// the layout of GridAcc (four rows and a quarter of the columns a thread).
+// Warp 0: TMA producer.  Warp 1: MMA issue and TMEM.  Warp 2: the scales, far
+// enough ahead for their latency from DRAM (three blocks ahead: 0.47 µs a K
+// block, whatever the tile).  The others: epilogue, in the layout of GridAcc
+// (four rows and a quarter of the columns a thread).
 template <int BNT, int OUT_F32>
 __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
     gemm_fp8_block_narrow(const __grid_constant__ NarrowParams p) {
@@ -651,7 +655,7 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < L::BUFS; ++b) {
-      mbar_init(&tfull[b], 1);
+      mbar_init(&tfull[b], 2);   // the MMAs and the scales
       mbar_init(&tempty[b], L::EWARPS);
     }
     mbar_init(drain, 1);
@@ -664,9 +668,9 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  // epilogue warps: rows 32·(warp mod 4), columns NC·((warp − 2) / 4)
+  // epilogue warps: rows 32·(warp mod 4), columns NC·((warp − 3) / 4)
   const int quarter = warp & 3;
-  const int colw = warp >= 2 ? (warp - 2) / 4 * L::NC : 0;
+  const int colw = warp >= 3 ? (warp - 3) / 4 * L::NC : 0;
   uint64_t acc[L::NC / 2];   // [chunk][unit][row]
 #pragma unroll
   for (int i = 0; i < L::NC / 2; ++i) acc[i] = 0;
@@ -730,27 +734,29 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
       tc_commit(drain);
       mbar_wait(drain, 0, &no_abort, nullptr, 0);
     }
-  } else {
-    // scales by asynchronous copies NSLOTS − 1 K blocks ahead, each warp's
-    // apart: 32 rows, NC columns (column 16g + 8u + 2q + e kept at
+  } else if (warp == 2) {
+    // the 128 rows' scales, then the columns' (column 16g + 8u + 2q + e at
     // 16g + 4q + 2u + e, so that a thread reads its four of 16 at once)
-    float* myrows = scales + (warp - 2) * NSLOTS * (32 + L::NC);
-    float* mycols = myrows + NSLOTS * 32;
-    const int r = r0 + quarter * 32 + lane;
+    static_assert(NAHEAD + 2 * L::BUFS <= NSLOTS, "slots are read when reused");
     const int at = (lane & 16) + ((lane >> 1) & 3) * 4 + ((lane >> 3) & 1) * 2 +
                    (lane & 1);
-    const float* pr = p.sr + kb0 * p.ldsr +
-                      (r < p.R ? (p.r_row ? r : r / BM) : 0);
+    const float* pr = p.sr + kb0 * p.ldsr;
     const float* pt = p.st + kb0 * p.ldst;
     int fkb = kb0, fslot = 0;
     auto fetch = [&]() {
       if (fkb < kb1) {
-        cp_async4(myrows + fslot * 32 + lane, pr, r < p.R);
+        float* rows = scales + fslot * L::SLOT;
 #pragma unroll
-        for (int j = 0; j < (L::NC + 31) / 32; ++j) {
-          const int t = t0 + colw + 32 * j + lane;
-          if (32 * j + lane < L::NC)
-            cp_async4(mycols + fslot * L::NC + 32 * j + at,
+        for (int j = 0; j < BM / 32; ++j) {
+          const int r = r0 + 32 * j + lane;
+          cp_async4(rows + 32 * j + lane,
+                    pr + (r < p.R ? (p.r_row ? r : r / BM) : 0), r < p.R);
+        }
+#pragma unroll
+        for (int j = 0; j < (BNT + 31) / 32; ++j) {
+          const int t = t0 + 32 * j + lane;
+          if (32 * j + lane < BNT)
+            cp_async4(rows + BM + 32 * j + at,
                       pt + (t < p.T ? (p.t_row ? t : t / BM) : 0), t < p.T);
         }
         pr += p.ldsr;
@@ -760,8 +766,27 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
       }
       cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < NSLOTS - 1; ++i) fetch();
+#pragma unroll 1
+    for (int i = 0; i < NAHEAD; ++i) fetch();
+    int buf = 0;
+    uint32_t par = 1;   // of the phase before this block's on its barrier
+    for (int kb = kb0; kb < kb1; ++kb) {
+      // block kb − BUFS complete: this block's phase is open, and the slot that
+      // the next copies go to (of kb − BUFS·2 or before) has been read
+      if (kb - kb0 >= L::BUFS &&
+          !mbar_wait_warp(&tfull[buf], par, abort_flag, p.status, 55))
+        break;
+      fetch();
+      cp_async_wait<NAHEAD>();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tfull[buf]);
+      if (++buf == L::BUFS) {
+        buf = 0;
+        par ^= 1;
+      }
+    }
+    cp_async_wait<0>();
+  } else {
     const uint32_t taddr0 =
         tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + colw;
     constexpr int W = 8 * L::UNITS;   // columns of a chunk
@@ -786,10 +811,8 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
       if (!mbar_wait_warp(&tfull[buf], par, abort_flag, p.status, 54)) break;
       tc_fence_after();
       load(buf, 0, x[0]);
-      cp_async_wait<NSLOTS - 2>();   // this block's group is complete
-      __syncwarp();   // for every lane's, and the last block's are read
-      const float* rs = myrows + slot * 32 + (lane >> 2);
-      const float* cs = mycols + slot * L::NC;
+      const float* rs = scales + slot * L::SLOT + quarter * 32 + (lane >> 2);
+      const float* cs = scales + slot * L::SLOT + BM + colw;
       uint64_t s2[4], w2[L::UNITS];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -813,7 +836,6 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_relaxed(&tempty[buf]);
-          fetch();
         }
 #pragma unroll
         for (int u = 0; u < L::UNITS; ++u)
@@ -830,7 +852,6 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
         par ^= 1;
       }
     }
-    cp_async_wait<0>();
   }
 
   tc_fence_before();
@@ -843,7 +864,7 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
   // [column][row] over the operand ring, which is free once every CTA is here.
   const int w = (BNT + p.split - 1) / p.split;
   if (p.split > 1) cluster_sync();
-  if (warp >= 2) {
+  if (warp >= 3) {
     const uint32_t mine = smem_u32(smem);
 #pragma unroll
     for (int c = 0; c < L::CHUNKS; ++c)
@@ -875,11 +896,11 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
     cluster_sync();
   else
     __syncthreads();
-  if (warp >= 2) {
+  if (warp >= 3) {
     const float* in = reinterpret_cast<const float*>(smem);
     const int row = quarter * 32 + lane;
     if (r0 + row < p.R) {
-      for (int i = (warp - 2) / 4; i < w; i += L::EWARPS / 4) {
+      for (int i = (warp - 3) / 4; i < w; i += L::EWARPS / 4) {
         const int col = part * w + i;
         if (col >= BNT || t0 + col >= p.T) break;
         float v = 0.0f;
