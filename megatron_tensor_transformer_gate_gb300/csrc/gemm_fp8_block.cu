@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <type_traits>
 
@@ -295,7 +296,7 @@ struct GridAcc {
 //   warps 4–11  epilogue, warp w on TMEM lanes 32·(w mod 4) of half (w − 4)/4.
 // The epilogue's 128 sums a thread need more than the 168 registers that 384
 // threads can have, so the first warpgroup hands some over (128·56 + 256·224
-// = 384·168).
+// = 384·168; with column scales 128·40 + 256·232).
 template <int B_ROW, int OUT_F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     gemm_fp8_block_wide(const __grid_constant__ Params p) {
@@ -345,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(B_ROW ? 40 : 56));
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer --
       uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
@@ -496,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       cp_async_wait<0>();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(B_ROW ? 232 : 224));
     // ------------------------------------------------------------ epilogue --
     using Acc = typename std::conditional<B_ROW != 0, GridAcc, RowAcc>::type;
     const int quarter = warp & 3;          // TMEM lanes this warp may read
@@ -530,8 +531,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
         const float* cols = rows + BM + half * BNH;
 #pragma unroll
         for (int c = 0; c < Acc::CHUNKS; ++c) {
-          Acc::wait(r[c & 1]);
           a.columns(cols, c, lane);
+          Acc::wait(r[c & 1]);
           if (c + 1 < Acc::CHUNKS) {
             Acc::load(taddr, c + 1, r[(c + 1) & 1]);
           } else {
@@ -600,6 +601,7 @@ struct NarrowParams {
   int t_tiles, split;
   void* c;
   int64_t ldc;
+  int vec;                 // four outputs of a row start on 4·(their size)
   unsigned* status;
 };
 
@@ -859,36 +861,24 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, L::COLS);
 
-  // The cluster's parts: rank j adds up columns [j·w, (j + 1)·w) of the tile in
-  // rank order; every CTA hands it its own through j's shared memory, [rank]
-  // [column][row] over the operand ring, which is free once every CTA is here.
-  const int w = (BNT + p.split - 1) / p.split;
-  if (p.split > 1) cluster_sync();
+  // Every CTA leaves its sums in its own shared memory, [column][row] over the
+  // operand ring (pitch 132: the lanes' rows and columns fall on 32 banks);
+  // rank j of the cluster adds up columns [j·w, (j + 1)·w) in rank order.
+  constexpr int PITCH = BM + 4;
+  float* out = reinterpret_cast<float*>(smem);
   if (warp >= 3) {
-    const uint32_t mine = smem_u32(smem);
 #pragma unroll
     for (int c = 0; c < L::CHUNKS; ++c)
 #pragma unroll
       for (int u = 0; u < L::UNITS; ++u) {
-        const int col = colw + 8 * L::UNITS * (c >> 1) + 8 * u + 2 * (lane & 3);
+        float* d = out + (colw + 8 * L::UNITS * (c >> 1) + 8 * u +
+                          2 * (lane & 3)) * PITCH +
+                   quarter * 32 + 16 * (c & 1) + (lane >> 2);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (t0 + col + e >= p.T) continue;
-          const int j = (col + e) / w;
-          uint32_t dst = mine;
-          if (p.split > 1)
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                         : "=r"(dst)
-                         : "r"(mine), "r"(j));
-          dst += ((uint32_t)(part * w + col + e - j * w) * BM + quarter * 32 +
-                  16 * (c & 1) + (lane >> 2)) * 4;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 v = unpack_f32x2(acc[(c * L::UNITS + u) * 2 + i]);
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 32 * i),
-                         "f"(e ? v.y : v.x)
-                         : "memory");
-          }
+        for (int i = 0; i < 2; ++i) {
+          const float2 v = unpack_f32x2(acc[(c * L::UNITS + u) * 2 + i]);
+          d[8 * i] = v.x;
+          d[PITCH + 8 * i] = v.y;
         }
       }
   }
@@ -897,18 +887,53 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
   else
     __syncthreads();
   if (warp >= 3) {
-    const float* in = reinterpret_cast<const float*>(smem);
-    const int row = quarter * 32 + lane;
-    if (r0 + row < p.R) {
-      for (int i = (warp - 3) / 4; i < w; i += L::EWARPS / 4) {
-        const int col = part * w + i;
-        if (col >= BNT || t0 + col >= p.T) break;
-        float v = 0.0f;
-        for (int k = 0; k < p.split; ++k) v += in[(k * w + i) * BM + row];
-        RowAcc::put<OUT_F32>(p.c, (int64_t)(t0 + col) * p.ldc + r0 + row, v);
+    // a warp per column, four rows a lane
+    const int w = (BNT + p.split - 1) / p.split;
+    const int end = min(min((part + 1) * w, BNT), p.T - t0);
+    const int row = r0 + 4 * lane;
+    uint32_t from[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < p.split) from[k] = cluster_addr(out + 4 * lane, k);
+#pragma unroll 2
+    for (int col = part * w + warp - 3; col < end; col += L::EWARPS) {
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.split == 1) {
+        const float4 x = *reinterpret_cast<const float4*>(out + 4 * lane +
+                                                          col * PITCH);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        float x[8][4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < p.split)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[k][0]), "=f"(x[k][1]), "=f"(x[k][2]),
+                           "=f"(x[k][3])
+                         : "r"(from[k] + col * PITCH * 4));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < p.split) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += x[k][j];
+          }
+      }
+      const int64_t at = (int64_t)(t0 + col) * p.ldc + row;
+      if (p.vec && row + 4 <= p.R) {
+        if (OUT_F32)
+          *reinterpret_cast<float4*>(static_cast<float*>(p.c) + at) =
+              make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.c) + at) =
+              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (row + j < p.R) RowAcc::put<OUT_F32>(p.c, at + j, v[j]);
       }
     }
   }
+  if (p.split > 1) cluster_sync();   // no CTA leaves while it is read
 }
 
 // ==================================================================== host ==
@@ -1032,6 +1057,8 @@ int narrow(const GemmFp8Block& g, cudaStream_t s, unsigned* status, int bn,
   p.split = split;
   p.c = g.c;
   p.ldc = g.ldc;
+  const uintptr_t four = g.out_f32 ? 16 : 8;
+  p.vec = reinterpret_cast<uintptr_t>(g.c) % four == 0 && g.ldc % 4 == 0;
   p.status = status;
   const int64_t grid =
       (g.N + BM - 1) / BM * (int64_t)p.t_tiles * split;
@@ -1049,6 +1076,48 @@ int narrow(const GemmFp8Block& g, cudaStream_t s, unsigned* status, int bn,
   }
 }
 
+// Which form, and the narrow one's rows of A a tile and split of K, by an
+// estimate in µs from what both were measured to take on 152 SMs:
+//  * narrow: 4 a wave of CTAs, and the K blocks' time (0.34 to 0.40 each,
+//    latency of the ring) beside the bytes at 6.4 TB/s, 0.3 of the shorter of
+//    the two not hidden.  Estimated / measured: 1×4096×4096 split 8 7.0 / 7.8,
+//    split 2 10 / 10; 48×8192×28672 split 4 47 / 45, split 1 98 / 90;
+//    128×8192×28672 split 2 60 / 56, split 4 64 / 62; 512×4096×4096 18 / 19;
+//  * wide: 6, and 0.5 a K block of each round of tiles (0.72 with a scale for
+//    each row of B).  512×4096×4096 22 / 21, 1024×8192×8192 70 / 70,
+//    256×8192×28672 118 / 111 (narrow, split 1: 105 / 98).
+// Clusters of more than four CTAs leave SMs of a GPC empty.
+struct Plan {
+  int bn = 0;      // 0: wide
+  int split = 1;
+};
+Plan choose(const GemmFp8Block& g, int64_t kblocks) {
+  const int sms = device_sm_count();
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  const bool b_row = g.b_group == kFp8Row;
+  const int64_t tiles = up(g.M, 2 * BM) * up(g.N, BN);
+  Plan best;
+  double least = 6.0 + up(tiles, std::max(sms / 2, 1)) * kblocks *
+                           (b_row ? 0.72 : 0.5);
+  const double bytes = ((double)g.M + (double)g.N) * (double)g.K / 6.4e6;
+  const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+  const double kb_us = bn <= 32 ? 0.34 : bn <= 64 ? 0.37 : 0.40;
+  const int64_t t = up(g.N, BM) * up(g.M, bn);
+  for (int split = 1; split <= 8 && split <= kblocks; ++split) {
+    const double slots = sms * (bn <= 64 ? 2 : 1) * (split > 4 ? 0.85 : 1.0);
+    const double waves = std::max(1.0, std::ceil(t * split / slots));
+    const double work = waves * up(kblocks, split) * kb_us;
+    const double us = 4.0 * waves + std::max(work, bytes) +
+                      0.3 * std::min(work, bytes);
+    if (us < least) {
+      least = us;
+      best.bn = bn;
+      best.split = split;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 int gemm_fp8_block(const GemmFp8Block& g, void* stream, unsigned* status) {
@@ -1058,17 +1127,8 @@ int gemm_fp8_block(const GemmFp8Block& g, void* stream, unsigned* status) {
   {
     ProfScope ps(s, KF_GEMM_TC_FP8, 2.0 * g.M * g.N * g.K,
                  (double)(g.M + g.N) * g.K + (g.out_f32 ? 4.0 : 2.0) * g.M * g.N);
-    if (g.M <= 128) {
-      const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
-      const int64_t tiles = (g.N + BM - 1) / BM;
-      int split = 1;
-      while (split < 8 && split * 2 <= kblocks &&
-             tiles * split * 2 <= 2 * device_sm_count())
-        split *= 2;
-      err = narrow(g, s, status, bn, split);
-    } else {
-      err = wide(g, s, status);
-    }
+    const Plan pl = choose(g, kblocks);
+    err = pl.bn ? narrow(g, s, status, pl.bn, pl.split) : wide(g, s, status);
   }
   if (err) return err;
   count_launch();
