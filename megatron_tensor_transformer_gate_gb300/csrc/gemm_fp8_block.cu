@@ -94,7 +94,7 @@ struct RowAcc {
   static constexpr int CHUNKS = 4;      // of 32 columns
   using Chunk = uint32_t[32];
   uint64_t acc[64];
-  uint64_t s2;
+  float s, sn;   // this block's multiplier, the next one's
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0;
@@ -106,11 +106,12 @@ struct RowAcc {
   __device__ __forceinline__ static void wait(Chunk& r) { tmem_ld_wait(r); }
   __device__ __forceinline__ void scales(const float* rows, const float* cols,
                                          int half, int lane) {
-    const uint32_t s = __float_as_uint(rows[lane] * cols[half]);
-    s2 = pack_f32x2(s, s);
+    sn = rows[lane] * cols[half];
   }
+  __device__ __forceinline__ void next() { s = sn; }
   __device__ __forceinline__ void columns(const float*, int, int) {}
   __device__ __forceinline__ void add(const Chunk& r, int c) {
+    const uint64_t s2 = pack_f32x2(__float_as_uint(s), __float_as_uint(s));
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       fma_f32x2(acc[c * 16 + i], pack_f32x2(r[2 * i], r[2 * i + 1]), s2);
@@ -183,7 +184,8 @@ struct GridAcc {
   static constexpr int CHUNKS = 8;
   using Chunk = uint32_t[16];
   uint64_t acc[64];   // [chunk][unit][row]
-  uint64_t s2[4], w2[4];
+  float s[4], sn[4];
+  uint64_t w2[4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0;
@@ -197,10 +199,11 @@ struct GridAcc {
   __device__ __forceinline__ void scales(const float* rows, const float*, int,
                                          int lane) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t s = __float_as_uint(rows[(lane >> 2) + 8 * j]);
-      s2[j] = pack_f32x2(s, s);
-    }
+    for (int j = 0; j < 4; ++j) sn[j] = rows[(lane >> 2) + 8 * j];
+  }
+  __device__ __forceinline__ void next() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = sn[j];
   }
   // cols: the half's 128 scales, column 16g + 8u + 2q + e at 16g + 4q + 2u + e
   __device__ __forceinline__ void columns(const float* cols, int c, int lane) {
@@ -213,13 +216,19 @@ struct GridAcc {
                                   (lane & 3) * 4)));
   }
   __device__ __forceinline__ void add(const Chunk& r, int c) {
+    uint64_t s2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t v = __float_as_uint(s[(c & 1) * 2 + i]);
+      s2[i] = pack_f32x2(v, v);
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         fma_f32x2(acc[c * 8 + u * 2 + i],
                   pack_f32x2(r[4 * u + 2 * i], r[4 * u + 2 * i + 1]),
-                  mul_f32x2(s2[(c & 1) * 2 + i], w2[u]));
+                  mul_f32x2(s2[i], w2[u]));
   }
   // The four lanes of a row exchange what makes 16 bytes in each: 64 bytes of
   // a row a store.
@@ -511,8 +520,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     int64_t it = 0;
     bool ok = true, ready = false;
     typename Acc::Chunk r[2];   // a chunk being added, the next on its way
+    Acc a;
+    auto slot = [&](int64_t i) { return scales + (i & (SLOTS - 1)) * SLOT; };
+    auto begin = [&](int64_t i) {   // block i is there: its first chunk, scales
+      tc_fence_after();
+      Acc::load(taddr0 + (i & 1) * BNH, 0, r[0]);
+      a.scales(slot(i) + quarter * 32, slot(i) + BM, half, lane);
+    };
     for (int t = cid; ok && t < p.total_tiles; t += ncl) {
-      Acc a;
       a.clear();
       for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
         const int buf = it & 1;
@@ -523,29 +538,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
             ok = false;
             break;
           }
-          tc_fence_after();
-          Acc::load(taddr, 0, r[0]);
+          begin(it);
         }
-        const float* rows = scales + (it & (SLOTS - 1)) * SLOT;
-        a.scales(rows + quarter * 32, rows + BM, half, lane);
-        const float* cols = rows + BM + half * BNH;
+        a.next();
+        const float* cols = slot(it) + BM + half * BNH;
 #pragma unroll
         for (int c = 0; c < Acc::CHUNKS; ++c) {
           a.columns(cols, c, lane);
+          // whether the next block is there is asked in the shadow of a load
+          if (c + 1 == Acc::CHUNKS)
+            ready = mbar_test_warp(&tf[buf ^ 1], ((it + 1) >> 1) & 1);
           Acc::wait(r[c & 1]);
           if (c + 1 < Acc::CHUNKS) {
             Acc::load(taddr, c + 1, r[(c + 1) & 1]);
           } else {
-            // the buffer is read: the MMAs may have it back
+            // the buffer is read (by all lanes: the wait is the warp's): the
+            // MMAs may have it back
             tc_fence_before();
-            __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(&te[buf]);
-            // the next block's first chunk, if it is there already
-            ready = mbar_test_warp(&tf[buf ^ 1], ((it + 1) >> 1) & 1);
-            if (ready) {
-              tc_fence_after();
-              Acc::load(taddr0 + (buf ^ 1) * BNH, 0, r[0]);
-            }
+            if (ready) begin(it + 1);
           }
           a.add(r[c & 1], c);
         }
