@@ -49,7 +49,7 @@ struct Params {
 // ==================================================================== wide ==
 constexpr int BN = 256;
 constexpr int BNH = BN / 2;                    // B rows loaded by each CTA
-constexpr int STAGES = 4;
+constexpr int STAGES = 4;                      // even: see the MMA issue
 constexpr int STAGE_BYTES = 3 * TILE_BYTES;    // 128 rows of A, 256 of B
 constexpr int TMEM_COLS = 512;                 // two halves × two K blocks × 128
 constexpr int WIDE_THREADS = 384;
@@ -297,9 +297,12 @@ struct GridAcc {
 // (cta_group::1), so that handing a TMEM buffer over and back stays inside
 // the SM.  Roles:
 //   warp 0      TMA producer, a ring of four K blocks;
-//   warps 1, 2  MMA issue, 128 of the tile's columns each, two TMEM buffers
-//               a half (one thread's waits, MMAs and commits for a K block
-//               take longer beside eight busy epilogue warps than its MMAs);
+//   warps 1, 2  MMA issue, every other K block each, the tile's columns in
+//               two halves with two TMEM buffers a half.  Beside eight busy
+//               epilogue warps one thread's waits and commits for a K block
+//               take about 400 cycles, in which the other's MMAs (512) run;
+//               with a half of every K block each, both idled together and a
+//               block took 919 cycles;
 //   warp 3      the scales, by asynchronous copies up to six K blocks ahead;
 //               its arrival joins the MMAs' commit on the epilogue's barrier;
 //   warps 4–11  epilogue, warp w on TMEM lanes 32·(w mod 4) of half (w − 4)/4.
@@ -334,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4);    // both halves' MMAs of both CTAs
+      mbar_init(&empty[s], 2);    // both CTAs' MMAs: B arrives from both
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(&tfull[b], 2);    // the MMAs and the scales
@@ -406,37 +409,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     } else if ((warp == 1 || warp == 2) && lane == 0) {
       // -------------------------------------------------------- MMA issue --
       constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BNH);
-      const int half = warp - 1;
+      const int buf = warp - 1;   // every other K block
       const uint64_t ad0 = smem_desc_sw128(smem_u32(smA), 16, 1024);
-      const uint64_t bd0 =
-          smem_desc_sw128(smem_u32(smB + half * TILE_BYTES), 16, 1024);
-      uint32_t stage = 0, phase = 0, buf = 0, tphase = 1;
-      for (int64_t it = 0; it < blocks; ++it) {
-        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, 43) ||
-            !mbar_wait(&tempty[2 * half + buf], tphase, abort_flag, p.status,
-                       44))
-          break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + (2 * half + buf) * BNH;
+      const uint64_t bd0 = smem_desc_sw128(smem_u32(smB), 16, 1024);
+      uint32_t stage = buf, phase = 0, tphase = 1;
+      for (int64_t it = buf; it < blocks; it += 2) {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, 43)) break;
         const uint64_t ad = ad0 + stage * (TILE_BYTES >> 4);
         const uint64_t bd = bd0 + stage * (2 * TILE_BYTES >> 4);
-        tc_mma_f8(d, ad, bd, IDESC, 0);
-        tc_mma_f8(d, ad + 2, bd + 2, IDESC, 1);
-        tc_mma_f8(d, ad + 4, bd + 4, IDESC, 1);
-        tc_mma_f8(d, ad + 6, bd + 6, IDESC, 1);
-        tc_commit(&tfull[2 * half + buf]);
+        int half = 0;
+#pragma unroll
+        for (; half < 2; ++half) {
+          if (!mbar_wait(&tempty[2 * half + buf], tphase, abort_flag, p.status,
+                         44))
+            break;
+          tc_fence_after();
+          const uint32_t d = tmem_base + (2 * half + buf) * BNH;
+          const uint64_t bh = bd + half * (TILE_BYTES >> 4);
+          tc_mma_f8(d, ad, bh, IDESC, 0);
+          tc_mma_f8(d, ad + 2, bh + 2, IDESC, 1);
+          tc_mma_f8(d, ad + 4, bh + 4, IDESC, 1);
+          tc_mma_f8(d, ad + 6, bh + 6, IDESC, 1);
+          tc_commit(&tfull[2 * half + buf]);
+        }
+        if (half < 2) break;
         tc_commit_multicast(&empty[stage], 3);
-        if (++stage == STAGES) {
-          stage = 0;
+        stage += 2;
+        if (stage >= STAGES) {
+          stage -= STAGES;
           phase ^= 1;
         }
-        tphase ^= buf;
-        buf ^= 1;
+        tphase ^= 1;
       }
       if (*abort_flag) {
         volatile int no_abort = 0;
-        tc_commit(&drain[half]);
-        mbar_wait(&drain[half], 0, &no_abort, nullptr, 0);
+        tc_commit(&drain[buf]);
+        mbar_wait(&drain[buf], 0, &no_abort, nullptr, 0);
       }
     } else if (warp == 3) {
       // ----------------------------------------------------------- scales --
