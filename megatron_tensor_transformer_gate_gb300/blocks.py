@@ -171,3 +171,127 @@ class TPLayer:
         g = grads if grads is not None else self.alloc_grads(P)
         B.layer_bwd(self.desc, dout, x, P, self.ws, g, self.scratch, stream)
         return g
+
+
+class TPBlockFP8MLP:
+    """Residual + RMSNorm + SwiGLU MLP with every product, forward and
+    backward, on block-scaled E4M3 operands:
+
+        x1 = x + r,  Y = RMSNorm(x1)·γ,  [G | U] = Y·W1ᵀ,
+        Z = (SiLU(G) ⊙ U)·W2ᵀ
+
+    for T tokens (one for a generated token, or a batch).  Z is handed on
+    without x1: the next norm adds it as its r.  Scales are 1×128 along each
+    product's reduction axis for activations and gradients, 128×128 for
+    weights; γ, x, r, x1, Z and the gradients are bf16 (weight gradients in
+    ``grad_dtype``, bf16 or fp32).
+
+    W1 is [2·h_ffn, h] (gate rows, then up rows), W2 [h, h_ffn], both bf16 or
+    fp32, unsharded.  Each of the n logical shards holds h_ffn/n hidden units,
+    a multiple of 128 so that no block of 128 crosses a shard: quantizing the
+    whole tensors is then quantizing each shard's, and the g and f sums are
+    taken in the products' accumulation (the fused mode; no other).
+
+    ``train=False`` keeps neither what the backward reads nor the transposed
+    weights."""
+
+    def __init__(self, T, h, h_ffn, n=1, *, eps=1e-5, train=True,
+                 grad_dtype=torch.bfloat16, device="cuda"):
+        if min(T, h, h_ffn, n) < 1 or h % 8 or h > 16384:
+            raise ValueError("sizes: T, n ≥ 1, h a multiple of 8 up to 16384")
+        if h_ffn % n or (h_ffn // n) % 128:
+            raise ValueError("h_ffn/n: a multiple of 128")
+        if grad_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("grad_dtype: bfloat16 or float32")
+        self.T, self.h, self.f, self.n = T, h, h_ffn, n
+        self.eps, self.train, self.grad_dtype = eps, train, grad_dtype
+        self.device = device
+        bf16 = dict(dtype=torch.bfloat16, device=device)
+        pair = lambda r, c: B.fp8_block_empty(r, c, device=device)
+        self.rstd = torch.empty(T, dtype=torch.float32, device=device)
+        self.y, self.a = pair(T, h), pair(T, h_ffn)
+        self.gu = torch.empty((T, 2 * h_ffn), **bf16)
+        self.weights = None
+        if train:
+            self.x1 = None
+            self.y16 = torch.empty((T, h), **bf16)
+            self.yt, self.at = pair(h, T), pair(h_ffn, T)
+            self.dz, self.dzt = pair(T, h), pair(h, T)
+            self.dgu, self.dgut = pair(T, 2 * h_ffn), pair(2 * h_ffn, T)
+            self.da = torch.empty((T, h_ffn), **bf16)
+            self.dy = torch.empty((T, h), **bf16)
+            self.norm_scratch = _buf(B.rmsnorm_bwd_scratch_bytes(T, h), device)
+
+    def load_weights(self, W1, W2, stream=None):
+        """Quantize W1 and W2 (after every update of them)."""
+        if tuple(W1.shape) != (2 * self.f, self.h) or \
+                tuple(W2.shape) != (self.h, self.f):
+            raise ValueError(f"W1 {(2 * self.f, self.h)} and W2 "
+                             f"{(self.h, self.f)}, got {tuple(W1.shape)} and "
+                             f"{tuple(W2.shape)}")
+        if self.weights is None:
+            self.weights = [
+                [B.fp8_block_empty(*s, B.FP8_BLOCK, self.device)
+                 if s is not None else (None, None) for s in
+                 (W.shape, W.shape[::-1] if self.train else None)]
+                for W in (W1, W2)]
+        for W, (q, qt) in zip((W1, W2), self.weights):
+            B.quantize_fp8_block(W, *q, *qt, stream=stream)
+
+    def forward(self, x, gamma, r=None, out=None, x1=None, stream=None):
+        """(x1, Z).  x1 may be given (x or r among it); without r it is x."""
+        if self.weights is None:
+            raise RuntimeError("load_weights comes first")
+        if r is None:
+            x1 = x if x1 is None else x1
+        elif x1 is None:
+            x1 = torch.empty_like(x)
+        if out is None:
+            out = torch.empty((self.T, self.h), dtype=torch.bfloat16,
+                              device=self.device)
+        (w1, _), (w2, _) = self.weights
+        keep = self.train
+        B.add_rmsnorm_fp8_fwd(x, r, gamma, None if x1 is x and r is None
+                              else x1, *self.y, self.rstd,
+                              y=self.y16 if keep else None, eps=self.eps,
+                              stream=stream)
+        B.gemm_fp8_block(*self.y, *w1, self.gu, stream=stream)
+        B.swiglu_fp8_fwd(self.gu, *self.a, *(self.at if keep else ()),
+                         stream=stream)
+        B.gemm_fp8_block(*self.a, *w2, out, stream=stream)
+        if keep:
+            B.quantize_fp8_block(self.y16, qt=self.yt[0], st=self.yt[1],
+                                 stream=stream)
+            self.x1 = x1
+        return x1, out
+
+    def alloc_grads(self):
+        kw = dict(device=self.device)
+        return {"dX": torch.empty((self.T, self.h), dtype=torch.bfloat16, **kw),
+                "dgamma": torch.empty(self.h, dtype=torch.bfloat16, **kw),
+                "dW1": torch.empty((2 * self.f, self.h),
+                                   dtype=self.grad_dtype, **kw),
+                "dW2": torch.empty((self.h, self.f), dtype=self.grad_dtype,
+                                   **kw)}
+
+    def backward(self, dZ, gamma, dx1=None, grads=None, stream=None):
+        """Gradients after a forward of the same inputs (x1 unchanged since):
+        dX, of x and of r alike; dgamma, dW1, dW2.  dx1 is the gradient that
+        reaches x1 past the norm (the residual stream's).  The quantizations
+        pass gradients through."""
+        if not self.train or self.x1 is None:
+            raise RuntimeError("a forward of a block with train=True comes "
+                               "first")
+        g = grads if grads is not None else self.alloc_grads()
+        (_, w1t), (_, w2t) = self.weights
+        B.quantize_fp8_block(dZ, *self.dz, *self.dzt, stream=stream)
+        B.gemm_fp8_block(*self.dz, *w2t, self.da, stream=stream)
+        B.gemm_fp8_block(*self.dzt, *self.at, g["dW2"], stream=stream)
+        B.swiglu_fp8_bwd(self.da, self.gu, *self.dgu, *self.dgut,
+                         stream=stream)
+        B.gemm_fp8_block(*self.dgu, *w1t, self.dy, stream=stream)
+        B.gemm_fp8_block(*self.dgut, *self.yt, g["dW1"], stream=stream)
+        B.rmsnorm_bwd(self.dy, self.x1, gamma, self.rstd, g["dX"],
+                      g["dgamma"], self.norm_scratch, dres=dx1, eps=self.eps,
+                      stream=stream)
+        return g

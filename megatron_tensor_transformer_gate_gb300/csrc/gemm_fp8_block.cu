@@ -49,9 +49,9 @@ struct Params {
 // ==================================================================== wide ==
 constexpr int BN = 256;
 constexpr int BNH = BN / 2;                    // B rows loaded by each CTA
-constexpr int STAGES = 4;                      // even: see the MMA issue
+constexpr int STAGES = 4;
 constexpr int STAGE_BYTES = 3 * TILE_BYTES;    // 128 rows of A, 256 of B
-constexpr int TMEM_COLS = 512;                 // two halves × two K blocks × 128
+constexpr int TMEM_COLS = 512;                 // two K blocks × 256
 constexpr int WIDE_THREADS = 384;
 // Scales of the tile's 128 rows and of its columns (two blocks', or 256) for
 // one K block; staged this many blocks deep.
@@ -297,18 +297,16 @@ struct GridAcc {
 // (cta_group::1), so that handing a TMEM buffer over and back stays inside
 // the SM.  Roles:
 //   warp 0      TMA producer, a ring of four K blocks;
-//   warps 1, 2  MMA issue, every other K block each, the tile's columns in
-//               two halves with two TMEM buffers a half.  Beside eight busy
-//               epilogue warps one thread's waits and commits for a K block
-//               take about 400 cycles, in which the other's MMAs (512) run;
-//               with a half of every K block each, both idled together and a
-//               block took 919 cycles;
+//   warps 1, 2  MMA issue, every other K block and one TMEM buffer each: beside
+//               eight busy epilogue warps one thread's waits and commits for a
+//               K block take about 400 cycles, in which the other's MMAs (512)
+//               run;
 //   warp 3      the scales, by asynchronous copies up to six K blocks ahead;
 //               its arrival joins the MMAs' commit on the epilogue's barrier;
 //   warps 4–11  epilogue, warp w on TMEM lanes 32·(w mod 4) of half (w − 4)/4.
 // The epilogue's 128 sums a thread need more than the 168 registers that 384
-// threads can have, so the first warpgroup hands some over (128·56 + 256·224
-// = 384·168; with column scales 128·40 + 256·232).
+// threads can have, so the first warpgroup hands some over (128·40 + 256·232
+// = 384·168).
 template <int B_ROW, int OUT_F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     gemm_fp8_block_wide(const __grid_constant__ Params p) {
@@ -321,9 +319,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   uint8_t* staging = reinterpret_cast<uint8_t*>(scales + SLOTS * SLOT);
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * STAGING);
   uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;    // [half][buffer]
-  uint64_t* tempty = tfull + 4;
-  uint64_t* drain = tempty + 4;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -339,12 +337,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 2);    // both CTAs' MMAs: B arrives from both
     }
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 2);    // the MMAs and the scales
-      mbar_init(&tempty[b], 4);   // a lane of each of the half's warps
+      mbar_init(&tempty[b], 8);   // a lane of each epilogue warp
+      mbar_init(&drain[b], 1);
     }
-    mbar_init(&drain[0], 1);
-    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.ma);
@@ -358,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(B_ROW ? 40 : 56));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer --
       uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
@@ -408,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       }
     } else if ((warp == 1 || warp == 2) && lane == 0) {
       // -------------------------------------------------------- MMA issue --
-      constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BNH);
+      constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BN);
       const int buf = warp - 1;   // every other K block
       const uint64_t ad0 = smem_desc_sw128(smem_u32(smA), 16, 1024);
       const uint64_t bd0 = smem_desc_sw128(smem_u32(smB), 16, 1024);
@@ -417,22 +414,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
         if (!mbar_wait(&full[stage], phase, abort_flag, p.status, 43)) break;
         const uint64_t ad = ad0 + stage * (TILE_BYTES >> 4);
         const uint64_t bd = bd0 + stage * (2 * TILE_BYTES >> 4);
-        int half = 0;
-#pragma unroll
-        for (; half < 2; ++half) {
-          if (!mbar_wait(&tempty[2 * half + buf], tphase, abort_flag, p.status,
-                         44))
-            break;
-          tc_fence_after();
-          const uint32_t d = tmem_base + (2 * half + buf) * BNH;
-          const uint64_t bh = bd + half * (TILE_BYTES >> 4);
-          tc_mma_f8(d, ad, bh, IDESC, 0);
-          tc_mma_f8(d, ad + 2, bh + 2, IDESC, 1);
-          tc_mma_f8(d, ad + 4, bh + 4, IDESC, 1);
-          tc_mma_f8(d, ad + 6, bh + 6, IDESC, 1);
-          tc_commit(&tfull[2 * half + buf]);
-        }
-        if (half < 2) break;
+        if (!mbar_wait(&tempty[buf], tphase, abort_flag, p.status, 44)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * BN;
+        tc_mma_f8(d, ad, bd, IDESC, 0);
+        tc_mma_f8(d, ad + 2, bd + 2, IDESC, 1);
+        tc_mma_f8(d, ad + 4, bd + 4, IDESC, 1);
+        tc_mma_f8(d, ad + 6, bd + 6, IDESC, 1);
+        tc_commit(&tfull[buf]);
         tc_commit_multicast(&empty[stage], 3);
         stage += 2;
         if (stage >= STAGES) {
@@ -497,24 +486,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       for (int i = 0; i < AHEAD; ++i) fetch();
       for (int64_t it = 0; it < blocks; ++it) {
         const int buf = it & 1;
-        // Block it − 2 complete on both halves: this block's phase is open,
-        // and block it − 4, whose slot the next copies go to, has been read
-        // (the MMAs of it − 2 waited for its buffers).
+        // Block it − 2 complete: this block's phase is open, and block it − 4,
+        // whose slot the next copies go to, has been read (the MMAs of it − 2
+        // waited for its buffer).
         if (it >= 2) {
           const uint32_t par = ((it - 2) >> 1) & 1;
-          if (!mbar_wait_warp(&tfull[buf], par, abort_flag, p.status, 46) ||
-              !mbar_wait_warp(&tfull[2 + buf], par, abort_flag, p.status, 47))
+          if (!mbar_wait_warp(&tfull[buf], par, abort_flag, p.status, 46))
             break;
         }
         fetch();
         cp_async_wait<AHEAD>();
         __syncwarp();
-        if (lane < 2) mbar_arrive(&tfull[2 * lane + buf]);
+        if (lane == 0) mbar_arrive(&tfull[buf]);
       }
       cp_async_wait<0>();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(B_ROW ? 232 : 224));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ------------------------------------------------------------ epilogue --
     using Acc = typename std::conditional<B_ROW != 0, GridAcc, RowAcc>::type;
     const int quarter = warp & 3;          // TMEM lanes this warp may read
@@ -522,9 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     uint4* stage = reinterpret_cast<uint4*>(staging + (warp - 4) * STAGING);
     const uint32_t taddr0 = tmem_base +
                             (static_cast<uint32_t>(quarter * 32) << 16) +
-                            2 * half * BNH;
-    uint64_t* tf = tfull + 2 * half;
-    uint64_t* te = tempty + 2 * half;
+                            half * BNH;
     int64_t it = 0;
     bool ok = true, ready = false;
     typename Acc::Chunk r[2];   // a chunk being added, the next on its way
@@ -532,16 +518,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     auto slot = [&](int64_t i) { return scales + (i & (SLOTS - 1)) * SLOT; };
     auto begin = [&](int64_t i) {   // block i is there: its first chunk, scales
       tc_fence_after();
-      Acc::load(taddr0 + (i & 1) * BNH, 0, r[0]);
+      Acc::load(taddr0 + (i & 1) * BN, 0, r[0]);
       a.scales(slot(i) + quarter * 32, slot(i) + BM, half, lane);
     };
     for (int t = cid; ok && t < p.total_tiles; t += ncl) {
       a.clear();
       for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
         const int buf = it & 1;
-        const uint32_t taddr = taddr0 + buf * BNH;
+        const uint32_t taddr = taddr0 + buf * BN;
         if (!ready) {
-          if (!mbar_wait_warp(&tf[buf], (it >> 1) & 1, abort_flag, p.status,
+          if (!mbar_wait_warp(&tfull[buf], (it >> 1) & 1, abort_flag, p.status,
                               45)) {
             ok = false;
             break;
@@ -555,7 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
           a.columns(cols, c, lane);
           // whether the next block is there is asked in the shadow of a load
           if (c + 1 == Acc::CHUNKS)
-            ready = mbar_test_warp(&tf[buf ^ 1], ((it + 1) >> 1) & 1);
+            ready = mbar_test_warp(&tfull[buf ^ 1], ((it + 1) >> 1) & 1);
           Acc::wait(r[c & 1]);
           if (c + 1 < Acc::CHUNKS) {
             Acc::load(taddr, c + 1, r[(c + 1) & 1]);
@@ -563,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
             // the buffer is read (by all lanes: the wait is the warp's): the
             // MMAs may have it back
             tc_fence_before();
-            if (lane == 0) mbar_arrive_relaxed(&te[buf]);
+            if (lane == 0) mbar_arrive_relaxed(&tempty[buf]);
             if (ready) begin(it + 1);
           }
           a.add(r[c & 1], c);
@@ -1102,9 +1088,10 @@ int narrow(const GemmFp8Block& g, cudaStream_t s, unsigned* status, int bn,
 //    the two not hidden.  Estimated / measured: 1×4096×4096 split 8 7.0 / 7.8,
 //    split 2 10 / 10; 48×8192×28672 split 4 47 / 45, split 1 98 / 90;
 //    128×8192×28672 split 2 60 / 56, split 4 64 / 62; 512×4096×4096 18 / 19;
-//  * wide: 6, and 0.5 a K block of each round of tiles (0.72 with a scale for
-//    each row of B).  512×4096×4096 22 / 21, 1024×8192×8192 70 / 70,
-//    256×8192×28672 118 / 111 (narrow, split 1: 105 / 98).
+//  * wide: 5, and for each round of tiles 2 and 0.46 a K block (0.66 with a
+//    scale for each row of B).  512×4096×4096 22 / 21, 1024×8192×8192 68 / 68,
+//    256×8192×28672 110 / 108 (narrow, split 1: 105 / 98),
+//    8192×8192×4096 239 / 232.
 // Clusters of more than four CTAs leave SMs of a GPC empty.
 struct Plan {
   int bn = 0;      // 0: wide
@@ -1116,8 +1103,8 @@ Plan choose(const GemmFp8Block& g, int64_t kblocks) {
   const bool b_row = g.b_group == kFp8Row;
   const int64_t tiles = up(g.M, 2 * BM) * up(g.N, BN);
   Plan best;
-  double least = 6.0 + up(tiles, std::max(sms / 2, 1)) * kblocks *
-                           (b_row ? 0.72 : 0.5);
+  double least = 5.0 + up(tiles, std::max(sms / 2, 1)) *
+                           (2.0 + kblocks * (b_row ? 0.66 : 0.46));
   const double bytes = ((double)g.M + (double)g.N) * (double)g.K / 6.4e6;
   const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
   const double kb_us = bn <= 32 ? 0.34 : bn <= 64 ? 0.37 : 0.40;

@@ -21,7 +21,7 @@ Pins: tests/test_fp8_block_host.py.
 
 import numpy as np
 
-from .fp8 import E4M3_MAX, e4m3_decode, e4m3_encode
+from .fp8 import E4M3_MAX, e4m3_decode, e4m3_encode, round_bf16
 
 GROUP = 128
 FLOOR = np.float32(2.0 ** -100)
@@ -93,3 +93,28 @@ def swiglu_grad(dA, gu):
     s = 1.0 / (1.0 + np.exp(-g))
     return np.concatenate([dA * u * s * (1.0 + g * (1.0 - s)), dA * g * s],
                           axis=1)
+
+
+def mlp(x, r, gamma, W1, W2, dZ, dx1, eps):
+    """The residual + RMSNorm + SwiGLU MLP with block-scaled operands, forward
+    and backward, each step's stored tensor rounded as the device stores it
+    (bf16, or E4M3 codes of the values before any other rounding)."""
+    from .norm import rmsnorm_backward, rmsnorm_forward
+    x1 = round_bf16(x if r is None else x + r)
+    y = rmsnorm_forward(x1, gamma, eps)["y"]
+
+    def deq(v, group):
+        return dequantize(*quantize(v, group))
+
+    w1, w2 = deq(W1, "block"), deq(W2, "block")
+    gu = round_bf16(deq(y, "row") @ w1.T)
+    a = swiglu(gu)
+    Z = deq(a, "row") @ w2.T
+    dA = round_bf16(deq(dZ, "row") @ w2)
+    dW2 = deq(dZ.T, "row") @ deq(a.T, "row").T
+    dgu = swiglu_grad(dA, gu)
+    dY = round_bf16(deq(dgu, "row") @ w1)
+    dW1 = deq(dgu.T, "row") @ deq(round_bf16(y).T, "row").T
+    n = rmsnorm_backward(dY, x1, gamma, eps, dres=dx1)
+    return {"x1": x1, "Z": Z, "dX": n["dx"], "dgamma": n["dgamma"],
+            "dW1": dW1, "dW2": dW2}
