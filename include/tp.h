@@ -434,7 +434,10 @@ tp_status tp_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* qa,
  * whole block reads as NaN.
  * (The per-tensor tp_quantize_fp8 stores the factor r as its scale; here the
  * scale is what a code is multiplied by.)
- * Sizes: 1 ≤ rows, cols ≤ 2^30, at most 2^31 − 1 tiles of 128×128. */
+ * Sizes: 1 ≤ rows, cols ≤ 2^30, at most 2^31 − 1 tiles of 128×128.  No call
+ * below needs a workspace or keeps anything between calls, and none leaves
+ * the order of a sum open: the same inputs give the same bits.  Outputs do
+ * not overlap inputs or each other, except where said. */
 typedef enum { TP_FP8_ROW = 0, TP_FP8_BLOCK = 1 } tp_fp8_group;
 
 /* Codes of x (TP_F32 or TP_BF16, [rows, cols], row stride ldx ≥ cols) in q
@@ -466,7 +469,7 @@ tp_status tp_swiglu_fp8_bwd(int64_t T, int64_t f, const void* dA,
                             tp_stream stream);
 
 /* Residual addition and RMSNorm into codes (TP_FP8_ROW); x, r, x1, y [T, h]
- * and γ [h] bf16, dense, 1 ≤ h ≤ 16384:
+ * and γ [h] bf16, dense, 1 ≤ h ≤ 16384, ε ≥ 0:
  *   x1 = x + r (rounded to bf16),  rstd_t = 1/sqrt(mean_j x1_tj² + ε),
  *   y = x1·rstd·γ (fp32), its codes in q and s.
  * r NULL: x1 = x.  x1 NULL (only where r is): not written; it may be x or r

@@ -1277,6 +1277,7 @@ extern "C" tp_status tp_add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps,
     if (!x || !gamma || !rstd) return TP_ERR_NULL;
     if (r != nullptr && x1 == nullptr) return TP_ERR_NULL;
     if (T < 1 || T > kMaxDim || h < 1 || h > 16384) return TP_ERR_SHAPE;
+    if (!(eps >= 0.0f)) return TP_ERR_ARG;
     const tp_status rc = check_fp8_operand(T, h, TP_FP8_ROW, q, ldq, s, lds);
     if (rc != TP_OK) return rc;
     for (const void* p : {x, r, gamma, (const void*)x1, (const void*)y})

@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "common.cuh"
@@ -653,6 +654,20 @@ double out_bytes(const Fp8BlockOut& o, int64_t rows, int64_t cols) {
 }
 
 // ----------------------------------------------------- residual + RMSNorm --
+// Sets a kernel's dynamic shared memory limit once per device.
+template <typename K>
+int allow_smem(K kernel, int bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load()) return cudaSuccess;
+  err = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) done[dev].store(true);
+  return err;
+}
+
 struct NormArgs {
   // x1 may be x or r: no read-only loads, and each element is read before it
   // is written, by the same thread
@@ -895,19 +910,11 @@ __global__ void __launch_bounds__(THREADS, CTAS)
 
 template <int THREADS, int V, int CTAS, int STAGES>
 int launch_norm_staged(const NormArgs& p, cudaStream_t s) {
-  static bool done[64];
+  static std::atomic<bool> done[64];
   auto kernel = add_rmsnorm_fp8_staged_kernel<THREADS, V, CTAS, STAGES>;
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev >= 64 || !done[dev]) {
-    // V vectors of 16 bytes a thread, x and r
-    err = cudaFuncSetAttribute(kernel,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               STAGES * 2 * V * THREADS * 16);
-    if (err != cudaSuccess) return err;
-    if (dev < 64) done[dev] = true;
-  }
+  // V vectors of 16 bytes a thread, x and r
+  const int err = allow_smem(kernel, STAGES * 2 * V * THREADS * 16, done);
+  if (err) return err;
   const size_t smem = (size_t)STAGES * (p.r != nullptr ? 2 : 1) * p.h * 2;
   const int64_t grid =
       std::min<int64_t>(p.rows, (int64_t)device_sm_count() * CTAS);
@@ -991,17 +998,9 @@ int swiglu_fp8_bwd(int64_t T, int64_t f, const void* da, int64_t ldda,
   // a few rows: spread over half-warps instead (1 x 28672: 2.8 us)
   if (f % TILE || (o.qt == nullptr && T < 64))
     return launch_tiles<false>(src, kFp8Row, T, 2 * f, o, bytes, s);
-  static bool done[64];
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev >= 64 || !done[dev]) {
-    err = cudaFuncSetAttribute(swiglu_bwd_pair_kernel,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               PAIR_SMEM);
-    if (err != cudaSuccess) return err;
-    if (dev < 64) done[dev] = true;
-  }
+  static std::atomic<bool> done[64];
+  const int err = allow_smem(swiglu_bwd_pair_kernel, PAIR_SMEM, done);
+  if (err) return err;
   const int64_t pairs = f / TILE, rt = (T + TILE - 1) / TILE;
   {
     ProfScope ps(s, KF_QUANT, 0.0, bytes);

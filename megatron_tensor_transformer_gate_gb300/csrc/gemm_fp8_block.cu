@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <type_traits>
@@ -949,30 +950,26 @@ bool operand_map(CUtensorMap* m, const uint8_t* q, int64_t rows, int64_t K,
 
 constexpr int kMaxDevices = 64;
 
-// Attributes of a kernel, set once per device.
-template <typename K>
-int prepare_kernel(K kernel, int smem, bool (&done)[kMaxDevices]) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+int current_device(int& dev) {
+  const cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  if (dev >= 0 && dev < kMaxDevices && done[dev]) return cudaSuccess;
-  err = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev] = true;
-  return err;
+  return dev < 0 || dev >= kMaxDevices ? cudaErrorInvalidDevice : cudaSuccess;
 }
 
+// Clusters of the wide kernel that the device holds at once; the first call on
+// a device sets the kernel's attributes.
 template <int B_ROW, int OUT_F32>
 int launch_wide(const Params& prm, cudaStream_t s) {
-  static bool done[kMaxDevices];
-  static int clusters[kMaxDevices];
+  static std::atomic<int> clusters[kMaxDevices];
   auto kernel = gemm_fp8_block_wide<B_ROW, OUT_F32>;
-  int err = prepare_kernel(kernel, WIDE_SMEM, done);
+  int dev = 0, err = current_device(dev);
   if (err) return err;
-  int dev = 0;
-  if ((err = cudaGetDevice(&dev))) return err;
-  int ncl = dev < kMaxDevices ? clusters[dev] : 0;
+  int ncl = clusters[dev].load();
   if (ncl == 0) {
+    if ((err = cudaFuncSetAttribute(kernel,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    WIDE_SMEM)))
+      return err;
     // the register hand-over sums to 384·168: refuse a build with fewer
     cudaFuncAttributes fa;
     if ((err = cudaFuncGetAttributes(&fa, kernel))) return err;
@@ -984,7 +981,7 @@ int launch_wide(const Params& prm, cudaStream_t s) {
     cfg.dynamicSmemBytes = WIDE_SMEM;
     if ((err = cudaOccupancyMaxActiveClusters(&ncl, kernel, &cfg))) return err;
     if (ncl < 1) return cudaErrorInvalidConfiguration;
-    if (dev < kMaxDevices) clusters[dev] = ncl;
+    clusters[dev].store(ncl);
   }
   const int grid = 2 * std::min(prm.total_tiles, ncl);
   kernel<<<grid, WIDE_THREADS, WIDE_SMEM, s>>>(prm);
@@ -993,10 +990,17 @@ int launch_wide(const Params& prm, cudaStream_t s) {
 
 template <int BNT, int OUT_F32>
 int launch_narrow(const NarrowParams& prm, unsigned grid, cudaStream_t s) {
-  static bool done[kMaxDevices];
+  static std::atomic<bool> done[kMaxDevices];
   auto kernel = gemm_fp8_block_narrow<BNT, OUT_F32>;
-  const int err = prepare_kernel(kernel, Narrow<BNT>::SMEM, done);
+  int dev = 0, err = current_device(dev);
   if (err) return err;
+  if (!done[dev].load()) {
+    if ((err = cudaFuncSetAttribute(kernel,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Narrow<BNT>::SMEM)))
+      return err;
+    done[dev].store(true);
+  }
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(grid);

@@ -150,8 +150,8 @@ def test_norm_refusals(tp):
     L = tp.lib()
 
     def norm(T=4, h=100, x=FAKE, r=FAKE, g=FAKE, x1=FAKE, y=None, rstd=FAKE,
-             q=FAKE, ldq=112, s=FAKE, lds=4):
-        return L.tp_add_rmsnorm_fp8_fwd(T, h, 1e-5, x, r, g, x1, y, rstd, q,
+             q=FAKE, ldq=112, s=FAKE, lds=4, eps=1e-5):
+        return L.tp_add_rmsnorm_fp8_fwd(T, h, eps, x, r, g, x1, y, rstd, q,
                                         ldq, s, lds, None)
 
     assert norm(x=None) == NULL and norm(g=None) == NULL
@@ -161,6 +161,7 @@ def test_norm_refusals(tp):
     assert norm(h=16385, ldq=16400) == SHAPE
     assert norm(ldq=100) == SHAPE and norm(lds=3) == SHAPE
     assert norm(y=ODD) == ARG
+    assert norm(eps=-1e-5) == ARG and norm(eps=float("nan")) == ARG
     assert norm(rstd=ctypes.c_void_p(0x100002)) == ARG
 
 

@@ -299,7 +299,8 @@ PRODUCTS = [(1, 1, 1), (1, 16, 16), (1, 129, 130), (1, 1000, 4096),
             (48, 384, 1376), (64, 256, 640), (65, 130, 260), (128, 128, 384),
             (129, 257, 513), (200, 1024, 512), (256, 256, 128),
             (300, 520, 208), (513, 384, 4096), (700, 260, 1100),
-            (2600, 2400, 300)]
+            (2600, 2400, 300), (2600, 2400, 40), (1000, 16, 512),
+            (3000, 5, 300), (300, 5000, 128), (150, 700, 3000)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -402,3 +403,27 @@ def test_products_on_a_side_stream_and_in_a_graph(tp):
         check_product(cs, *small, "graph, small")
         check_product(cw, *wide, "graph, wide")
         assert torch.equal(cs, es) and torch.equal(cw, ew)
+
+
+@pytest.mark.parametrize("M", [1, 200])
+def test_offsets_past_32_bits(tp, M):
+    # 4.6 G elements: the last rows' codes, scales and products
+    N, K, tail = 70000, 65536, 300
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    w = torch.empty((N, K), dtype=torch.bfloat16, device="cuda")
+    w.zero_()
+    w[-tail:] = torch.randn((tail, K), generator=gen, device="cuda")
+    q, s = tp.fp8_block_empty(N, K)
+    tp.quantize_fp8_block(w, q, s)
+    tp.device_status()
+    wf = w[-tail:].float().cpu().numpy()
+    del w
+    wq, ws = ob.quantize(wf, "row")
+    np.testing.assert_array_equal(s[:, -tail:].cpu().numpy(), ws)
+    np.testing.assert_array_equal(codes(q[-tail:]), wq)
+    qa, sa = operand(tp, M, K, "row", 1)
+    C = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    tp.gemm_fp8_block(qa, sa, q, s, C)
+    tp.device_status()
+    assert not bool(C[:, :-tail].any())
+    check_product(C[:, -tail:], qa, sa, q[-tail:], s[:, -tail:], "tail")
