@@ -156,11 +156,12 @@ SIGNATURES = {
 }
 
 _lib = None
+_tpcall = None   # the CPython module of the block-scaled calls (csrc/pycall.c)
 
 
 def lib():
     """The loaded library (raises if it has not been built)."""
-    global _lib
+    global _lib, _tpcall
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(
@@ -171,7 +172,15 @@ def lib():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        _lib = L
+        from . import _tpcall as fast
+        fast.bind(torch.bfloat16, torch.float32, torch.float8_e4m3fn,
+                  torch.uint8, torch._C._cuda_getDevice,
+                  torch._C._cuda_getCurrentRawStream,
+                  *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
+                    ("tp_quantize_fp8_block", "tp_swiglu_fp8_fwd",
+                     "tp_swiglu_fp8_bwd", "tp_add_rmsnorm_fp8_fwd",
+                     "tp_gemm_fp8_block")))
+        _lib, _tpcall = L, fast
     return _lib
 
 
@@ -259,9 +268,10 @@ def fp8_block_empty(rows, cols, group=FP8_ROW, device="cuda"):
     return q, s
 
 
-# The checks of a call run before every launch and are on the path of a
-# generated token, where the launch itself takes about 3 µs: each is one
-# expression over attributes read once, and only a failed one looks for words.
+# The checks of a call run before every launch, which for a generated token is
+# most of its time.  csrc/pycall.c makes them for arguments in their ordinary
+# form and calls the C entry (3 to 5 µs a call); where it finds anything else
+# it answers None, and the functions below check again and say what is wrong.
 def _shape(t):
     return tuple(t.shape)
 
@@ -370,10 +380,25 @@ def _fp8_outs(rows, cols, dev, q, s, qt, st):
     return a[:4] + b[:4], ga
 
 
+def _load():
+    lib()
+    return _tpcall
+
+
+def _done(rc, where):
+    """Whether _tpcall made the call (an error of it is raised)."""
+    if rc:
+        check(rc, where)
+    return rc is not None
+
+
 def quantize_fp8_block(x, q=None, s=None, qt=None, st=None, stream=None):
     """Block-scaled E4M3 codes of x (bf16 or fp32 [rows, cols]) into (q, s),
     of its transpose into (qt, st); the scales' shape says whether a scale
     belongs to 128 elements of a row or to a 128×128 block."""
+    if _done((_tpcall or _load()).quantize(x, q, s, qt, st, stream),
+             "tp_quantize_fp8_block"):
+        return
     rows, cols, ld, dev = _matrix(x, "x")
     outs, group = _fp8_outs(rows, cols, dev, q, s, qt, st)
     check(lib().tp_quantize_fp8_block(dtype_code(x), group, rows, cols,
@@ -399,6 +424,9 @@ def _gate_up(gu):
 def swiglu_fp8_fwd(gu, q=None, s=None, qt=None, st=None, stream=None):
     """Codes of SiLU(G)⊙U ([T, f]) into (q, s), of its transpose into
     (qt, st); gu is [G | U], bf16 [T, 2f]."""
+    if _done((_tpcall or _load()).swiglu(gu, q, s, qt, st, stream),
+             "tp_swiglu_fp8_fwd"):
+        return
     T, f, ld, dev = _gate_up(gu)
     outs, group = _fp8_outs(T, f, dev, q, s, qt, st)
     if group != FP8_ROW and T > 1:
@@ -411,6 +439,9 @@ def swiglu_fp8_fwd(gu, q=None, s=None, qt=None, st=None, stream=None):
 def swiglu_fp8_bwd(dA, gu, q=None, s=None, qt=None, st=None, stream=None):
     """Codes of [dG | dU] ([T, 2f]) into (q, s), of its transpose into
     (qt, st), from dA (bf16 [T, f]) and the forward's gu."""
+    if _done((_tpcall or _load()).swiglu_bwd(dA, gu, q, s, qt, st, stream),
+             "tp_swiglu_fp8_bwd"):
+        return
     T, f, ld, dev = _gate_up(gu)
     rows, cols, ldda, _ = _matrix(dA, "dA")
     if dA.dtype is not torch.bfloat16:
@@ -430,6 +461,9 @@ def add_rmsnorm_fp8_fwd(x, r, gamma, x1, q, s, rstd, y=None, eps=1e-5,
     """x1 = x + r (r None: x1 is x and may be None), the codes of
     RMSNorm(x1)·γ into (q, s), rstd [T] fp32, and y (bf16, optional); x1 may
     be x or r."""
+    if _done((_tpcall or _load()).norm(x, r, gamma, x1, q, s, rstd, y, eps, stream),
+             "tp_add_rmsnorm_fp8_fwd"):
+        return
     T, h, _, dev = _matrix(x, "x")
     bf16, shape = torch.bfloat16, (T, h)
     px = _dense(x, "x", bf16, shape, dev)
@@ -451,6 +485,9 @@ def add_rmsnorm_fp8_fwd(x, r, gamma, x1, q, s, rstd, y=None, eps=1e-5,
 def gemm_fp8_block(qa, sa, qb, sb, C, stream=None):
     """C[M, N] (bf16 or fp32) = A·Bᵀ of the block-scaled A = (qa, sa) [M, K]
     and B = (qb, sb) [N, K]."""
+    if _done((_tpcall or _load()).gemm(qa, sa, qb, sb, C, stream),
+             "tp_gemm_fp8_block"):
+        return
     M, N, ldc, dev = _matrix(C, "C")
     K = qa.shape[-1]
     pa, lda, psa, ldsa, ga = _fp8_pair(qa, sa, "qa", M, K, dev)

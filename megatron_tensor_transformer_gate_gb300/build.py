@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtp.so")
+PYCALL = os.path.join(PKG, "_tpcall.so")
 
 SOURCES = ["api.cu", "gemm_tc.cu", "gemm_simt.cu", "elementwise.cu",
            "attn_fwd_tc.cu", "attn_bwd_tc.cu", "fp8.cu", "fp8_block.cu",
@@ -60,9 +62,28 @@ def _compile(src, verbose=False):
     return obj, (r.stdout + r.stderr).strip() or None
 
 
+def _build_pycall():
+    """``_tpcall.so``: the CPython module beside the binding (host code)."""
+    src = os.path.join(CSRC, "pycall.c")
+    if os.path.exists(PYCALL) and os.path.getmtime(PYCALL) >= max(
+            os.path.getmtime(src), os.path.getmtime(__file__)):
+        return
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("gcc not found")
+    tmp = PYCALL + ".tmp"
+    r = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC",
+                        "-I", sysconfig.get_paths()["include"], src, "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed for pycall.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PYCALL)
+
+
 def build(verbose=False, jobs=None):
     """Compile every source and link ``libtp.so``; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
+    _build_pycall()
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 4)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
         results = list(ex.map(lambda s: _compile(s, verbose), SOURCES))

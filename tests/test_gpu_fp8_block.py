@@ -427,3 +427,51 @@ def test_offsets_past_32_bits(tp, M):
     tp.device_status()
     assert not bool(C[:, :-tail].any())
     check_product(C[:, -tail:], qa, sa, q[-tail:], s[:, -tail:], "tail")
+
+
+class NoFast:
+    """Stands in for the CPython module: leaves every call to Python."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+def test_both_ways_of_calling_agree(tp, monkeypatch):
+    T, h = 5, 1000
+    x, r, gu = activation(T, h, 1), activation(T, h, 2), activation(T, 2 * h, 3)
+    gamma = torch.ones(h, dtype=torch.bfloat16, device="cuda")
+    dA = activation(T, h, 4)
+    w, ws = operand(tp, 300, h, "block", 5)
+
+    def calls():
+        out = []
+        rstd = torch.empty(T, dtype=torch.float32, device="cuda")
+        x1, y = torch.empty_like(x), torch.empty_like(x)
+        q, s = room(tp, T, h)
+        tp.add_rmsnorm_fp8_fwd(x, r, gamma, x1, q, s, rstd, y=y)
+        C = torch.empty((T, 300), dtype=torch.bfloat16, device="cuda")
+        tp.gemm_fp8_block(q, s, w, ws, C)
+        out += [x1, y, rstd, q, s, C]
+        for f, cols in ((lambda *a: tp.quantize_fp8_block(x, *a), h),
+                        (lambda *a: tp.swiglu_fp8_fwd(gu, *a), h),
+                        (lambda *a: tp.swiglu_fp8_bwd(dA, gu, *a), 2 * h)):
+            both = room(tp, T, cols) + room(tp, cols, T)
+            f(*both)
+            out += both
+        return out
+
+    fast = calls()
+    # the ordinary call is the module's: it returned a status, not None
+    q, s = room(tp, T, h)
+    assert tp._tpcall.quantize(x, q, s, None, None, None) == 0
+    assert tp._tpcall.quantize(x, q, s, None, None,
+                               torch.cuda.current_stream()) == 0
+    for bad in ((x.cpu(), q, s), (x, q, None), (x, q[:, :-1], s),
+                (x.half(), q, s), (x, q, s.double()), (x.t(), q, s), (1, q, s)):
+        assert tp._tpcall.quantize(*bad, None, None, None) is None
+    monkeypatch.setattr(tp, "_tpcall", NoFast())
+    slow = calls()
+    for a, b in zip(fast, slow):
+        assert a.dtype == b.dtype
+        v = torch.uint8 if a.element_size() == 1 else a.dtype
+        assert torch.equal(a.view(v), b.view(v))
