@@ -657,6 +657,12 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
   const int kb0 = (int)((int64_t)p.kblocks * part / p.split);
   const int kb1 = (int)((int64_t)p.kblocks * (part + 1) / p.split);
 
+  auto copy = [&](int kb, uint32_t stage) {
+    mbar_arrive_expect_tx(&full[stage], L::STAGE);
+    tma_load_3d(smR + stage * TILE_BYTES, &p.mr, &full[stage], kb * BK, 0, r0);
+    tma_load_3d(smT + stage * L::T_BYTES, &p.mt, &full[stage], kb * BK, 0, t0);
+  };
+  const int primed = min(kb1 - kb0, L::STAGES);
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -669,6 +675,8 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    // the ring is filled while TMEM is allocated and the warps meet
+    for (int s = 0; s < primed; ++s) copy(kb0 + s, s);
   }
   if (warp == 1) tmem_alloc(tmem_slot, L::COLS);
   tc_fence_before();
@@ -685,17 +693,12 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      uint32_t stage = 0, phase = 1, armed = (1u << primed) - 1, armed_par = 0;
+      for (int kb = kb0 + primed; kb < kb1; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, 51))
           break;
-        mbar_arrive_expect_tx(&full[stage], L::STAGE);
-        armed |= 1u << stage;
         armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-        tma_load_3d(smR + stage * TILE_BYTES, &p.mr, &full[stage], kb * BK, 0,
-                    r0);
-        tma_load_3d(smT + stage * L::T_BYTES, &p.mt, &full[stage], kb * BK, 0,
-                    t0);
+        copy(kb, stage);
         if (++stage == L::STAGES) {
           stage = 0;
           phase ^= 1;
