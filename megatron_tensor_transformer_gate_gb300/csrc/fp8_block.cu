@@ -135,10 +135,16 @@ struct CopyF32 {
   __device__ int64_t col_tile(int64_t j, int64_t) const { return j; }
 };
 
-// σ(x), the quotient by the approximate division (2 ulp): the values only go
-// to E4M3, and an IEEE division is a third of the kernel's instructions.
+// σ(x) = 1 / (1 + 2^(−x·log2 e)) by the special-function unit's exponential
+// and reciprocal (1 and 2 ulp; 1 + inf gives 0): the values only go to E4M3,
+// and an IEEE division or a denormal-preserving exponential would be a third
+// of these kernels' instructions, which are what bounds them.
 __device__ __forceinline__ float sigmoid_approx(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(-x));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;"
+      : "=f"(r)
+      : "f"(1.0f + ex2_approx(x * -1.4426950408889634f)));
+  return r;
 }
 
 // A = SiLU(G)·U.
@@ -160,7 +166,7 @@ struct SwigluSource {
     unpack8(x[1], u);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      v[j] = __fdividef(g[j], 1.0f + __expf(-g[j])) * u[j];
+      v[j] = g[j] * sigmoid_approx(g[j]) * u[j];
   }
   __device__ int64_t col_tile(int64_t j, int64_t) const { return j; }
 };
@@ -255,17 +261,15 @@ struct Held {
     }
   }
 };
-// Largest magnitudes two at a time on the packed values (a bf16 maximum is
-// exact; like fmaxf it takes the other operand where one is NaN).
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+// max(m, |a|) on two packed values (a bf16 maximum is exact; like fmaxf it
+// takes the other operand where one is NaN).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t a) {
   __nv_bfloat162 x, y;
-  a &= 0x7FFF7FFFu;
-  b &= 0x7FFF7FFFu;
-  memcpy(&x, &a, 4);
-  memcpy(&y, &b, 4);
-  x = __hmax2(x, y);
-  memcpy(&a, &x, 4);
-  return a;
+  memcpy(&x, &m, 4);
+  memcpy(&y, &a, 4);
+  x = __hmax2(x, __habs2(y));
+  memcpy(&m, &x, 4);
+  return m;
 }
 template <int W>
 struct Held<CopyBf16<W>> {
@@ -284,9 +288,9 @@ struct Held<CopyBf16<W>> {
     return j & 1 ? t.y : t.x;
   }
   __device__ __forceinline__ float row_max(int i) const {
-    const uint32_t m = max_abs2(max_abs2(u[i].x, u[i].y),
-                                max_abs2(u[i].z, u[i].w));
-    const float2 t = unpack_bf16x2(max_abs2(m, 0));
+    const float2 t = unpack_bf16x2(
+        max_abs2(max_abs2(max_abs2(max_abs2(0u, u[i].x), u[i].y), u[i].z),
+                 u[i].w));
     return fmaxf(t.x, t.y);
   }
   __device__ __forceinline__ void col_max(float* m) const {
@@ -379,6 +383,9 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
   const int half = lane >> 4, l = lane & 15;
   const int64_t r0 = rt * TILE + (warp * 2 + half) * R;
   const int64_t c0 = ct * TILE + l * 8;
+  // this thread's rows and columns that exist
+  const int nr = (int)(rows - r0 < R ? rows - r0 : R);
+  const int nc = (int)(cols - c0 < 8 ? cols - c0 : 8);
   float colr[8];   // the factor of each of this thread's columns
   float rowr[R];   // and of each of its rows
   if (GROUP == kFp8Row) {
@@ -388,7 +395,7 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
       for (int i = 0; i < R; ++i) m[i] = h.row_max(i);
       // lanes 0 to 7 get the factors, 8 to 15 the scales, of row l mod R
       const float x = factor_or_scale(rows_max<R>(m, l), l & 8);
-      if (l >= 8 && l < 8 + R && r0 + l - 8 < rows)
+      if (l >= 8 && l < 8 + R && l - 8 < nr)
         o.s[ct * o.lds + r0 + l - 8] = x;
 #pragma unroll
       for (int i = 0; i < R; ++i)
@@ -445,15 +452,16 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
     }
   }
 
-  if (o.q != nullptr && c0 < cols) {
-    const int valid = (int)(cols - c0 < 8 ? cols - c0 : 8);
+  if (o.q != nullptr && nc > 0) {
+    uint8_t* q = o.q + r0 * o.ldq + c0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (r0 + i < rows) {
+      if (i < nr) {
         float v[8];
         h.row(i, v);
-        store8(o.q + (r0 + i) * o.ldq + c0, codes8(v, rowr[i]), valid);
+        store8(q, codes8(v, rowr[i]), nc);
       }
+      q += o.ldq;
     }
   }
   if (o.qt != nullptr) {
@@ -480,14 +488,19 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
     __syncthreads();
     const int64_t rr = rt * TILE + l * 8;   // eight rows of the source
     const int valid = (int)(rows - rr < 8 ? rows - rr : 8);
+    // columns 2R·warp + half + 2i of the tile
+    const int first = warp * 2 * R + half;
+    const int64_t left = cols - ct * TILE - first;
+    const int nt = (int)(left < TILE ? left : TILE);
+    uint8_t* q = o.qt + (ct * TILE + first) * o.ldqt + rr;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int c = (warp * R + i) * 2 + half;
-      const int64_t cc = ct * TILE + c;
+      const int c = first + 2 * i;
       const int chunk = l ^ (c >> 3);
       const uint2 u =
           *reinterpret_cast<const uint2*>(tile_t + c * TILE + chunk * 8);
-      if (cc < cols && valid > 0) store8(o.qt + cc * o.ldqt + rr, u, valid);
+      if (2 * i < nt && valid > 0) store8(q, u, valid);
+      q += 2 * o.ldqt;
     }
   }
 }
