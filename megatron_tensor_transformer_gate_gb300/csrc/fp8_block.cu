@@ -768,15 +768,23 @@ __device__ __forceinline__ uint4 load8_plain(const __nv_bfloat16* p,
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// THREADS threads a row, which stays in their registers (V vectors of eight
-// columns each, 16 neighbouring threads hold one group of 128); a warp per
-// row (eight rows a CTA) up to 512 columns, else a CTA per row.  γ is read
+// Threads of a row of h columns with V vectors of eight columns each: whole
+// warps, no more than the row has work for.
+int norm_threads(int h, int V) {
+  const int vectors = (h + 7) / 8;
+  return ((vectors + V - 1) / V + 31) / 32 * 32;
+}
+
+// At most THREADS threads a row, which stays in their registers (V vectors of
+// eight columns each, 16 neighbouring threads hold one group of 128); a warp
+// per row (eight rows a CTA) up to 512 columns, else a CTA per row.  γ is read
 // before the row's sum is known, so that its latency is not paid after it.
 template <int THREADS, int V, int CTAS, int W>
 __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
     add_rmsnorm_fp8_kernel(const NormArgs p) {
   constexpr bool WARP = THREADS == 32;
   __shared__ float red[THREADS / 32];
+  const int threads = WARP ? 32 : blockDim.x;
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
   const int64_t row =
       WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
@@ -787,7 +795,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
   uint4 u[V], ur[V], g[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = (k * THREADS + tid) * 8;
+    const int c = (k * threads + tid) * 8;
     u[k] = ur[k] = make_uint4(0, 0, 0, 0);
     if (c < h) {
       u[k] = load8_plain<W>(x + c, h - c);
@@ -796,14 +804,14 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = (k * THREADS + tid) * 8;
+    const int c = (k * threads + tid) * 8;
     g[k] = make_uint4(0, 0, 0, 0);
     if (c < h) g[k] = load8<W>(p.gamma + c, h - c);
   }
   float ss = 0.0f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = (k * THREADS + tid) * 8;
+    const int c = (k * threads + tid) * 8;
     ss += add_squares(u[k], ur[k], p.r != nullptr);
     if (p.x1 != nullptr && c < h) save8<W>(p.x1 + row * h + c, u[k], h - c);
   }
@@ -814,33 +822,35 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
     __syncthreads();
     ss = 0.0f;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) ss += red[w];
+    for (int w = 0; w < THREADS / 32; ++w)
+      if (w * 32 < threads) ss += red[w];
   }
   const float rs = rsqrtf(ss / (float)h + p.eps);
   if (tid == 0) p.rstd[row] = rs;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = (k * THREADS + tid) * 8;
+    const int c = (k * threads + tid) * 8;
     emit_norm<W>(p, row, c, h - c, u[k], g[k], rs);
   }
 }
 
 // Many rows of 16-byte aligned vectors: a CTA works through every gridDim-th
-// row, thread 0 copying x and r of the rows to come into a ring of STAGES
+// row, thread 0 copying x and r of the rows to come into a ring of one or two
 // stages (bulk copies), so that loads are in flight all the time and γ is
 // read once.  Waits are bounded; the block agrees on every outcome.
-template <int THREADS, int V, int CTAS, int STAGES>
+constexpr int MAX_STAGES = 2;
+template <int THREADS, int V, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS)
-    add_rmsnorm_fp8_staged_kernel(const NormArgs p) {
+    add_rmsnorm_fp8_staged_kernel(const NormArgs p, int stages) {
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ uint64_t full[STAGES];
+  __shared__ uint64_t full[MAX_STAGES];
   __shared__ float red[2][THREADS / 32];
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, h = p.h;
+  const int tid = threadIdx.x, threads = blockDim.x, h = p.h;
   const int nin = p.r != nullptr ? 2 : 1;
   const uint32_t row_bytes = (uint32_t)h * 2;
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -853,12 +863,12 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   };
   const int64_t step = gridDim.x;
   if (tid == 0)
-    for (int i = 0; i < STAGES; ++i)
+    for (int i = 0; i < stages; ++i)
       if (blockIdx.x + i * step < p.rows) issue(blockIdx.x + i * step, i);
   uint4 g[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = (k * THREADS + tid) * 8;
+    const int c = (k * threads + tid) * 8;
     g[k] = c < h ? load16<16>(p.gamma + c) : make_uint4(0, 0, 0, 0);
   }
   int sg = 0;
@@ -875,7 +885,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
     float ss = 0.0f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = (k * THREADS + tid) * 8;
+      const int c = (k * threads + tid) * 8;
       u[k] = make_uint4(0, 0, 0, 0);
       uint4 ur = u[k];
       if (c < h) {
@@ -891,19 +901,20 @@ __global__ void __launch_bounds__(THREADS, CTAS)
     for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
     if ((tid & 31) == 0) red[odd][tid >> 5] = ss;
     __syncthreads();   // the sums are there, the stage is read
-    if (tid == 0 && row + STAGES * step < p.rows) issue(row + STAGES * step, sg);
+    if (tid == 0 && row + stages * step < p.rows) issue(row + stages * step, sg);
     ss = 0.0f;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) ss += red[odd][w];
+    for (int w = 0; w < THREADS / 32; ++w)
+      if (w * 32 < threads) ss += red[odd][w];
     odd = !odd;
     const float rs = rsqrtf(ss / (float)h + p.eps);
     if (tid == 0) p.rstd[row] = rs;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = (k * THREADS + tid) * 8;
+      const int c = (k * threads + tid) * 8;
       emit_norm<16>(p, row, c, h - c, u[k], g[k], rs);
     }
-    if (++sg == STAGES) {
+    if (++sg == stages) {
       sg = 0;
       par ^= 1;
     }
@@ -911,9 +922,9 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   if (row < p.rows && tid == 0) {
     // gave up: let the copies in flight land before the block exits
     volatile int no_abort = 0;
-    for (int i = 0; i < STAGES && row + i * step < p.rows; ++i) {
+    for (int i = 0; i < stages && row + i * step < p.rows; ++i) {
       mbar_wait(&full[sg], par, &no_abort, nullptr, 0);
-      if (++sg == STAGES) {
+      if (++sg == stages) {
         sg = 0;
         par ^= 1;
       }
@@ -921,17 +932,19 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   }
 }
 
-template <int THREADS, int V, int CTAS, int STAGES>
-int launch_norm_staged(const NormArgs& p, cudaStream_t s) {
+template <int THREADS, int V, int CTAS>
+int launch_norm_staged(const NormArgs& p, int stages, cudaStream_t s) {
   static std::atomic<bool> done[64];
-  auto kernel = add_rmsnorm_fp8_staged_kernel<THREADS, V, CTAS, STAGES>;
+  auto kernel = add_rmsnorm_fp8_staged_kernel<THREADS, V, CTAS>;
   // V vectors of 16 bytes a thread, x and r
-  const int err = allow_smem(kernel, STAGES * 2 * V * THREADS * 16, done);
+  const int err = allow_smem(kernel, MAX_STAGES * 2 * V * THREADS * 16, done);
   if (err) return err;
-  const size_t smem = (size_t)STAGES * (p.r != nullptr ? 2 : 1) * p.h * 2;
-  const int64_t grid =
-      std::min<int64_t>(p.rows, (int64_t)device_sm_count() * CTAS);
-  kernel<<<(unsigned)grid, THREADS, smem, s>>>(p);
+  const size_t smem = (size_t)stages * (p.r != nullptr ? 2 : 1) * p.h * 2;
+  // CTAS on an SM with all THREADS; of smaller ones more fit
+  const int threads = norm_threads(p.h, V);
+  const int64_t grid = std::min<int64_t>(
+      p.rows, (int64_t)device_sm_count() * (CTAS * THREADS / threads));
+  kernel<<<(unsigned)grid, threads, smem, s>>>(p, stages);
   return cudaGetLastError();
 }
 
@@ -943,15 +956,20 @@ int launch_norm(const NormArgs& p, cudaStream_t s) {
   else if (p.h <= 512)
     add_rmsnorm_fp8_kernel<32, 2, 4, W><<<(T + 7) / 8, 256, 0, s>>>(p);
   else if (p.h <= 1024)
-    add_rmsnorm_fp8_kernel<128, 1, 8, W><<<T, 128, 0, s>>>(p);
+    add_rmsnorm_fp8_kernel<128, 1, 8, W>
+        <<<T, norm_threads(p.h, 1), 0, s>>>(p);
   else if (p.h <= 2048)
-    add_rmsnorm_fp8_kernel<256, 1, 4, W><<<T, 256, 0, s>>>(p);
+    add_rmsnorm_fp8_kernel<256, 1, 4, W>
+        <<<T, norm_threads(p.h, 1), 0, s>>>(p);
   else if (p.h <= 4096)
-    add_rmsnorm_fp8_kernel<512, 1, 2, W><<<T, 512, 0, s>>>(p);
+    add_rmsnorm_fp8_kernel<512, 1, 2, W>
+        <<<T, norm_threads(p.h, 1), 0, s>>>(p);
   else if (p.h <= 8192)
-    add_rmsnorm_fp8_kernel<512, 2, 2, W><<<T, 512, 0, s>>>(p);
+    add_rmsnorm_fp8_kernel<512, 2, 2, W>
+        <<<T, norm_threads(p.h, 2), 0, s>>>(p);
   else
-    add_rmsnorm_fp8_kernel<1024, 2, 1, W><<<T, 1024, 0, s>>>(p);
+    add_rmsnorm_fp8_kernel<1024, 2, 1, W>
+        <<<T, norm_threads(p.h, 2), 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -1043,17 +1061,18 @@ int add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps, const void* x,
                   2.0 * (y != nullptr) + 1.0) * T * h);
     // The ring pays where a CTA has several rows to run ahead on.
     const bool many = T >= 4 * (int64_t)device_sm_count();
+    const int stages = y == nullptr && h > 4096 ? 2 : 1;
     if (w == 16 && h > 512 && many) {
       if (h <= 1024)
-        err = launch_norm_staged<128, 1, 12, 4>(p, st);
+        err = launch_norm_staged<128, 1, 12>(p, stages, st);
       else if (h <= 2048)
-        err = launch_norm_staged<256, 1, 6, 4>(p, st);
+        err = launch_norm_staged<128, 2, 8>(p, stages, st);
       else if (h <= 4096)
-        err = launch_norm_staged<256, 2, 4, 3>(p, st);
+        err = launch_norm_staged<256, 2, 4>(p, stages, st);
       else if (h <= 8192)
-        err = launch_norm_staged<512, 2, 2, 3>(p, st);
+        err = launch_norm_staged<512, 2, 2>(p, stages, st);
       else
-        err = launch_norm_staged<512, 4, 1, 3>(p, st);
+        err = launch_norm_staged<512, 4, 1>(p, stages, st);
     } else if (w == 16) {
       err = launch_norm<16>(p, st);
     } else if (w == 8) {
