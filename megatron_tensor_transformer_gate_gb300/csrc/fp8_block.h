@@ -6,6 +6,7 @@
 // (TP_FP8_BLOCK: 128×128 blocks).  The element's value is q·s.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace tp {
@@ -58,5 +59,7 @@ struct GemmFp8Block {
   int64_t ldc = 0;
 };
 int gemm_fp8_block(const GemmFp8Block& p, void* stream, unsigned* status);
+// gemm_fp8_block_thin.cu: its form for M ≤ 8.
+int gemm_fp8_block_thin(const GemmFp8Block& p, cudaStream_t s);
 
 }  // namespace tp

@@ -5,9 +5,10 @@
 // kind::f8f6f4 of K = 32 into fresh TMEM columns); the epilogue warps read it
 // back while the next block runs, multiply it by sa·sb and add it to the
 // output tile, which stays in their registers over the whole K loop.  Two
-// forms:
-//  * wide: persistent clusters of two CTAs, 256×256 tiles (cta_group::2),
-//    for products that fill the card with such tiles;
+// forms here (up to eight rows of A have a third, gemm_fp8_block_thin.cu):
+//  * wide: persistent clusters of two CTAs, each with 128×256 of a 256×256
+//    tile and half of its B, which both get (TMA multicast), for products that
+//    fill the card with such tiles;
 //  * narrow: one CTA per 128×BN tile with B's rows (the weight) on the
 //    instruction's M side, BN = 16 to 128 rows of A, and K split over a
 //    cluster whose CTAs add up their parts through distributed shared memory
@@ -38,7 +39,7 @@ struct Params {
   CUtensorMap ma, mb;
   const float *sa, *sb;
   int64_t ldsa, ldsb;
-  int a_row, b_row;        // a scale for each row (1) or for 128 rows (0)
+  int a_row;               // sa: a scale for each row (1) or for 128 rows (0)
   int M, N, kblocks;
   int m_tiles, n_tiles, total_tiles, group_m;
   void* c;
@@ -1031,7 +1032,6 @@ int wide(const GemmFp8Block& g, cudaStream_t s, unsigned* status) {
   p.ldsa = g.ldsa;
   p.ldsb = g.ldsb;
   p.a_row = g.a_group == kFp8Row;
-  p.b_row = g.b_group == kFp8Row;
   p.M = (int)g.M;
   p.N = (int)g.N;
   p.kblocks = (int)((g.K + BK - 1) / BK);
@@ -1044,9 +1044,10 @@ int wide(const GemmFp8Block& g, cudaStream_t s, unsigned* status) {
   const int es = g.out_f32 ? 4 : 2;
   p.vec = (reinterpret_cast<uintptr_t>(g.c) & 15u) == 0 && g.ldc * es % 16 == 0;
   p.status = status;
+  const bool b_row = g.b_group == kFp8Row;
   if (g.out_f32)
-    return p.b_row ? launch_wide<1, 1>(p, s) : launch_wide<0, 1>(p, s);
-  return p.b_row ? launch_wide<1, 0>(p, s) : launch_wide<0, 0>(p, s);
+    return b_row ? launch_wide<1, 1>(p, s) : launch_wide<0, 1>(p, s);
+  return b_row ? launch_wide<1, 0>(p, s) : launch_wide<0, 0>(p, s);
 }
 
 int narrow(const GemmFp8Block& g, cudaStream_t s, unsigned* status, int bn,
@@ -1135,13 +1136,16 @@ Plan choose(const GemmFp8Block& g, int64_t kblocks) {
 
 int gemm_fp8_block(const GemmFp8Block& g, void* stream, unsigned* status) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t kblocks = (g.K + BK - 1) / BK;
   int err;
   {
     ProfScope ps(s, KF_GEMM_TC_FP8, 2.0 * g.M * g.N * g.K,
                  (double)(g.M + g.N) * g.K + (g.out_f32 ? 4.0 : 2.0) * g.M * g.N);
-    const Plan pl = choose(g, kblocks);
-    err = pl.bn ? narrow(g, s, status, pl.bn, pl.split) : wide(g, s, status);
+    if (g.M <= 8) {   // measured there
+      err = gemm_fp8_block_thin(g, s);
+    } else {
+      const Plan pl = choose(g, (g.K + BK - 1) / BK);
+      err = pl.bn ? narrow(g, s, status, pl.bn, pl.split) : wide(g, s, status);
+    }
   }
   if (err) return err;
   count_launch();

@@ -295,6 +295,7 @@ def check_product(C, qa, sa, qb, sb, what):
 
 
 PRODUCTS = [(1, 1, 1), (1, 16, 16), (1, 129, 130), (1, 1000, 4096),
+            (8, 40, 2064), (7, 1030, 3333), (8, 17, 28700), (9, 130, 1300),
             (2, 256, 128), (5, 300, 77), (16, 136, 1000), (17, 520, 2100),
             (48, 384, 1376), (64, 256, 640), (65, 130, 260), (128, 128, 384),
             (129, 257, 513), (200, 1024, 512), (256, 256, 128),
