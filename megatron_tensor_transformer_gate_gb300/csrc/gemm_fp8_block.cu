@@ -187,7 +187,7 @@ struct GridAcc {
   using Chunk = uint32_t[16];
   uint64_t acc[64];   // [chunk][unit][row]
   float s[4], sn[4];
-  uint64_t w2[4];
+  uint64_t w2[2][4];   // the columns' of the pair of chunks added, of the next
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0;
@@ -208,13 +208,13 @@ struct GridAcc {
     for (int j = 0; j < 4; ++j) s[j] = sn[j];
   }
   // cols: the half's 128 scales, column 16g + 8u + 2q + e at 16g + 4q + 2u + e
-  __device__ __forceinline__ void columns(const float* cols, int c, int lane) {
-    if (c & 1) return;
+  __device__ __forceinline__ void columns(const float* cols, int pair,
+                                          int lane) {
 #pragma unroll
     for (int u = 0; u < 4; u += 2)   // in order: hoisted loads cost spills
       asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-                   : "=l"(w2[u]), "=l"(w2[u + 1])
-                   : "r"(smem_u32(cols + 32 * (c >> 1) + 8 * u +
+                   : "=l"(w2[pair & 1][u]), "=l"(w2[pair & 1][u + 1])
+                   : "r"(smem_u32(cols + 32 * pair + 8 * u +
                                   (lane & 3) * 4)));
   }
   __device__ __forceinline__ void add(const Chunk& r, int c) {
@@ -230,7 +230,7 @@ struct GridAcc {
       for (int i = 0; i < 2; ++i)
         fma_f32x2(acc[c * 8 + u * 2 + i],
                   pack_f32x2(r[4 * u + 2 * i], r[4 * u + 2 * i + 1]),
-                  mul_f32x2(s2[i], w2[u]));
+                  mul_f32x2(s2[i], w2[(c >> 1) & 1][u]));
   }
   // The four lanes of a row exchange what makes 16 bytes in each: 64 bytes of
   // a row a store.
@@ -522,6 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       tc_fence_after();
       Acc::load(taddr0 + (i & 1) * BN, 0, r[0]);
       a.scales(slot(i) + quarter * 32, slot(i) + BM, half, lane);
+      a.columns(slot(i) + BM + half * BNH, 0, lane);
     };
     for (int t = cid; ok && t < p.total_tiles; t += ncl) {
       a.clear();
@@ -540,7 +541,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
         const float* cols = slot(it) + BM + half * BNH;
 #pragma unroll
         for (int c = 0; c < Acc::CHUNKS; ++c) {
-          a.columns(cols, c, lane);
+          if ((c & 1) == 1 && c + 1 < Acc::CHUNKS)
+            a.columns(cols, c / 2 + 1, lane);
           // whether the next block is there is asked in the shadow of a load
           if (c + 1 == Acc::CHUNKS)
             ready = mbar_test_warp(&tfull[buf ^ 1], ((it + 1) >> 1) & 1);
@@ -594,6 +596,8 @@ struct Narrow {
   static constexpr int STAGES = BNT <= 32 ? 5 : BNT <= 64 ? 4 : 6;
   static constexpr int BUFS = 4;
   static constexpr int COLS = BUFS * BNT;    // TMEM: 64, 128, 256, 512
+  static_assert(COLS >= 32 && COLS <= 512 && (COLS & (COLS - 1)) == 0,
+                "what TMEM is handed out in");
   static constexpr int SLOT = BM + BNT;                        // floats
   static constexpr int SCALES = NSLOTS * SLOT;
   static constexpr int SMEM = STAGES * STAGE + SCALES * 4 + 1024 + 256;
