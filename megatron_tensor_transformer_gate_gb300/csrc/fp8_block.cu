@@ -1,6 +1,10 @@
 // fp8_block.cu — the operators that write block-scaled E4M3 codes:
 // quantization, SwiGLU (forward and backward) and residual + RMSNorm.
 //
+// All of them read and write every byte once, so DRAM is their floor (figures
+// here are against a copy's 6.67 TB/s, device time of a launch, inputs not in
+// L2).
+//
 // With amax the largest magnitude of a block of 128 (1×128 or 128×128),
 //   r = 448 / amax,  s = amax / 448  (fp32),  q = e4m3(x·r),
 // values are taken in fp32 straight from the producing formula (SwiGLU, norm:
@@ -28,6 +32,15 @@ namespace {
 // flight.  A source's R, BATCH and CTAS (on an SM) are what its values leave
 // room for: bf16 values are kept as loaded (8 rows, four CTAs of 256
 // threads), computed ones as fp32 (4 rows, two CTAs of 512).
+//
+// Measured: 128×128 blocks and their transpose of a bf16 8192×28672 146 µs
+// (6.4 TB/s, 97 %); row scales both ways of 8192×8192 51 µs (5.3 TB/s, 79 %),
+// of 8192×8191 (rows on two bytes) 82; SwiGLU both ways 8192×11008 104 µs
+// (78 %).  With row scales both ways a value is scaled and rounded twice, by
+// different factors, and the kernel is bound by instruction issue (three
+// quarters of the issue slots, the ALU two thirds busy) more than by DRAM;
+// loading the next tile asynchronously while one is worked on measured slower
+// (SwiGLU 123 against 117 µs at that stage).
 constexpr int TILE = 128;
 
 __device__ __forceinline__ void unpack8(const uint4& u, float* v) {
@@ -174,7 +187,7 @@ struct SwigluSource {
 // [dG | dU]: dG = dA·U·s·(1 + G·(1 − s)), dU = dA·G·s with s = σ(G).  The
 // multiplier of the up side is read for dG alone; which side a column is on
 // may change inside eight columns when f is not a multiple of 8.
-template <bool VEC>   // 16-byte loads: f a multiple of 8, rows aligned
+template <int W>   // 16: f a multiple of 8
 struct SwigluBwdSource {
   static constexpr int RAW = 3, R = 4, BATCH = 2, CTAS = 2;
   const __nv_bfloat16 *da, *gu;
@@ -183,13 +196,13 @@ struct SwigluBwdSource {
                                       uint4* u) const {
     const __nv_bfloat16* pa = da + r * ldda;
     const __nv_bfloat16* pg = gu + r * ld;
-    if (VEC) {   // all eight columns on one side
-      const bool up = c >= f;
+    const bool up = c >= f;
+    if (W == 16 || up || c + 8 <= f) {   // all eight columns on one side
       const int64_t k = up ? c - f : c;
-      u[0] = __ldg(reinterpret_cast<const uint4*>(pa + k));
-      u[1] = __ldg(reinterpret_cast<const uint4*>(pg + k));
-      u[2] = up ? make_uint4(0, 0, 0, 0)
-                : __ldg(reinterpret_cast<const uint4*>(pg + f + k));
+      const int valid = W == 16 || cols - c >= 8 ? 8 : (int)(cols - c);
+      u[0] = load8<W>(pa + k, valid);
+      u[1] = load8<W>(pg + k, valid);
+      u[2] = up ? make_uint4(0, 0, 0, 0) : load8<W>(pg + f + k, valid);
       return;
     }
     const uint16_t* ha = reinterpret_cast<const uint16_t*>(pa);
@@ -221,7 +234,7 @@ struct SwigluBwdSource {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float s = sigmoid_approx(g[j]);
-      v[j] = c + (VEC ? 0 : j) < f ? a[j] * u[j] * s * (1.0f + g[j] * (1.0f - s))
+      v[j] = c + (W == 16 ? 0 : j) < f ? a[j] * u[j] * s * (1.0f + g[j] * (1.0f - s))
                        : a[j] * g[j] * s;
     }
   }
@@ -507,7 +520,8 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
 
 // Row scales alone (no transpose): a half-warp takes R rows of one group of 128
 // columns, nothing passes through shared memory, and a single row spreads over
-// as many half-warps as it has groups.
+// as many half-warps as it has groups.  8192×8192 bf16 37 µs (5.4 TB/s, 81 %),
+// SwiGLU 8192×11008 78 µs (87 %), 1×28672 2.4 µs (1×128 2.3).
 template <typename SRC>
 __global__ void __launch_bounds__(256, 4)
     quantize_rows_kernel(const SRC src, int64_t rows, int64_t cols,
@@ -580,13 +594,16 @@ __global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
 
 // The SwiGLU backward where dG's and dU's tiles line up (f a multiple of 128):
 // one CTA makes both from one read of dA, G and U and one σ; dU waits in
-// shared memory, each thread's in its own slots, while dG leaves.
+// shared memory, each thread's in its own slots, while dG leaves.  8192×11008
+// both ways 191 µs (4.8 TB/s, 71 %; 260 with a CTA for each of the two), rows
+// alone 140 (77 %, against 194).  Bound by issue, like the tiles above, and by what two CTAs
+// of 512 threads can have in flight (all four rows' loads at once spill).
 struct Fp32Rows {
   static constexpr int R = 4;
 };
 constexpr int PAIR_SMEM = 128 * 128 * 4;
 __global__ void __launch_bounds__(512, 2)
-    swiglu_bwd_pair_kernel(const SwigluBwdSource<true> src, int64_t rows,
+    swiglu_bwd_pair_kernel(const SwigluBwdSource<16> src, int64_t rows,
                            int64_t pairs, const Fp8BlockOut o) {
   extern __shared__ float4 kept[];   // [row][half of eight][thread]
   __shared__ TileScratch<4> sm;
@@ -759,6 +776,10 @@ __device__ __forceinline__ uint4 load8_plain(const __nv_bfloat16* p,
                 b = reinterpret_cast<const uint2*>(p)[1];
     return make_uint4(a.x, a.y, b.x, b.y);
   }
+  if (W == 4 && valid >= 8) {
+    const uint32_t* a = reinterpret_cast<const uint32_t*>(p);
+    return make_uint4(a[0], a[1], a[2], a[3]);
+  }
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -779,6 +800,8 @@ int norm_threads(int h, int V) {
 // eight columns each, 16 neighbouring threads hold one group of 128); a warp
 // per row (eight rows a CTA) up to 512 columns, else a CTA per row.  γ is read
 // before the row's sum is known, so that its latency is not paid after it.
+// Few rows are bound by latency (1×8192 2.9 µs, 600×8192 10: load, sum, output
+// in turn), 1001×4100 (rows on eight bytes, 3.3 waves of CTAs) by it 11 µs.
 template <int THREADS, int V, int CTAS, int W>
 __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
     add_rmsnorm_fp8_kernel(const NormArgs p) {
@@ -838,6 +861,8 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, CTAS)
 // row, thread 0 copying x and r of the rows to come into a ring of one or two
 // stages (bulk copies), so that loads are in flight all the time and γ is
 // read once.  Waits are bounded; the block agrees on every outcome.
+// Bound by DRAM: 8192×8192 with the bf16 output 97 µs (6.2 TB/s, 93 %),
+// without 77 (92 %), 8192×4096 40 (88 %), 8192×2048 21 (83 %).
 constexpr int MAX_STAGES = 2;
 template <int THREADS, int V, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS)
@@ -1022,13 +1047,20 @@ int swiglu_fp8_bwd(int64_t T, int64_t f, const void* da, int64_t ldda,
   const auto* x = static_cast<const __nv_bfloat16*>(gu);
   const double bytes = 6.0 * T * f + out_bytes(o, T, 2 * f);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (width(gu, ldgu * 2) < 16 || width(da, ldda * 2) < 16 || f % 8)
-    return launch_tiles<false>(SwigluBwdSource<false>{a, x, ldda, ldgu, f},
-                               kFp8Row, T, 2 * f, o, bytes, s);
-  const SwigluBwdSource<true> src{a, x, ldda, ldgu, f};
-  // a few rows: spread over half-warps instead (1 x 28672: 2.8 us)
-  if (f % TILE || (o.qt == nullptr && T < 64))
+  auto go = [&](const auto& src) {
     return launch_tiles<false>(src, kFp8Row, T, 2 * f, o, bytes, s);
+  };
+  switch (std::min({width(gu, ldgu * 2), width(da, ldda * 2),
+                    width(nullptr, f * 2)})) {
+    case 16: break;
+    case 8: return go(SwigluBwdSource<8>{a, x, ldda, ldgu, f});
+    case 4: return go(SwigluBwdSource<4>{a, x, ldda, ldgu, f});
+    default: return go(SwigluBwdSource<2>{a, x, ldda, ldgu, f});
+  }
+  const SwigluBwdSource<16> src{a, x, ldda, ldgu, f};
+  // A few rows spread over half-warps instead (f = 28672, rows / pair in µs:
+  // 1 row 2.4 / 5.7, 64 rows 6.8 / 7.8, 128 rows 11.4 / 9.2, 512 34.9 / 26.2).
+  if (f % TILE || (o.qt == nullptr && T <= 64)) return go(src);
   static std::atomic<bool> done[64];
   const int err = allow_smem(swiglu_bwd_pair_kernel, PAIR_SMEM, done);
   if (err) return err;
@@ -1059,8 +1091,14 @@ int add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps, const void* x,
     ProfScope ps(st, KF_NORM, 4.0 * T * h,
                  (2.0 + 2.0 * (r != nullptr) + 2.0 * (x1 != nullptr) +
                   2.0 * (y != nullptr) + 1.0) * T * h);
-    // The ring pays where a CTA has several rows to run ahead on.
-    const bool many = T >= 4 * (int64_t)device_sm_count();
+    // The ring pays where a CTA has rows to run ahead on (one CTA a row /
+    // ring in µs: 600×8192 10.0 / 10.2, 1000×8192 15.6 / 14.1, 600×16384 with y
+    // 21.8 / 18.5, 600×2048 4.1 / 4.7, 2000×2048 8.6 / 8.0, 1000×1024 3.8 /
+    // 4.4, 2000×1024 5.9 / 5.9).  Its second stage helps long rows without y
+    // (8192×8192 78 against 79 to 81 µs) and costs the others (with y 96
+    // against 112: more reads in flight between the writes).
+    const int ctas = h <= 1024 ? 12 : h <= 2048 ? 8 : h <= 4096 ? 4 : 2;
+    const bool many = T >= (int64_t)device_sm_count() * std::max(3, ctas);
     const int stages = y == nullptr && h > 4096 ? 2 : 1;
     if (w == 16 && h > 512 && many) {
       if (h <= 1024)
@@ -1077,6 +1115,8 @@ int add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps, const void* x,
       err = launch_norm<16>(p, st);
     } else if (w == 8) {
       err = launch_norm<8>(p, st);
+    } else if (w == 4) {
+      err = launch_norm<4>(p, st);
     } else {
       err = launch_norm<2>(p, st);
     }

@@ -309,6 +309,17 @@ struct GridAcc {
 // The epilogue's 128 sums a thread need more than the 168 registers that 384
 // threads can have, so the first warpgroup hands some over (128·40 + 256·232
 // = 384·168).
+//
+// Measured: 8192×8192×4096 with a scale for 128×128 of B 233 µs (2360 TFLOP/s),
+// with one for each of its rows 321 (1715); 8192×8192×28672 1440 µs alone
+// (2670), 1630 in a loop at the power limit.  What bounds it is the chain of a
+// K block: its MMAs (512 cycles on an idle SM, nearer 700 while the epilogue
+// reads TMEM), the read back and the hand-over both ways take some 1900 cycles
+// together, and the two halves of TMEM hide one block's behind another's, so
+// that one ends every 900 to 1000; the tensor pipe is busy 72 % of the time.
+// With scales for rows of both sides the epilogue multiplies twice as often
+// and a block ends every 1350 to 1400.  (Removing the epilogue's additions
+// altogether gains 10 %, the scales' products 10 % of the second form.)
 template <int B_ROW, int OUT_F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     gemm_fp8_block_wide(const __grid_constant__ Params p) {
@@ -636,6 +647,10 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
 // enough ahead for their latency from DRAM (three blocks ahead: 0.47 µs a K
 // block, whatever the tile).  The others: epilogue, in the layout of GridAcc
 // (four rows and a quarter of the columns a thread).
+//
+// Bound by the read of B: 48×8192×28672 45 µs (5.3 TB/s, 79 % of a copy's
+// rate; 16 rows 42), and where that is short by a K block's latency through
+// the ring, the MMAs and TMEM: 16×4096×4096 8.5 µs.
 template <int BNT, int OUT_F32>
 __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
     gemm_fp8_block_narrow(const __grid_constant__ NarrowParams p) {
@@ -1097,8 +1112,8 @@ int narrow(const GemmFp8Block& g, cudaStream_t s, unsigned* status, int bn,
 // estimate in µs from what both were measured to take on 152 SMs:
 //  * narrow: 4 a wave of CTAs, and the K blocks' time (0.34 to 0.40 each,
 //    latency of the ring) beside the bytes at 6.4 TB/s, 0.3 of the shorter of
-//    the two not hidden.  Estimated / measured: 1×4096×4096 split 8 7.0 / 7.8,
-//    split 2 10 / 10; 48×8192×28672 split 4 47 / 45, split 1 98 / 90;
+//    the two not hidden.  Estimated / measured: 16×4096×4096 split 8 7.0 / 8.5,
+//    48×8192×28672 split 4 47 / 45, split 1 98 / 90;
 //    128×8192×28672 split 2 60 / 56, split 4 64 / 62; 512×4096×4096 18 / 19;
 //  * wide: 5, and for each round of tiles 2 and 0.46 a K block (0.66 with a
 //    scale for each row of B).  512×4096×4096 22 / 21, 1024×8192×8192 68 / 68,

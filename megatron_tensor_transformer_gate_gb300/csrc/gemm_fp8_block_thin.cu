@@ -13,7 +13,7 @@
 // Measured beside the tcgen05 form for few rows, whose barriers, ring, TMEM
 // and cluster sum are what a small product waits for (µs, weight from DRAM):
 // 1×512×2000 3.3 against 4.4, 1×4096×4096 5.5 against 7.6 (2.5 is the read of
-// B at copy speed, 2.4 an empty launch), 1×8192×8192 15.8 / 16.3,
+// B at copy speed, 2.0 the smallest launch), 1×8192×8192 15.8 / 16.3,
 // 1×28672×8192 41.0 / 42.2, 1×8192×28672 43.2 / 42.1, 8×28672×8192 42.8 / 42.4;
 // with a second group of eight rows it falls behind (16×8192×28672 65 / 42),
 // so nine rows are where that form starts.  Bound by DRAM: 5.7 TB/s at
