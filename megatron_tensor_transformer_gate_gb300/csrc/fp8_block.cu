@@ -104,6 +104,12 @@ __device__ __forceinline__ void save8(__nv_bfloat16* p, const uint4& u,
   }
 }
 
+// How many of a thread's eight columns exist, of `left`; WHOLE: all of them.
+template <bool WHOLE>
+__device__ __forceinline__ int columns(int64_t left) {
+  return WHOLE || left >= 8 ? 8 : (int)left;
+}
+
 // A source: raw() loads eight columns of a row (W: the bytes that its rows'
 // starts and pitch are multiples of, at most 16) (columns at and beyond `cols`
 // give 0), value() makes them fp32.
@@ -112,9 +118,10 @@ struct CopyBf16 {
   static constexpr int RAW = 1, R = 8, BATCH = 8, CTAS = 4;
   const __nv_bfloat16* x;
   int64_t ld;
+  template <bool WHOLE>
   __device__ __forceinline__ void raw(int64_t r, int64_t c, int64_t cols,
                                       uint4* u) const {
-    u[0] = load8<W>(x + r * ld + c, (int)(cols - c < 8 ? cols - c : 8));
+    u[0] = load8<W>(x + r * ld + c, columns<WHOLE>(cols - c));
   }
   __device__ int64_t col_tile(int64_t j, int64_t) const { return j; }
 };
@@ -124,10 +131,11 @@ struct CopyF32 {
   static constexpr int RAW = 2, R = 4, BATCH = 4, CTAS = 2;
   const float* x;
   int64_t ld;
+  template <bool WHOLE>
   __device__ __forceinline__ void raw(int64_t r, int64_t c, int64_t cols,
                                       uint4* u) const {
     const float* p = x + r * ld + c;
-    if (cols - c >= 8) {
+    if (WHOLE || cols - c >= 8) {
       u[0] = load16<W>(p);
       u[1] = load16<W>(p + 4);
     } else {
@@ -166,12 +174,13 @@ struct SwigluSource {
   static constexpr int RAW = 2, R = 4, BATCH = 4, CTAS = 2;
   const __nv_bfloat16* gu;
   int64_t ld, f;
+  template <bool WHOLE>
   __device__ __forceinline__ void raw(int64_t r, int64_t c, int64_t cols,
                                       uint4* u) const {
-    const int valid = (int)(cols - c < 8 ? cols - c : 8);
+    const int valid = columns<WHOLE || W == 16>(cols - c);   // 16: f % 8 == 0
     const __nv_bfloat16* p = gu + r * ld + c;
-    u[0] = load8<W>(p, W == 16 ? 8 : valid);   // W = 16: f a multiple of 8
-    u[1] = load8<W>(p + f, W == 16 ? 8 : valid);
+    u[0] = load8<W>(p, valid);
+    u[1] = load8<W>(p + f, valid);
   }
   __device__ __forceinline__ void value(const uint4* x, int64_t, float* v) const {
     float g[8], u[8];
@@ -192,6 +201,7 @@ struct SwigluBwdSource {
   static constexpr int RAW = 3, R = 4, BATCH = 2, CTAS = 2;
   const __nv_bfloat16 *da, *gu;
   int64_t ldda, ld, f;
+  template <bool WHOLE>
   __device__ __forceinline__ void raw(int64_t r, int64_t c, int64_t cols,
                                       uint4* u) const {
     const __nv_bfloat16* pa = da + r * ldda;
@@ -199,7 +209,7 @@ struct SwigluBwdSource {
     const bool up = c >= f;
     if (W == 16 || up || c + 8 <= f) {   // all eight columns on one side
       const int64_t k = up ? c - f : c;
-      const int valid = W == 16 || cols - c >= 8 ? 8 : (int)(cols - c);
+      const int valid = columns<WHOLE || W == 16>(cols - c);
       u[0] = load8<W>(pa + k, valid);
       u[1] = load8<W>(pg + k, valid);
       u[2] = up ? make_uint4(0, 0, 0, 0) : load8<W>(pg + f + k, valid);
@@ -319,8 +329,31 @@ struct Held<CopyBf16<W>> {
   }
 };
 
+// A thread's elements of rows r0 and on, columns c0 to c0 + 7.
+template <bool WHOLE, typename SRC>
+__device__ __forceinline__ void load_held(Held<SRC>& h, const SRC& src,
+                                          int64_t r0, int64_t c0, int64_t rows,
+                                          int64_t cols) {
+#pragma unroll
+  for (int b = 0; b < SRC::R; b += SRC::BATCH) {
+    uint4 u[SRC::BATCH][SRC::RAW];
+#pragma unroll
+    for (int i = 0; i < SRC::BATCH; ++i) {
+      if (!WHOLE) {
+#pragma unroll
+        for (int k = 0; k < SRC::RAW; ++k) u[i][k] = make_uint4(0, 0, 0, 0);
+      }
+      if (WHOLE || (r0 + b + i < rows && c0 < cols))
+        src.template raw<WHOLE>(r0 + b + i, c0, cols, u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < SRC::BATCH; ++i) h.take(src, b + i, u[i], c0);
+  }
+}
+
+template <bool WHOLE>
 __device__ __forceinline__ void store8(uint8_t* p, uint2 c, int valid) {
-  if (valid >= 8) {
+  if (WHOLE || valid >= 8) {
     *reinterpret_cast<uint2*>(p) = c;
   } else {
 #pragma unroll
@@ -384,7 +417,7 @@ struct TileScratch {
 // bytes; a column's largest magnitude takes one shuffle and one pass through
 // shared memory; R rows of a column pack into one R-byte shared-memory store
 // of the transposed tile, whose rows then leave the same way.
-template <int GROUP, typename H>
+template <int GROUP, bool WHOLE, typename H>
 __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
                                           int64_t rows, int64_t cols,
                                           int64_t rt, int64_t ct,
@@ -397,8 +430,8 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
   const int64_t r0 = rt * TILE + (warp * 2 + half) * R;
   const int64_t c0 = ct * TILE + l * 8;
   // this thread's rows and columns that exist
-  const int nr = (int)(rows - r0 < R ? rows - r0 : R);
-  const int nc = (int)(cols - c0 < 8 ? cols - c0 : 8);
+  const int nr = WHOLE || rows - r0 >= R ? R : (int)(rows - r0);
+  const int nc = columns<WHOLE>(cols - c0);
   float colr[8];   // the factor of each of this thread's columns
   float rowr[R];   // and of each of its rows
   if (GROUP == kFp8Row) {
@@ -472,7 +505,7 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
       if (i < nr) {
         float v[8];
         h.row(i, v);
-        store8(q, codes8(v, rowr[i]), nc);
+        store8<WHOLE>(q, codes8(v, rowr[i]), nc);
       }
       q += o.ldq;
     }
@@ -500,11 +533,11 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
     }
     __syncthreads();
     const int64_t rr = rt * TILE + l * 8;   // eight rows of the source
-    const int valid = (int)(rows - rr < 8 ? rows - rr : 8);
+    const int valid = columns<WHOLE>(rows - rr);
     // columns 2R·warp + half + 2i of the tile
     const int first = warp * 2 * R + half;
     const int64_t left = cols - ct * TILE - first;
-    const int nt = (int)(left < TILE ? left : TILE);
+    const int nt = WHOLE || left >= TILE ? TILE : (int)left;
     uint8_t* q = o.qt + (ct * TILE + first) * o.ldqt + rr;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -512,7 +545,7 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
       const int chunk = l ^ (c >> 3);
       const uint2 u =
           *reinterpret_cast<const uint2*>(tile_t + c * TILE + chunk * 8);
-      if (2 * i < nt && valid > 0) store8(q, u, valid);
+      if (2 * i < nt && valid > 0) store8<WHOLE>(q, u, valid);
       q += 2 * o.ldqt;
     }
   }
@@ -522,29 +555,14 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
 // columns, nothing passes through shared memory, and a single row spreads over
 // as many half-warps as it has groups.  8192×8192 bf16 37 µs (5.4 TB/s, 81 %),
 // SwiGLU 8192×11008 78 µs (87 %), 1×28672 2.4 µs (1×128 2.3).
-template <typename SRC>
-__global__ void __launch_bounds__(256, 4)
-    quantize_rows_kernel(const SRC src, int64_t rows, int64_t cols,
-                         int64_t col_tiles, const Fp8BlockOut o) {
+template <bool WHOLE, typename SRC>
+__device__ __forceinline__ void emit_rows(const SRC& src, int64_t r0,
+                                          int64_t c0, int64_t ct, int64_t rows,
+                                          int64_t cols, const Fp8BlockOut& o) {
   constexpr int R = SRC::R;
   const int lane = threadIdx.x & 31, l = lane & 15;
-  const int64_t hw = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int64_t rt = hw / col_tiles;
-  const int64_t ct = src.col_tile(hw - rt * col_tiles, col_tiles);
-  const int64_t r0 = rt * R, c0 = ct * TILE + l * 8;   // r0 ≥ rows: no work
   Held<SRC> h;
-#pragma unroll
-  for (int b = 0; b < R; b += SRC::BATCH) {
-    uint4 u[SRC::BATCH][SRC::RAW];
-#pragma unroll
-    for (int i = 0; i < SRC::BATCH; ++i) {
-#pragma unroll
-      for (int k = 0; k < SRC::RAW; ++k) u[i][k] = make_uint4(0, 0, 0, 0);
-      if (r0 + b + i < rows && c0 < cols) src.raw(r0 + b + i, c0, cols, u[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < SRC::BATCH; ++i) h.take(src, b + i, u[i], c0);
-  }
+  load_held<WHOLE>(h, src, r0, c0, rows, cols);
   float m[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) m[i] = h.row_max(i);
@@ -552,16 +570,33 @@ __global__ void __launch_bounds__(256, 4)
   const float x = factor_or_scale(rows_max<R>(m, l), l & 8);
   if (l >= 8 && l < 8 + R && r0 + l - 8 < rows)
     o.s[ct * o.lds + r0 + l - 8] = x;
-  const int valid = (int)(cols - c0 < 8 ? cols - c0 : 8);
+  const int nc = columns<WHOLE>(cols - c0);
+  uint8_t* q = o.q + r0 * o.ldq + c0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const float f = __shfl_sync(0xffffffffu, x, (lane & 16) | i);
-    if (r0 + i < rows && valid > 0) {
+    if (WHOLE || (r0 + i < rows && nc > 0)) {
       float v[8];
       h.row(i, v);
-      store8(o.q + (r0 + i) * o.ldq + c0, codes8(v, f), valid);
+      store8<WHOLE>(q, codes8(v, f), nc);
     }
+    q += o.ldq;
   }
+}
+template <typename SRC>
+__global__ void __launch_bounds__(256, 4)
+    quantize_rows_kernel(const SRC src, int64_t rows, int64_t cols,
+                         int64_t col_tiles, const Fp8BlockOut o) {
+  constexpr int R = SRC::R;
+  const int l = threadIdx.x & 15;
+  const int64_t hw = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t rt = hw / col_tiles;
+  const int64_t ct = src.col_tile(hw - rt * col_tiles, col_tiles);
+  const int64_t r0 = rt * R, c0 = ct * TILE + l * 8;   // r0 ≥ rows: no work
+  if (__all_sync(0xffffffffu, r0 + R <= rows && c0 + 8 <= cols))
+    emit_rows<true>(src, r0, c0, ct, rows, cols, o);
+  else
+    emit_rows<false>(src, r0, c0, ct, rows, cols, o);
 }
 
 template <typename SRC, int GROUP>
@@ -576,20 +611,15 @@ __global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
   const int64_t r0 = rt * TILE + (warp * 2 + (lane >> 4)) * R;
   const int64_t c0 = ct * TILE + (lane & 15) * 8;
 
+  // tiles that are whole (all but the last of an axis) are spared every bound
   Held<SRC> h;
-#pragma unroll
-  for (int b = 0; b < R; b += SRC::BATCH) {
-    uint4 u[SRC::BATCH][SRC::RAW];
-#pragma unroll
-    for (int i = 0; i < SRC::BATCH; ++i) {
-#pragma unroll
-      for (int k = 0; k < SRC::RAW; ++k) u[i][k] = make_uint4(0, 0, 0, 0);
-      if (r0 + b + i < rows && c0 < cols) src.raw(r0 + b + i, c0, cols, u[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < SRC::BATCH; ++i) h.take(src, b + i, u[i], c0);
+  if (rows - rt * TILE >= TILE && cols - ct * TILE >= TILE) {
+    load_held<true>(h, src, r0, c0, rows, cols);
+    emit_tile<GROUP, true>(h, o, rows, cols, rt, ct, sm);
+  } else {
+    load_held<false>(h, src, r0, c0, rows, cols);
+    emit_tile<GROUP, false>(h, o, rows, cols, rt, ct, sm);
   }
-  emit_tile<GROUP>(h, o, rows, cols, rt, ct, sm);
 }
 
 // The SwiGLU backward where dG's and dU's tiles line up (f a multiple of 128):
@@ -619,7 +649,8 @@ __global__ void __launch_bounds__(512, 2)
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) x[i][k] = make_uint4(0, 0, 0, 0);
-      if (r0 + b + i < rows) src.raw(r0 + b + i, c0, 2 * src.f, x[i]);
+      if (r0 + b + i < rows)
+        src.raw<true>(r0 + b + i, c0, 2 * src.f, x[i]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -637,7 +668,11 @@ __global__ void __launch_bounds__(512, 2)
       kept[((b + i) * 2 + 1) * 512 + tid] = make_float4(u[4], u[5], u[6], u[7]);
     }
   }
-  emit_tile<kFp8Row>(h, o, rows, 2 * src.f, rt, ct, sm);
+  const bool whole = rows - rt * TILE >= TILE;
+  if (whole)
+    emit_tile<kFp8Row, true>(h, o, rows, 2 * src.f, rt, ct, sm);
+  else
+    emit_tile<kFp8Row, false>(h, o, rows, 2 * src.f, rt, ct, sm);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 a = kept[(i * 2) * 512 + tid], b = kept[(i * 2 + 1) * 512 + tid];
@@ -645,7 +680,10 @@ __global__ void __launch_bounds__(512, 2)
     h.v[i][4] = b.x; h.v[i][5] = b.y; h.v[i][6] = b.z; h.v[i][7] = b.w;
   }
   __syncthreads();   // the scratch is read
-  emit_tile<kFp8Row>(h, o, rows, 2 * src.f, rt, pairs + ct, sm);
+  if (whole)
+    emit_tile<kFp8Row, true>(h, o, rows, 2 * src.f, rt, pairs + ct, sm);
+  else
+    emit_tile<kFp8Row, false>(h, o, rows, 2 * src.f, rt, pairs + ct, sm);
 }
 
 // BLOCKS: whether the source is also quantized in 128×128 blocks.
@@ -759,7 +797,7 @@ __device__ __forceinline__ void emit_norm(const NormArgs& p, int64_t row,
   const float f = __shfl_sync(0xffffffffu, x, lane & 16);
   if ((lane & 15) == 8 && c - 64 < p.h) p.s[(c >> 7) * p.lds + row] = x;
   if (valid <= 0) return;
-  store8(p.q + row * p.ldq + c, codes8(v, f), valid);
+  store8<false>(p.q + row * p.ldq + c, codes8(v, f), valid);
   if (p.y != nullptr)
     save8<W>(p.y + row * p.h + c,
              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
