@@ -455,9 +455,10 @@ tp_status tp_quantize_fp8_block(int32_t dtype, int32_t group, int64_t rows,
  * gives.  Forward: A = SiLU(G) ⊙ U, [T, f].  Backward: from dA (bf16
  * [T, f], row stride ldda ≥ f) the gradient [dG | dU], [T, 2·f]:
  *   dG = dA ⊙ U ⊙ σ(G)·(1 + G·(1 − σ(G))),  dU = dA ⊙ G·σ(G).
- * Values are computed in fp32 and rounded once, to E4M3.  q, s: the rows'
- * codes (the next product's operand); qt, st: the transpose's (the weight
- * gradient's operand); either pair may be NULL, not both. */
+ * Values are computed in fp32 (a σ below 2^-126 is 0) and rounded once, to
+ * E4M3.  q, s: the rows' codes (the next product's operand); qt, st: the
+ * transpose's (the weight gradient's operand); either pair may be NULL, not
+ * both. */
 tp_status tp_swiglu_fp8_fwd(int64_t T, int64_t f, const void* gu,
                             int64_t ldgu, void* q, int64_t ldq, float* s,
                             int64_t lds, void* qt, int64_t ldqt, float* st,

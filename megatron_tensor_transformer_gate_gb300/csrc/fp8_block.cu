@@ -29,18 +29,20 @@ namespace {
 // lane l of 16) holds R rows (2w + g)·R + i and columns 8l + j.  A thread's
 // loads are issued BATCH rows at a time before any is used (a source's
 // raw()): the registers of the CTAs on an SM are the buffer of what is in
-// flight.  A source's R, BATCH and CTAS (on an SM) are what its values leave
-// room for: bf16 values are kept as loaded (8 rows, four CTAs of 256
-// threads), computed ones as fp32 (4 rows, two CTAs of 512).
+// flight.  A source's shapes (rows a thread, BATCH, CTAs on an SM) are what its
+// values leave room for: bf16 values are kept as loaded (8 rows, four CTAs of
+// 256 threads), computed ones as fp32.  For these three CTAs of 256 threads
+// (8 rows) overlap loads and arithmetic better than two of 512 (4 rows), whose
+// phases fall into step: SwiGLU both ways 97 against 109 µs at 8192×11008,
+// fp32 8192×8192 62 against 68.
 //
-// Measured: 128×128 blocks and their transpose of a bf16 8192×28672 146 µs
-// (6.4 TB/s, 97 %); row scales both ways of 8192×8192 51 µs (5.3 TB/s, 79 %),
-// of 8192×8191 (rows on two bytes) 82; SwiGLU both ways 8192×11008 104 µs
-// (78 %).  With row scales both ways a value is scaled and rounded twice, by
-// different factors, and the kernel is bound by instruction issue (three
-// quarters of the issue slots, the ALU two thirds busy) more than by DRAM;
-// loading the next tile asynchronously while one is worked on measured slower
-// (SwiGLU 123 against 117 µs at that stage).
+// Measured: 128×128 blocks and their transpose of a bf16 8192×28672 142 µs
+// (6.6 TB/s, 99 %); row scales both ways of 8192×8192 45.5 µs (5.9 TB/s, 89 %),
+// of 8192×8191 (rows on two bytes) 68; of fp32 8192×8192 62 (97 %); SwiGLU both
+// ways 8192×11008 97 µs (84 %).  With row scales both ways a value is scaled
+// and rounded twice, by different factors: instructions, and the two barriers
+// around the columns' maxima, count beside DRAM there.  Loading the next tile
+// asynchronously while one is worked on measured slower.
 constexpr int TILE = 128;
 
 __device__ __forceinline__ void unpack8(const uint4& u, float* v) {
@@ -110,12 +112,20 @@ __device__ __forceinline__ int columns(int64_t left) {
   return WHOLE || left >= 8 ? 8 : (int)left;
 }
 
+// Rows a thread, rows whose loads are issued together, CTAs on an SM.
+template <int R_, int BATCH_, int CTAS_>
+struct Shape {
+  static constexpr int R = R_, BATCH = BATCH_, CTAS = CTAS_;
+};
+
 // A source: raw() loads eight columns of a row (W: the bytes that its rows'
 // starts and pitch are multiples of, at most 16) (columns at and beyond `cols`
 // give 0), value() makes them fp32.
 template <int W>
 struct CopyBf16 {
-  static constexpr int RAW = 1, R = 8, BATCH = 8, CTAS = 4;
+  static constexpr int RAW = 1;
+  using Rows = Shape<8, 8, 4>;
+  using Tile = Shape<8, 8, 4>;
   const __nv_bfloat16* x;
   int64_t ld;
   template <bool WHOLE>
@@ -128,7 +138,9 @@ struct CopyBf16 {
 
 template <int W>
 struct CopyF32 {
-  static constexpr int RAW = 2, R = 4, BATCH = 4, CTAS = 2;
+  static constexpr int RAW = 2;
+  using Rows = Shape<4, 4, 4>;
+  using Tile = Shape<8, 1, 3>;
   const float* x;
   int64_t ld;
   template <bool WHOLE>
@@ -147,7 +159,8 @@ struct CopyF32 {
       u[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
   }
-  __device__ __forceinline__ void value(const uint4* u, int64_t, float* v) const {
+  __device__ __forceinline__ void value(const uint4* u, int64_t,
+                                        float* v) const {
     v[0] = __uint_as_float(u[0].x); v[1] = __uint_as_float(u[0].y);
     v[2] = __uint_as_float(u[0].z); v[3] = __uint_as_float(u[0].w);
     v[4] = __uint_as_float(u[1].x); v[5] = __uint_as_float(u[1].y);
@@ -171,7 +184,9 @@ __device__ __forceinline__ float sigmoid_approx(float x) {
 // A = SiLU(G)·U.
 template <int W>
 struct SwigluSource {
-  static constexpr int RAW = 2, R = 4, BATCH = 4, CTAS = 2;
+  static constexpr int RAW = 2;
+  using Rows = Shape<4, 4, 4>;
+  using Tile = Shape<8, 1, 3>;
   const __nv_bfloat16* gu;
   int64_t ld, f;
   template <bool WHOLE>
@@ -182,7 +197,8 @@ struct SwigluSource {
     u[0] = load8<W>(p, valid);
     u[1] = load8<W>(p + f, valid);
   }
-  __device__ __forceinline__ void value(const uint4* x, int64_t, float* v) const {
+  __device__ __forceinline__ void value(const uint4* x, int64_t,
+                                        float* v) const {
     float g[8], u[8];
     unpack8(x[0], g);
     unpack8(x[1], u);
@@ -198,7 +214,9 @@ struct SwigluSource {
 // may change inside eight columns when f is not a multiple of 8.
 template <int W>   // 16: f a multiple of 8
 struct SwigluBwdSource {
-  static constexpr int RAW = 3, R = 4, BATCH = 2, CTAS = 2;
+  static constexpr int RAW = 3;
+  using Rows = Shape<4, 2, 4>;
+  using Tile = Shape<4, 2, 2>;
   const __nv_bfloat16 *da, *gu;
   int64_t ldda, ld, f;
   template <bool WHOLE>
@@ -244,8 +262,9 @@ struct SwigluBwdSource {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float s = sigmoid_approx(g[j]);
-      v[j] = c + (W == 16 ? 0 : j) < f ? a[j] * u[j] * s * (1.0f + g[j] * (1.0f - s))
-                       : a[j] * g[j] * s;
+      v[j] = c + (W == 16 ? 0 : j) < f
+                 ? a[j] * u[j] * s * (1.0f + g[j] * (1.0f - s))
+                 : a[j] * g[j] * s;
     }
   }
   // the dG tile and the dU tile of the same hidden units run side by side, so
@@ -256,9 +275,9 @@ struct SwigluBwdSource {
 };
 
 // What a thread keeps of its R×8 elements: bf16 as loaded, else fp32.
-template <typename SRC>
+template <typename SRC, int ROWS>
 struct Held {
-  static constexpr int R = SRC::R;
+  static constexpr int R = ROWS;
   float v[R][8];
   __device__ __forceinline__ void take(const SRC& src, int i, const uint4* u,
                                        int64_t c) {
@@ -295,14 +314,16 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t a) {
   return m;
 }
 template <int W>
-struct Held<CopyBf16<W>> {
+struct Held<CopyBf16<W>, 8> {
   static constexpr int R = 8;
   uint4 u[8];
   __device__ __forceinline__ void take(const CopyBf16<W>&, int i,
                                        const uint4* x, int64_t) {
     u[i] = x[0];
   }
-  __device__ __forceinline__ void row(int i, float* o) const { unpack8(u[i], o); }
+  __device__ __forceinline__ void row(int i, float* o) const {
+    unpack8(u[i], o);
+  }
   __device__ __forceinline__ uint32_t word(int i, int w) const {
     return w == 0 ? u[i].x : w == 1 ? u[i].y : w == 2 ? u[i].z : u[i].w;
   }
@@ -330,15 +351,15 @@ struct Held<CopyBf16<W>> {
 };
 
 // A thread's elements of rows r0 and on, columns c0 to c0 + 7.
-template <bool WHOLE, typename SRC>
-__device__ __forceinline__ void load_held(Held<SRC>& h, const SRC& src,
+template <bool WHOLE, int BATCH, typename SRC, int R>
+__device__ __forceinline__ void load_held(Held<SRC, R>& h, const SRC& src,
                                           int64_t r0, int64_t c0, int64_t rows,
                                           int64_t cols) {
 #pragma unroll
-  for (int b = 0; b < SRC::R; b += SRC::BATCH) {
-    uint4 u[SRC::BATCH][SRC::RAW];
+  for (int b = 0; b < R; b += BATCH) {
+    uint4 u[BATCH][SRC::RAW];
 #pragma unroll
-    for (int i = 0; i < SRC::BATCH; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       if (!WHOLE) {
 #pragma unroll
         for (int k = 0; k < SRC::RAW; ++k) u[i][k] = make_uint4(0, 0, 0, 0);
@@ -347,7 +368,7 @@ __device__ __forceinline__ void load_held(Held<SRC>& h, const SRC& src,
         src.template raw<WHOLE>(r0 + b + i, c0, cols, u[i]);
     }
 #pragma unroll
-    for (int i = 0; i < SRC::BATCH; ++i) h.take(src, b + i, u[i], c0);
+    for (int i = 0; i < BATCH; ++i) h.take(src, b + i, u[i], c0);
   }
 }
 
@@ -435,18 +456,8 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
   float colr[8];   // the factor of each of this thread's columns
   float rowr[R];   // and of each of its rows
   if (GROUP == kFp8Row) {
-    if (o.q != nullptr) {
-      float m[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) m[i] = h.row_max(i);
-      // lanes 0 to 7 get the factors, 8 to 15 the scales, of row l mod R
-      const float x = factor_or_scale(rows_max<R>(m, l), l & 8);
-      if (l >= 8 && l < 8 + R && l - 8 < nr)
-        o.s[ct * o.lds + r0 + l - 8] = x;
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        rowr[i] = __shfl_sync(0xffffffffu, x, (lane & 16) | i);
-    }
+    // The columns' maxima first: their pass through shared memory, and the
+    // divisions of 256 threads, run while the rows' codes are made.
     if (o.qt != nullptr) {
       float cm[8];
       h.col_max(cm);
@@ -470,11 +481,18 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
         else if (ct * TILE + c < cols)
           o.st[rt * o.ldst + ct * TILE + c] = x;
       }
-      __syncthreads();
-      const float4* d = reinterpret_cast<const float4*>(&sm.colf[l * 8]);
-      const float4 x = d[0], y = d[1];
-      colr[0] = x.x; colr[1] = x.y; colr[2] = x.z; colr[3] = x.w;
-      colr[4] = y.x; colr[5] = y.y; colr[6] = y.z; colr[7] = y.w;
+    }
+    if (o.q != nullptr) {
+      float m[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) m[i] = h.row_max(i);
+      // lanes 0 to 7 get the factors, 8 to 15 the scales, of row l mod R
+      const float x = factor_or_scale(rows_max<R>(m, l), l & 8);
+      if (l >= 8 && l < 8 + R && l - 8 < nr)
+        o.s[ct * o.lds + r0 + l - 8] = x;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        rowr[i] = __shfl_sync(0xffffffffu, x, (lane & 16) | i);
     }
   } else {
     float m = 0.0f;
@@ -509,6 +527,13 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
       }
       q += o.ldq;
     }
+  }
+  if (GROUP == kFp8Row && o.qt != nullptr) {
+    __syncthreads();   // the columns' factors
+    const float4* d = reinterpret_cast<const float4*>(&sm.colf[l * 8]);
+    const float4 x = d[0], y = d[1];
+    colr[0] = x.x; colr[1] = x.y; colr[2] = x.z; colr[3] = x.w;
+    colr[4] = y.x; colr[5] = y.y; colr[6] = y.z; colr[7] = y.w;
   }
   if (o.qt != nullptr) {
     // transposed tile: column c's 128 bytes in 16 chunks of 8, chunk k stored
@@ -553,16 +578,16 @@ __device__ __forceinline__ void emit_tile(const H& h, const Fp8BlockOut& o,
 
 // Row scales alone (no transpose): a half-warp takes R rows of one group of 128
 // columns, nothing passes through shared memory, and a single row spreads over
-// as many half-warps as it has groups.  8192×8192 bf16 37 µs (5.4 TB/s, 81 %),
-// SwiGLU 8192×11008 78 µs (87 %), 1×28672 2.4 µs (1×128 2.3).
+// as many half-warps as it has groups.  8192×8192 bf16 33 µs (6.1 TB/s, 91 %),
+// SwiGLU 8192×11008 80 µs (84 %), 1×28672 2.4 µs (1×128 2.3).
 template <bool WHOLE, typename SRC>
 __device__ __forceinline__ void emit_rows(const SRC& src, int64_t r0,
                                           int64_t c0, int64_t ct, int64_t rows,
                                           int64_t cols, const Fp8BlockOut& o) {
-  constexpr int R = SRC::R;
+  constexpr int R = SRC::Rows::R;
   const int lane = threadIdx.x & 31, l = lane & 15;
-  Held<SRC> h;
-  load_held<WHOLE>(h, src, r0, c0, rows, cols);
+  Held<SRC, R> h;
+  load_held<WHOLE, SRC::Rows::BATCH>(h, src, r0, c0, rows, cols);
   float m[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) m[i] = h.row_max(i);
@@ -584,10 +609,10 @@ __device__ __forceinline__ void emit_rows(const SRC& src, int64_t r0,
   }
 }
 template <typename SRC>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(256, SRC::Rows::CTAS)
     quantize_rows_kernel(const SRC src, int64_t rows, int64_t cols,
                          int64_t col_tiles, const Fp8BlockOut o) {
-  constexpr int R = SRC::R;
+  constexpr int R = SRC::Rows::R;
   const int l = threadIdx.x & 15;
   const int64_t hw = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   const int64_t rt = hw / col_tiles;
@@ -600,10 +625,10 @@ __global__ void __launch_bounds__(256, 4)
 }
 
 template <typename SRC, int GROUP>
-__global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
+__global__ void __launch_bounds__(2048 / SRC::Tile::R, SRC::Tile::CTAS)
     quantize_tile_kernel(const SRC src, int64_t rows, int64_t cols,
                          int64_t col_tiles, const Fp8BlockOut o) {
-  constexpr int R = SRC::R;
+  constexpr int R = SRC::Tile::R, BATCH = SRC::Tile::BATCH;
   __shared__ TileScratch<R> sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t rt = blockIdx.x / col_tiles;
@@ -612,12 +637,12 @@ __global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
   const int64_t c0 = ct * TILE + (lane & 15) * 8;
 
   // tiles that are whole (all but the last of an axis) are spared every bound
-  Held<SRC> h;
+  Held<SRC, R> h;
   if (rows - rt * TILE >= TILE && cols - ct * TILE >= TILE) {
-    load_held<true>(h, src, r0, c0, rows, cols);
+    load_held<true, BATCH>(h, src, r0, c0, rows, cols);
     emit_tile<GROUP, true>(h, o, rows, cols, rt, ct, sm);
   } else {
-    load_held<false>(h, src, r0, c0, rows, cols);
+    load_held<false, BATCH>(h, src, r0, c0, rows, cols);
     emit_tile<GROUP, false>(h, o, rows, cols, rt, ct, sm);
   }
 }
@@ -625,35 +650,37 @@ __global__ void __launch_bounds__(2048 / SRC::R, SRC::CTAS)
 // The SwiGLU backward where dG's and dU's tiles line up (f a multiple of 128):
 // one CTA makes both from one read of dA, G and U and one σ; dU waits in
 // shared memory, each thread's in its own slots, while dG leaves.  8192×11008
-// both ways 191 µs (4.8 TB/s, 71 %; 260 with a CTA for each of the two), rows
-// alone 140 (77 %, against 194).  Bound by issue, like the tiles above, and by what two CTAs
-// of 512 threads can have in flight (all four rows' loads at once spill).
-struct Fp32Rows {
-  static constexpr int R = 4;
-};
+// both ways 189 µs (4.8 TB/s, 72 %; 223 with a CTA for each of the two), rows
+// alone 138 (78 %, against 154).  Bound by issue, like the tiles above, and by
+// what two CTAs of 512 threads can have in flight (all four rows' loads at once
+// spill; 256 threads of eight rows 195 to 229).
+struct Fp32Rows {};
 constexpr int PAIR_SMEM = 128 * 128 * 4;
-__global__ void __launch_bounds__(512, 2)
+using PairShape = Shape<4, 2, 2>;
+constexpr int PAIR_THREADS = 2048 / PairShape::R;
+__global__ void __launch_bounds__(PAIR_THREADS, PairShape::CTAS)
     swiglu_bwd_pair_kernel(const SwigluBwdSource<16> src, int64_t rows,
                            int64_t pairs, const Fp8BlockOut o) {
   extern __shared__ float4 kept[];   // [row][half of eight][thread]
-  __shared__ TileScratch<4> sm;
+  constexpr int R = PairShape::R, BATCH = PairShape::BATCH;
+  __shared__ TileScratch<R> sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t rt = blockIdx.x / pairs, ct = blockIdx.x - rt * pairs;
-  const int64_t r0 = rt * TILE + (warp * 2 + (lane >> 4)) * 4;
+  const int64_t r0 = rt * TILE + (warp * 2 + (lane >> 4)) * R;
   const int64_t c0 = ct * TILE + (lane & 15) * 8;
-  Held<Fp32Rows> h;
+  Held<Fp32Rows, R> h;
 #pragma unroll
-  for (int b = 0; b < 4; b += 2) {
-    uint4 x[2][3];
+  for (int b = 0; b < R; b += BATCH) {
+    uint4 x[BATCH][3];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) x[i][k] = make_uint4(0, 0, 0, 0);
       if (r0 + b + i < rows)
         src.raw<true>(r0 + b + i, c0, 2 * src.f, x[i]);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       float a[8], g[8], u[8];
       unpack8(x[i][0], a);
       unpack8(x[i][1], g);
@@ -664,8 +691,9 @@ __global__ void __launch_bounds__(512, 2)
         h.v[b + i][j] = a[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
         u[j] = a[j] * g[j] * s;
       }
-      kept[((b + i) * 2) * 512 + tid] = make_float4(u[0], u[1], u[2], u[3]);
-      kept[((b + i) * 2 + 1) * 512 + tid] = make_float4(u[4], u[5], u[6], u[7]);
+      float4* k = kept + (b + i) * 2 * PAIR_THREADS + tid;
+      k[0] = make_float4(u[0], u[1], u[2], u[3]);
+      k[PAIR_THREADS] = make_float4(u[4], u[5], u[6], u[7]);
     }
   }
   const bool whole = rows - rt * TILE >= TILE;
@@ -674,8 +702,9 @@ __global__ void __launch_bounds__(512, 2)
   else
     emit_tile<kFp8Row, false>(h, o, rows, 2 * src.f, rt, ct, sm);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 a = kept[(i * 2) * 512 + tid], b = kept[(i * 2 + 1) * 512 + tid];
+  for (int i = 0; i < R; ++i) {
+    const float4* k = kept + i * 2 * PAIR_THREADS + tid;
+    const float4 a = k[0], b = k[PAIR_THREADS];
     h.v[i][0] = a.x; h.v[i][1] = a.y; h.v[i][2] = a.z; h.v[i][3] = a.w;
     h.v[i][4] = b.x; h.v[i][5] = b.y; h.v[i][6] = b.z; h.v[i][7] = b.w;
   }
@@ -696,15 +725,15 @@ int launch_tiles(const SRC& src, int group, int64_t rows, int64_t cols,
   {
     ProfScope ps(s, KF_QUANT, 0.0, bytes);
     if (o.qt == nullptr && group == kFp8Row) {
-      const int64_t half_warps = ct * ((rows + SRC::R - 1) / SRC::R);
+      const int64_t half_warps = ct * ((rows + SRC::Rows::R - 1) / SRC::Rows::R);
       quantize_rows_kernel<SRC><<<(unsigned)((half_warps + 15) / 16), 256, 0,
                                   s>>>(src, rows, cols, ct, o);
     } else if (!BLOCKS || group == kFp8Row)
       quantize_tile_kernel<SRC, kFp8Row>
-          <<<grid, 2048 / SRC::R, 0, s>>>(src, rows, cols, ct, o);
+          <<<grid, 2048 / SRC::Tile::R, 0, s>>>(src, rows, cols, ct, o);
     else if constexpr (BLOCKS)
       quantize_tile_kernel<SRC, kFp8Block>
-          <<<grid, 2048 / SRC::R, 0, s>>>(src, rows, cols, ct, o);
+          <<<grid, 2048 / SRC::Tile::R, 0, s>>>(src, rows, cols, ct, o);
   }
   count_launch();
   return cudaGetLastError();
@@ -1096,16 +1125,21 @@ int swiglu_fp8_bwd(int64_t T, int64_t f, const void* da, int64_t ldda,
     default: return go(SwigluBwdSource<2>{a, x, ldda, ldgu, f});
   }
   const SwigluBwdSource<16> src{a, x, ldda, ldgu, f};
-  // A few rows spread over half-warps instead (f = 28672, rows / pair in µs:
-  // 1 row 2.4 / 5.7, 64 rows 6.8 / 7.8, 128 rows 11.4 / 9.2, 512 34.9 / 26.2).
-  if (f % TILE || (o.qt == nullptr && T <= 64)) return go(src);
+  // Where tiles are too few to fill the SMs, two CTAs finish them sooner than
+  // one (separate / pair in µs, rows alone: 1×28672 2.8 / 6.0, 64×28672 5.6 /
+  // 8.0, 128×28672 9.4 / 9.0, 512×28672 27.9 / 25.6, 512×4096 6.5 / 7.1; both
+  // ways: 128×28672 11.9 / 12.1, 256×4096 6.0 / 8.4, 512×4096 8.1 / 9.1,
+  // 8192×11008 223 / 189).
+  if (f % TILE || T * f < device_sm_count() * 3 / 2 * (TILE * TILE))
+    return go(src);
   static std::atomic<bool> done[64];
   const int err = allow_smem(swiglu_bwd_pair_kernel, PAIR_SMEM, done);
   if (err) return err;
   const int64_t pairs = f / TILE, rt = (T + TILE - 1) / TILE;
   {
     ProfScope ps(s, KF_QUANT, 0.0, bytes);
-    swiglu_bwd_pair_kernel<<<(unsigned)(pairs * rt), 512, PAIR_SMEM, s>>>(
+    swiglu_bwd_pair_kernel<<<(unsigned)(pairs * rt), PAIR_THREADS, PAIR_SMEM,
+                             s>>>(
         src, T, pairs, o);
   }
   count_launch();

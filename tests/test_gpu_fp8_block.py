@@ -173,7 +173,8 @@ def close_codes(q, s, v, slack, what, mag=None):
 
 @pytest.mark.parametrize("T,f", [(1, 1), (1, 28), (1, 1376), (3, 130),
                                  (128, 128), (130, 264), (300, 77),
-                                 (257, 344), (130, 256), (257, 384)])
+                                 (257, 344), (130, 256), (257, 384),
+                                 (300, 12544), (1900, 2048)])
 def test_swiglu_forward_and_backward(tp, T, f):
     gu = activation(T, 2 * f, T + f)
     gu[0, 0] = 120.0                          # σ = 1 and σ = 0 to the last bit
