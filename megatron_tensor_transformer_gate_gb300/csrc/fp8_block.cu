@@ -89,7 +89,7 @@ template <int W>
 __device__ __forceinline__ void save8(__nv_bfloat16* p, const uint4& u,
                                       int valid) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  if (W == 16 && valid >= 8) {
+  if (W == 16) {   // rows of a multiple of eight
     *reinterpret_cast<uint4*>(p) = u;
   } else if (W == 8 && valid >= 8) {
     reinterpret_cast<uint2*>(p)[0] = make_uint2(u.x, u.y);
@@ -826,7 +826,7 @@ __device__ __forceinline__ void emit_norm(const NormArgs& p, int64_t row,
   const float f = __shfl_sync(0xffffffffu, x, lane & 16);
   if ((lane & 15) == 8 && c - 64 < p.h) p.s[(c >> 7) * p.lds + row] = x;
   if (valid <= 0) return;
-  store8<false>(p.q + row * p.ldq + c, codes8(v, f), valid);
+  store8<W == 16>(p.q + row * p.ldq + c, codes8(v, f), valid);
   if (p.y != nullptr)
     save8<W>(p.y + row * p.h + c,
              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
@@ -837,7 +837,7 @@ __device__ __forceinline__ void emit_norm(const NormArgs& p, int64_t row,
 template <int W>
 __device__ __forceinline__ uint4 load8_plain(const __nv_bfloat16* p,
                                              int valid) {
-  if (W == 16 && valid >= 8) return *reinterpret_cast<const uint4*>(p);
+  if (W == 16) return *reinterpret_cast<const uint4*>(p);
   if (W == 8 && valid >= 8) {
     const uint2 a = reinterpret_cast<const uint2*>(p)[0],
                 b = reinterpret_cast<const uint2*>(p)[1];
