@@ -120,34 +120,37 @@ struct RowAcc {
   }
   // Stores go through 2 KB of shared memory, 64 bytes of each row at a time
   // (16-byte piece k of row r at k ^ (r / 2 mod 4)): a warp's store then
-  // writes 64 bytes in each of eight rows instead of 16 in each of 32.
+  // writes 64 bytes in each of eight rows instead of 16 in each of 32, or,
+  // where rows are not 16-byte aligned or end inside the tile, one row's
+  // elements side by side (2000×2500×4096 45 µs; by each thread into its own
+  // row 95).
   template <int OUT_F32>
   __device__ __forceinline__ void store(const Params& p, uint4* stage, int m0,
                                         int n0, int lane) const {
     const bool whole = p.vec && n0 + BNH <= p.N;
     constexpr int W = OUT_F32 ? 16 : 32;   // columns in 64 bytes
     constexpr int ES = OUT_F32 ? 4 : 2;
-    if (whole) {
 #pragma unroll
-      for (int c = 0; c < BNH / W; ++c) {
-        __syncwarp();
+    for (int c = 0; c < BNH / W; ++c) {
+      __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (OUT_F32) {
-              const float2 x = unpack_f32x2(acc[c * 8 + k * 2 + (j >> 1)]);
-              w[j] = __float_as_uint(j & 1 ? x.y : x.x);
-            } else {
-              const float2 x = unpack_f32x2(acc[c * 16 + k * 4 + j]);
-              w[j] = pack_bf16x2(x.x, x.y);
-            }
+        for (int j = 0; j < 4; ++j) {
+          if (OUT_F32) {
+            const float2 x = unpack_f32x2(acc[c * 8 + k * 2 + (j >> 1)]);
+            w[j] = __float_as_uint(j & 1 ? x.y : x.x);
+          } else {
+            const float2 x = unpack_f32x2(acc[c * 16 + k * 4 + j]);
+            w[j] = pack_bf16x2(x.x, x.y);
           }
-          stage[lane * 4 + (k ^ ((lane >> 1) & 3))] =
-              make_uint4(w[0], w[1], w[2], w[3]);
         }
-        __syncwarp();
+        stage[lane * 4 + (k ^ ((lane >> 1) & 3))] =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+      if (whole) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = i * 8 + (lane >> 2), k = lane & 3;
@@ -157,14 +160,30 @@ struct RowAcc {
                 ((int64_t)(m0 + r) * p.ldc + n0 + c * W) * ES + k * 16) =
                 stage[r * 4 + (k ^ ((r >> 1) & 3))];
         }
+      } else {
+        rows_out<OUT_F32>(p, stage, m0, n0 + c * W, lane);
       }
-    } else if (m0 + lane < p.M) {
-      const int64_t at = (int64_t)(m0 + lane) * p.ldc + n0;
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const float2 x = unpack_f32x2(acc[i]);
-        if (n0 + 2 * i < p.N) put<OUT_F32>(p.c, at + 2 * i, x.x);
-        if (n0 + 2 * i + 1 < p.N) put<OUT_F32>(p.c, at + 2 * i + 1, x.y);
+    }
+  }
+  // 32 staged rows of 64 bytes, a row's elements side by side.
+  template <int OUT_F32>
+  __device__ __forceinline__ static void rows_out(const Params& p,
+                                                  const uint4* stage, int m0,
+                                                  int n0, int lane) {
+    constexpr int W = OUT_F32 ? 16 : 32, EACH = W / 4;   // EACH: of a piece
+    const int col = lane & (W - 1), n = n0 + col;
+#pragma unroll 4
+    for (int r = lane / W; r < 32; r += 32 / W) {
+      const int at = (r * 4 + ((col / EACH) ^ ((r >> 1) & 3))) * EACH +
+                     (col & (EACH - 1));
+      if (m0 + r < p.M && n < p.N) {
+        const int64_t to = (int64_t)(m0 + r) * p.ldc + n;
+        if (OUT_F32)
+          static_cast<float*>(p.c)[to] =
+              reinterpret_cast<const float*>(stage)[at];
+        else
+          static_cast<__nv_bfloat16*>(p.c)[to] =
+              reinterpret_cast<const __nv_bfloat16*>(stage)[at];
       }
     }
   }
@@ -233,12 +252,39 @@ struct GridAcc {
                   mul_f32x2(s2[i], w2[(c >> 1) & 1][u]));
   }
   // The four lanes of a row exchange what makes 16 bytes in each: 64 bytes of
-  // a row a store.
+  // a row a store.  Rows that are not 16-byte aligned or end inside the tile
+  // go through shared memory, as in RowAcc (2000×2500×4096 59 µs, 64 without).
   template <int OUT_F32>
-  __device__ __forceinline__ void store(const Params& p, uint4*, int m0,
+  __device__ __forceinline__ void store(const Params& p, uint4* stage, int m0,
                                         int n0, int lane) const {
     const int q = lane & 3;
-    const bool whole = p.vec && n0 + BNH <= p.N;
+    if (!p.vec || n0 + BNH > p.N) {
+      constexpr int W = OUT_F32 ? 16 : 32;   // columns in 64 bytes
+#pragma unroll
+      for (int g = 0; g < BNH / W; ++g) {
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {   // rows 8h + lane / 4
+          const int r = 8 * h + (lane >> 2);
+#pragma unroll
+          for (int v = 0; v < W / 8; ++v) {
+            const int col = g * W + 8 * v;   // and 2q
+            const float2 x = unpack_f32x2(
+                acc[(col / 32 * 2 + (h >> 1)) * 8 + col % 32 / 8 * 2 +
+                    (h & 1)]);
+            const int piece = OUT_F32 ? 2 * v + (q >> 1) : v;
+            uint4* to = stage + r * 4 + (piece ^ ((r >> 1) & 3));
+            if (OUT_F32)
+              reinterpret_cast<float2*>(to)[q & 1] = x;
+            else
+              reinterpret_cast<uint32_t*>(to)[q] = pack_bf16x2(x.x, x.y);
+          }
+        }
+        __syncwarp();
+        RowAcc::rows_out<OUT_F32>(p, stage, m0, n0 + g * W, lane);
+      }
+      return;
+    }
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
@@ -246,16 +292,7 @@ struct GridAcc {
         const int m = m0 + 16 * (c & 1) + 8 * i + (lane >> 2);
         const int nc = n0 + 32 * (c >> 1);
         const int64_t at = (int64_t)m * p.ldc + nc;
-        if (!whole) {
-          if (m >= p.M) continue;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float2 x = unpack_f32x2(acc[c * 8 + u * 2 + i]);
-            const int n = 8 * u + 2 * q;
-            if (nc + n < p.N) RowAcc::put<OUT_F32>(p.c, at + n, x.x);
-            if (nc + n + 1 < p.N) RowAcc::put<OUT_F32>(p.c, at + n + 1, x.y);
-          }
-        } else if (OUT_F32) {
+        if (OUT_F32) {
 #pragma unroll
           for (int u = 0; u < 4; u += 2) {
             // even lanes: four columns of unit u, odd lanes: of unit u + 1
@@ -311,7 +348,7 @@ struct GridAcc {
 // = 384·168).
 //
 // Measured: 8192×8192×4096 with a scale for 128×128 of B 233 µs (2360 TFLOP/s),
-// with one for each of its rows 321 (1715); 8192×8192×28672 1440 µs alone
+// with one for each of its rows 319 (1720); 8192×8192×28672 1440 µs alone
 // (2670), 1630 in a loop at the power limit.  What bounds it is the chain of a
 // K block: its MMAs (512 cycles on an idle SM, nearer 700 while the epilogue
 // reads TMEM), the read back and the hand-over both ways take some 1900 cycles

@@ -302,7 +302,9 @@ PRODUCTS = [(1, 1, 1), (1, 16, 16), (1, 129, 130), (1, 1000, 4096),
             (129, 257, 513), (200, 1024, 512), (256, 256, 128),
             (300, 520, 208), (513, 384, 4096), (700, 260, 1100),
             (2600, 2400, 300), (2600, 2400, 40), (1000, 16, 512),
-            (3000, 5, 300), (300, 5000, 128), (150, 700, 3000)]
+            (3000, 5, 300), (300, 5000, 128), (150, 700, 3000),
+            # tiles of a partial round cut into strips: four, two, no whole ones
+            (2000, 2500, 700), (2500, 2000, 40), (1500, 1450, 4100)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
