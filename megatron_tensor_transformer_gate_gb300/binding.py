@@ -461,8 +461,8 @@ def add_rmsnorm_fp8_fwd(x, r, gamma, x1, q, s, rstd, y=None, eps=1e-5,
     """x1 = x + r (r None: x1 is x and may be None), the codes of
     RMSNorm(x1)·γ into (q, s), rstd [T] fp32, and y (bf16, optional); x1 may
     be x or r."""
-    if _done((_tpcall or _load()).norm(x, r, gamma, x1, q, s, rstd, y, eps, stream),
-             "tp_add_rmsnorm_fp8_fwd"):
+    if _done((_tpcall or _load()).norm(x, r, gamma, x1, q, s, rstd, y, eps,
+                                       stream), "tp_add_rmsnorm_fp8_fwd"):
         return
     T, h, _, dev = _matrix(x, "x")
     bf16, shape = torch.bfloat16, (T, h)
