@@ -303,8 +303,9 @@ PRODUCTS = [(1, 1, 1), (1, 16, 16), (1, 129, 130), (1, 1000, 4096),
             (300, 520, 208), (513, 384, 4096), (700, 260, 1100),
             (2600, 2400, 300), (2600, 2400, 40), (1000, 16, 512),
             (3000, 5, 300), (300, 5000, 128), (150, 700, 3000),
-            # tiles of a partial round cut into strips: four, two, no whole ones
-            (2000, 2500, 700), (2500, 2000, 40), (1500, 1450, 4100)]
+            # 256×256 tiles with rows of C off 16 bytes
+            (2000, 2500, 700), (2000, 2501, 300), (2500, 2000, 40),
+            (1500, 1450, 4100)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -334,7 +335,8 @@ def test_product_block_scaled_a(tp, M, N, K, ga, gb):
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("M,N,K", [(3, 200, 300), (300, 270, 400)])
+@pytest.mark.parametrize("M,N,K", [(3, 200, 300), (300, 270, 400),
+                                   (2000, 2300, 200)])
 @pytest.mark.parametrize("off", [0, 1, 8])
 def test_product_into_a_slice_leaves_the_rest(tp, M, N, K, off, out):
     qa, sa = operand(tp, M, K, "row", 3)
