@@ -9,6 +9,7 @@ machine without a GPU driver.
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -64,29 +65,39 @@ def _compile(src, verbose=False):
 
 def _build_pycall():
     """``_tpcall.so``: the CPython module beside the binding (host code)."""
-    src = os.path.join(CSRC, "pycall.c")
+    src = os.path.join(CSRC, "pycall.cpp")
     if os.path.exists(PYCALL) and os.path.getmtime(PYCALL) >= max(
             os.path.getmtime(src), os.path.getmtime(__file__)):
         return
-    cc = shutil.which("gcc") or shutil.which("cc")
-    if cc is None:
-        raise RuntimeError("gcc not found")
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found")
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = PYCALL + ".tmp"
-    r = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC",
-                        "-I", sysconfig.get_paths()["include"], src, "-o", tmp],
-                       capture_output=True, text=True)
+    r = subprocess.run(
+        [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o", tmp,
+         "-I", sysconfig.get_paths()["include"],
+         "-I", os.path.join(torch, "include"),
+         "-I", os.path.join(torch, "include", "torch", "csrc", "api",
+                            "include"),
+         "-I", os.path.join(cuda, "include"),
+         "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu",
+         "-lc10", "-lc10_cuda"], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cc} failed for pycall.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cxx} failed for pycall.cpp:\n{r.stdout}\n"
+                           f"{r.stderr}")
     os.replace(tmp, PYCALL)
 
 
 def build(verbose=False, jobs=None):
     """Compile every source and link ``libtp.so``; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
-    _build_pycall()
-    jobs = jobs or min(len(SOURCES), os.cpu_count() or 4)
+    jobs = jobs or min(len(SOURCES) + 1, os.cpu_count() or 4)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
+        pycall = ex.submit(_build_pycall)
         results = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        pycall.result()
     objs = [o for o, _ in results]
     if verbose:
         for o, log in results:
