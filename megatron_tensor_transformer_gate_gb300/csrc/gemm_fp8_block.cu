@@ -345,7 +345,7 @@ struct GridAcc {
 // = 384·168).
 //
 // Measured: 8192×8192×4096 with a scale for 128×128 of B 233 µs (2360 TFLOP/s),
-// with one for each of its rows 319 (1720); 8192×8192×28672 1440 µs alone
+// with one for each of its rows 315 (1745); 8192×8192×28672 1440 µs alone
 // (2670), 1630 in a loop at the power limit.  What bounds it is the chain of a
 // K block: its MMAs (512 cycles on an idle SM, nearer 700 while the epilogue
 // reads TMEM), the read back and the hand-over both ways take some 1900 cycles
@@ -450,26 +450,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
           if (armed & (1u << s))
             mbar_wait(&full[s], (armed_par >> s) & 1u, &no_abort, nullptr, 0);
       }
-    } else if ((warp == 1 || warp == 2) && lane == 0) {
+    } else if ((warp == 1 || warp == 2) && (B_ROW || lane == 0)) {
       // -------------------------------------------------------- MMA issue --
+      // With row scales the warp waits as one and elects the issuing thread,
+      // whose operands then sit in uniform registers: 1 to 2 % sooner there
+      // (8192×8192×4096 315 against 319 µs), but with a scale for 128×128 of B,
+      // where the issuing thread waits more, 3 % later (4096×8192×28672 766 /
+      // 742), so there one thread goes alone.
       constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BN);
-      const int buf = warp - 1;   // every other K block
+      const int buf =   // every other K block
+          (B_ROW ? __shfl_sync(0xffffffffu, warp, 0) : warp) - 1;
       const uint64_t ad0 = smem_desc_sw128(smem_u32(smA), 16, 1024);
       const uint64_t bd0 = smem_desc_sw128(smem_u32(smB), 16, 1024);
+      auto wait = [&](uint64_t* bar, uint32_t par, unsigned site) {
+        return B_ROW ? mbar_wait_warp(bar, par, abort_flag, p.status, site)
+                     : mbar_wait(bar, par, abort_flag, p.status, site);
+      };
       uint32_t stage = buf, phase = 0, tphase = 1;
       for (int64_t it = buf; it < blocks; it += 2) {
-        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, 43)) break;
+        if (!wait(&full[stage], phase, 43)) break;
         const uint64_t ad = ad0 + stage * (TILE_BYTES >> 4);
         const uint64_t bd = bd0 + stage * (2 * TILE_BYTES >> 4);
-        if (!mbar_wait(&tempty[buf], tphase, abort_flag, p.status, 44)) break;
+        if (!wait(&tempty[buf], tphase, 44)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * BN;
-        tc_mma_f8(d, ad, bd, IDESC, 0);
-        tc_mma_f8(d, ad + 2, bd + 2, IDESC, 1);
-        tc_mma_f8(d, ad + 4, bd + 4, IDESC, 1);
-        tc_mma_f8(d, ad + 6, bd + 6, IDESC, 1);
-        tc_commit(&tfull[buf]);
-        tc_commit_multicast(&empty[stage], 3);
+        if (!B_ROW || elect_one()) {
+          tc_mma_f8(d, ad, bd, IDESC, 0);
+          tc_mma_f8(d, ad + 2, bd + 2, IDESC, 1);
+          tc_mma_f8(d, ad + 4, bd + 4, IDESC, 1);
+          tc_mma_f8(d, ad + 6, bd + 6, IDESC, 1);
+          tc_commit(&tfull[buf]);
+          tc_commit_multicast(&empty[stage], 3);
+        }
+        if (B_ROW) __syncwarp();
         stage += 2;
         if (stage >= STAGES) {
           stage -= STAGES;
@@ -477,7 +490,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
         }
         tphase ^= 1;
       }
-      if (*abort_flag) {
+      const bool gave_up =
+          B_ROW ? __any_sync(0xffffffffu, *abort_flag) : *abort_flag != 0;
+      if (gave_up && (!B_ROW || elect_one())) {   // the thread of the MMAs
         volatile int no_abort = 0;
         tc_commit(&drain[buf]);
         mbar_wait(&drain[buf], 0, &no_abort, nullptr, 0);
