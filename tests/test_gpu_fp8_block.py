@@ -66,7 +66,8 @@ def same_codes(q, s, want, what):
 
 # ---------------------------------------------------------------- quantize --
 SHAPES = [(1, 1), (1, 8), (1, 4096), (3, 130), (7, 129), (128, 128),
-          (129, 257), (127, 1000), (300, 12), (777, 1000), (260, 384)]
+          (129, 257), (127, 1000), (300, 12), (777, 1000), (260, 384),
+          (2500, 4100)]       # more tiles than four for each SM
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -174,7 +175,8 @@ def close_codes(q, s, v, slack, what, mag=None):
 @pytest.mark.parametrize("T,f", [(1, 1), (1, 28), (1, 1376), (3, 130),
                                  (128, 128), (130, 264), (300, 77),
                                  (257, 344), (130, 256), (257, 384),
-                                 (300, 12544), (1900, 2048)])
+                                 (300, 12544), (1900, 2048),
+                                 (2500, 4101), (2500, 4104)])
 def test_swiglu_forward_and_backward(tp, T, f):
     gu = activation(T, 2 * f, T + f)
     gu[0, 0] = 120.0                          # σ = 1 and σ = 0 to the last bit
