@@ -195,21 +195,6 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The same box into the same place of every CTA of `mask`, each counting the
-// bytes on its own barrier at that place.
-__device__ __forceinline__ void tma_load_3d_multicast(void* smem_dst,
-                                                      const CUtensorMap* map,
-                                                      uint64_t* bar, int c0,
-                                                      int c1, int c2,
-                                                      uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_"
-      "tx::bytes.multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(
-          smem_u32(smem_dst)),
-      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "h"(mask)
-      : "memory");
-}
-
 // ------------------------------------------------------------- CTA pairs --
 // A cluster of two CTAs (ranks 0 and 1) sharing one tcgen05.mma of M=256:
 // rank 0 issues the MMAs, each rank holds its half of the operands and of
@@ -237,6 +222,14 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster_addr) {
   asm volatile(
       "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+          bar_cluster_addr)
+      : "memory");
+}
+// The same without the release (as mbar_arrive_relaxed).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(
+    uint32_t bar_cluster_addr) {
+  asm volatile(
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
           bar_cluster_addr)
       : "memory");
 }
@@ -379,16 +372,6 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
       "[%0];" ::"r"(smem_u32(bar))
-      : "memory");
-}
-
-// The same on the barrier at this place in every CTA of `mask`.
-__device__ __forceinline__ void tc_commit_multicast(uint64_t* bar,
-                                                    uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."
-      "multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(mask)
       : "memory");
 }
 

@@ -6,9 +6,9 @@
 // back while the next block runs, multiply it by sa·sb and add it to the
 // output tile, which stays in their registers over the whole K loop.  Two
 // forms here (up to eight rows of A have a third, gemm_fp8_block_thin.cu):
-//  * wide: persistent clusters of two CTAs, each with 128×256 of a 256×256
-//    tile and half of its B, which both get (TMA multicast), for products that
-//    fill the card with such tiles;
+//  * wide: persistent pairs of CTAs, each with 128×256 of a 256×256 tile and
+//    half of its B (cta_group::2), for products that fill the card with such
+//    tiles;
 //  * narrow: one CTA per 128×BN tile with B's rows (the weight) on the
 //    instruction's M side, BN = 16 to 128 rows of A, and K split over a
 //    cluster whose CTAs add up their parts through distributed shared memory
@@ -51,8 +51,8 @@ struct Params {
 // ==================================================================== wide ==
 constexpr int BN = 256;
 constexpr int BNH = BN / 2;                    // B rows loaded by each CTA
-constexpr int STAGES = 4;
-constexpr int STAGE_BYTES = 3 * TILE_BYTES;    // 128 rows of A, 256 of B
+constexpr int STAGES = 6;                      // even: two threads take turns
+constexpr int STAGE_BYTES = 2 * TILE_BYTES;    // 128 rows of A, 128 of B
 constexpr int TMEM_COLS = 512;                 // two K blocks × 256
 constexpr int WIDE_THREADS = 384;
 // Scales of the tile's 128 rows and of its columns (two blocks', or 256) for
@@ -328,15 +328,17 @@ struct GridAcc {
   }
 };
 
-// Two CTAs, each with 128 rows of a 256×256 tile; every CTA loads its A rows
-// and half of B, the half into both (multicast).  The MMAs are the CTA's own
-// (cta_group::1), so that handing a TMEM buffer over and back stays inside
-// the SM.  Roles:
-//   warp 0      TMA producer, a ring of four K blocks;
-//   warps 1, 2  MMA issue, every other K block and one TMEM buffer each: beside
-//               eight busy epilogue warps one thread's waits and commits for a
-//               K block take about 400 cycles, in which the other's MMAs (512)
-//               run;
+// Two CTAs, each with 128 rows of a 256×256 tile: every CTA loads its A rows
+// and half of B, and rank 0 (the leader) issues MMAs of M = 256 that read both
+// halves (cta_group::2).  No load is multicast: such a load is for one GPU's own
+// memory, and one library serves every rank of a run on several (its form, two
+// rings of B and MMAs of each CTA's own, took 237 µs where this one takes 242,
+// 8192×8192×4096, and the same 315 with row scales).  Roles:
+//   warp 0      TMA producer, a ring of six K blocks;
+//   warps 1, 2  of the leader: MMA issue, every other K block and one TMEM
+//               buffer each: beside eight busy epilogue warps one thread's
+//               waits and commits for a K block take about 400 cycles, in which
+//               the other's MMAs (512) run;
 //   warp 3      the scales, by asynchronous copies up to six K blocks ahead;
 //               its arrival joins the MMAs' commit on the epilogue's barrier;
 //   warps 4–11  epilogue, warp w on TMEM lanes 32·(w mod 4) of half (w − 4)/4.
@@ -344,8 +346,8 @@ struct GridAcc {
 // threads can have, so the first warpgroup hands some over (128·40 + 256·232
 // = 384·168).
 //
-// Measured: 8192×8192×4096 with a scale for 128×128 of B 233 µs (2360 TFLOP/s),
-// with one for each of its rows 315 (1745); 8192×8192×28672 1440 µs alone
+// Measured: 8192×8192×4096 with a scale for 128×128 of B 242 µs (2270 TFLOP/s),
+// with one for each of its rows 315 (1747); 8192×8192×28672 1440 µs alone
 // (2670), 1630 in a loop at the power limit.  What bounds it is the chain of a
 // K block: its MMAs (512 cycles on an idle SM, nearer 700 while the epilogue
 // reads TMEM), the read back and the hand-over both ways take some 1900 cycles
@@ -362,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smA = smem;
   uint8_t* smB = smem + STAGES * TILE_BYTES;
-  float* scales = reinterpret_cast<float*>(smB + STAGES * 2 * TILE_BYTES);
+  float* scales = reinterpret_cast<float*>(smB + STAGES * TILE_BYTES);
   uint8_t* staging = reinterpret_cast<uint8_t*>(scales + SLOTS * SLOT);
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * STAGING);
   uint64_t* empty = full + STAGES;
@@ -375,26 +377,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank() & 1u;
+  const bool leader = rank == 0;
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
   const int64_t blocks =
       (int64_t)((p.total_tiles - cid + ncl - 1) / ncl) * p.kblocks;
 
   if (threadIdx.x == 0) {
+    // full: the leader's counts both CTAs' bytes; empty: the leader's commits
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);    // both CTAs' MMAs: B arrives from both
+      mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&tfull[b], 2);    // the MMAs and the scales
-      mbar_init(&tempty[b], 8);   // a lane of each epilogue warp
-      mbar_init(&drain[b], 1);
+      mbar_init(&tfull[b], 2);        // the MMAs and the CTA's own scales
+      mbar_init(&tempty[b], 2 * 8);   // the leader's: a lane of each epilogue
+      mbar_init(&drain[b], 1);        // warp of both
     }
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.ma);
     tma_prefetch_desc(&p.mb);
   }
-  if (warp == 1) tmem_alloc(tmem_slot, TMEM_COLS);
+  if (warp == 1) tmem_alloc_pair(tmem_slot, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // barriers of both CTAs initialised before any remote use
@@ -405,6 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer --
+      const uint32_t full0 = cluster_addr(full, 0);   // the leader's full[0]
       uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
       bool ok = true;
       for (int t = cid; ok && t < p.total_tiles; t += ncl) {
@@ -417,14 +422,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
-          armed |= 1u << stage;
-          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-          tma_load_3d(smA + stage * TILE_BYTES, &p.ma, &full[stage], kb * BK, 0,
-                      m0);
-          // this CTA's half of B, into both
-          tma_load_3d_multicast(smB + (2 * stage + rank) * TILE_BYTES, &p.mb,
-                                &full[stage], kb * BK, 0, n0, 3);
+          if (leader) {
+            mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
+            armed |= 1u << stage;
+            armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+          }
+          const uint32_t fb = full0 + stage * 8;
+          tma_load_3d_pair(smA + stage * TILE_BYTES, &p.ma, fb, kb * BK, 0, m0);
+          tma_load_3d_pair(smB + stage * TILE_BYTES, &p.mb, fb, kb * BK, 0, n0);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -432,8 +437,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
         }
       }
       if (ok) {
-        // both CTAs' last commits land on this CTA's empty barriers before it
-        // may exit
+        // the leader's last commits land on this CTA's empty barriers before
+        // it may exit
         for (int i = 0; i < STAGES; ++i) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status, 42))
             break;
@@ -443,21 +448,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
           }
         }
       }
-      if (*abort_flag) {
+      if (*abort_flag && leader) {
         // let every copy counted on this CTA's barriers land
         volatile int no_abort = 0;
         for (int s = 0; s < STAGES; ++s)
           if (armed & (1u << s))
             mbar_wait(&full[s], (armed_par >> s) & 1u, &no_abort, nullptr, 0);
       }
-    } else if ((warp == 1 || warp == 2) && (B_ROW || lane == 0)) {
+    } else if (leader && (warp == 1 || warp == 2) && (B_ROW || lane == 0)) {
       // -------------------------------------------------------- MMA issue --
       // With row scales the warp waits as one and elects the issuing thread,
       // whose operands then sit in uniform registers: 1 to 2 % sooner there
       // (8192×8192×4096 315 against 319 µs), but with a scale for 128×128 of B,
       // where the issuing thread waits more, 3 % later (4096×8192×28672 766 /
       // 742), so there one thread goes alone.
-      constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BN);
+      constexpr uint32_t IDESC = idesc_e4m3_f32(2 * BM, BN);
       const int buf =   // every other K block
           (B_ROW ? __shfl_sync(0xffffffffu, warp, 0) : warp) - 1;
       const uint64_t ad0 = smem_desc_sw128(smem_u32(smA), 16, 1024);
@@ -470,17 +475,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       for (int64_t it = buf; it < blocks; it += 2) {
         if (!wait(&full[stage], phase, 43)) break;
         const uint64_t ad = ad0 + stage * (TILE_BYTES >> 4);
-        const uint64_t bd = bd0 + stage * (2 * TILE_BYTES >> 4);
+        const uint64_t bd = bd0 + stage * (TILE_BYTES >> 4);
         if (!wait(&tempty[buf], tphase, 44)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * BN;
         if (!B_ROW || elect_one()) {
-          tc_mma_f8(d, ad, bd, IDESC, 0);
-          tc_mma_f8(d, ad + 2, bd + 2, IDESC, 1);
-          tc_mma_f8(d, ad + 4, bd + 4, IDESC, 1);
-          tc_mma_f8(d, ad + 6, bd + 6, IDESC, 1);
-          tc_commit(&tfull[buf]);
-          tc_commit_multicast(&empty[stage], 3);
+          tc_mma_f8_pair(d, ad, bd, IDESC, 0);
+          tc_mma_f8_pair(d, ad + 2, bd + 2, IDESC, 1);
+          tc_mma_f8_pair(d, ad + 4, bd + 4, IDESC, 1);
+          tc_mma_f8_pair(d, ad + 6, bd + 6, IDESC, 1);
+          tc_commit_pair(&tfull[buf], 3);
+          tc_commit_pair(&empty[stage], 3);
         }
         if (B_ROW) __syncwarp();
         stage += 2;
@@ -494,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
           B_ROW ? __any_sync(0xffffffffu, *abort_flag) : *abort_flag != 0;
       if (gave_up && (!B_ROW || elect_one())) {   // the thread of the MMAs
         volatile int no_abort = 0;
-        tc_commit(&drain[buf]);
+        tc_commit_pair(&drain[buf], 1);
         mbar_wait(&drain[buf], 0, &no_abort, nullptr, 0);
       }
     } else if (warp == 3) {
@@ -573,6 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     const uint32_t taddr0 = tmem_base +
                             (static_cast<uint32_t>(quarter * 32) << 16) +
                             half * BNH;
+    const uint32_t tempty0 = cluster_addr(tempty, 0);   // the leader's
     int64_t it = 0;
     bool ok = true, ready = false;
     typename Acc::Chunk r[2];   // a chunk being added, the next on its way
@@ -613,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
             // the buffer is read (by all lanes: the wait is the warp's): the
             // MMAs may have it back
             tc_fence_before();
-            if (lane == 0) mbar_arrive_relaxed(&tempty[buf]);
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8);
             if (ready) begin(it + 1);
           }
           a.add(r[c & 1], c);
@@ -634,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   __syncthreads();
   cluster_sync();   // neither CTA leaves while the pair still uses it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
+  if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
 }
 
 // ================================================================== narrow ==
