@@ -75,16 +75,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
                : "memory");
 }
 
-// The same without the release: orders nothing but what the caller has waited
-// for (tcgen05.wait::ld and a tcgen05 fence).  A release waits for the loads
-// and copies that the thread has in flight.
-__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
-  asm volatile(
-      "mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -225,7 +215,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster_addr) {
           bar_cluster_addr)
       : "memory");
 }
-// The same without the release (as mbar_arrive_relaxed).
+// The same without the release: orders nothing but what the caller has waited
+// for (tcgen05.wait::ld and a tcgen05 fence).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(
     uint32_t bar_cluster_addr) {
   asm volatile(

@@ -93,7 +93,8 @@ __device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr,
 // RowAcc: a scale for each row (sa) times one for the columns.  A thread has
 // one row and all 128 columns, so one multiplier serves them all.
 struct RowAcc {
-  static constexpr int CHUNKS = 4;      // of 32 columns
+  static constexpr int CHUNKS = 4;        // of 32 columns
+  static constexpr int SCALES_READ = 0;   // before this chunk all have been
   using Chunk = uint32_t[32];
   uint64_t acc[64];
   float s, sn;   // this block's multiplier, the next one's
@@ -200,6 +201,7 @@ struct RowAcc {
 // products.  Chunk c: rows 16·(c mod 2), columns 32·(c / 2).
 struct GridAcc {
   static constexpr int CHUNKS = 8;
+  static constexpr int SCALES_READ = 6;
   using Chunk = uint32_t[16];
   uint64_t acc[64];   // [chunk][unit][row]
   float s[4], sn[4];
@@ -339,8 +341,8 @@ struct GridAcc {
 //               buffer each: beside eight busy epilogue warps one thread's
 //               waits and commits for a K block take about 400 cycles, in which
 //               the other's MMAs (512) run;
-//   warp 3      the scales, by asynchronous copies up to six K blocks ahead;
-//               its arrival joins the MMAs' commit on the epilogue's barrier;
+//   warp 3      the scales, by asynchronous copies four K blocks ahead; its
+//               arrival joins the MMAs' commit on the epilogue's barrier;
 //   warps 4–11  epilogue, warp w on TMEM lanes 32·(w mod 4) of half (w − 4)/4.
 // The epilogue's 128 sums a thread need more than the 168 registers that 384
 // threads can have, so the first warpgroup hands some over (128·40 + 256·232
@@ -370,7 +372,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* sread = tempty + 2;
+  uint64_t* drain = sread + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -391,7 +394,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 2);        // the MMAs and the CTA's own scales
       mbar_init(&tempty[b], 2 * 8);   // the leader's: a lane of each epilogue
-      mbar_init(&drain[b], 1);        // warp of both
+      mbar_init(&sread[b], 8);        // warp of both; sread: of this CTA
+      mbar_init(&drain[b], 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -455,21 +459,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
           if (armed & (1u << s))
             mbar_wait(&full[s], (armed_par >> s) & 1u, &no_abort, nullptr, 0);
       }
-    } else if (leader && (warp == 1 || warp == 2) && (B_ROW || lane == 0)) {
+    } else if (leader && (warp == 1 || warp == 2)) {
       // -------------------------------------------------------- MMA issue --
-      // With row scales the warp waits as one and elects the issuing thread,
-      // whose operands then sit in uniform registers: 1 to 2 % sooner there
-      // (8192×8192×4096 315 against 319 µs), but with a scale for 128×128 of B,
-      // where the issuing thread waits more, 3 % later (4096×8192×28672 766 /
-      // 742), so there one thread goes alone.
+      // The warp waits as one and elects the issuing thread, whose operands
+      // then sit in uniform registers (8192×8192×4096 242 µs, by one thread
+      // that waits alone 248; with row scales 319 / 320).
       constexpr uint32_t IDESC = idesc_e4m3_f32(2 * BM, BN);
-      const int buf =   // every other K block
-          (B_ROW ? __shfl_sync(0xffffffffu, warp, 0) : warp) - 1;
+      const int buf = __shfl_sync(0xffffffffu, warp, 0) - 1;
       const uint64_t ad0 = smem_desc_sw128(smem_u32(smA), 16, 1024);
       const uint64_t bd0 = smem_desc_sw128(smem_u32(smB), 16, 1024);
       auto wait = [&](uint64_t* bar, uint32_t par, unsigned site) {
-        return B_ROW ? mbar_wait_warp(bar, par, abort_flag, p.status, site)
-                     : mbar_wait(bar, par, abort_flag, p.status, site);
+        return mbar_wait_warp(bar, par, abort_flag, p.status, site);
       };
       uint32_t stage = buf, phase = 0, tphase = 1;
       for (int64_t it = buf; it < blocks; it += 2) {
@@ -479,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
         if (!wait(&tempty[buf], tphase, 44)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * BN;
-        if (!B_ROW || elect_one()) {
+        if (elect_one()) {
           tc_mma_f8_pair(d, ad, bd, IDESC, 0);
           tc_mma_f8_pair(d, ad + 2, bd + 2, IDESC, 1);
           tc_mma_f8_pair(d, ad + 4, bd + 4, IDESC, 1);
@@ -487,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
           tc_commit_pair(&tfull[buf], 3);
           tc_commit_pair(&empty[stage], 3);
         }
-        if (B_ROW) __syncwarp();
+        __syncwarp();
         stage += 2;
         if (stage >= STAGES) {
           stage -= STAGES;
@@ -495,9 +495,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
         }
         tphase ^= 1;
       }
-      const bool gave_up =
-          B_ROW ? __any_sync(0xffffffffu, *abort_flag) : *abort_flag != 0;
-      if (gave_up && (!B_ROW || elect_one())) {   // the thread of the MMAs
+      const bool gave_up = __any_sync(0xffffffffu, *abort_flag);
+      if (gave_up && elect_one()) {   // the thread of the MMAs
         volatile int no_abort = 0;
         tc_commit_pair(&drain[buf], 1);
         mbar_wait(&drain[buf], 0, &no_abort, nullptr, 0);
@@ -505,6 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     } else if (warp == 3) {
       // ----------------------------------------------------------- scales --
       constexpr int AHEAD = 4;
+      static_assert(AHEAD + 2 <= SLOTS, "slots are read when reused");
       int ft = cid, fk = 0, fslot = 0;
       int m0 = 0, n0 = 0;
       auto fetch = [&]() {
@@ -553,12 +553,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       for (int i = 0; i < AHEAD; ++i) fetch();
       for (int64_t it = 0; it < blocks; ++it) {
         const int buf = it & 1;
-        // Block it − 2 complete: this block's phase is open, and block it − 4,
-        // whose slot the next copies go to, has been read (the MMAs of it − 2
-        // waited for its buffer).
+        // The epilogue has read the scales of block it − 2: its MMAs are
+        // complete, so that this block's phase is open, and the slot that the
+        // next copies go to, of block it − 4, is free.
         if (it >= 2) {
           const uint32_t par = ((it - 2) >> 1) & 1;
-          if (!mbar_wait_warp(&tfull[buf], par, abort_flag, p.status, 46))
+          if (!mbar_wait_warp(&sread[buf], par, abort_flag, p.status, 46))
             break;
         }
         fetch();
@@ -590,6 +590,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
       a.scales(slot(i) + quarter * 32, slot(i) + BM, half, lane);
       a.columns(slot(i) + BM + half * BNH, 0, lane);
     };
+    // The warp's reads of a block's scales come before the copies into their
+    // slot.  The buffer's arrival below orders TMEM alone: a release to the
+    // leader's SM for each block would double the kernel's time.  Placed where
+    // little is in flight this one costs 1 to 2 % (242 against 239 µs, with row
+    // scales 319 / 313; at the block's end 248, 326).
+    auto slot_read = [&](int buf) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sread[buf]);
+    };
     for (int t = cid; ok && t < p.total_tiles; t += ncl) {
       a.clear();
       for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
@@ -612,7 +621,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
           // whether the next block is there is asked in the shadow of a load
           if (c + 1 == Acc::CHUNKS)
             ready = mbar_test_warp(&tfull[buf ^ 1], ((it + 1) >> 1) & 1);
+          if (B_ROW && c == Acc::SCALES_READ) slot_read(buf);
           Acc::wait(r[c & 1]);
+          if (!B_ROW && c == Acc::SCALES_READ) slot_read(buf);
           if (c + 1 < Acc::CHUNKS) {
             Acc::load(taddr, c + 1, r[(c + 1) & 1]);
           } else {
@@ -857,10 +868,11 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
     int buf = 0;
     uint32_t par = 1;   // of the phase before this block's on its barrier
     for (int kb = kb0; kb < kb1; ++kb) {
-      // block kb − BUFS complete: this block's phase is open, and the slot that
-      // the next copies go to (of kb − BUFS·2 or before) has been read
+      // the epilogue is done with block kb − BUFS: this block's phase is open,
+      // and the slot that the next copies go to (of kb − BUFS·2 or before) is
+      // free
       if (kb - kb0 >= L::BUFS &&
-          !mbar_wait_warp(&tfull[buf], par, abort_flag, p.status, 55))
+          !mbar_wait_warp(&tempty[buf], par, abort_flag, p.status, 55))
         break;
       fetch();
       cp_async_wait<NAHEAD>();
@@ -919,9 +931,11 @@ __global__ void __launch_bounds__(Narrow<BNT>::THREADS, Narrow<BNT>::CTAS)
         if (c + 1 < L::CHUNKS) {
           load(buf, c + 1, x[(c + 1) & 1]);
         } else {
+          // a release: the scales' reads are ordered before the copies that
+          // reuse their slot as well
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_relaxed(&tempty[buf]);
+          if (lane == 0) mbar_arrive(&tempty[buf]);
         }
 #pragma unroll
         for (int u = 0; u < L::UNITS; ++u)

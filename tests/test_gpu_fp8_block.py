@@ -325,6 +325,28 @@ def test_product(tp, M, N, K, ga, gb, out):
     assert torch.equal(C, again)              # no order of sums is left open
 
 
+@pytest.mark.parametrize("gb", ["row", "block"])
+@pytest.mark.parametrize("M,N,K", [(2600, 2400, 5200), (40, 300, 28672),
+                                   (128, 300, 28672), (300, 264, 16500)])
+def test_product_whose_scales_go_round_their_ring(tp, M, N, K, gb):
+    # K blocks that differ by powers of two: a block that met another's scales
+    # would be off by far more than the bound
+    def with_steps(rows, group, seed):
+        q, s = operand(tp, rows, K, group, seed)
+        g = torch.Generator().manual_seed(seed)
+        s *= torch.exp2(torch.randint(-6, 7, (s.shape[0], 1), generator=g
+                                      ).float()).cuda()
+        return q, s
+
+    qa, sa = with_steps(M, "row", 21)
+    qb, sb = with_steps(N, gb, 22)
+    for out in (torch.float32, torch.bfloat16):
+        C = torch.empty((M, N), dtype=out, device="cuda")
+        tp.gemm_fp8_block(qa, sa, qb, sb, C)
+        tp.device_status()
+        check_product(C, qa, sa, qb, sb, f"{M}x{N}x{K}")
+
+
 @pytest.mark.parametrize("ga,gb", [("block", "block"), ("block", "row")])
 @pytest.mark.parametrize("M,N,K", [(3, 200, 300), (140, 270, 400),
                                    (600, 400, 900)])
