@@ -499,6 +499,18 @@ tp_status tp_gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void* qa,
                             int32_t out_dtype, void* C, int64_t ldc,
                             tp_stream stream);
 
+/* The form that tp_gemm_fp8_block takes for these sizes on a device of `sms`
+ * SMs (0: the current one's): *form of tp_fp8_form, *rows of A a tile, K in
+ * *split parts.  Host code alone. */
+typedef enum {
+  TP_FP8_THIN = 0,    /* at most eight rows of A */
+  TP_FP8_NARROW = 1,  /* 16 to 128 rows of A a tile, K split over a cluster */
+  TP_FP8_WIDE = 2     /* 256×256 tiles */
+} tp_fp8_form;
+tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
+                                 int32_t b_group, int32_t sms, int32_t* form,
+                                 int32_t* rows, int32_t* split);
+
 /* ------------------------------------------------------------ profiling --
  * Per-kernel-family device time for roofline reporting.  While enabled,
  * every kernel the library launches is bracketed by two CUDA events recorded

@@ -20,6 +20,7 @@ GELU, SWIGLU = 0, 1
 FUSED, MATERIALISED, OVERLAP, SP = 0, 1, 2, 3
 SCOPE_MLP, SCOPE_ATTN, SCOPE_LAYER = 0, 1, 2
 FP8_ROW, FP8_BLOCK = 0, 1
+FP8_FORMS = ("thin", "narrow", "wide")
 
 STATUS = {0: "TP_OK", 1: "TP_ERR_NULL", 2: "TP_ERR_SHAPE", 3: "TP_ERR_DTYPE",
           4: "TP_ERR_WORKSPACE", 5: "TP_ERR_UNSUPPORTED", 6: "TP_ERR_CUDA",
@@ -140,6 +141,8 @@ SIGNATURES = {
     "tp_gemm_fp8_block": (_I32, [_I64, _I64, _I64] +
                           [_P, _I64, _P, _I64, _I32] * 2 +
                           [_I32, _P, _I64, _P]),
+    "tp_gemm_fp8_block_form": (_I32, [_I64, _I64, _I64, _I32, _I32] +
+                               [ctypes.POINTER(_I32)] * 3),
     "tp_mlp_flops": (_I32, [_MP, _U64P, _U64P]),
     "tp_attn_flops": (_I32, [_AP, _U64P, _U64P]),
     "tp_gemm": (_I32, [_I32, _I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _I32,
@@ -493,6 +496,16 @@ def gemm_fp8_block(qa, sa, qb, sb, C, stream=None):
                                   psb, ldsb, gb, dtype_code(C), C.data_ptr(),
                                   ldc, raw_stream(stream, dev)),
           "tp_gemm_fp8_block")
+
+
+def gemm_fp8_block_form(M, N, K, b_group=FP8_BLOCK, sms=0):
+    """(form, rows of A a tile, parts of K) that gemm_fp8_block takes for these
+    sizes on a device of ``sms`` SMs (0: the current one's)."""
+    out = [_I32() for _ in range(3)]
+    check(lib().tp_gemm_fp8_block_form(M, N, K, b_group, sms,
+                                       *map(ctypes.byref, out)),
+          "tp_gemm_fp8_block_form")
+    return FP8_FORMS[out[0].value], out[1].value, out[2].value
 
 
 def act_memory(b, s, h, h_ffn, n_q, n_kv, d, n, dtype=BF16, act=SWIGLU,

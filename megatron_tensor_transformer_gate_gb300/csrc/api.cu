@@ -1332,6 +1332,25 @@ extern "C" tp_status tp_gemm_fp8_block(
   });
 }
 
+extern "C" tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
+                                            int32_t b_group, int32_t sms,
+                                            int32_t* form, int32_t* rows,
+                                            int32_t* split) {
+  return guarded([&]() -> tp_status {
+    if (!form || !rows || !split) return TP_ERR_NULL;
+    if (b_group != TP_FP8_ROW && b_group != TP_FP8_BLOCK) return TP_ERR_DTYPE;
+    if (M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+      return TP_ERR_SHAPE;
+    if (sms < 0) return TP_ERR_ARG;
+    const Fp8BlockPlan p =
+        plan_fp8_block(M, N, K, b_group, sms ? sms : device_sm_count());
+    *form = p.form;
+    *rows = p.rows;
+    *split = p.split;
+    return TP_OK;
+  });
+}
+
 // ------------------------------------------------------------- profiling --
 extern "C" tp_status tp_profile_enable(int32_t max_launches) {
   return guarded([&]() -> tp_status {

@@ -59,6 +59,15 @@ struct GemmFp8Block {
   int64_t ldc = 0;
 };
 int gemm_fp8_block(const GemmFp8Block& p, void* stream, unsigned* status);
+// What it takes for sizes M, N, K on `sms` SMs.
+enum Fp8BlockForm { kFp8Thin = 0, kFp8Narrow = 1, kFp8Wide = 2 };   // tp.h
+struct Fp8BlockPlan {
+  int form = kFp8Wide;
+  int rows = 256;      // of A a tile
+  int split = 1;       // parts of K
+};
+Fp8BlockPlan plan_fp8_block(int64_t M, int64_t N, int64_t K, int b_group,
+                            int sms);
 // gemm_fp8_block_thin.cu: its form for M ≤ 8.
 int gemm_fp8_block_thin(const GemmFp8Block& p, cudaStream_t s);
 

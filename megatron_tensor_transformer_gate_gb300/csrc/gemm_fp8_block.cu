@@ -1189,22 +1189,17 @@ int narrow(const GemmFp8Block& g, cudaStream_t s, unsigned* status, int bn,
 //    256×8192×28672 110 / 108 (narrow, split 1: 105 / 98),
 //    8192×8192×4096 239 / 232.
 // Clusters of more than four CTAs leave SMs of a GPC empty.
-struct Plan {
-  int bn = 0;      // 0: wide
-  int split = 1;
-};
-Plan choose(const GemmFp8Block& g, int64_t kblocks) {
-  const int sms = device_sm_count();
+Fp8BlockPlan choose(int64_t M, int64_t N, int64_t K, bool b_row, int sms) {
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  const bool b_row = g.b_group == kFp8Row;
-  const int64_t tiles = up(g.M, 2 * BM) * up(g.N, BN);
-  Plan best;
+  const int64_t kblocks = up(K, BK);
+  const int64_t tiles = up(M, 2 * BM) * up(N, BN);
+  Fp8BlockPlan best;
   double least = 5.0 + up(tiles, std::max(sms / 2, 1)) *
                            (2.0 + kblocks * (b_row ? 0.66 : 0.46));
-  const double bytes = ((double)g.M + (double)g.N) * (double)g.K / 6.4e6;
-  const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+  const double bytes = ((double)M + (double)N) * (double)K / 6.4e6;
+  const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const double kb_us = bn <= 32 ? 0.34 : bn <= 64 ? 0.37 : 0.40;
-  const int64_t t = up(g.N, BM) * up(g.M, bn);
+  const int64_t t = up(N, BM) * up(M, bn);
   for (int split = 1; split <= 8 && split <= kblocks; ++split) {
     const double slots = sms * (bn <= 64 ? 2 : 1) * (split > 4 ? 0.85 : 1.0);
     const double waves = std::max(1.0, std::ceil(t * split / slots));
@@ -1213,7 +1208,8 @@ Plan choose(const GemmFp8Block& g, int64_t kblocks) {
                       0.3 * std::min(work, bytes);
     if (us < least) {
       least = us;
-      best.bn = bn;
+      best.form = kFp8Narrow;
+      best.rows = bn;
       best.split = split;
     }
   }
@@ -1222,18 +1218,29 @@ Plan choose(const GemmFp8Block& g, int64_t kblocks) {
 
 }  // namespace
 
+Fp8BlockPlan plan_fp8_block(int64_t M, int64_t N, int64_t K, int b_group,
+                            int sms) {
+  if (M > 8) return choose(M, N, K, b_group == kFp8Row, sms);
+  Fp8BlockPlan p;   // measured in gemm_fp8_block_thin.cu
+  p.form = kFp8Thin;
+  p.rows = 8;
+  return p;
+}
+
 int gemm_fp8_block(const GemmFp8Block& g, void* stream, unsigned* status) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Fp8BlockPlan pl =
+      plan_fp8_block(g.M, g.N, g.K, g.b_group, device_sm_count());
   int err;
   {
     ProfScope ps(s, KF_GEMM_TC_FP8, 2.0 * g.M * g.N * g.K,
                  (double)(g.M + g.N) * g.K + (g.out_f32 ? 4.0 : 2.0) * g.M * g.N);
-    if (g.M <= 8) {   // measured there
+    if (pl.form == kFp8Thin)
       err = gemm_fp8_block_thin(g, s);
-    } else {
-      const Plan pl = choose(g, (g.K + BK - 1) / BK);
-      err = pl.bn ? narrow(g, s, status, pl.bn, pl.split) : wide(g, s, status);
-    }
+    else if (pl.form == kFp8Narrow)
+      err = narrow(g, s, status, pl.rows, pl.split);
+    else
+      err = wide(g, s, status);
   }
   if (err) return err;
   count_launch();

@@ -326,9 +326,11 @@ def test_product(tp, M, N, K, ga, gb, out):
 
 
 @pytest.mark.parametrize("gb", ["row", "block"])
-@pytest.mark.parametrize("M,N,K", [(2600, 2400, 5200), (40, 300, 28672),
-                                   (128, 300, 28672), (300, 264, 16500)])
-def test_product_whose_scales_go_round_their_ring(tp, M, N, K, gb):
+@pytest.mark.parametrize("form,M,N,K", [
+    ("wide", 1080, 4330, 2600),       # nine clusters go on to a second tile
+    ("wide", 430, 4980, 9000), ("narrow", 40, 300, 28672),
+    ("narrow", 128, 300, 28672), ("narrow", 300, 264, 16500)])
+def test_product_whose_scales_go_round_their_ring(tp, form, M, N, K, gb):
     # K blocks that differ by powers of two: a block that met another's scales
     # would be off by far more than the bound
     def with_steps(rows, group, seed):
@@ -338,6 +340,7 @@ def test_product_whose_scales_go_round_their_ring(tp, M, N, K, gb):
                                       ).float()).cuda()
         return q, s
 
+    assert tp.gemm_fp8_block_form(M, N, K, GROUPS[gb])[0] == form
     qa, sa = with_steps(M, "row", 21)
     qb, sb = with_steps(N, gb, 22)
     for out in (torch.float32, torch.bfloat16):
