@@ -436,7 +436,7 @@ tp_status tp_gemm_fp8(int64_t M, int64_t N, int64_t K, const void* qa,
  * scale is what a code is multiplied by.)
  * Sizes: 1 ≤ rows, cols ≤ 2^30, at most 2^31 − 1 tiles of 128×128.  No call
  * below needs a workspace or keeps anything between calls, and none leaves
- * the order of a sum open: the same inputs give the same bits.  Outputs do
+ * the order of a sum open: the same call gives the same bits.  Outputs do
  * not overlap inputs or each other, except where said. */
 typedef enum { TP_FP8_ROW = 0, TP_FP8_BLOCK = 1 } tp_fp8_group;
 
@@ -486,7 +486,10 @@ tp_status tp_add_rmsnorm_fp8_fwd(int64_t T, int64_t h, float eps,
 /* C[M, N] = Σ_b Σ_{k in block b} (qa·sa)[m, k]·(qb·sb)[n, k] over the blocks
  * b of 128 along K: A [M, K] and B [N, K] block-scaled E4M3, each with the
  * scales of its own tp_fp8_group; products within a block accumulate in fp32
- * on the tensor cores, the blocks' sums times sa·sb in fp32 in order of b.
+ * on the tensor cores, the blocks' sums times sa·sb in fp32.  Their order is
+ * fixed by M, N, K, B's group and the device's SMs, which choose the form
+ * (tp_gemm_fp8_block_form); so the same call gives the same bits, but a row's
+ * may differ between batches of different sizes.
  * C: out_dtype TP_BF16 or TP_F32, row stride ldc ≥ N.  With X the input, W
  * [out, in] the weight in TP_FP8_BLOCK and dY the output's gradient:
  *   Y  = X·Wᵀ       A = X (rows),            B = W;
@@ -501,11 +504,16 @@ tp_status tp_gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void* qa,
 
 /* The form that tp_gemm_fp8_block takes for these sizes on a device of `sms`
  * SMs (0: the current one's): *form of tp_fp8_form, *rows of A a tile, K in
- * *split parts.  Host code alone. */
+ * *split parts.  Host code alone.  The order of the n = ⌈K/128⌉ blocks' sums:
+ *   thin    at most eight rows of A: blocks j, j + 8, j + 16, … in turn, then
+ *           these sums in order of j;
+ *   narrow  16 to 128 rows of A a tile: blocks ⌊n·j/split⌋ up to
+ *           ⌊n·(j + 1)/split⌋ in order, then these sums in order of j;
+ *   wide    256×256 tiles: in order of b. */
 typedef enum {
-  TP_FP8_THIN = 0,    /* at most eight rows of A */
-  TP_FP8_NARROW = 1,  /* 16 to 128 rows of A a tile, K split over a cluster */
-  TP_FP8_WIDE = 2     /* 256×256 tiles */
+  TP_FP8_THIN = 0,
+  TP_FP8_NARROW = 1,
+  TP_FP8_WIDE = 2
 } tp_fp8_form;
 tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
                                  int32_t b_group, int32_t sms, int32_t* form,

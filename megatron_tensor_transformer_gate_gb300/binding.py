@@ -484,7 +484,9 @@ def add_rmsnorm_fp8_fwd(x, r, gamma, x1, q, s, rstd, y=None, eps=1e-5,
 
 def gemm_fp8_block(qa, sa, qb, sb, C, stream=None):
     """C[M, N] (bf16 or fp32) = A·Bᵀ of the block-scaled A = (qa, sa) [M, K]
-    and B = (qb, sb) [N, K]."""
+    and B = (qb, sb) [N, K].  The K blocks' sums are added in an order fixed by
+    the sizes (gemm_fp8_block_form): a row's last bits may differ between
+    batches of different sizes."""
     if _done((_tpcall or _load()).gemm(qa, sa, qb, sb, C, stream),
              "tp_gemm_fp8_block"):
         return

@@ -14,7 +14,7 @@
 //    cluster whose CTAs add up their parts through distributed shared memory
 //    in rank order: the form for few rows of A, which reads the weight once.
 // Neither keeps anything between calls or needs a workspace, and no sum's
-// order is left open.
+// order is left open: it is the form's, which the sizes choose.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -2,6 +2,7 @@
 of scales, capture and streams, with the form that a case is meant for asserted.
 Bounds: tests/test_gpu_fp8_block.py."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -29,6 +30,49 @@ def test_form(tp, M, N, K, want, gb, out):
     tp.gemm_fp8_block(qa, sa, qb, sb, C)
     tp.device_status()
     check_product(C, qa, sa, qb, sb, f"{M}x{N}x{K} {want}")
+
+
+def documented_sum(terms, form, split):
+    """The K blocks' sums added in fp32 in the order that the header gives."""
+    n = len(terms)
+    if form == "thin":
+        parts = [range(j, n, 8) for j in range(8)]
+    else:
+        parts = [range(n * j // split, n * (j + 1) // split)
+                 for j in range(split)]
+    sums = []
+    for p in parts:
+        v = np.float32(0)
+        for b in p:
+            v = np.float32(v + terms[b])
+        sums.append(v)
+    total = np.float32(0)
+    for v in sums:
+        total = np.float32(total + v)
+    return total
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 100, 5000), (3, 100, 1), (8, 64, 1290),
+                                   (9, 100, 4999), (37, 100, 900),
+                                   (280, 3300, 2600), WIDE])
+def test_order_of_the_blocks_sums(tp, M, N, K):
+    # one product of 1·1 a block, so that its sum is the two scales' product
+    name, _, split = tp.gemm_fp8_block_form(M, N, K, GROUPS["block"])
+    nb = (K + 127) // 128
+    qa, sa = tp.fp8_block_empty(M, K)
+    qb, sb = tp.fp8_block_empty(N, K, GROUPS["block"])
+    for q in (qa, qb):
+        q.view(torch.uint8).zero_()
+        q.view(torch.uint8)[:, ::128] = 0x38          # 1.0
+    rng = np.random.default_rng(K)
+    s = (rng.standard_normal(nb) * 10.0 ** rng.integers(-3, 4, nb)
+         ).astype(np.float32)
+    sa.copy_(torch.from_numpy(s).cuda()[:, None].expand_as(sa))
+    sb.fill_(1.0)
+    C = torch.empty((M, N), dtype=torch.float32, device="cuda")
+    tp.gemm_fp8_block(qa, sa, qb, sb, C)
+    want = documented_sum(s, name, split)
+    assert bool((C == float(want)).all()), (name, split, want, C[0, 0])
 
 
 @pytest.mark.parametrize("gb", ["row", "block"])
