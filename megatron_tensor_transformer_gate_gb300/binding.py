@@ -8,10 +8,22 @@ raises.
 """
 
 import ctypes
+import importlib.util
 import os
+import warnings
 
-import torch
 
+class _Torch:
+    """torch, imported when it is first used: what counts bytes and operations
+    needs only ctypes."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtp.so")
 
@@ -159,12 +171,11 @@ SIGNATURES = {
 }
 
 _lib = None
-_tpcall = None   # the CPython module of the block-scaled calls (csrc/pycall.cpp)
 
 
 def lib():
     """The loaded library (raises if it has not been built)."""
-    global _lib, _tpcall
+    global _lib
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(
@@ -175,12 +186,7 @@ def lib():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        from . import _tpcall as fast
-        fast.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
-                    ("tp_quantize_fp8_block", "tp_swiglu_fp8_fwd",
-                     "tp_swiglu_fp8_bwd", "tp_add_rmsnorm_fp8_fwd",
-                     "tp_gemm_fp8_block")))
-        _lib, _tpcall = L, fast
+        _lib = L
     return _lib
 
 
@@ -272,6 +278,40 @@ def fp8_block_empty(rows, cols, group=FP8_ROW, device="cuda"):
 # most of its time.  csrc/pycall.cpp makes them for arguments in their ordinary
 # form and calls the C entry (2.7 to 4 µs a call); where it finds anything else
 # it answers None, and the functions below check again and say what is wrong.
+# Where it is not built for this Python and torch they make every call.
+_tpcall = None   # that module, or its stand-in
+
+
+class _EveryCallInPython:
+    @staticmethod
+    def quantize(*_):
+        return None
+
+    swiglu = swiglu_bwd = norm = gemm = quantize
+
+
+def _load():
+    global _tpcall
+    L = lib()
+    torch.Tensor   # the module links against torch's libraries as loaded
+    try:
+        from .build import pycall_path
+        spec = importlib.util.spec_from_file_location(__package__ + "._tpcall",
+                                                      pycall_path())
+        fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(fast)
+        fast.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
+                    ("tp_quantize_fp8_block", "tp_swiglu_fp8_fwd",
+                     "tp_swiglu_fp8_bwd", "tp_add_rmsnorm_fp8_fwd",
+                     "tp_gemm_fp8_block")))
+    except ImportError as e:
+        warnings.warn("the block-scaled calls' module is not built for this "
+                      f"Python and torch, each call takes longer: {e}")
+        fast = _EveryCallInPython
+    _tpcall = fast
+    return fast
+
+
 def _shape(t):
     return tuple(t.shape)
 
@@ -321,7 +361,7 @@ def _dense(t, what, dtype, shape, dev):
 def _refuse_pair(q, s, what, rows, cols, dev):
     if s is None:
         raise ValueError(f"{what}: codes without scales")
-    if q.dtype not in _CODE_TYPES:
+    if not _is_code(q):
         raise TypeError(f"{what}: E4M3 codes, got {q.dtype}")
     if s.dtype != torch.float32:
         raise TypeError(f"{what} scales: float32, got {s.dtype}")
@@ -335,14 +375,15 @@ def _refuse_pair(q, s, what, rows, cols, dev):
     raise ValueError(f"{what} scales: {_shape(s)} for codes {(rows, cols)}")
 
 
-_CODE_TYPES = (torch.float8_e4m3fn, torch.uint8)
+def _is_code(q):
+    return q.dtype is torch.float8_e4m3fn or q.dtype is torch.uint8
 
 
 def _fp8_pair(q, s, what, rows, cols, dev):
     """(address, ldq, address of the scales, lds, group) of a block-scaled
     matrix of this shape on this device."""
     kb, rb = (cols + 127) >> 7, (rows + 127) >> 7
-    if s is None or q.shape != (rows, cols) or q.dtype not in _CODE_TYPES or \
+    if s is None or q.shape != (rows, cols) or not _is_code(q) or \
             s.dtype is not torch.float32 or q.get_device() != dev or \
             s.get_device() != dev or s.dim() != 2:
         _refuse_pair(q, s, what, rows, cols, dev)
@@ -378,11 +419,6 @@ def _fp8_outs(rows, cols, dev, q, s, qt, st):
     if ga != gb:
         raise ValueError("q and qt have scales of different groups")
     return a[:4] + b[:4], ga
-
-
-def _load():
-    lib()
-    return _tpcall
 
 
 def _done(rc, where):
