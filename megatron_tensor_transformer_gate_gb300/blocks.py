@@ -283,6 +283,14 @@ class TPBlockFP8MLP:
             raise RuntimeError("a forward of a block with train=True comes "
                                "first")
         g = grads if grads is not None else self.alloc_grads()
+        # what the norm's backward takes as it is (the products check theirs)
+        dev = self.x1.get_device()
+        for t, what, shape in ((gamma, "gamma", (self.h,)),
+                               (dx1, "dx1", (self.T, self.h)),
+                               (g["dX"], "dX", (self.T, self.h)),
+                               (g["dgamma"], "dgamma", (self.h,))):
+            if t is not None:
+                B._dense(t, what, torch.bfloat16, shape, dev)
         (_, w1t), (_, w2t) = self.weights
         B.quantize_fp8_block(dZ, *self.dz, *self.dzt, stream=stream)
         B.gemm_fp8_block(*self.dz, *w2t, self.da, stream=stream)
