@@ -9,6 +9,8 @@ four TP reductions (attention g and MLP g in forward, MLP f and attention f
 in backward).
 """
 
+import contextlib
+
 import torch
 
 from . import binding as B
@@ -173,6 +175,13 @@ class TPLayer:
         return g
 
 
+def _made_on(stream):
+    """Memory that a call makes for itself belongs to the stream it runs on: of
+    another stream's pool it may still be in use there."""
+    return contextlib.nullcontext() if stream is None else \
+        torch.cuda.stream(stream)
+
+
 class TPBlockFP8MLP:
     """Residual + RMSNorm + SwiGLU MLP with every product, forward and
     backward, on block-scaled E4M3 operands:
@@ -230,11 +239,12 @@ class TPBlockFP8MLP:
                              f"{(self.h, self.f)}, got {tuple(W1.shape)} and "
                              f"{tuple(W2.shape)}")
         if self.weights is None:
-            self.weights = [
-                [B.fp8_block_empty(*s, B.FP8_BLOCK, self.device)
-                 if s is not None else (None, None) for s in
-                 (W.shape, W.shape[::-1] if self.train else None)]
-                for W in (W1, W2)]
+            with _made_on(stream):
+                self.weights = [
+                    [B.fp8_block_empty(*s, B.FP8_BLOCK, self.device)
+                     if s is not None else (None, None) for s in
+                     (W.shape, W.shape[::-1] if self.train else None)]
+                    for W in (W1, W2)]
         for W, (q, qt) in zip((W1, W2), self.weights):
             B.quantize_fp8_block(W, *q, *qt, stream=stream)
 
@@ -242,13 +252,14 @@ class TPBlockFP8MLP:
         """(x1, Z).  x1 may be given (x or r among it); without r it is x."""
         if self.weights is None:
             raise RuntimeError("load_weights comes first")
-        if r is None:
-            x1 = x if x1 is None else x1
-        elif x1 is None:
-            x1 = torch.empty_like(x)
-        if out is None:
-            out = torch.empty((self.T, self.h), dtype=torch.bfloat16,
-                              device=self.device)
+        with _made_on(stream):
+            if r is None:
+                x1 = x if x1 is None else x1
+            elif x1 is None:
+                x1 = torch.empty_like(x)
+            if out is None:
+                out = torch.empty((self.T, self.h), dtype=torch.bfloat16,
+                                  device=self.device)
         (w1, _), (w2, _) = self.weights
         keep = self.train
         B.add_rmsnorm_fp8_fwd(x, r, gamma, None if x1 is x and r is None
@@ -282,7 +293,8 @@ class TPBlockFP8MLP:
         if not self.train or self.x1 is None:
             raise RuntimeError("a forward of a block with train=True comes "
                                "first")
-        g = grads if grads is not None else self.alloc_grads()
+        with _made_on(stream):
+            g = grads if grads is not None else self.alloc_grads()
         # what the norm's backward takes as it is (the products check theirs)
         dev = self.x1.get_device()
         for t, what, shape in ((gamma, "gamma", (self.h,)),

@@ -121,6 +121,32 @@ def test_step_captured_and_replayed_next_to_an_eager_one(tp):
     tp.device_status()
 
 
+def pool_of(t):
+    """The stream whose memory pool a tensor is of."""
+    return next(s["stream"] for s in torch.cuda.memory_snapshot()
+                if 0 <= t.data_ptr() - s["address"] < s["total_size"])
+
+
+def test_memory_made_in_a_call_is_of_its_stream(tp):
+    T, h, f = 150, 384, 512
+    t = tensors(T, h, f, 8)
+    here, _, d = run(t, T, h, f)
+    side = torch.cuda.Stream()
+    m = TPBlockFP8MLP(T, h, f, eps=EPS)
+    side.wait_stream(torch.cuda.current_stream())
+    m.load_weights(d["W1"], d["W2"], stream=side)
+    x1, Z = m.forward(d["x"], d["gamma"], r=d["r"], stream=side)
+    g = m.backward(d["dZ"], d["gamma"], dx1=d["dx1"], stream=side)
+    side.synchronize()
+    tp.device_status()
+    got = dict(g, x1=x1, Z=Z)
+    for k, v in got.items():
+        assert torch.equal(v, here[k]), k
+        assert pool_of(v) == side.cuda_stream, k
+    for pair in (p for w in m.weights for p in w):
+        assert all(pool_of(v) == side.cuda_stream for v in pair)
+
+
 def test_block_refuses(tp):
     for a in ((0, 256, 256), (4, 252, 256), (4, 256, 200), (4, 16392, 256)):
         with pytest.raises(ValueError):
