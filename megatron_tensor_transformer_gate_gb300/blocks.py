@@ -193,7 +193,10 @@ class TPBlockFP8MLP:
     without x1: the next norm adds it as its r.  Scales are 1×128 along each
     product's reduction axis for activations and gradients, 128×128 for
     weights; γ, x, r, x1, Z and the gradients are bf16 (weight gradients in
-    ``grad_dtype``, bf16 or fp32).
+    ``grad_dtype``, bf16 or fp32).  Each operand's codes are made from fp32 values
+    or from the bf16 tensor that the step before stores, with one exception: the
+    codes of Yᵀ, for dW1, are of Y rounded to bf16 (those of Y, for the forward,
+    are not), so that dW1's operand is rounded twice.
 
     W1 is [2·h_ffn, h] (gate rows, then up rows), W2 [h, h_ffn], both bf16 or
     fp32, unsharded.  Each of the n logical shards holds h_ffn/n hidden units,

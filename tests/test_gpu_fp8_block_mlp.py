@@ -121,6 +121,19 @@ def test_step_captured_and_replayed_next_to_an_eager_one(tp):
     tp.device_status()
 
 
+def test_what_the_saved_codes_are_made_of(tp):
+    # Yᵀ's codes are of the stored bf16 Y, Aᵀ's of the fp32 values of A's own
+    T, h, f = 130, 264, 256
+    _, m, _ = run(tensors(T, h, f, 9), T, h, f)
+    yt, st = ob.quantize(m.y16.float().cpu().numpy().T, "row")
+    assert (m.yt[0].contiguous().view(torch.uint8).cpu().numpy() == yt).all()
+    assert (m.yt[1].cpu().numpy() == st).all()
+    at = tp.fp8_block_empty(f, T)
+    tp.swiglu_fp8_fwd(m.gu, qt=at[0], st=at[1])
+    assert torch.equal(at[0].view(torch.uint8), m.at[0].view(torch.uint8))
+    assert torch.equal(at[1], m.at[1])
+
+
 def pool_of(t):
     """The stream whose memory pool a tensor is of."""
     return next(s["stream"] for s in torch.cuda.memory_snapshot()
