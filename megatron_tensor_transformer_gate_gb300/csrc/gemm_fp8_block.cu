@@ -123,7 +123,7 @@ struct RowAcc {
   // (16-byte piece k of row r at k ^ (r / 2 mod 4)): a warp's store then
   // writes 64 bytes in each of eight rows instead of 16 in each of 32, or,
   // where rows are not 16-byte aligned or end inside the tile, one row's
-  // elements side by side (2000×2500×4096 41 µs; by each thread into its own
+  // elements side by side (2000×2500×4096 43 µs; by each thread into its own
   // row 95).
   template <int OUT_F32>
   __device__ __forceinline__ void store(const Params& p, uint4* stage, int m0,
@@ -252,7 +252,8 @@ struct GridAcc {
   }
   // The four lanes of a row exchange what makes 16 bytes in each: 64 bytes of
   // a row a store.  Rows that are not 16-byte aligned or end inside the tile
-  // go through shared memory, as in RowAcc (2000×2500×4096 59 µs, 64 without).
+  // go through shared memory, as in RowAcc (2000×2500×4096 53 µs; when it was
+  // put in 59, and 64 without).
   template <int OUT_F32>
   __device__ __forceinline__ void store(const Params& p, uint4* stage, int m0,
                                         int n0, int lane) const {
@@ -333,9 +334,9 @@ struct GridAcc {
 // Two CTAs, each with 128 rows of a 256×256 tile: every CTA loads its A rows
 // and half of B, and rank 0 (the leader) issues MMAs of M = 256 that read both
 // halves (cta_group::2).  No load is multicast: such a load is for one GPU's own
-// memory, and one library serves every rank of a run on several (its form, two
-// rings of B and MMAs of each CTA's own, took 237 µs where this one takes 242,
-// 8192×8192×4096, and the same 315 with row scales).  Roles:
+// memory, and one library serves every rank of a run on several (with it, and
+// MMAs of each CTA's own, 8192×8192×4096 took 237 µs where the pair's took 242
+// on the same GPU, with row scales 315 both).  Roles:
 //   warp 0      TMA producer, a ring of six K blocks;
 //   warps 1, 2  of the leader: MMA issue, every other K block and one TMEM
 //               buffer each: beside eight busy epilogue warps one thread's
@@ -349,15 +350,17 @@ struct GridAcc {
 // = 384·168).
 //
 // Measured: 8192×8192×4096 with a scale for 128×128 of B 242 µs (2270 TFLOP/s),
-// with one for each of its rows 315 (1747); 8192×8192×28672 1440 µs alone
-// (2670), 1630 in a loop at the power limit.  What bounds it is the chain of a
-// K block: its MMAs (512 cycles on an idle SM, nearer 700 while the epilogue
-// reads TMEM), the read back and the hand-over both ways take some 1900 cycles
-// together, and the two halves of TMEM hide one block's behind another's, so
-// that one ends every 900 to 1000; the tensor pipe is busy 72 % of the time.
-// With scales for rows of both sides the epilogue multiplies twice as often
-// and a block ends every 1350 to 1400.  (Removing the epilogue's additions
-// altogether gains 10 %, the scales' products 10 % of the second form.)
+// with one for each of its rows 318 (1730); 8192×8192×28672 1490 µs alone (2580,
+// SM clock at 2070 MHz), 1578 in a loop at the power limit (1942 MHz).  What
+// bounds it is the chain of a K block: its MMAs (512 cycles on an idle SM, nearer
+// 700 while the epilogue reads TMEM), the read back and the hand-over both ways
+// take some 1900 cycles together, and the two halves of TMEM hide one block's
+// behind another's, so that one ends every 980 to 1100; the tensor pipe is
+// active 53 % of the cycles, the tcgen05 pipe 59 %.  With scales for rows of
+// both sides the epilogue multiplies twice as often and a block ends every 1400
+// to 1450 (39 and 44 %).  Removing the epilogue's additions altogether gains
+// 10 %, the scales' products 10 % of the second kind (both measured with MMAs
+// of each CTA's own).
 template <int B_ROW, int OUT_F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WIDE_THREADS, 1)
     gemm_fp8_block_wide(const __grid_constant__ Params p) {
@@ -1185,9 +1188,9 @@ int narrow(const GemmFp8Block& g, cudaStream_t s, unsigned* status, int bn,
 //    48×8192×28672 split 4 47 / 45, split 1 98 / 90;
 //    128×8192×28672 split 2 60 / 56, split 4 64 / 62; 512×4096×4096 18 / 19;
 //  * wide: 5, and for each round of tiles 2 and 0.46 a K block (0.66 with a
-//    scale for each row of B).  512×4096×4096 22 / 21, 1024×8192×8192 68 / 68,
-//    256×8192×28672 110 / 108 (narrow, split 1: 105 / 98),
-//    8192×8192×4096 239 / 232.
+//    scale for each row of B).  512×4096×4096 22 / 21, 1024×8192×8192 68 / 70,
+//    256×8192×28672 110 / 111 (narrow, split 1: 105 / 97),
+//    8192×8192×4096 239 / 242.
 // Clusters of more than four CTAs leave SMs of a GPC empty.
 Fp8BlockPlan choose(int64_t M, int64_t N, int64_t K, bool b_row, int sms) {
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
