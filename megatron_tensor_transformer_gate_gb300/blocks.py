@@ -241,20 +241,24 @@ class TPBlockFP8MLP:
             raise ValueError(f"W1 {(2 * self.f, self.h)} and W2 "
                              f"{(self.h, self.f)}, got {tuple(W1.shape)} and "
                              f"{tuple(W2.shape)}")
-        if self.weights is None:
+        weights, self.weights = self.weights, None   # none, should a call fail
+        if weights is None:
             with _made_on(stream):
-                self.weights = [
+                weights = [
                     [B.fp8_block_empty(*s, B.FP8_BLOCK, self.device)
                      if s is not None else (None, None) for s in
                      (W.shape, W.shape[::-1] if self.train else None)]
                     for W in (W1, W2)]
-        for W, (q, qt) in zip((W1, W2), self.weights):
+        for W, (q, qt) in zip((W1, W2), weights):
             B.quantize_fp8_block(W, *q, *qt, stream=stream)
+        self.weights = weights
 
     def forward(self, x, gamma, r=None, out=None, x1=None, stream=None):
         """(x1, Z).  x1 may be given (x or r among it); without r it is x."""
         if self.weights is None:
             raise RuntimeError("load_weights comes first")
+        if self.train:
+            self.x1 = None   # what the last forward saved is overwritten
         with _made_on(stream):
             if r is None:
                 x1 = x if x1 is None else x1

@@ -1,5 +1,5 @@
-"""Refusals of TPBlockFP8MLP's backward (no GPU needed: it refuses before its
-first call)."""
+"""What TPBlockFP8MLP refuses before its first call, and what is left of a call
+that failed (no GPU needed: CPU tensors are refused)."""
 
 import pytest
 import torch
@@ -31,3 +31,27 @@ def test_backward_refuses(tp, which, bad, kind):
     (a if which in a else a["grads"])[which] = bad
     with pytest.raises(kind, match=f"^{which}"):
         m.backward(**a)
+
+
+def test_weights_that_failed_to_load_are_not_used(tp):
+    m = TPBlockFP8MLP(T, H, F, device="cpu")
+    x, gamma = torch.zeros(T, H, dtype=torch.bfloat16), \
+        torch.ones(H, dtype=torch.bfloat16)
+    for weights in (None, [[(None, None)] * 2] * 2):   # first, and an update
+        m.weights = weights
+        with pytest.raises(ValueError, match="not on a GPU"):
+            m.load_weights(torch.zeros(2 * F, H), torch.zeros(H, F))
+        with pytest.raises(RuntimeError, match="load_weights"):
+            m.forward(x, gamma)
+
+
+def test_no_backward_after_a_forward_that_failed(tp):
+    m = TPBlockFP8MLP(T, H, F, device="cpu")
+    x, gamma = torch.zeros(T, H, dtype=torch.bfloat16), \
+        torch.ones(H, dtype=torch.bfloat16)
+    m.x1 = x                                   # as after a forward
+    m.weights = [[(None, None)] * 2] * 2
+    with pytest.raises(ValueError, match="not on a GPU"):
+        m.forward(x, gamma)
+    with pytest.raises(RuntimeError, match="forward"):
+        m.backward(x, gamma)
