@@ -42,8 +42,8 @@
  *    launch, with nothing enqueued.  A failed launch returns TP_ERR_CUDA.
  *    Device-side waits are bounded; one that runs out records a device status
  *    word that tp_device_status() returns as TP_ERR_DEVICE_TIMEOUT (or
- *    TP_ERR_RANGE for an fp16 overflow).  No C++ exception crosses this
- *    boundary.
+ *    TP_ERR_RANGE for an fp16 overflow, TP_ERR_PAGE for a bad page table).
+ *    No C++ exception crosses this boundary.
  */
 #ifndef TP_H_
 #define TP_H_
@@ -65,12 +65,14 @@ typedef enum {
   TP_ERR_CUDA = 6,            /* a CUDA runtime/driver call failed */
   TP_ERR_DEVICE_TIMEOUT = 7,  /* a bounded device wait ran out */
   TP_ERR_ARG = 8,             /* misaligned pointer or other bad argument */
-  TP_ERR_RANGE = 9            /* an fp16 attention operand overflowed */
+  TP_ERR_RANGE = 9,           /* a value overflowed fp16 */
+  TP_ERR_PAGE = 10            /* a page or length outside the cache */
 } tp_status;
 
 /* TP_FP8 (E4M3, δ = 1): an FP8 payload in the accountants; for the MLP it
  * selects forward GEMMs on per-tensor scaled E4M3 operands (bf16 storage). */
-typedef enum { TP_F32 = 0, TP_BF16 = 1, TP_FP8 = 2 } tp_dtype;  /* δ = 4, 2, 1 */
+typedef enum { TP_F32 = 0, TP_BF16 = 1, TP_FP8 = 2,             /* δ = 4, 2, 1 */
+               TP_F16 = 3 } tp_dtype;  /* TP_F16: key-value caches alone */
 typedef enum { TP_GELU = 0, TP_SWIGLU = 1 } tp_act;
 /* TP_REDUCE_OVERLAP: materialised partials, summed band by band (row bands
  * of the GEMM, up to 4) on a second stream while the GEMM computes the next
@@ -519,6 +521,88 @@ tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
                                  int32_t b_group, int32_t sms, int32_t* form,
                                  int32_t* rows, int32_t* split);
 
+/* ------------------------------------------------------- key-value cache --
+ * The cache of an attention layer whose sequences grow a few tokens at a
+ * time: two pools of pages, K and V, each [pages, page, n_kv, d] in TP_BF16,
+ * TP_F16 or TP_FP8.  A pool's vectors (d adjacent elements, one head of one
+ * token) lie anywhere: element strides of a page, a token and a head, shared
+ * by both pools, vectors apart from each other and on multiples of 16 bytes.
+ * TP_FP8 vectors are E4M3 codes with one fp32 scale each in ks and vs
+ * [pages, page, n_kv] (strides of their own, again shared): as in
+ * tp_quantize_fp8_block's TP_FP8_ROW, s = amax / 448, code = E4M3(x·448/amax)
+ * and the element's value is code·s.
+ * table[i·table_stride + c], device int32, is the page of sequence i's tokens
+ * [c·page, (c + 1)·page); lens[i], device int32, how many tokens the sequence
+ * has, the newest ones of a call among them.  Only the entries that a call's
+ * tokens need are read; sequences may share pages that are only read.  A
+ * length below one is that of an idle place in the batch.
+ * A call reads the table and the lengths on the device, when it runs.  An
+ * entry outside [0, pages), or a length beyond table_cols·page, is not
+ * followed: the tokens there are left out and tp_device_status returns
+ * TP_ERR_PAGE. */
+typedef struct {
+  int32_t dtype;         /* TP_BF16, TP_F16 or TP_FP8 */
+  int32_t b;             /* sequences (1 to 65536) */
+  int32_t n_kv, d;       /* heads (1 to 1024) and their size, 64 or 128 */
+  int32_t page;          /* tokens a page (1 to 2^20) */
+  int32_t table_cols;    /* pages that a row of the table can list (≥ 1) */
+  int64_t pages;         /* pages in a pool */
+  void *k, *v;
+  int64_t page_stride, token_stride, head_stride;        /* elements */
+  float *ks, *vs;        /* TP_FP8 alone, else ignored */
+  int64_t s_page_stride, s_token_stride, s_head_stride;  /* elements */
+  const int32_t* table;
+  int64_t table_stride;  /* ≥ table_cols, unless b = 1 */
+  const int32_t* lens;
+} tp_kv_cache;
+
+/* Write new tokens: rows of K and V ([rows, n_kv, d], TP_BF16 or TP_F16; a
+ * row's and a head's element strides are multiples of 8, such as those of the
+ * QKV projection's output), each value rounded once to the cache's type (an
+ * fp16 cache reports TP_ERR_RANGE for what fp16 does not hold).  The new
+ * tokens are their sequence's last ones: of m rows, row j belongs to position
+ * lens[i] − m + j, and to no token where that is negative (an idle place;
+ * padding in front of a short prompt).  start NULL: rows = b·m, m for each
+ * sequence in turn; else device int32 [b + 1], not decreasing: sequence i's
+ * are rows start[i] up to start[i + 1], and rows outside [start[0], start[b])
+ * are no tokens.  Rows of no token are not read and nothing is written for
+ * them.  Positions that two rows of one call share hold either's value. */
+tp_status tp_kv_cache_write(const tp_kv_cache* c, int32_t dtype, int64_t rows,
+                            const void* K, int64_t k_row, int64_t k_head,
+                            const void* V, int64_t v_row, int64_t v_head,
+                            const int32_t* start, tp_stream stream);
+
+/* Its inverse: the cached vectors into rows of K and V, rounded once.  Rows
+ * of no token are left as they were.  With m = lens[i] the whole sequence is
+ * read, with less its end. */
+tp_status tp_kv_cache_read(const tp_kv_cache* c, int32_t dtype, int64_t rows,
+                           void* K, int64_t k_row, int64_t k_head, void* V,
+                           int64_t v_row, int64_t v_head, const int32_t* start,
+                           tp_stream stream);
+
+/* Attention of the newest tokens over the cache, which holds them already.
+ * q, out: [rows, n_q, d] of `dtype` (TP_BF16 or TP_F16; TP_F16 not over a
+ * TP_BF16 cache: TP_ERR_UNSUPPORTED), row and head strides multiples of 8;
+ * rows = b·m, the last m tokens of each sequence: row j of sequence i is the
+ * token at p = lens[i] − m + j and sees the tokens t ≤ p.  Query head j reads
+ * kv head ⌊j·n_kv/n_q⌋.
+ *   x_t = scale·q·k_t,  out = Σ_t e^(x_t)·v_t / Σ_t e^(x_t),
+ *   lse = ln Σ_t e^(x_t)     (fp32 [rows, n_q] dense; NULL: not written).
+ * A row that sees nothing (p < 0) has out = 0 and lse = −∞.  Scores, sums and
+ * what is added of v are fp32.  What a masked or unused place of a page holds
+ * (infinities and NaN among it) has no influence.
+ * The same call gives the same bits; how a sequence's tokens are split, and
+ * with it a sum's order, depends on the lengths of the whole batch.
+ * ws: scratch, not kept between calls; calls that overlap on the GPU (two
+ * streams, two graphs) need one each. */
+size_t tp_attn_decode_workspace_bytes(const tp_kv_cache* c, int64_t rows,
+                                      int32_t n_q);
+tp_status tp_attn_decode(const tp_kv_cache* c, int32_t dtype, int64_t rows,
+                         int32_t n_q, float scale, const void* q,
+                         int64_t q_row, int64_t q_head, void* out,
+                         int64_t o_row, int64_t o_head, float* lse, void* ws,
+                         size_t ws_bytes, tp_stream stream);
+
 /* ------------------------------------------------------------ profiling --
  * Per-kernel-family device time for roofline reporting.  While enabled,
  * every kernel the library launches is bracketed by two CUDA events recorded
@@ -531,7 +615,8 @@ tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
  * summed algorithmic FLOPs and bytes.  Families: 0 tcgen05 GEMM, 1 fp32
  * GEMM, 2 attention forward, 3 attention backward dK/dV, 4 attention
  * backward dQ, 5 shard-partial reduce, 6 other elementwise, 7 RMSNorm,
- * 8 tcgen05 GEMM on E4M3 operands, 9 FP8 amax / quantize. */
+ * 8 tcgen05 GEMM on E4M3 operands, 9 FP8 amax / quantize, 10 key-value cache
+ * (written, read), 11 attention over it. */
 typedef struct {
   uint64_t launches;
   double ms;
@@ -545,8 +630,8 @@ tp_status tp_profile_read(int32_t family, tp_profile_entry* out);
 
 /* ----------------------------------------------------------------- status */
 /* Synchronises `stream`, returns and clears the device status word
- * (TP_OK, TP_ERR_DEVICE_TIMEOUT or TP_ERR_RANGE), or TP_ERR_CUDA if the
- * stream failed. */
+ * (TP_OK, TP_ERR_DEVICE_TIMEOUT, TP_ERR_RANGE or TP_ERR_PAGE), or TP_ERR_CUDA
+ * if the stream failed. */
 tp_status tp_device_status(tp_stream stream);
 const char* tp_status_string(tp_status s);
 /* Failure-path self-test: enqueues one kernel whose single wait (on an

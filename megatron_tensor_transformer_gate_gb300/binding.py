@@ -7,6 +7,7 @@ kernels; there is no fallback — if the library has not been built, ``lib()``
 raises.
 """
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -27,7 +28,7 @@ torch = _Torch()
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtp.so")
 
-F32, BF16, FP8 = 0, 1, 2
+F32, BF16, FP8, F16 = 0, 1, 2, 3   # F16: key-value caches alone
 GELU, SWIGLU = 0, 1
 FUSED, MATERIALISED, OVERLAP, SP = 0, 1, 2, 3
 SCOPE_MLP, SCOPE_ATTN, SCOPE_LAYER = 0, 1, 2
@@ -36,7 +37,8 @@ FP8_FORMS = ("thin", "narrow", "wide")
 
 STATUS = {0: "TP_OK", 1: "TP_ERR_NULL", 2: "TP_ERR_SHAPE", 3: "TP_ERR_DTYPE",
           4: "TP_ERR_WORKSPACE", 5: "TP_ERR_UNSUPPORTED", 6: "TP_ERR_CUDA",
-          7: "TP_ERR_DEVICE_TIMEOUT", 8: "TP_ERR_ARG", 9: "TP_ERR_RANGE"}
+          7: "TP_ERR_DEVICE_TIMEOUT", 8: "TP_ERR_ARG", 9: "TP_ERR_RANGE",
+          10: "TP_ERR_PAGE"}
 
 
 class TPError(RuntimeError):
@@ -95,6 +97,20 @@ class LayerDesc(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_int32) for k in
+                 ("dtype", "b", "n_kv", "d", "page", "table_cols")] +
+                [("pages", ctypes.c_int64),
+                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] +
+                [(k, ctypes.c_int64) for k in
+                 ("page_stride", "token_stride", "head_stride")] +
+                [("ks", ctypes.c_void_p), ("vs", ctypes.c_void_p)] +
+                [(k, ctypes.c_int64) for k in
+                 ("s_page_stride", "s_token_stride", "s_head_stride")] +
+                [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                 ("lens", ctypes.c_void_p)])
+
+
 class ProfileEntry(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_uint64), ("ms", ctypes.c_double),
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
@@ -102,7 +118,7 @@ class ProfileEntry(ctypes.Structure):
 
 KERNEL_FAMILIES = ["gemm_tc", "gemm_simt", "attn_fwd", "attn_bwd_dkdv",
                    "attn_bwd_dq", "reduce", "elementwise", "rmsnorm",
-                   "gemm_tc_fp8", "quantize_fp8"]
+                   "gemm_tc_fp8", "quantize_fp8", "kv_cache", "attn_decode"]
 
 _P = ctypes.c_void_p
 _I64, _I32, _F, _SZ, _U64 = (ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
@@ -110,6 +126,7 @@ _I64, _I32, _F, _SZ, _U64 = (ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
 _MP = ctypes.POINTER(MlpDesc)
 _AP = ctypes.POINTER(AttnDesc)
 _LP = ctypes.POINTER(LayerDesc)
+_CP = ctypes.POINTER(KvCache)
 _U64P = ctypes.POINTER(ctypes.c_uint64)
 
 # name -> (restype, argtypes); mirrors include/tp.h
@@ -155,6 +172,13 @@ SIGNATURES = {
                           [_I32, _P, _I64, _P]),
     "tp_gemm_fp8_block_form": (_I32, [_I64, _I64, _I64, _I32, _I32] +
                                [ctypes.POINTER(_I32)] * 3),
+    "tp_kv_cache_write": (_I32, [_CP, _I32, _I64] + [_P, _I64, _I64] * 2 +
+                          [_P, _P]),
+    "tp_kv_cache_read": (_I32, [_CP, _I32, _I64] + [_P, _I64, _I64] * 2 +
+                         [_P, _P]),
+    "tp_attn_decode_workspace_bytes": (_SZ, [_CP, _I64, _I32]),
+    "tp_attn_decode": (_I32, [_CP, _I32, _I64, _I32, _F] +
+                       [_P, _I64, _I64] * 2 + [_P, _P, _SZ, _P]),
     "tp_mlp_flops": (_I32, [_MP, _U64P, _U64P]),
     "tp_attn_flops": (_I32, [_AP, _U64P, _U64P]),
     "tp_gemm": (_I32, [_I32, _I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _I32,
@@ -544,6 +568,206 @@ def gemm_fp8_block_form(M, N, K, b_group=FP8_BLOCK, sms=0):
                                        *map(ctypes.byref, out)),
           "tp_gemm_fp8_block_form")
     return FP8_FORMS[out[0].value], out[1].value, out[2].value
+
+
+# ------------------------------------------------------- key-value cache --
+# A cache is (k, v, ks, vs): pools k and v [pages, page, n_kv, d] in bf16, fp16
+# or E4M3 codes (float8_e4m3fn or uint8), any strides with adjacent elements of
+# a vector, the same for both; for codes the fp32 scales ks and vs
+# [pages, page, n_kv], else None.  table [b, cols] and lens [b] are int32: the
+# pages of each sequence in order, and how many tokens it has.
+_KV_TYPES = {}   # torch dtype -> tp_dtype, filled when torch is there
+
+
+def _kv_type(t, what):
+    if not _KV_TYPES:
+        _KV_TYPES.update({torch.bfloat16: BF16, torch.float16: F16,
+                          torch.float8_e4m3fn: FP8, torch.uint8: FP8})
+    code = _KV_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: bfloat16, float16 or E4M3 codes, got "
+                        f"{t.dtype}")
+    return code
+
+
+def kv_cache_empty(pages, page, n_kv, d, dtype=BF16, device="cuda"):
+    """Room for a cache of ``pages`` pages of ``page`` tokens: (k, v, ks, vs).
+    A head's tokens of a page are neighbours in memory."""
+    td = {BF16: torch.bfloat16, F16: torch.float16,
+          FP8: torch.float8_e4m3fn}.get(dtype)
+    if td is None:
+        raise TypeError("a cache's dtype: BF16, F16 or FP8")
+
+    def pool(*tail, dt):
+        return torch.empty((pages, n_kv, page) + tail, dtype=dt,
+                           device=device).transpose(1, 2)
+
+    k, v = pool(d, dt=td), pool(d, dt=td)
+    if dtype != FP8:
+        return k, v, None, None
+    return k, v, pool(dt=torch.float32), pool(dt=torch.float32)
+
+
+def _on_device(t, what, dims, dtype, dev):
+    """Refuse a tensor of another rank, type or device."""
+    if t.dim() != dims:
+        raise ValueError(f"{what}: {dims} axes, got {_shape(t)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{what}: {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, not cuda:{dev}")
+
+
+def _kv_cache(cache, table, lens):
+    """(KvCache, device) of a cache with its page table and lengths."""
+    if len(cache) == 2:
+        cache = (*cache, None, None)
+    k, v, ks, vs = cache
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError("k: not on a GPU")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"k is on cuda:{dev}, the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()}")
+    code = _kv_type(k, "k")
+    _on_device(k, "k", 4, None, dev)
+    _on_device(v, "v", 4, k.dtype, dev)
+    pages, page, n_kv, d = k.shape
+    if k.shape != v.shape:
+        raise ValueError(f"v: shape {_shape(k)}, got {_shape(v)}")
+    if k.stride() != v.stride():
+        raise ValueError(f"k and v: the same strides, got {k.stride()} and "
+                         f"{v.stride()}")
+    sp, st, sh, unit = k.stride()
+    if unit != 1 and d != 1:
+        raise ValueError(f"k: adjacent elements of a vector, strides "
+                         f"{k.stride()}")
+    s = (None, None, 0, 0, 0)
+    if code == FP8:
+        if ks is None or vs is None:
+            raise ValueError("ks, vs: codes without scales")
+        for t, what in ((ks, "ks"), (vs, "vs")):
+            _on_device(t, what, 3, torch.float32, dev)
+            if t.shape != (pages, page, n_kv):
+                raise ValueError(f"{what}: shape {(pages, page, n_kv)}, got "
+                                 f"{_shape(t)}")
+        if ks.stride() != vs.stride():
+            raise ValueError(f"ks and vs: the same strides, got {ks.stride()} "
+                             f"and {vs.stride()}")
+        s = (ks.data_ptr(), vs.data_ptr(), *ks.stride())
+    elif ks is not None or vs is not None:
+        raise ValueError("ks, vs: scales of a cache that has none")
+    _on_device(table, "table", 2, torch.int32, dev)
+    _on_device(lens, "lens", 1, torch.int32, dev)
+    b, cols = table.shape
+    if cols > 1 and table.stride(1) != 1:
+        raise ValueError(f"table: columns must be adjacent, strides "
+                         f"{table.stride()}")
+    if lens.shape[0] != b or (b > 1 and lens.stride(0) != 1):
+        raise ValueError(f"lens: {b} adjacent lengths, got {_shape(lens)}, "
+                         f"strides {lens.stride()}")
+    return KvCache(code, b, n_kv, d, page, cols, pages, k.data_ptr(),
+                   v.data_ptr(), sp, st, sh, *s, table.data_ptr(),
+                   table.stride(0), lens.data_ptr()), dev
+
+
+def _kv_rows(t, what, rows, heads, d, dtype, dev):
+    """(address, row stride, head stride) of [rows, heads, d]."""
+    _on_device(t, what, 3, dtype, dev)
+    if t.shape != (rows, heads, d):
+        raise ValueError(f"{what}: shape {(rows, heads, d)}, got {_shape(t)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{what}: adjacent elements of a vector, strides "
+                         f"{t.stride()}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _kv_16bit(t, what):
+    code = _kv_type(t, what)
+    if code == FP8:
+        raise TypeError(f"{what}: bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _kv_move(fn, where, cache, table, lens, k, v, start, stream):
+    c, dev = _kv_cache(cache, table, lens)
+    code, rows = _kv_16bit(k, "k rows"), k.shape[0]
+    args = [_kv_rows(t, what, rows, c.n_kv, c.d, k.dtype, dev)
+            for t, what in ((k, "k rows"), (v, "v rows"))]
+    at = None
+    if start is not None:
+        _on_device(start, "start", 1, torch.int32, dev)
+        if start.shape[0] != c.b + 1 or start.stride(0) != 1:
+            raise ValueError(f"start: {c.b + 1} adjacent rows, got "
+                             f"{_shape(start)}, strides {start.stride()}")
+        at = start.data_ptr()
+    elif rows % c.b:
+        raise ValueError(f"{rows} rows are not the same number for each of "
+                         f"{c.b} sequences: start says which are whose")
+    check(fn(ctypes.byref(c), code, rows, *args[0], *args[1], at,
+             raw_stream(stream, dev)), where)
+
+
+def kv_cache_write(k, v, cache, table, lens, start=None, stream=None):
+    """New tokens' k and v rows ([rows, n_kv, d], bf16 or fp16) into the cache.
+    lens counts them already: they are the last tokens of their sequences, the
+    same number of each, or rows start[i] up to start[i + 1] (int32 [b + 1])
+    those of sequence i.  Rows that would lie in front of a sequence, and rows
+    outside [start[0], start[b]), are not read."""
+    _kv_move(lib().tp_kv_cache_write, "tp_kv_cache_write", cache, table, lens,
+             k, v, start, stream)
+
+
+def kv_cache_read(cache, table, lens, k, v, start=None, stream=None):
+    """What kv_cache_write with the same arguments writes, read back into k and
+    v: the last tokens of each sequence (with start, as many as it says: whole
+    sequences where start adds up lens).  Other rows are left as they were."""
+    _kv_move(lib().tp_kv_cache_read, "tp_kv_cache_read", cache, table, lens,
+             k, v, start, stream)
+
+
+def attn_decode_workspace_bytes(cache, table, lens, rows, n_q):
+    c, _ = _kv_cache(cache, table, lens)
+    return lib().tp_attn_decode_workspace_bytes(ctypes.byref(c), rows, n_q)
+
+
+def attn_decode(q, cache, table, lens, out, lse=None, scale=None, ws=None,
+                stream=None):
+    """out = softmax(scale·q·Kᵀ)·V of the newest tokens over the cache, which
+    holds them already: q and out [b·m, n_q, d] (bf16, or fp16 but over a bf16
+    cache), the last m tokens of each sequence, each seeing its sequence up to
+    itself; a row that sees nothing gives 0.  lse (fp32 [b·m, n_q], optional):
+    log of the sum of e^score, -inf of such a row.  scale: 1/√d.  ws: scratch
+    of attn_decode_workspace_bytes, of this call alone while it runs; made
+    anew where it is None."""
+    c, dev = _kv_cache(cache, table, lens)
+    code = _kv_16bit(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q: 3 axes, got {_shape(q)}")
+    rows, n_q, d = q.shape
+    pq = _kv_rows(q, "q", rows, n_q, c.d, q.dtype, dev)
+    po = _kv_rows(out, "out", rows, n_q, c.d, q.dtype, dev)
+    if code == F16 and c.dtype == BF16:
+        raise TypeError("q: bfloat16 over a bfloat16 cache, got float16")
+    if rows % c.b or n_q % c.n_kv:
+        raise ValueError(f"q: {rows} rows and {n_q} heads for {c.b} sequences "
+                         f"and {c.n_kv} kv heads")
+    pl = None if lse is None else _dense(lse, "lse", torch.float32,
+                                         (rows, n_q), dev)
+    need = lib().tp_attn_decode_workspace_bytes(ctypes.byref(c), rows, n_q)
+    if ws is None and need:
+        with contextlib.nullcontext() if stream is None else \
+                torch.cuda.stream(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    size = 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: contiguous, on cuda:{dev}")
+        size = ws.numel() * ws.element_size()
+    check(lib().tp_attn_decode(
+        ctypes.byref(c), code, rows, n_q,
+        d ** -0.5 if scale is None else scale, *pq, *po, pl, ptr(ws), size,
+        raw_stream(stream, dev)), "tp_attn_decode")
 
 
 def act_memory(b, s, h, h_ffn, n_q, n_kv, d, n, dtype=BF16, act=SWIGLU,

@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libtp.so")
 
 SOURCES = ["api.cu", "gemm_tc.cu", "gemm_simt.cu", "elementwise.cu",
            "attn_fwd_tc.cu", "attn_bwd_tc.cu", "fp8.cu", "fp8_block.cu",
-           "gemm_fp8_block.cu", "gemm_fp8_block_thin.cu", "account.cpp"]
+           "gemm_fp8_block.cu", "gemm_fp8_block_thin.cu", "kv_cache.cu",
+           "attn_decode.cu", "account.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                 "-Xcompiler", "-O3", "-I", INCLUDE]

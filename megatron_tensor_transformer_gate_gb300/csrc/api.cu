@@ -2,11 +2,13 @@
 // and the launch sequence of each block.  Every compute call only enqueues
 // kernels on the caller's stream; nothing here allocates memory.
 #include <algorithm>
+#include <array>
 #include <atomic>
 #include <cfenv>
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "../../include/tp.h"
 #include "attention.h"
@@ -14,6 +16,7 @@
 #include "elementwise.h"
 #include "fp8_block.h"
 #include "gemm.h"
+#include "kv_cache.h"
 #include "profile.h"
 
 #include <vector>
@@ -1162,6 +1165,7 @@ extern "C" tp_status tp_gemm_fp8(int64_t M, int64_t N, int64_t K,
 namespace {
 
 constexpr int64_t kMaxDim = 1 << 30;
+constexpr int64_t kMaxStride = (int64_t)1 << 60;
 
 bool aligned4(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
@@ -1351,6 +1355,191 @@ extern "C" tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
   });
 }
 
+// ------------------------------------------------------- key-value cache --
+namespace {
+
+// Of the vectors of `d` elements at these strides and counts no two overlap.
+bool apart(int64_t d, std::array<std::pair<int64_t, int64_t>, 3> dims) {
+  std::sort(dims.begin(), dims.end());
+  int64_t extent = d;
+  for (const auto& [stride, count] : dims) {
+    if (count == 1) continue;
+    if (stride < extent) return false;
+    if (stride > kMaxStride / count) return false;
+    extent += stride * (count - 1);
+  }
+  return true;
+}
+
+// Strides of an axis that has one place only are not looked at.
+int64_t used(int64_t stride, int64_t count) { return count > 1 ? stride : 0; }
+
+// The descriptor with the strides of single places cleared.
+tp_status check_kv_cache(const tp_kv_cache* d, tp_kv_cache* c) {
+  if (d == nullptr) return TP_ERR_NULL;
+  if (d->dtype != TP_BF16 && d->dtype != TP_F16 && d->dtype != TP_FP8)
+    return TP_ERR_DTYPE;
+  if (d->b < 1 || d->b > 65536 || d->n_kv < 1 || d->n_kv > 1024 ||
+      d->page < 1 || d->page > (1 << 20) || d->table_cols < 1 ||
+      d->pages < 1 || d->pages > INT32_MAX)
+    return TP_ERR_SHAPE;
+  if (d->d != 64 && d->d != 128) return TP_ERR_UNSUPPORTED;
+  const bool fp8 = d->dtype == TP_FP8;
+  if (!d->k || !d->v || !d->table || !d->lens || (fp8 && (!d->ks || !d->vs)))
+    return TP_ERR_NULL;
+  *c = *d;
+  c->page_stride = used(d->page_stride, d->pages);
+  c->token_stride = used(d->token_stride, d->page);
+  c->head_stride = used(d->head_stride, d->n_kv);
+  const int64_t unit = fp8 ? 16 : 8;
+  if (c->page_stride % unit || c->token_stride % unit || c->head_stride % unit)
+    return TP_ERR_SHAPE;
+  if (!apart(d->d, {{{c->page_stride, d->pages},
+                     {c->token_stride, d->page},
+                     {c->head_stride, d->n_kv}}}))
+    return TP_ERR_SHAPE;
+  if (fp8) {
+    c->s_page_stride = used(d->s_page_stride, d->pages);
+    c->s_token_stride = used(d->s_token_stride, d->page);
+    c->s_head_stride = used(d->s_head_stride, d->n_kv);
+    if (!apart(1, {{{c->s_page_stride, d->pages},
+                    {c->s_token_stride, d->page},
+                    {c->s_head_stride, d->n_kv}}}))
+      return TP_ERR_SHAPE;
+    if (!aligned4(d->ks) || !aligned4(d->vs)) return TP_ERR_ARG;
+  }
+  c->table_stride = used(d->table_stride, d->b);
+  if (d->b > 1 && d->table_stride < d->table_cols) return TP_ERR_SHAPE;
+  if (!aligned16(d->k) || !aligned16(d->v) || !aligned4(d->table) ||
+      !aligned4(d->lens))
+    return TP_ERR_ARG;
+  return TP_OK;
+}
+
+// Rows [rows, heads, d] of a 16-bit type: vectors on 16 bytes, those that are
+// written apart from each other.
+tp_status check_rows(int64_t rows, int64_t heads, int64_t d, const void* p,
+                     int64_t row, int64_t head, bool written,
+                     int64_t* row_used, int64_t* head_used) {
+  if (p == nullptr) return TP_ERR_NULL;
+  *row_used = used(row, rows);
+  *head_used = used(head, heads);
+  if (*row_used % 8 || *head_used % 8 || *row_used < 0 || *head_used < 0 ||
+      *row_used > kMaxStride / rows || *head_used > kMaxStride / heads)
+    return TP_ERR_SHAPE;
+  if (written &&
+      !apart(d, {{{*row_used, rows}, {*head_used, heads}, {0, 1}}}))
+    return TP_ERR_SHAPE;
+  return aligned16(p) ? TP_OK : TP_ERR_ARG;
+}
+
+tp_status check_kv_rows(const tp_kv_cache* d, int32_t dtype, int64_t rows,
+                        const void* K, int64_t k_row, int64_t k_head,
+                        const void* V, int64_t v_row, int64_t v_head,
+                        const int32_t* start, bool written, tp_kv_cache* c,
+                        KvRows* r) {
+  tp_status rc = check_kv_cache(d, c);
+  if (rc != TP_OK) return rc;
+  if (dtype != TP_BF16 && dtype != TP_F16) return TP_ERR_DTYPE;
+  if (rows < 1 || rows > kMaxDim || rows * c->n_kv > ((int64_t)1 << 32))
+    return TP_ERR_SHAPE;
+  if (start == nullptr && rows % c->b) return TP_ERR_SHAPE;
+  if (!aligned4(start)) return TP_ERR_ARG;
+  r->rows = rows;
+  r->k = const_cast<void*>(K);
+  r->v = const_cast<void*>(V);
+  r->start = start;
+  rc = check_rows(rows, c->n_kv, c->d, K, k_row, k_head, written, &r->k_row,
+                  &r->k_head);
+  if (rc != TP_OK) return rc;
+  return check_rows(rows, c->n_kv, c->d, V, v_row, v_head, written, &r->v_row,
+                    &r->v_head);
+}
+
+bool decode_shape(const tp_kv_cache* c, int64_t rows, int32_t n_q) {
+  return rows >= 1 && rows % c->b == 0 && n_q >= 1 && n_q <= (1 << 16) &&
+         n_q % c->n_kv == 0 && rows <= INT32_MAX / n_q;
+}
+
+}  // namespace
+
+extern "C" tp_status tp_kv_cache_write(const tp_kv_cache* d, int32_t dtype,
+                                       int64_t rows, const void* K,
+                                       int64_t k_row, int64_t k_head,
+                                       const void* V, int64_t v_row,
+                                       int64_t v_head, const int32_t* start,
+                                       tp_stream stream) {
+  return guarded([&]() -> tp_status {
+    tp_kv_cache c;
+    KvRows r;
+    const tp_status rc = check_kv_rows(d, dtype, rows, K, k_row, k_head, V,
+                                       v_row, v_head, start, false, &c, &r);
+    if (rc != TP_OK) return rc;
+    return cuda_status(
+        kv_cache_write(c, dtype, r, device_status_ptr(), stream));
+  });
+}
+
+extern "C" tp_status tp_kv_cache_read(const tp_kv_cache* d, int32_t dtype,
+                                      int64_t rows, void* K, int64_t k_row,
+                                      int64_t k_head, void* V, int64_t v_row,
+                                      int64_t v_head, const int32_t* start,
+                                      tp_stream stream) {
+  return guarded([&]() -> tp_status {
+    tp_kv_cache c;
+    KvRows r;
+    const tp_status rc = check_kv_rows(d, dtype, rows, K, k_row, k_head, V,
+                                       v_row, v_head, start, true, &c, &r);
+    if (rc != TP_OK) return rc;
+    return cuda_status(
+        kv_cache_read(c, dtype, r, device_status_ptr(), stream));
+  });
+}
+
+extern "C" size_t tp_attn_decode_workspace_bytes(const tp_kv_cache* c,
+                                                 int64_t rows, int32_t n_q) {
+  if (c == nullptr || c->b < 1 || c->n_kv < 1 || !decode_shape(c, rows, n_q))
+    return 0;
+  return attn_decode_ws_bytes(*c, rows, n_q);
+}
+
+extern "C" tp_status tp_attn_decode(const tp_kv_cache* d, int32_t dtype,
+                                    int64_t rows, int32_t n_q, float scale,
+                                    const void* q, int64_t q_row,
+                                    int64_t q_head, void* out, int64_t o_row,
+                                    int64_t o_head, float* lse, void* ws,
+                                    size_t ws_bytes, tp_stream stream) {
+  return guarded([&]() -> tp_status {
+    tp_kv_cache c;
+    tp_status rc = check_kv_cache(d, &c);
+    if (rc != TP_OK) return rc;
+    if (dtype != TP_BF16 && dtype != TP_F16) return TP_ERR_DTYPE;
+    if (dtype == TP_F16 && c.dtype == TP_BF16) return TP_ERR_UNSUPPORTED;
+    if (!decode_shape(&c, rows, n_q)) return TP_ERR_SHAPE;
+    if (!std::isfinite(scale)) return TP_ERR_ARG;
+    DecodeArgs a;
+    a.rows = rows;
+    a.n_q = n_q;
+    a.scale = scale;
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.ws = ws;
+    rc = check_rows(rows, n_q, c.d, q, q_row, q_head, false, &a.q_row,
+                    &a.q_head);
+    if (rc != TP_OK) return rc;
+    rc = check_rows(rows, n_q, c.d, out, o_row, o_head, true, &a.o_row,
+                    &a.o_head);
+    if (rc != TP_OK) return rc;
+    if (!aligned4(lse) || !aligned16(ws)) return TP_ERR_ARG;
+    const size_t need = attn_decode_ws_bytes(c, rows, n_q);
+    if (need > 0 && ws == nullptr) return TP_ERR_NULL;
+    if (ws_bytes < need) return TP_ERR_WORKSPACE;
+    return cuda_status(
+        attn_decode(c, dtype, a, device_status_ptr(), stream));
+  });
+}
+
 // ------------------------------------------------------------- profiling --
 extern "C" tp_status tp_profile_enable(int32_t max_launches) {
   return guarded([&]() -> tp_status {
@@ -1414,7 +1603,9 @@ extern "C" tp_status tp_device_status(tp_stream stream) {
     if (cudaMemcpy(p, zero, sizeof(zero), cudaMemcpyHostToDevice) !=
         cudaSuccess)
       return TP_ERR_CUDA;
-    return h[0] == kDevRange ? TP_ERR_RANGE : TP_ERR_DEVICE_TIMEOUT;
+    return h[0] == kDevRange  ? TP_ERR_RANGE
+           : h[0] == kDevPage ? TP_ERR_PAGE
+                              : TP_ERR_DEVICE_TIMEOUT;
   }
   return TP_OK;
 }
@@ -1430,7 +1621,8 @@ extern "C" const char* tp_status_string(tp_status s) {
     case TP_ERR_CUDA: return "CUDA call failed";
     case TP_ERR_DEVICE_TIMEOUT: return "a bounded device wait timed out";
     case TP_ERR_ARG: return "misaligned pointer or bad argument";
-    case TP_ERR_RANGE: return "an attention-core operand exceeded the fp16 range";
+    case TP_ERR_RANGE: return "a value exceeded the fp16 range";
+    case TP_ERR_PAGE: return "a page or a length is outside the cache";
   }
   return "unknown status";
 }

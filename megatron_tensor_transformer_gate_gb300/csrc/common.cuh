@@ -17,7 +17,12 @@ namespace tp {
 // ----------------------------------------------------------------- status --
 // Device status word layout: [0] = first error code (0 = none), [1] = site id
 // of the wait that ran out, [2] = block id.  Written once (first error wins).
-enum DeviceError : unsigned { kDevOk = 0, kDevTimeout = 7, kDevRange = 9 };
+enum DeviceError : unsigned {
+  kDevOk = 0,
+  kDevTimeout = 7,
+  kDevRange = 9,
+  kDevPage = 10
+};
 
 // About two seconds at the GB300's 2.07 GHz maximum SM clock.
 constexpr long long kWaitTimeoutCycles = 4LL << 30;

@@ -21,7 +21,9 @@ enum KernelFamily : int {
   KF_NORM = 7,
   KF_GEMM_TC_FP8 = 8,
   KF_QUANT = 9,
-  KF_COUNT = 10
+  KF_KV_CACHE = 10,
+  KF_ATTN_DECODE = 11,
+  KF_COUNT = 12
 };
 
 // RAII bracket around one kernel launch.
