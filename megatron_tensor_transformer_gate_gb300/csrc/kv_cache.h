@@ -35,6 +35,7 @@ struct DecodeArgs {
   int64_t o_row, o_head;
   float* lse;
   void* ws;
+  int bf16 = 0;   // q and out, else fp16 (set by attn_decode)
 };
 size_t attn_decode_ws_bytes(const tp_kv_cache& c, int64_t rows, int n_q);
 int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,

@@ -146,6 +146,45 @@ def test_a_nan_among_the_tokens_stays_in_its_heads(tp):
     assert torch.equal(torch.isnan(lse).cpu(), bad)
 
 
+@pytest.mark.parametrize("lens", [[40, 0], [900, 3]])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
+def test_queries_that_are_nan(tp, kind, lens):
+    c = Cache(lens, 16, 2, 64, kind, 92)
+    _, q = queries(c, 2, 4, BF16, 9)
+    q[:, 1] = float("nan")
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    out, lse = out.cpu(), lse.cpu()
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    assert not torch.isnan(out[:, [0, 2, 3]]).any()
+    assert not torch.isnan(lse[:, [0, 2, 3]]).any()
+    if lens[1] == 0:
+        assert not out[1].any() and torch.isneginf(lse[1]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
+def test_a_nan_in_a_token_that_a_row_does_not_see(tp, kind):
+    # the third of four new tokens has NaN keys and values
+    c = Cache([50, 6], 16, 1, 128, kind, 93)
+    x, q = queries(c, 8, 8, BF16, 9)
+    clean, _ = attend(tp, c, q)
+    for i, n in enumerate(c.lens):
+        at = int(c.table[i][(n - 2) // 16]), (n - 2) % 16
+        for t in c.cache[:2]:
+            if kind == "e4m3":
+                t.view(torch.uint8)[at] = 0x7f
+            else:
+                t[at] = float("nan")
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    for i in range(2):
+        rows = slice(4 * i, 4 * i + 2)
+        assert torch.equal(out[rows], clean[rows])
+        assert torch.isfinite(lse[rows]).all()
+        rows = slice(4 * i + 2, 4 * i + 4)
+        assert torch.isnan(out[rows]).all() and torch.isnan(lse[rows]).all()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_pages_outside_the_pool(tp, kind):
     # their tokens are left out, everything else is as if they were not there
