@@ -545,7 +545,8 @@ typedef struct {
   int32_t b;             /* sequences (1 to 65536) */
   int32_t n_kv, d;       /* heads (1 to 1024) and their size, 64 or 128 */
   int32_t page;          /* tokens a page (1 to 2^20) */
-  int32_t table_cols;    /* pages that a row of the table can list (≥ 1) */
+  int32_t table_cols;    /* pages that a row of the table can list (≥ 1; no
+                          * more than 2^30 tokens) */
   int64_t pages;         /* pages in a pool */
   void *k, *v;
   int64_t page_stride, token_stride, head_stride;        /* elements */

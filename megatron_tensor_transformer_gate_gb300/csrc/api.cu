@@ -1381,7 +1381,8 @@ tp_status check_kv_cache(const tp_kv_cache* d, tp_kv_cache* c) {
     return TP_ERR_DTYPE;
   if (d->b < 1 || d->b > 65536 || d->n_kv < 1 || d->n_kv > 1024 ||
       d->page < 1 || d->page > (1 << 20) || d->table_cols < 1 ||
-      d->pages < 1 || d->pages > INT32_MAX)
+      d->pages < 1 || d->pages > INT32_MAX ||
+      d->table_cols > kMaxDim / d->page)   // tokens that the table can list
     return TP_ERR_SHAPE;
   if (d->d != 64 && d->d != 128) return TP_ERR_UNSUPPORTED;
   const bool fp8 = d->dtype == TP_FP8;

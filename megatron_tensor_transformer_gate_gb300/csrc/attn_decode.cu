@@ -33,6 +33,7 @@
 // M of its own, so that scales of any size keep the weights in fp16's range.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -44,12 +45,9 @@
 namespace tp {
 namespace {
 
-constexpr int WARPS = 4;
-constexpr int THREADS = 32 * WARPS;
-constexpr int CTAS = 2;               // on an SM
-constexpr int STEP = 16;              // tokens of a warp at a time
-constexpr int BLOCK = STEP * WARPS;   // tokens of a CTA at a time
-constexpr int MIN_BLOCKS = 2;         // of a CTA, where there is little to do
+constexpr int UNIT_TOKENS = 256;   // a segment's fixed cost, in tokens of work
+constexpr int MAX_CTAS = 4;        // on an SM
+constexpr int MIN_SLOTS = 3;       // of a CTA, where there is little to do
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -77,15 +75,23 @@ struct Conf {
   static constexpr int SIZE = CACHE == TP_FP8 ? 1 : 2;
   static constexpr int ROW = D * SIZE;             // bytes
   static constexpr int ROWS = 8 * NT;
+  static constexpr int WARPS = 4;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int CTAS = 2;                   // on an SM
+  static constexpr int STEP = ROW == 256 || NT == 4 ? 16 : 32;   // tokens of a warp at a time
+  static constexpr int BLOCK = STEP * WARPS;       // of a CTA
+  static constexpr int EXTRA = (UNIT_TOKENS + BLOCK - 1) / BLOCK;
   static constexpr int TILE = STEP * ROW;
-  // K, V, the scales and the valid tokens of a step
-  static constexpr int STAGE = 2 * TILE + (CACHE == TP_FP8 ? 128 : 0);
-  static constexpr int STAGES = ROW == 256 ? 3 : ROW == 128 ? 6 : 8;
+  // K, V and the scales of a step
+  static constexpr int STAGE = 2 * TILE + (CACHE == TP_FP8 ? 8 * STEP : 0);
+  static constexpr int STAGES = STEP * ROW >= 4096 ? 3 : 5;
   static constexpr int RING = STAGES * STAGE;
-  static constexpr int JOIN = ROWS * (D + 4) * 4;  // of a warp, over its ring
-  static constexpr int SMEM = WARPS * (RING > JOIN ? RING : JOIN);
   static constexpr bool QREG = NT < 4;             // Q in registers
+  static constexpr int JOIN = (WARPS / 2) * 8 * (D + 4) * 4;
   static constexpr int QSMEM = QREG ? 0 : ROWS * D * 2;
+  static constexpr int ALIGN = 256;
+  static constexpr int SMEM =
+      WARPS * RING + (JOIN > QSMEM ? JOIN : QSMEM) + ALIGN;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src,
@@ -133,14 +139,13 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4],
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two E4M3 codes (the lower 16 bits) as fp16.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t u) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
-      : "=r"(y)
+// Four E4M3 codes as two pairs of fp16.
+__device__ __forceinline__ void codes_f16(uint32_t u, uint32_t& lo,
+                                          uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(u));
-  return y;
 }
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
@@ -149,45 +154,60 @@ __device__ __forceinline__ float lg2_approx(float x) {
 }
 
 // Byte offset of 16-byte chunk ch of row r in a tile, spread so that eight
-// rows' same chunk lie in different banks.
+// rows' same chunk lie in different banks.  Rows lie on multiples of their
+// size, so chunk ch ^ x lies at that of ch with 16·x flipped in.
 template <int ROW>
 __device__ __forceinline__ uint32_t spread(int r, int ch) {
   return ROW >= 128 ? r * ROW + ((ch ^ (r & 7)) << 4)
                     : r * ROW + ((ch ^ ((r >> 1) & 3)) << 4);
 }
 
-// A sequence's tokens that are followed, and the blocks they take (at least
-// one, so that a sequence without any has its rows written too).
+// A sequence's tokens that are followed.
 __device__ __forceinline__ int tokens_of(const tp_kv_cache& c, int seq) {
   const int64_t cap = (int64_t)c.table_cols * c.page;
   const int n = c.lens[seq];
   return n < 0 ? 0 : n > cap ? (int)cap : n;
 }
+// The blocks they take (at least one, so that a sequence without any has its
+// rows written too).
+template <int BLOCK>
 __device__ __forceinline__ int blocks_of(int n) {
   return n <= BLOCK ? 1 : (n - 1) / BLOCK + 1;
 }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b;
+}
 
-// The pages of a warp's next tokens: lane l holds table entries base + l and
-// base + 32 + l of a sequence, the second ones read ahead.
+// Elements e … e + 3 of a row's head.
+__device__ __forceinline__ void store4(const DecodeArgs& a, int64_t row,
+                                       int head, int e, float4 v) {
+  uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.o_row +
+                  head * a.o_head + e;
+  *reinterpret_cast<uint2*>(dst) =
+      a.bf16 ? make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w))
+             : make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+}
+
+// The pages of a warp's next tokens: lane l holds entries base + l and
+// base + 32 + l of a table row, the second ones read ahead.
 struct Pages {
-  const int32_t* row;
   int base, end, cur, next;   // entries from `end` on are not read
-  __device__ __forceinline__ int get(int col) const {
+  __device__ __forceinline__ int get(const int32_t* row, int col) const {
     return col < end ? row[col] : -1;
   }
-  __device__ __forceinline__ void start(const int32_t* r, int first, int last,
-                                        int lane) {
-    row = r;
+  __device__ __forceinline__ void start(const int32_t* row, int first,
+                                        int last, int lane) {
     base = first;
     end = last;
-    cur = get(base + lane);
-    next = get(base + 32 + lane);
+    cur = get(row, base + lane);
+    next = get(row, base + 32 + lane);
   }
-  __device__ __forceinline__ void move_to(int col, int lane) {
+  __device__ __forceinline__ void move_to(const int32_t* row, int col,
+                                          int lane) {
     while (col >= base + 32) {
       base += 32;
       cur = next;
-      next = get(base + 32 + lane);
+      next = get(row, base + 32 + lane);
     }
   }
   __device__ __forceinline__ int at(int col) const {   // base ≤ col < base + 64
@@ -197,33 +217,95 @@ struct Pages {
   }
 };
 
+template <bool FIRST, class A, class B>
+__device__ __forceinline__ auto& pick(A& a, B& b) {
+  if constexpr (FIRST)
+    return a;
+  else
+    return b;
+}
+
+// A segment: blocks [blk0, blk1) of a unit.  Units take nb + EXTRA slots of
+// the CTAs' pieces, so that many short ones weigh what they cost; the blocks
+// lie behind the extra ones.
+struct Segment {
+  int seq, kvh, tile;
+  int len, n;            // the sequence's tokens, those that are followed
+  int nb, blk0, blk1;
+  int64_t first;         // slot of the unit's first block
+  int there;             // 0: the piece ended before
+};
+
+// Walks a CTA's piece, slots [at, stop) of all.
+template <class C>
+struct Walk {
+  int64_t at, stop, before;   // before: slots in front of the sequence
+  int seq, per_seq;           // units of a sequence
+
+  // The next segment with blocks of the piece.
+  __device__ __forceinline__ void next(const Params& p, Segment* s) {
+    s->there = 1;
+    while (at < stop) {
+      s->len = max(p.c.lens[seq], 0);
+      s->n = tokens_of(p.c, seq);
+      s->nb = blocks_of<C::BLOCK>(s->n);
+      const int w = s->nb + C::EXTRA;
+      const int64_t in_seq = at - before;
+      const int unit = (int)quotient(in_seq, w);
+      const int x0 = (int)(in_seq - (int64_t)unit * w);
+      const int x1 = (int)min((int64_t)w, x0 + (stop - at));
+      s->seq = seq;
+      s->kvh = unit / p.tiles;
+      s->tile = unit - s->kvh * p.tiles;
+      s->first = before + (int64_t)unit * w + C::EXTRA;
+      s->blk0 = max(0, x0 - C::EXTRA);
+      s->blk1 = max(0, x1 - C::EXTRA);
+      at += x1 - x0;
+      if (unit == per_seq - 1 && x1 == w) {
+        before += (int64_t)w * per_seq;
+        ++seq;
+      }
+      if (s->blk1 > s->blk0) return;
+    }
+    s->there = 0;
+  }
+};
+
 template <int CACHE, int D, int NT>
-__global__ void __launch_bounds__(THREADS, CTAS)
+__global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
+                                  Conf<CACHE, D, NT>::CTAS)
     decode_kernel(const Params p) {
   using C = Conf<CACHE, D, NT>;
   constexpr bool FP8 = CACHE == TP_FP8, BF = CACHE == TP_BF16;
+  constexpr int WARPS = C::WARPS, THREADS = C::THREADS, STAGES = C::STAGES;
+  constexpr int STEP = C::STEP, BLOCK = C::BLOCK, MT = STEP / 16;
   constexpr int KS = D / 16;          // steps of 16 elements
   constexpr int ROW = C::ROW, CHUNKS = ROW / 16;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ unsigned char smem_raw[];
   __shared__ int64_t sum_of[WARPS];
-  __shared__ int64_t s_before;
-  __shared__ int s_seq;
-  __shared__ uint32_t valid_of[WARPS][C::STAGES];
+  __shared__ Walk<C> s_walk;
+  __shared__ Segment segs[3];   // the one computed, the next, the one after it
+  __shared__ uint32_t valid_of[WARPS][STAGES];
+  __shared__ float s_qf[C::ROWS];
   __shared__ float s_m[WARPS][C::ROWS], s_top[WARPS][C::ROWS],
       s_l[WARPS][C::ROWS];
   const tp_kv_cache& c = p.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int per_block = c.n_kv * p.tiles;   // units of a sequence
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's piece: blocks [at, stop) of all, and where `at` lies
-  int64_t at, stop;
-  int64_t total;
+  // ---- this CTA's piece of all slots, and the sequence in which it begins
+  const int units = c.n_kv * p.tiles;   // of a sequence
+  int64_t total, ctas;
   {
     const int span = (c.b + THREADS - 1) / THREADS;
     const int i0 = min(tid * span, c.b), i1 = min(i0 + span, c.b);
+    auto slots = [&](int i) -> int64_t {
+      return (int64_t)(blocks_of<BLOCK>(tokens_of(c, i)) + C::EXTRA) *
+             units;
+    };
     int64_t sum = 0;
-    for (int i = i0; i < i1; ++i) sum += blocks_of(tokens_of(c, i));
+    for (int i = i0; i < i1; ++i) sum += slots(i);
     int64_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -231,6 +313,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       if (lane >= o) inc += v;
     }
     if (lane == 31) sum_of[warp] = inc;
+    if (tid == 0) p.cuts[blockIdx.x].tile = -1;
     __syncthreads();
     int64_t before = inc - sum;
     total = 0;
@@ -239,60 +322,189 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       if (w < warp) before += sum_of[w];
       total += sum_of[w];
     }
-    total *= per_block;
-    const int64_t most = (total + MIN_BLOCKS - 1) / MIN_BLOCKS;
-    const int64_t ctas = most < gridDim.x ? most : gridDim.x;
-    if (blockIdx.x >= ctas) {
-      if (tid == 0) p.cuts[blockIdx.x].tile = -1;
-      return;
-    }
-    at = total * blockIdx.x / ctas;
-    stop = total * (blockIdx.x + 1) / ctas;
-    before *= per_block;
-    sum *= per_block;
+    ctas = min((total + MIN_SLOTS - 1) / MIN_SLOTS, (int64_t)gridDim.x);
+    if (blockIdx.x >= ctas) return;
+    const int64_t at = quotient(total * blockIdx.x, ctas);
     if (before <= at && at < before + sum) {   // one thread
       int i = i0;
       for (;; ++i) {
-        const int64_t w = (int64_t)blocks_of(tokens_of(c, i)) * per_block;
+        const int64_t w = slots(i);
         if (at < before + w) break;
         before += w;
       }
-      s_seq = i;
-      s_before = before;
+      s_walk.at = at;
+      s_walk.stop = quotient(total * (blockIdx.x + 1), ctas);
+      s_walk.before = before;
+      s_walk.seq = i;
+      s_walk.per_seq = units;
+      s_walk.next(p, &segs[0]);
+      s_walk.next(p, &segs[1]);
     }
     __syncthreads();
-    if (tid == 0) p.cuts[blockIdx.x].tile = -1;
   }
-  const int64_t begin = at;
-  int seq = s_seq;
-  int64_t before = s_before;   // blocks in front of the sequence
+  if (!segs[0].there) return;
 
-  const uint32_t ring = smem_u32(smem) + warp * C::RING;
-  unsigned char* const q_smem =
-      smem + WARPS * (C::RING > C::JOIN ? C::RING : C::JOIN);
   const float scale = p.a.scale * LOG2E;
   const char* const kpool = static_cast<const char*>(c.k);
   const int64_t to_v = static_cast<const char*>(c.v) - kpool;
   const bool whole_pages = c.page % STEP == 0;
+  const int skip_cols = BLOCK / c.page, skip_off = BLOCK % c.page;
+  unsigned char* const smem =
+      smem_raw + (-smem_u32(smem_raw) & (C::ALIGN - 1));
+  float* const join = reinterpret_cast<float*>(smem + WARPS * C::RING);
+  unsigned char* const ring = smem + warp * C::RING;
+  constexpr int LANES = CHUNKS, PER = 32 / LANES;   // of a row, rows a copy
+  const int sub = lane / LANES, ch = lane % LANES;
+  const int64_t row_bytes = c.token_stride * C::SIZE;
 
-  while (at < stop) {
-    // ---- the segment: blocks [blk0, blk1) of a unit
-    const int len = max(c.lens[seq], 0);
-    const int n = tokens_of(c, seq);
-    const int nb = blocks_of(n);
-    const int unit = (int)((at - before) / nb);
-    const int blk0 = (int)((at - before) - (int64_t)unit * nb);
-    const int blk1 = (int)min((int64_t)nb, blk0 + (stop - at));
-    const int kvh = unit / p.tiles, tile = unit - kvh * p.tiles;
-    const int row0 = tile * C::ROWS, rows = p.per_seq * p.group;
-    const int64_t qrow = (int64_t)seq * p.per_seq;
+  // ---- loads: the warp's steps of a segment, and of the one after it
+  struct Load {
+    int left;              // steps that are still to be issued
+    int t0, col, off;      // the next one's first token and its place
+  };
+  Load now = {};
+  Pages pages, pages2;     // of `now`, and of the segment after the computed
+  int cs = 0, ls = 0;      // the segments that are computed and loaded
+  auto row_of = [&](const Segment& s) {
+    return c.table + (int64_t)s.seq * c.table_stride;
+  };
+  auto plan = [&](const Segment& s) {
+    Load l = {};
+    if (!s.there) return l;   // nothing else of it is set
+    l.t0 = s.blk0 * BLOCK + warp * STEP;
+    const int end = min(s.n, s.blk1 * BLOCK) - 1;   // the last token
+    l.left = l.t0 <= end ? (end - l.t0) / BLOCK + 1 : 0;
+    l.col = l.t0 / c.page;
+    l.off = l.t0 - l.col * c.page;
+    return l;
+  };
+  auto read_pages = [&](const Segment& s, Pages& pg) {
+    const Load l = plan(s);
+    if (l.left > 0)
+      pg.start(row_of(s), l.col, (min(s.n, s.blk1 * BLOCK) - 1) / c.page + 1,
+               lane);
+    else
+      pg = Pages{0, 0, -1, -1};
+  };
+  int issued = 0, slot = 0;   // steps, and the ring's place of the next one
+  auto issue = [&]() {
+    const uint32_t dst = smem_u32(ring) + slot * C::STAGE;
+    const Segment& sg = segs[ls];
+    pages.move_to(row_of(sg), now.col, lane);
+    const int rest = sg.n - now.t0;   // ≥ 1
+    const int kvh = sg.kvh;
+    const int tok = lane % STEP;
+    uint32_t valid;
+    const char* src;
+    int64_t place = 0;
+    int page, off;   // of the lane's token
+    if (whole_pages) {
+      page = pages.at(now.col);
+      off = now.off + tok;
+      if (page < 0 || page >= c.pages) {
+        record_error(p.status, kDevPage, 44);
+        valid = 0;
+      } else {
+        valid = rest >= STEP ? 0xffffffffu >> (32 - STEP) : (1u << rest) - 1u;
+      }
+      src = kpool + ((page * c.page_stride + (now.off + sub) * c.token_stride +
+                      kvh * c.head_stride) *
+                         C::SIZE +
+                     16 * ch);
+    } else {
+      bool in = tok < rest;
+      const int ahead = in ? (now.off + tok) / c.page : 0;
+      page = pages.at(now.col + ahead);
+      off = now.off + tok - ahead * c.page;
+      if (in && (page < 0 || page >= c.pages)) {
+        in = false;
+        record_error(p.status, kDevPage, 44);
+      }
+      valid = __ballot_sync(0xffffffffu, in) & (0xffffffffu >> (32 - STEP));
+      place = (page * c.page_stride + off * c.token_stride +
+               kvh * c.head_stride) *
+                  C::SIZE +
+              reinterpret_cast<int64_t>(kpool);
+      src = nullptr;
+    }
+    if (FP8) {   // 16 tokens: scales of K in half of the lanes, V in the other
+      const bool in = (valid >> tok) & 1;
+      const int64_t at = in ? page * c.s_page_stride + off * c.s_token_stride +
+                                  kvh * c.s_head_stride
+                            : 0;
+      float* d = reinterpret_cast<float*>(ring + slot * C::STAGE + 2 * C::TILE);
+      if (STEP == 16) {
+        cp_async4(d + lane, (lane < 16 ? c.ks : c.vs) + at, in);
+      } else {
+        cp_async4(d + lane, c.ks + at, in);
+        cp_async4(d + STEP + lane, c.vs + at, in);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < STEP / PER; ++k) {
+      const int r = k * PER + sub;
+      const bool in = (valid >> r) & 1;
+      const char* s = src;
+      if (!whole_pages)
+        s = reinterpret_cast<const char*>(
+                __shfl_sync(0xffffffffu, place, r)) +
+            16 * ch;
+      else
+        src += PER * row_bytes;
+      if (!in) s = kpool;   // nothing is read
+      const uint32_t d = dst + spread<ROW>(r, ch);
+      cp_async16(d, s, in);
+      cp_async16(d + C::TILE, s + to_v, in);
+    }
+    cp_async_commit();
+    if (lane == 0) valid_of[warp][slot] = valid;
+    if (++slot == STAGES) slot = 0;
+    ++issued;
+    --now.left;
+    now.t0 += BLOCK;
+    now.col += skip_cols;
+    now.off += skip_off;
+    if (now.off >= c.page) {
+      now.off -= c.page;
+      ++now.col;
+    }
+  };
+
+  read_pages(segs[0], pages);
+  read_pages(segs[1], pages2);
+  now = plan(segs[0]);
+  int done = 0, stage = 0;   // steps that are computed, the next one's place
+  bool first_segment = true;
+  // Issues what there is until the ring is full; the slot of the step before
+  // `done` is free.
+  auto fill = [&]() {
+    while (issued < done + STAGES) {
+      if (now.left == 0) {
+        if (ls != cs) break;   // no further than one segment ahead
+        const int to = cs == 2 ? 0 : cs + 1;
+        const Load l = plan(segs[to]);
+        if (l.left == 0) break;
+        now = l;
+        pages = pages2;
+        ls = to;
+      }
+      issue();
+    }
+  };
+
+  for (;;) {
+    fill();
+    const Segment& seg = segs[cs];
+    if (tid == 32) s_walk.next(p, &segs[cs == 0 ? 2 : cs - 1]);
+    const int row0 = seg.tile * C::ROWS, rows = p.per_seq * p.group;
+    const int len = seg.len, n = seg.n;
+    const int64_t qrow = (int64_t)seg.seq * p.per_seq;
     if (len > n && tid == 0) record_error(p.status, kDevPage, 43);
 
     // ---- Q: lane (g, t) holds elements of row 8·nt + g as the products take
     // them (over codes, four neighbours of a step instead of two and two)
     uint32_t q[C::QREG ? NT : 1][KS][2];
-    float qf[NT][2];      // scale of the lane's rows 8·nt + 2·t4 (+ 1)
-    int lim[NT][2];       // tokens that they see
+    float qf[C::QREG ? NT : 1][2];   // scale of rows 8·nt + 2·t4 (+ 1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + 8 * nt + g;
@@ -300,7 +512,8 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       const int j = there ? r / p.group : 0;
       const uint16_t* src =
           static_cast<const uint16_t*>(p.a.q) + (qrow + j) * p.a.q_row +
-          (there ? (int64_t)(kvh * p.group + r - j * p.group) * p.a.q_head : 0);
+          (there ? (int64_t)(seg.kvh * p.group + r - j * p.group) * p.a.q_head
+                 : 0);
       uint32_t u[KS][2];
       float amax = 0.0f;
 #pragma unroll
@@ -311,13 +524,15 @@ __global__ void __launch_bounds__(THREADS, CTAS)
       }
       float f = 1.0f;
       if (!BF) {
-        float2 x[KS][2];
+        auto pair = [&](uint32_t x) {
+          return p.a.bf16 ? unpack_bf16x2(x) : unpack_f16x2(x);
+        };
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            x[s][h] = p.a.bf16 ? unpack_bf16x2(u[s][h]) : unpack_f16x2(u[s][h]);
-            amax = fmaxf(amax, fmaxf(fabsf(x[s][h].x), fabsf(x[s][h].y)));
+            const float2 x = pair(u[s][h]);
+            amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
           }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -332,100 +547,33 @@ __global__ void __launch_bounds__(THREADS, CTAS)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            u[s][h] = pack_f16x2(x[s][h].x * down, x[s][h].y * down);
+          for (int h = 0; h < 2; ++h) {
+            const float2 x = pair(u[s][h]);
+            u[s][h] = pack_f16x2(x.x * down, x.y * down);
+          }
       }
       f *= scale;
-      qf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
-      qf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rr = row0 + 8 * nt + 2 * t4 + h;
-        lim[nt][h] = rr < rows
-                         ? min(n, len - p.per_seq + 1 + rr / p.group)
-                         : n;
-      }
       if constexpr (C::QREG) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           q[nt][s][0] = u[s][0];
           q[nt][s][1] = u[s][1];
         }
-      } else if (warp == 0) {   // [nt][s][lane] pairs of registers
+        qf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
+        qf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+      } else if (nt % WARPS == warp) {   // [nt][s][lane] pairs of registers
+        if (t4 == 0) s_qf[8 * nt + g] = f;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-          reinterpret_cast<uint2*>(q_smem)[(nt * KS + s) * 32 + lane] =
+          reinterpret_cast<uint2*>(join)[(nt * KS + s) * 32 + lane] =
               make_uint2(u[s][0], u[s][1]);
       }
     }
     if constexpr (!C::QREG) __syncthreads();
 
-    // ---- the warp's steps: 16 tokens from 64·blk + 16·warp on
-    const int first = blk0 * BLOCK + warp * STEP;
-    const int steps =
-        first < n ? min(blk1 - blk0, (n - 1 - first) / BLOCK + 1) : 0;
-    const int64_t head_at = (int64_t)kvh * c.head_stride * C::SIZE;
-    Pages pg;
-    pg.start(c.table + (int64_t)seq * c.table_stride,
-             steps > 0 ? first / c.page : 0, n > 0 ? (n - 1) / c.page + 1 : 0,
-             lane);
-    auto issue = [&](int i, int stage) {
-      const int t0 = first + i * BLOCK;
-      const uint32_t dst = ring + stage * C::STAGE;
-      // lane r < 16: the place of token t0 + r
-      const int tok = t0 + (lane & 15);
-      bool in = tok < n;
-      int64_t page;
-      int off;
-      if (whole_pages) {
-        const int col = t0 / c.page;
-        pg.move_to(col, lane);
-        page = pg.at(col);
-        off = tok - col * c.page;
-      } else {
-        const int col0 = t0 / c.page;
-        pg.move_to(col0, lane);
-        const int col = (in ? tok : t0) / c.page;
-        page = pg.at(col);
-        off = tok - col * c.page;
-      }
-      if (in && (page < 0 || page >= c.pages)) {
-        in = false;
-        record_error(p.status, kDevPage, 44);
-      }
-      const uint32_t valid = __ballot_sync(0xffffffffu, in) & 0xffffu;
-      if (lane == 0) valid_of[warp][stage] = valid;
-      if (FP8) {   // scales of K in lanes 0 to 15, of V in the others
-        const int64_t sat = in ? page * c.s_page_stride +
-                                     off * c.s_token_stride +
-                                     kvh * c.s_head_stride
-                               : 0;
-        cp_async4(reinterpret_cast<float*>(smem + warp * C::RING +
-                                           stage * C::STAGE + 2 * C::TILE) +
-                      lane,
-                  (lane < 16 ? c.ks : c.vs) + sat, in);
-      }
-      int64_t place = in ? (page * c.page_stride + off * c.token_stride) *
-                                   C::SIZE +
-                               head_at
-                         : 0;
-      constexpr int LANES = CHUNKS;            // of a row
-      constexpr int PER = 32 / LANES;          // rows of an instruction
-      const int ch = lane % LANES, sub = lane / LANES;
-#pragma unroll
-      for (int k = 0; k < STEP / PER; ++k) {
-        const int r = k * PER + sub;
-        const int64_t pl = __shfl_sync(0xffffffffu, place, r);
-        const char* src = kpool + pl + 16 * ch;
-        const bool ok = (valid >> r) & 1;
-        const uint32_t d = dst + spread<ROW>(r, ch);
-        cp_async16(d, src, ok);
-        cp_async16(d + C::TILE, src + to_v, ok);
-      }
-    };
-
     float o[KS][NT][4];
-    float m[NT][2], top[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2], over_codes[FP8 ? NT : 1][2];
+    auto& top = pick<FP8>(over_codes, m);   // maxima that the weights refer to
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -438,116 +586,151 @@ __global__ void __launch_bounds__(THREADS, CTAS)
         l[nt][h] = 0.0f;
       }
     }
-#pragma unroll
-    for (int s = 0; s < C::STAGES - 1; ++s) {
-      if (s < steps) issue(s, s);
-      cp_async_commit();
-    }
-    int stage = 0;
-    for (int i = 0; i < steps; ++i) {
-      cp_async_wait<C::STAGES - 2>();
-      __syncwarp();
-      {
-        const int ahead = i + C::STAGES - 1;
-        int to = stage + C::STAGES - 1;
-        if (to >= C::STAGES) to -= C::STAGES;
-        if (ahead < steps) issue(ahead, to);
-        cp_async_commit();
+
+    // tokens that row 8·nt + 2·t4 + h sees
+    auto seen = [&](int nt, int h) {
+      const int rr = row0 + 8 * nt + 2 * t4 + h;
+      return rr < rows ? min(n, len - p.per_seq + 1 + rr / p.group) : n;
+    };
+
+    // ---- the warp's steps: 16·MT tokens from BLOCK·blk + STEP·warp on
+    const int last = min(n, seg.blk1 * BLOCK);
+#pragma unroll 1
+    for (int t0 = seg.blk0 * BLOCK + warp * STEP; t0 < last; t0 += BLOCK) {
+      // this step's copies are done when those issued after it may not be
+      switch (issued - done - 1) {
+        case 0: cp_async_wait<0>(); break;
+        case 1: cp_async_wait<1>(); break;
+        case 2: cp_async_wait<2>(); break;
+        default: cp_async_wait<3>();
       }
-      const uint32_t kt = ring + stage * C::STAGE, vt = kt + C::TILE;
+      static_assert(STAGES <= 5, "waits for the ring's steps");
+      __syncwarp();
+      fill();
+      ++done;
+      const uint32_t kt = smem_u32(ring) + stage * C::STAGE, vt = kt + C::TILE;
       const uint32_t valid = valid_of[warp][stage];
-      const int t0 = first + i * BLOCK;
 
       // ---- Sᵀ = K·Qᵀ
-      float sc[NT][4];
+      float sc[MT][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[nt][j] = 0.0f;
-      auto add_scores = [&](const uint32_t(&a)[4], int s) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (C::QREG) {
-            mma<BF>(sc[nt], a, q[nt][s][0], q[nt][s][1]);
-          } else {
-            const uint2 u =
-                reinterpret_cast<const uint2*>(q_smem)[(nt * KS + s) * 32 +
-                                                       lane];
-            mma<BF>(sc[nt], a, u.x, u.y);
-          }
-        }
+          for (int j = 0; j < 4; ++j) sc[mt][nt][j] = 0.0f;
+      auto q_of = [&](int nt, int s) {
+        if constexpr (C::QREG)
+          return make_uint2(q[nt][s][0], q[nt][s][1]);
+        else
+          return reinterpret_cast<const uint2*>(join)[(nt * KS + s) * 32 +
+                                                      lane];
       };
       if constexpr (FP8) {
+        // rows 0–7 and 8–15 of chunk s, then of chunk s + 1
+        const uint32_t at = kt + spread<ROW>(lane & 15, lane >> 4);
 #pragma unroll
-        for (int s = 0; s < KS; s += 2) {
-          // rows 0–7 and 8–15 of chunk s, then of chunk s + 1
-          uint32_t u[4];
-          ldmatrix(kt + spread<ROW>((lane & 7) + (lane & 8), s + (lane >> 4)),
-                   u);
+        for (int s = 0; s < KS; s += 2)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {
-                codes_f16(u[2 * h]), codes_f16(u[2 * h + 1]),
-                codes_f16(u[2 * h] >> 16), codes_f16(u[2 * h + 1] >> 16)};
-            add_scores(a, s + h);
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t u[4];
+            ldmatrix((at ^ (s << 4)) + mt * 16 * ROW, u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t a[4];
+              codes_f16(u[2 * h], a[0], a[2]);
+              codes_f16(u[2 * h + 1], a[1], a[3]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint2 b = q_of(nt, s + h);
+                mma<BF>(sc[mt][nt], a, b.x, b.y);
+              }
+            }
           }
-        }
       } else {
+        const uint32_t at = kt + spread<ROW>(lane & 15, lane >> 4);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          uint32_t a[4];
-          ldmatrix(kt + spread<ROW>(lane & 15, 2 * s + (lane >> 4)), a);
-          add_scores(a, s);
-        }
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[4];
+            ldmatrix((at ^ (s << 5)) + mt * 16 * ROW, a);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 b = q_of(nt, s);
+              mma<BF>(sc[mt][nt], a, b.x, b.y);
+            }
+          }
       }
 
-      // ---- softmax of the lane's rows 2·t4, 2·t4 + 1 at tokens g and g + 8
-      float sk[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
+      // ---- softmax of the lane's rows 2·t4, 2·t4 + 1 at tokens 16·mt + g and
+      // 16·mt + g + 8
+      float sk[MT][2], lv[MT][2];
       if (FP8) {
         const float* ss = reinterpret_cast<const float*>(
-            smem + (kt - smem_u32(smem)) + 2 * C::TILE);
+            ring + stage * C::STAGE + 2 * C::TILE);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          sk[h] = ss[g + 8 * h];
-          lv[h] = lg2_approx(ss[16 + g + 8 * h]);
-        }
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sk[mt][h] = ss[16 * mt + g + 8 * h];
+            lv[mt][h] = lg2_approx(ss[STEP + 16 * mt + g + 8 * h]);
+          }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sc[nt][j] *= FP8 ? qf[nt][j & 1] * sk[j >> 1] : qf[nt][j & 1];
-      const bool mixed = p.per_seq > 1 && t0 > len - p.per_seq + 1 - STEP;
-      if (valid != 0xffffu || mixed) {
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int k = g + 8 * (j >> 1);
-            if (!((valid >> k) & 1) || t0 + k >= lim[nt][j & 1])
-              sc[nt][j] = -INFINITY;
+            float f;
+            if constexpr (C::QREG)
+              f = qf[nt][j & 1];
+            else
+              f = s_qf[8 * nt + 2 * t4 + (j & 1)];
+            sc[mt][nt][j] *= FP8 ? f * sk[mt][j >> 1] : f;
           }
-      }
-      bool more = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          more |= fmaxf(sc[nt][h], sc[nt][2 + h]) > m[nt][h];
-          if (FP8)
-            more |= fmaxf(sc[nt][h] + lv[0], sc[nt][2 + h] + lv[1]) >
-                    top[nt][h];
-        }
-      if (__any_sync(0xffffffffu, more)) {   // new maxima
+      const bool mixed = p.per_seq > 1 && t0 > len - p.per_seq + 1 - STEP;
+      if (valid != 0xffffffffu >> (32 - STEP) || mixed) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float x = fmaxf(m[nt][h], fmaxf(sc[nt][h], sc[nt][2 + h]));
-            float y = x;
+            const int end = seen(nt, h) - t0;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int k = 16 * mt + g + 8 * i;
+                if (!((valid >> k) & 1) || k >= end)
+                  sc[mt][nt][2 * i + h] = -INFINITY;
+              }
+          }
+      }
+      float hi[NT][2], hi2[NT][2];
+      bool rise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x = m[nt][h], y = top[nt][h];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            x = fmaxf(x, fmaxf(sc[mt][nt][h], sc[mt][nt][2 + h]));
             if (FP8)
-              y = fmaxf(top[nt][h],
-                        fmaxf(sc[nt][h] + lv[0], sc[nt][2 + h] + lv[1]));
+              y = fmaxf(y, fmaxf(sc[mt][nt][h] + lv[mt][0],
+                                 sc[mt][nt][2 + h] + lv[mt][1]));
+          }
+          hi[nt][h] = x;
+          hi2[nt][h] = FP8 ? y : x;
+          rise |= x > m[nt][h] || (FP8 && y > top[nt][h]);
+        }
+      if (__any_sync(0xffffffffu, rise)) {   // new maxima
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = hi[nt][h], y = hi2[nt][h];
 #pragma unroll
             for (int z = 4; z < 32; z <<= 1) {
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
@@ -559,8 +742,8 @@ __global__ void __launch_bounds__(THREADS, CTAS)
             const float f = top[nt][h] == -INFINITY
                                 ? 0.0f
                                 : ex2_approx(top[nt][h] - y);
-            m[nt][h] = x;
             top[nt][h] = y;
+            m[nt][h] = x;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
               o[s][nt][h] *= f;
@@ -569,103 +752,138 @@ __global__ void __launch_bounds__(THREADS, CTAS)
           }
       }
       // weights: 0 where a row has seen nothing yet
-      uint32_t b[NT][2], b2[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float ref = m[nt][j & 1] == -INFINITY ? 0.0f : m[nt][j & 1];
-          w[j] = ex2_approx(sc[nt][j] - ref);
-          l[nt][j & 1] += w[j];
-          if (FP8) {
-            const float far =
-                top[nt][j & 1] == -INFINITY ? 0.0f : top[nt][j & 1];
-            w[j] = sc[nt][j] == -INFINITY
-                       ? 0.0f
-                       : ex2_approx(sc[nt][j] + lv[j >> 1] - far);
-          }
-        }
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (BF) {
-            const uint32_t hi = pack_bf16x2(w[2 * h], w[2 * h + 1]);
-            const float2 f = unpack_bf16x2(hi);
-            b[nt][h] = movmatrix(hi);
-            b2[nt][h] =
-                movmatrix(pack_bf16x2(w[2 * h] - f.x, w[2 * h + 1] - f.y));
-          } else {
-            b[nt][h] = movmatrix(pack_f16x2(w[2 * h], w[2 * h + 1]));
-          }
-        }
-      }
-
-      // ---- Oᵀ += Vᵀ·Pᵀ
-      auto add_values = [&](const uint32_t(&a)[4], int s) {
-        if (!mixed) {
+          const float ref = m[nt][h] == -INFINITY ? 0.0f : m[nt][h];
+          const float far = top[nt][h] == -INFINITY ? 0.0f : top[nt][h];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma<BF>(o[s][nt], a, b[nt][0], b[nt][1]);
-            if (BF) mma<BF>(o[s][nt], a, b2[nt][0], b2[nt][1]);
-          }
-          return;
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float& x = sc[mt][nt][2 * k + h];
+              const float w = ex2_approx(x - ref);
+              l[nt][h] += w;
+              // (an infinite scale must not make NaN of a token left out)
+              if (FP8)
+                x = x == -INFINITY ? 0.0f : ex2_approx(x + lv[mt][k] - far);
+              else
+                x = w;
+            }
         }
+      if (mixed) {
         // Rows of several new tokens see different ends of this step.  What
         // a later token's v holds (NaN, say) must not reach a row that does
-        // not see it through a weight of 0: one product for each of them.
-        const int j1 = min(p.per_seq - 1, (row0 + C::ROWS - 1) / p.group);
-        for (int j = row0 / p.group; j <= j1; ++j) {
-          const int end = len - p.per_seq + 1 + j - t0;   // tokens seen
-          uint32_t cut[4];
+        // not see it through a weight of 0: the last tokens' products are
+        // added one by one, and their v then cleared.
+        const int k1 = min(STEP, n - t0);
+#pragma unroll 1
+        for (int k = max(0, len - p.per_seq + 1 - t0); k < k1; ++k) {
+          float w[NT][2];
+          uint32_t sees = 0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (t0 + k < seen(nt, h)) sees |= 1u << (2 * nt + h);
+              w[nt][h] = 0.0f;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float x = __shfl_sync(
+                      0xffffffffu, sc[mt][nt][2 * i + h], 4 * (k & 7) + t4);
+                  if (k >> 3 == 2 * mt + i) w[nt][h] = x;
+                }
+            }
+          unsigned char* const vrow = ring + stage * C::STAGE + C::TILE;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            float2 v;
+            if constexpr (FP8) {
+              v = pair_to_f32<TP_FP8>(*reinterpret_cast<const uint16_t*>(
+                  vrow + spread<ROW>(k, s) + 2 * g));
+            } else {
+              const uint32_t a = *reinterpret_cast<const uint16_t*>(
+                  vrow + spread<ROW>(k, 2 * s) + 2 * g);
+              const uint32_t b = *reinterpret_cast<const uint16_t*>(
+                  vrow + spread<ROW>(k, 2 * s + 1) + 2 * g);
+              v = pair_to_f32<CACHE>(a | b << 16);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (sees >> (2 * nt + h) & 1) {
+                  o[s][nt][h] = fmaf(w[nt][h], v.x, o[s][nt][h]);
+                  o[s][nt][2 + h] = fmaf(w[nt][h], v.y, o[s][nt][2 + h]);
+                }
+          }
+          __syncwarp();
+          if (lane < CHUNKS)
+            *reinterpret_cast<uint4*>(vrow + spread<ROW>(k, lane)) =
+                make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+      uint32_t b[MT][NT][2], b2[MT][NT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int k = 2 * t4 + 8 * h;
-            const uint32_t keep = (k < end ? 0xffffu : 0u) |
-                                  (k + 1 < end ? 0xffff0000u : 0u);
-            cut[2 * h] = a[2 * h] & keep;
-            cut[2 * h + 1] = a[2 * h + 1] & keep;
+            const float w0 = sc[mt][nt][2 * h], w1 = sc[mt][nt][2 * h + 1];
+            if (BF) {
+              const uint32_t x = pack_bf16x2(w0, w1);
+              const float2 f = unpack_bf16x2(x);
+              b[mt][nt][h] = movmatrix(x);
+              b2[mt][nt][h] = movmatrix(pack_bf16x2(w0 - f.x, w1 - f.y));
+            } else {
+              b[mt][nt][h] = movmatrix(pack_f16x2(w0, w1));
+            }
           }
+
+      // ---- Oᵀ += Vᵀ·Pᵀ
+      auto add_values = [&](const uint32_t(&a)[4], int s, int mt) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma<BF>(x, cut, b[nt][0], b[nt][1]);
-            if (BF) mma<BF>(x, cut, b2[nt][0], b2[nt][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((row0 + 8 * nt + 2 * t4 + (e & 1)) / p.group == j)
-                o[s][nt][e] += x[e];
-          }
+        for (int nt = 0; nt < NT; ++nt) {
+          mma<BF>(o[s][nt], a, b[mt][nt][0], b[mt][nt][1]);
+          if (BF) mma<BF>(o[s][nt], a, b2[mt][nt][0], b2[mt][nt][1]);
         }
       };
       if constexpr (FP8) {
+        const uint32_t at = vt + spread<ROW>(lane & 15, lane >> 4);
 #pragma unroll
-        for (int s = 0; s < KS; s += 2) {
-          uint32_t u[4];
-          ldmatrix_trans(
-              vt + spread<ROW>((lane & 7) + (lane & 8), s + (lane >> 4)), u);
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // elements 2g and 2g + 1 of tokens 2t, 2t + 1 to pairs of tokens
-            const uint32_t x = __byte_perm(u[2 * h], 0, 0x3120),
-                           y = __byte_perm(u[2 * h + 1], 0, 0x3120);
-            const uint32_t a[4] = {codes_f16(x), codes_f16(x >> 16),
-                                   codes_f16(y), codes_f16(y >> 16)};
-            add_values(a, s + h);
+          for (int s = 0; s < KS; s += 2) {
+            uint32_t u[4];
+            ldmatrix_trans((at ^ (s << 4)) + mt * 16 * ROW, u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // elements 2g, 2g + 1 of tokens 2t, 2t + 1 to pairs of tokens
+              uint32_t a[4];
+              codes_f16(__byte_perm(u[2 * h], 0, 0x3120), a[0], a[1]);
+              codes_f16(__byte_perm(u[2 * h + 1], 0, 0x3120), a[2], a[3]);
+              add_values(a, s + h, mt);
+            }
           }
-        }
       } else {
+        const uint32_t at =
+            vt + spread<ROW>((lane & 7) + ((lane >> 1) & 8), (lane >> 3) & 1);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          uint32_t a[4];
-          ldmatrix_trans(vt + spread<ROW>((lane & 7) + ((lane >> 1) & 8),
-                                          2 * s + ((lane >> 3) & 1)),
-                         a);
-          add_values(a, s);
-        }
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            uint32_t a[4];
+            ldmatrix_trans((at ^ (s << 5)) + mt * 16 * ROW, a);
+            add_values(a, s, mt);
+          }
       }
-      if (++stage == C::STAGES) stage = 0;
+      if (++stage == STAGES) stage = 0;
     }
-    cp_async_wait<0>();
 
     // ---- the warps' results together
 #pragma unroll
@@ -682,100 +900,118 @@ __global__ void __launch_bounds__(THREADS, CTAS)
           s_l[warp][r] = l[nt][h];
         }
       }
-    __syncthreads();   // every warp's ring is read
-    float* const join = reinterpret_cast<float*>(smem);
+    const bool part = seg.blk0 > 0 || seg.blk1 < seg.nb;
+    const int64_t part_at = 2 * (int64_t)blockIdx.x + !first_segment;
+    __syncthreads();   // and Q is read
+    if (seg.blk0 == 0 && seg.blk1 < seg.nb && tid == 0) {
+      // the CTA of slot x is the last one c with ⌊total·c / ctas⌋ ≤ x
+      const int64_t end = seg.first + seg.nb - 1;
+      Cut cut;
+      cut.seq = seg.seq;
+      cut.head = seg.kvh;
+      cut.tile = seg.tile;
+      cut.first_slot = (int)part_at;
+      cut.parts =
+          (int)(quotient((end + 1) * ctas - 1, total) - blockIdx.x + 1);
+      p.cuts[blockIdx.x] = cut;
+    }
+    // Halves of the warps take the other half's in, eight rows at a time, then
+    // all threads add what is left.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = 8 * nt + 2 * t4 + h;
         float all = s_top[0][r];
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) all = fmaxf(all, s_top[w][r]);
-        const float f = top[nt][h] == -INFINITY
-                            ? 0.0f
-                            : ex2_approx(top[nt][h] - all);
-        float* dst = join + (warp * C::ROWS + r) * (D + 4);
+        f[h] = top[nt][h] == -INFINITY ? 0.0f : ex2_approx(top[nt][h] - all);
+      }
+      float* const mine =
+          join + ((warp % (WARPS / 2)) * 8 + 2 * t4) * (D + 4) +
+          (FP8 ? 2 * g : g);
+      constexpr int PAIR = FP8 ? 1 : 8;
+      if (warp >= WARPS / 2) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const int e0 = 16 * s + (FP8 ? 2 * g : g);
-          dst[e0] = o[s][nt][h] * f;
-          dst[e0 + (FP8 ? 1 : 8)] = o[s][nt][2 + h] * f;
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            mine[h * (D + 4) + 16 * s] = o[s][nt][h] * f[h];
+            mine[h * (D + 4) + 16 * s + PAIR] = o[s][nt][2 + h] * f[h];
+          }
+      }
+      __syncthreads();
+      if (warp < WARPS / 2) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float* const d = mine + h * (D + 4) + 16 * s;
+            d[0] = fmaf(o[s][nt][h], f[h], d[0]);
+            d[PAIR] = fmaf(o[s][nt][2 + h], f[h], d[PAIR]);
+          }
+      }
+      __syncthreads();
+      constexpr int QUADS = D / 4;
+      for (int i = tid; i < 8 * QUADS; i += THREADS) {
+        const int r8 = i / QUADS, e = 4 * (i - r8 * QUADS);
+        const int r = 8 * nt + r8, rr = row0 + r;
+        if (rr >= rows) break;
+        float mm = s_m[0][r], tt = s_top[0][r];
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) {
+          mm = fmaxf(mm, s_m[w][r]);
+          tt = fmaxf(tt, s_top[w][r]);
+        }
+        float sum = 0.0f;
+        // a warp without a maximum has l = 0, or NaN of NaN scores
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+          sum = s_m[w][r] == -INFINITY
+                    ? sum + s_l[w][r]
+                    : fmaf(s_l[w][r], ex2_approx(s_m[w][r] - mm), sum);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < WARPS / 2; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(
+              join + (w * 8 + r8) * (D + 4) + e);
+          v.x += x.x;
+          v.y += x.y;
+          v.z += x.z;
+          v.w += x.w;
+        }
+        const bool none = sum == 0.0f;
+        const float y = none ? 0.0f : (FP8 ? ex2_approx(tt - mm) : 1.0f) / sum;
+        v.x *= y;
+        v.y *= y;
+        v.z *= y;
+        v.w *= y;
+        const float lse2 = none ? -INFINITY : mm + log2f(sum);
+        if (part) {
+          *reinterpret_cast<float4*>(p.part_o +
+                                     (part_at * C::ROWS + r) * D + e) = v;
+          if (e == 0) p.part_lse[part_at * C::ROWS + r] = lse2;
+        } else {
+          const int j = rr / p.group;
+          const int head = seg.kvh * p.group + rr - j * p.group;
+          store4(p.a, qrow + j, head, e, v);
+          if (e == 0 && p.a.lse != nullptr)
+            p.a.lse[(qrow + j) * p.a.n_q + head] = lse2 * LN2;
         }
       }
-    __syncthreads();
-    const bool part = blk0 > 0 || blk1 < nb;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (at != begin);
-    constexpr int QUADS = D / 4;
-    for (int i = tid; i < C::ROWS * QUADS; i += THREADS) {
-      const int r = i / QUADS, e = 4 * (i - r * QUADS);
-      const int rr = row0 + r;
-      if (rr >= rows) break;
-      float mm = s_m[0][r], tt = s_top[0][r];
-#pragma unroll
-      for (int w = 1; w < WARPS; ++w) {
-        mm = fmaxf(mm, s_m[w][r]);
-        tt = fmaxf(tt, s_top[w][r]);
-      }
-      float sum = 0.0f;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(
-            join + (w * C::ROWS + r) * (D + 4) + e);
-        v.x += x.x;
-        v.y += x.y;
-        v.z += x.z;
-        v.w += x.w;
-        // a warp without a maximum has l = 0, or NaN of NaN scores
-        sum = s_m[w][r] == -INFINITY
-                  ? sum + s_l[w][r]
-                  : fmaf(s_l[w][r], ex2_approx(s_m[w][r] - mm), sum);
-      }
-      const bool none = sum == 0.0f;
-      const float f = none ? 0.0f : (FP8 ? ex2_approx(tt - mm) : 1.0f) / sum;
-      v.x *= f;
-      v.y *= f;
-      v.z *= f;
-      v.w *= f;
-      const float lse2 = none ? -INFINITY : mm + log2f(sum);
-      if (part) {
-        *reinterpret_cast<float4*>(p.part_o + (slot * C::ROWS + r) * D + e) =
-            v;
-        if (e == 0) p.part_lse[slot * C::ROWS + r] = lse2;
-      } else {
-        const int j = rr / p.group;
-        const int head = kvh * p.group + rr - j * p.group;
-        const int64_t row = qrow + j;
-        uint16_t* dst = static_cast<uint16_t*>(p.a.out) + row * p.a.o_row +
-                        head * p.a.o_head + e;
-        *reinterpret_cast<uint2*>(dst) =
-            p.a.bf16 ? make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w))
-                     : make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
-        if (e == 0 && p.a.lse != nullptr)
-          p.a.lse[row * p.a.n_q + head] = lse2 * LN2;
-      }
+      __syncthreads();   // the sums, and `seg`, are read
     }
-    if (blk0 == 0 && blk1 < nb && tid == 0) {
-      // the CTA of the unit's last block: total·c / ctas ≤ it
-      const int64_t most = (total + MIN_BLOCKS - 1) / MIN_BLOCKS;
-      const int64_t ctas = most < gridDim.x ? most : gridDim.x;
-      const int64_t last = at + nb - 1;
-      const int end = (int)(((last + 1) * ctas - 1) / total);
-      Cut cut;
-      cut.seq = seq;
-      cut.head = kvh;
-      cut.tile = tile;
-      cut.first_slot = (int)slot;
-      cut.parts = end - (int)blockIdx.x + 1;
-      p.cuts[blockIdx.x] = cut;
+    first_segment = false;
+    const int old = cs;
+    cs = cs == 2 ? 0 : cs + 1;
+    if (!segs[cs].there) return;
+    if (ls == old) {   // nothing of this one is loaded yet
+      ls = cs;
+      now = plan(segs[cs]);
+      pages = pages2;
     }
-    at += blk1 - blk0;
-    if (at < stop && at - before >= (int64_t)nb * per_block) {
-      before += (int64_t)nb * per_block;
-      ++seq;
-    }
-    __syncthreads();   // the joined results are read
+    read_pages(segs[cs == 2 ? 0 : cs + 1], pages2);
   }
 }
 
@@ -789,10 +1025,14 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   __shared__ float s_max[JOIN_THREADS / 32];
   __shared__ float s_sum[TEAMS];
   __shared__ float4 s_o[TEAMS][TEAM];
+  // launched while the first kernel runs: everything is read after this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = p.cuts[blockIdx.x];
-  const int r = blockIdx.y, rr = cut.tile * tile_rows + r;
-  if (cut.tile < 0 || rr >= p.per_seq * p.group) return;
+  if (cut.tile < 0) return;
   const int tid = threadIdx.x;
+  for (int r = blockIdx.y; r < tile_rows; r += gridDim.y) {
+  const int rr = cut.tile * tile_rows + r;
+  if (rr >= p.per_seq * p.group) return;
   auto slot_of = [&](int i) -> int64_t {
     return i == 0 ? cut.first_slot : 2 * ((int64_t)blockIdx.x + i);
   };
@@ -824,7 +1064,7 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   s_o[team][e] = v;
   if (e == 0) s_sum[team] = sum;
   __syncthreads();
-  if (team != 0) return;
+  if (team == 0) {
   for (int k = 1; k < TEAMS; ++k) {
     const float4 u = s_o[k][e];
     sum += s_sum[k];
@@ -838,18 +1078,17 @@ __global__ void __launch_bounds__(JOIN_THREADS)
   const int j = rr / p.group;
   const int head = cut.head * p.group + rr - j * p.group;
   const int64_t row = (int64_t)cut.seq * p.per_seq + j;
-  uint16_t* dst = static_cast<uint16_t*>(p.a.out) + row * p.a.o_row +
-                  head * p.a.o_head + 4 * e;
   v.x *= f;
   v.y *= f;
   v.z *= f;
   v.w *= f;
-  *reinterpret_cast<uint2*>(dst) =
-      p.a.bf16 ? make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w))
-               : make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+  store4(p.a, row, head, 4 * e, v);
   if (e == 0 && p.a.lse != nullptr)
     p.a.lse[row * p.a.n_q + head] =
         none ? -INFINITY : (top + log2f(sum)) * LN2;
+  }
+  __syncthreads();
+  }
 }
 
 // Rows of a unit's tile: as few as hold them, 32 at most.
@@ -868,10 +1107,11 @@ Layout layout_of(int ctas, int tile_rows, int d) {
   return l;
 }
 
+// `sms` SMs' worth of CTAs.
 template <int CACHE, int D, int NT>
-int launch(const Params& p, int ctas, cudaStream_t s) {
+int launch(const Params& p, int sms, cudaStream_t s) {
   using C = Conf<CACHE, D, NT>;
-  constexpr int bytes = C::SMEM + C::QSMEM;
+  static_assert(C::CTAS <= MAX_CTAS, "the workspace has room for MAX_CTAS");
   static std::atomic<uint64_t> ready{0};   // devices whose attribute is set
   int dev = 0;
   int err = cudaGetDevice(&dev);
@@ -880,30 +1120,43 @@ int launch(const Params& p, int ctas, cudaStream_t s) {
   if (!(ready.load() & bit)) {
     err = cudaFuncSetAttribute(decode_kernel<CACHE, D, NT>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               bytes);
+                               C::SMEM);
     if (err) return err;
     ready.fetch_or(bit);
   }
-  decode_kernel<CACHE, D, NT><<<ctas, THREADS, bytes, s>>>(p);
-  return cudaGetLastError();
+  const int ctas = C::CTAS * sms;
+  decode_kernel<CACHE, D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
+  err = cudaGetLastError();
+  if (err) return err;
+  const int64_t unit = (int64_t)p.per_seq * p.group;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, (unsigned)std::min<int64_t>(unit, 8));
+  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, 8 * NT);
 }
 template <int CACHE, int D>
-int launch_rows(const Params& p, int tile_rows, int ctas, cudaStream_t s) {
-  return tile_rows == 8    ? launch<CACHE, D, 1>(p, ctas, s)
-         : tile_rows == 16 ? launch<CACHE, D, 2>(p, ctas, s)
-                           : launch<CACHE, D, 4>(p, ctas, s);
+int launch_rows(const Params& p, int tile_rows, int sms, cudaStream_t s) {
+  return tile_rows == 8    ? launch<CACHE, D, 1>(p, sms, s)
+         : tile_rows == 16 ? launch<CACHE, D, 2>(p, sms, s)
+                           : launch<CACHE, D, 4>(p, sms, s);
 }
 template <int CACHE>
-int launch_d(const Params& p, int tile_rows, int ctas, cudaStream_t s) {
-  return p.c.d == 128 ? launch_rows<CACHE, 128>(p, tile_rows, ctas, s)
-                      : launch_rows<CACHE, 64>(p, tile_rows, ctas, s);
+int launch_d(const Params& p, int tile_rows, int sms, cudaStream_t s) {
+  return p.c.d == 128 ? launch_rows<CACHE, 128>(p, tile_rows, sms, s)
+                      : launch_rows<CACHE, 64>(p, tile_rows, sms, s);
 }
 
 }  // namespace
 
 size_t attn_decode_ws_bytes(const tp_kv_cache& c, int64_t rows, int n_q) {
   const int64_t unit = rows / c.b * (n_q / c.n_kv);
-  return layout_of(CTAS * device_sm_count(), tile_rows_of(unit), c.d).bytes;
+  return layout_of(MAX_CTAS * device_sm_count(), tile_rows_of(unit), c.d).bytes;
 }
 
 int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,
@@ -918,8 +1171,8 @@ int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,
   const int tile_rows = tile_rows_of(unit);
   p.tiles = (int)((unit + tile_rows - 1) / tile_rows);
   p.status = status;
-  const int ctas = CTAS * device_sm_count();
-  const Layout l = layout_of(ctas, tile_rows, c.d);
+  const int sms = device_sm_count();
+  const Layout l = layout_of(MAX_CTAS * sms, tile_rows, c.d);
   char* ws = static_cast<char*>(a.ws);
   p.part_o = reinterpret_cast<float*>(ws + l.o);
   p.part_lse = reinterpret_cast<float*>(ws + l.lse);
@@ -928,16 +1181,9 @@ int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,
   // the lengths, and with them the work, are known on the device alone
   ProfScope prof(stream, KF_ATTN_DECODE, 0.0, 0.0);
   count_launch(2);
-  const int err = c.dtype == TP_BF16  ? launch_d<TP_BF16>(p, tile_rows, ctas, s)
-                  : c.dtype == TP_F16 ? launch_d<TP_F16>(p, tile_rows, ctas, s)
-                                      : launch_d<TP_FP8>(p, tile_rows, ctas, s);
-  if (err) return err;
-  const dim3 grid(ctas, (unsigned)(unit < tile_rows ? unit : tile_rows));
-  if (c.d == 128)
-    join_kernel<128><<<grid, JOIN_THREADS, 0, s>>>(p, tile_rows);
-  else
-    join_kernel<64><<<grid, JOIN_THREADS, 0, s>>>(p, tile_rows);
-  return cudaGetLastError();
+  return c.dtype == TP_BF16  ? launch_d<TP_BF16>(p, tile_rows, sms, s)
+         : c.dtype == TP_F16 ? launch_d<TP_F16>(p, tile_rows, sms, s)
+                             : launch_d<TP_FP8>(p, tile_rows, sms, s);
 }
 
 }  // namespace tp
