@@ -526,7 +526,8 @@ tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
  * time: two pools of pages, K and V, each [pages, page, n_kv, d] in TP_BF16,
  * TP_F16 or TP_FP8.  A pool's vectors (d adjacent elements, one head of one
  * token) lie anywhere: element strides of a page, a token and a head, shared
- * by both pools, vectors apart from each other and on multiples of 16 bytes.
+ * by both pools (below 2^31), vectors apart from each other and on multiples
+ * of 16 bytes.
  * TP_FP8 vectors are E4M3 codes with one fp32 scale each in ks and vs
  * [pages, page, n_kv] (strides of their own, again shared): as in
  * tp_quantize_fp8_block's TP_FP8_ROW, s = amax / 448, code = E4M3(x·448/amax)
@@ -584,8 +585,8 @@ tp_status tp_kv_cache_read(const tp_kv_cache* c, int32_t dtype, int64_t rows,
 /* Attention of the newest tokens over the cache, which holds them already.
  * q, out: [rows, n_q, d] of `dtype` (TP_BF16 or TP_F16; TP_F16 not over a
  * TP_BF16 cache: TP_ERR_UNSUPPORTED), row and head strides multiples of 8;
- * rows = b·m, the last m tokens of each sequence: row j of sequence i is the
- * token at p = lens[i] − m + j and sees the tokens t ≤ p.  Query head j reads
+ * rows = b·m, the last m tokens of each sequence (b·n_kv·⌈m·n_q/(32·n_kv)⌉·
+ * (table_cols·page/64 + 17) below 2^31): row j of sequence i is the token at p = lens[i] − m + j and sees the tokens t ≤ p.  Query head j reads
  * kv head ⌊j·n_kv/n_q⌋.
  *   x_t = scale·q·k_t,  out = Σ_t e^(x_t)·v_t / Σ_t e^(x_t),
  *   lse = ln Σ_t e^(x_t)     (fp32 [rows, n_q] dense; NULL: not written).

@@ -1395,6 +1395,8 @@ tp_status check_kv_cache(const tp_kv_cache* d, tp_kv_cache* c) {
   const int64_t unit = fp8 ? 16 : 8;
   if (c->page_stride % unit || c->token_stride % unit || c->head_stride % unit)
     return TP_ERR_SHAPE;
+  for (const int64_t x : {c->page_stride, c->token_stride, c->head_stride})
+    if (x > INT32_MAX) return TP_ERR_SHAPE;
   if (!apart(d->d, {{{c->page_stride, d->pages},
                      {c->token_stride, d->page},
                      {c->head_stride, d->n_kv}}}))
@@ -1403,6 +1405,9 @@ tp_status check_kv_cache(const tp_kv_cache* d, tp_kv_cache* c) {
     c->s_page_stride = used(d->s_page_stride, d->pages);
     c->s_token_stride = used(d->s_token_stride, d->page);
     c->s_head_stride = used(d->s_head_stride, d->n_kv);
+    for (const int64_t x :
+         {c->s_page_stride, c->s_token_stride, c->s_head_stride})
+      if (x > INT32_MAX) return TP_ERR_SHAPE;
     if (!apart(1, {{{c->s_page_stride, d->pages},
                     {c->s_token_stride, d->page},
                     {c->s_head_stride, d->n_kv}}}))
@@ -1457,9 +1462,16 @@ tp_status check_kv_rows(const tp_kv_cache* d, int32_t dtype, int64_t rows,
                     &r->v_head);
 }
 
+// Rows and heads that fit, and work that the kernel counts in 31 bits: blocks
+// of 64 tokens (and up to 16 more) of each sequence, kv head and 32 rows.
 bool decode_shape(const tp_kv_cache* c, int64_t rows, int32_t n_q) {
-  return rows >= 1 && rows % c->b == 0 && n_q >= 1 && n_q <= (1 << 16) &&
-         n_q % c->n_kv == 0 && rows <= INT32_MAX / n_q;
+  if (rows < 1 || rows % c->b || n_q < 1 || n_q > (1 << 16) ||
+      n_q % c->n_kv || rows > INT32_MAX / n_q)
+    return false;
+  const int64_t tiles = (rows / c->b * (n_q / c->n_kv) + 31) / 32;
+  const int64_t units = c->n_kv * tiles;   // < 2^31: tiles ≤ rows·n_q/n_kv
+  const int64_t slots = (int64_t)c->table_cols * c->page / 64 + 17;
+  return units <= INT32_MAX / slots / c->b;
 }
 
 }  // namespace

@@ -68,7 +68,10 @@ struct Params {
   float* part_lse;       // [2·CTAs][8·NT], log₂
   Cut* cuts;             // [CTAs]
   unsigned* status;
+  // the cache's strides (elements; a product of two is formed in 64 bits)
+  int page, pages, page_s, token_s, head_s, s_page_s, s_token_s, s_head_s;
 };
+__device__ __forceinline__ int64_t mul(int a, int b) { return (int64_t)a * b; }
 
 template <int CACHE, int D, int NT>
 struct Conf {
@@ -94,6 +97,10 @@ struct Conf {
       WARPS * RING + (JOIN > QSMEM ? JOIN : QSMEM) + ALIGN;
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src,
                                            bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
@@ -174,9 +181,18 @@ template <int BLOCK>
 __device__ __forceinline__ int blocks_of(int n) {
   return n <= BLOCK ? 1 : (n - 1) / BLOCK + 1;
 }
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b;
-}
+// `total` slots cut into `ctas` pieces of which the first `more` have one slot
+// more than the others (`share`).
+struct Pieces {
+  int total, ctas, share, more;
+  __device__ __forceinline__ int begin(int cta) const {
+    return cta * share + min(cta, more);
+  }
+  __device__ __forceinline__ int cta_of(int slot) const {
+    const int edge = more * (share + 1);
+    return slot < edge ? slot / (share + 1) : more + (slot - edge) / share;
+  }
+};
 
 // Elements e … e + 3 of a row's head.
 __device__ __forceinline__ void store4(const DecodeArgs& a, int64_t row,
@@ -232,44 +248,47 @@ struct Segment {
   int seq, kvh, tile;
   int len, n;            // the sequence's tokens, those that are followed
   int nb, blk0, blk1;
-  int64_t first;         // slot of the unit's first block
+  int first;             // slot of the unit's first block
   int there;             // 0: the piece ended before
 };
 
 // Walks a CTA's piece, slots [at, stop) of all.
-template <class C>
 struct Walk {
-  int64_t at, stop, before;   // before: slots in front of the sequence
-  int seq, per_seq;           // units of a sequence
-
-  // The next segment with blocks of the piece.
-  __device__ __forceinline__ void next(const Params& p, Segment* s) {
-    s->there = 1;
-    while (at < stop) {
-      s->len = max(p.c.lens[seq], 0);
-      s->n = tokens_of(p.c, seq);
-      s->nb = blocks_of<C::BLOCK>(s->n);
-      const int w = s->nb + C::EXTRA;
-      const int64_t in_seq = at - before;
-      const int unit = (int)quotient(in_seq, w);
-      const int x0 = (int)(in_seq - (int64_t)unit * w);
-      const int x1 = (int)min((int64_t)w, x0 + (stop - at));
-      s->seq = seq;
-      s->kvh = unit / p.tiles;
-      s->tile = unit - s->kvh * p.tiles;
-      s->first = before + (int64_t)unit * w + C::EXTRA;
-      s->blk0 = max(0, x0 - C::EXTRA);
-      s->blk1 = max(0, x1 - C::EXTRA);
-      at += x1 - x0;
-      if (unit == per_seq - 1 && x1 == w) {
-        before += (int64_t)w * per_seq;
-        ++seq;
-      }
-      if (s->blk1 > s->blk0) return;
-    }
-    s->there = 0;
-  }
+  int at, stop, before, seq;   // before: slots in front of the sequence
 };
+// The next segment with blocks of the piece (one thread).
+template <class C>
+__device__ __forceinline__ void next_segment(const Params& p, Walk* walk,
+                                             Segment* out) {
+  Walk w = *walk;
+  Segment s = {};
+  const int units = p.c.n_kv * p.tiles;
+#pragma unroll 1
+  while (w.at < w.stop && !s.there) {
+    s.len = max(p.c.lens[w.seq], 0);
+    s.n = tokens_of(p.c, w.seq);
+    s.nb = blocks_of<C::BLOCK>(s.n);
+    s.seq = w.seq;
+    const int weight = s.nb + C::EXTRA;
+    const int in_seq = w.at - w.before;
+    const int unit = in_seq / weight;
+    const int x0 = in_seq - unit * weight;
+    const int x1 = min(weight, x0 + (w.stop - w.at));
+    s.kvh = p.tiles == 1 ? unit : unit / p.tiles;
+    s.tile = unit - s.kvh * p.tiles;
+    s.first = w.before + unit * weight + C::EXTRA;
+    s.blk0 = max(0, x0 - C::EXTRA);
+    s.blk1 = max(0, x1 - C::EXTRA);
+    s.there = s.blk1 > s.blk0;
+    w.at += x1 - x0;
+    if (unit == units - 1 && x1 == weight) {
+      w.before += weight * units;
+      ++w.seq;
+    }
+  }
+  *walk = w;
+  *out = s;
+}
 
 template <int CACHE, int D, int NT>
 __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
@@ -282,155 +301,109 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
   constexpr int KS = D / 16;          // steps of 16 elements
   constexpr int ROW = C::ROW, CHUNKS = ROW / 16;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ int64_t sum_of[WARPS];
-  __shared__ Walk<C> s_walk;
+  __shared__ Walk s_walk;
   __shared__ Segment segs[3];   // the one computed, the next, the one after it
   __shared__ uint32_t valid_of[WARPS][STAGES];
   __shared__ float s_qf[C::ROWS];
   __shared__ float s_m[WARPS][C::ROWS], s_top[WARPS][C::ROWS],
       s_l[WARPS][C::ROWS];
+  __shared__ float s_ref[C::ROWS], s_out[C::ROWS];
   const tp_kv_cache& c = p.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this CTA's piece of all slots, and the sequence in which it begins
-  const int units = c.n_kv * p.tiles;   // of a sequence
-  int64_t total, ctas;
+  // (each warp for itself: lane l has sequences [l·span, (l + 1)·span))
+  Pieces pieces;
   {
-    const int span = (c.b + THREADS - 1) / THREADS;
-    const int i0 = min(tid * span, c.b), i1 = min(i0 + span, c.b);
-    auto slots = [&](int i) -> int64_t {
-      return (int64_t)(blocks_of<BLOCK>(tokens_of(c, i)) + C::EXTRA) *
-             units;
+    const int units = c.n_kv * p.tiles;   // of a sequence
+    const int span = (c.b + 31) / 32;
+    const int i0 = lane * span, i1 = min(i0 + span, c.b);
+    auto slots = [&](int i) {
+      return (blocks_of<BLOCK>(tokens_of(c, i)) + C::EXTRA) * units;
     };
-    int64_t sum = 0;
+    int sum = 0;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) sum += slots(i);
-    int64_t inc = sum;
+    int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    if (lane == 31) sum_of[warp] = inc;
-    if (tid == 0) p.cuts[blockIdx.x].tile = -1;
-    __syncthreads();
-    int64_t before = inc - sum;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) before += sum_of[w];
-      total += sum_of[w];
-    }
-    ctas = min((total + MIN_SLOTS - 1) / MIN_SLOTS, (int64_t)gridDim.x);
-    if (blockIdx.x >= ctas) return;
-    const int64_t at = quotient(total * blockIdx.x, ctas);
-    if (before <= at && at < before + sum) {   // one thread
+    pieces.total = __shfl_sync(0xffffffffu, inc, 31);
+    pieces.ctas =
+        min((pieces.total + MIN_SLOTS - 1) / MIN_SLOTS, (int)gridDim.x);
+    pieces.share = pieces.total / pieces.ctas;
+    pieces.more = pieces.total - pieces.share * pieces.ctas;
+    const int cta = blockIdx.x;
+    if (tid == 0) p.cuts[cta].tile = -1;
+    if (cta >= pieces.ctas) return;
+    const int at = pieces.begin(cta);
+    int before = inc - sum;
+    if (warp == 1 && before <= at && at < inc) {   // one lane
       int i = i0;
+#pragma unroll 1
       for (;; ++i) {
-        const int64_t w = slots(i);
+        const int w = slots(i);
         if (at < before + w) break;
         before += w;
       }
-      s_walk.at = at;
-      s_walk.stop = quotient(total * (blockIdx.x + 1), ctas);
-      s_walk.before = before;
-      s_walk.seq = i;
-      s_walk.per_seq = units;
-      s_walk.next(p, &segs[0]);
-      s_walk.next(p, &segs[1]);
+      s_walk = Walk{at, pieces.begin(cta + 1), before, i};
     }
-    __syncthreads();
+    __syncwarp();
   }
-  if (!segs[0].there) return;
 
   const float scale = p.a.scale * LOG2E;
   const char* const kpool = static_cast<const char*>(c.k);
   const int64_t to_v = static_cast<const char*>(c.v) - kpool;
-  const bool whole_pages = c.page % STEP == 0;
-  const int skip_cols = BLOCK / c.page, skip_off = BLOCK % c.page;
+  const bool whole_pages = p.page % STEP == 0;
+  const int skip_cols = BLOCK / p.page, skip_off = BLOCK % p.page;
   unsigned char* const smem =
       smem_raw + (-smem_u32(smem_raw) & (C::ALIGN - 1));
   float* const join = reinterpret_cast<float*>(smem + WARPS * C::RING);
   unsigned char* const ring = smem + warp * C::RING;
   constexpr int LANES = CHUNKS, PER = 32 / LANES;   // of a row, rows a copy
   const int sub = lane / LANES, ch = lane % LANES;
-  const int64_t row_bytes = c.token_stride * C::SIZE;
+  const int64_t copy_bytes = mul(PER, p.token_s) * C::SIZE;
 
   // ---- loads: the warp's steps of a segment, and of the one after it
   struct Load {
     int left;              // steps that are still to be issued
     int t0, col, off;      // the next one's first token and its place
   };
-  Load now = {};
-  Pages pages, pages2;     // of `now`, and of the segment after the computed
-  int cs = 0, ls = 0;      // the segments that are computed and loaded
+  Load now = {}, then;
+  Pages pages, pages2;     // of `now` and of `then`
+  int cur = 1, next = 2, find = 0;   // places in segs: turns below
+  int loads = 2;           // that of `now`
+  bool moved = true;       // `now` is the segment after the computed one
   auto row_of = [&](const Segment& s) {
     return c.table + (int64_t)s.seq * c.table_stride;
   };
-  auto plan = [&](const Segment& s) {
-    Load l = {};
-    if (!s.there) return l;   // nothing else of it is set
-    l.t0 = s.blk0 * BLOCK + warp * STEP;
-    const int end = min(s.n, s.blk1 * BLOCK) - 1;   // the last token
-    l.left = l.t0 <= end ? (end - l.t0) / BLOCK + 1 : 0;
-    l.col = l.t0 / c.page;
-    l.off = l.t0 - l.col * c.page;
-    return l;
-  };
-  auto read_pages = [&](const Segment& s, Pages& pg) {
-    const Load l = plan(s);
-    if (l.left > 0)
-      pg.start(row_of(s), l.col, (min(s.n, s.blk1 * BLOCK) - 1) / c.page + 1,
-               lane);
-    else
-      pg = Pages{0, 0, -1, -1};
-  };
   int issued = 0, slot = 0;   // steps, and the ring's place of the next one
   auto issue = [&]() {
-    const uint32_t dst = smem_u32(ring) + slot * C::STAGE;
-    const Segment& sg = segs[ls];
+    const Segment& sg = segs[loads];
     pages.move_to(row_of(sg), now.col, lane);
-    const int rest = sg.n - now.t0;   // ≥ 1
     const int kvh = sg.kvh;
+    const int rest = sg.n - now.t0;   // ≥ 1
     const int tok = lane % STEP;
-    uint32_t valid;
-    const char* src;
-    int64_t place = 0;
-    int page, off;   // of the lane's token
-    if (whole_pages) {
-      page = pages.at(now.col);
-      off = now.off + tok;
-      if (page < 0 || page >= c.pages) {
-        record_error(p.status, kDevPage, 44);
-        valid = 0;
-      } else {
-        valid = rest >= STEP ? 0xffffffffu >> (32 - STEP) : (1u << rest) - 1u;
-      }
-      src = kpool + ((page * c.page_stride + (now.off + sub) * c.token_stride +
-                      kvh * c.head_stride) *
-                         C::SIZE +
-                     16 * ch);
-    } else {
-      bool in = tok < rest;
-      const int ahead = in ? (now.off + tok) / c.page : 0;
-      page = pages.at(now.col + ahead);
-      off = now.off + tok - ahead * c.page;
-      if (in && (page < 0 || page >= c.pages)) {
-        in = false;
-        record_error(p.status, kDevPage, 44);
-      }
-      valid = __ballot_sync(0xffffffffu, in) & (0xffffffffu >> (32 - STEP));
-      place = (page * c.page_stride + off * c.token_stride +
-               kvh * c.head_stride) *
-                  C::SIZE +
-              reinterpret_cast<int64_t>(kpool);
-      src = nullptr;
+    constexpr uint32_t ALL = 0xffffffffu >> (32 - STEP);
+    const uint32_t dst = smem_u32(ring) + slot * C::STAGE;
+    // the page and the offset of the lane's token
+    bool in = tok < rest;
+    int off = now.off + tok, ahead = 0;
+    if (!whole_pages && in) ahead = off / p.page;
+    off -= ahead * p.page;
+    const int page = pages.at(now.col + ahead);
+    if (in && (page < 0 || page >= p.pages)) {
+      in = false;
+      record_error(p.status, kDevPage, 44);
     }
+    const uint32_t valid = __ballot_sync(0xffffffffu, in) & ALL;
     if (FP8) {   // 16 tokens: scales of K in half of the lanes, V in the other
-      const bool in = (valid >> tok) & 1;
-      const int64_t at = in ? page * c.s_page_stride + off * c.s_token_stride +
-                                  kvh * c.s_head_stride
+      const int64_t at = in ? mul(page, p.s_page_s) + mul(off, p.s_token_s) +
+                                  mul(kvh, p.s_head_s)
                             : 0;
       float* d = reinterpret_cast<float*>(ring + slot * C::STAGE + 2 * C::TILE);
       if (STEP == 16) {
@@ -440,21 +413,32 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
         cp_async4(d + STEP + lane, c.vs + at, in);
       }
     }
+    if (whole_pages && valid == ALL) {   // one page
+      const char* src = kpool +
+                        (mul(page, p.page_s) + mul(now.off + sub, p.token_s) +
+                         mul(kvh, p.head_s)) *
+                            C::SIZE +
+                        16 * ch;
 #pragma unroll
-    for (int k = 0; k < STEP / PER; ++k) {
-      const int r = k * PER + sub;
-      const bool in = (valid >> r) & 1;
-      const char* s = src;
-      if (!whole_pages)
-        s = reinterpret_cast<const char*>(
-                __shfl_sync(0xffffffffu, place, r)) +
-            16 * ch;
-      else
-        src += PER * row_bytes;
-      if (!in) s = kpool;   // nothing is read
-      const uint32_t d = dst + spread<ROW>(r, ch);
-      cp_async16(d, s, in);
-      cp_async16(d + C::TILE, s + to_v, in);
+      for (int k = 0; k < STEP / PER; ++k) {
+        const uint32_t d = dst + spread<ROW>(k * PER + sub, ch);
+        cp_async16(d, src);
+        cp_async16(d + C::TILE, src + to_v);
+        src += copy_bytes;
+      }
+    } else {
+      const int64_t place = in ? (mul(page, p.page_s) + mul(off, p.token_s) +
+                                  mul(kvh, p.head_s)) *
+                                     C::SIZE
+                               : 0;
+#pragma unroll 1
+      for (int k = 0; k < STEP / PER; ++k) {
+        const int r = k * PER + sub;
+        const char* src = kpool + __shfl_sync(0xffffffffu, place, r) + 16 * ch;
+        const uint32_t d = dst + spread<ROW>(r, ch);
+        cp_async16(d, src, (valid >> r) & 1);
+        cp_async16(d + C::TILE, src + to_v, (valid >> r) & 1);
+      }
     }
     cp_async_commit();
     if (lane == 0) valid_of[warp][slot] = valid;
@@ -464,129 +448,68 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
     now.t0 += BLOCK;
     now.col += skip_cols;
     now.off += skip_off;
-    if (now.off >= c.page) {
-      now.off -= c.page;
+    if (now.off >= p.page) {
+      now.off -= p.page;
       ++now.col;
     }
   };
 
-  read_pages(segs[0], pages);
-  read_pages(segs[1], pages2);
-  now = plan(segs[0]);
   int done = 0, stage = 0;   // steps that are computed, the next one's place
-  bool first_segment = true;
   // Issues what there is until the ring is full; the slot of the step before
   // `done` is free.
   auto fill = [&]() {
+#pragma unroll 1
     while (issued < done + STAGES) {
       if (now.left == 0) {
-        if (ls != cs) break;   // no further than one segment ahead
-        const int to = cs == 2 ? 0 : cs + 1;
-        const Load l = plan(segs[to]);
-        if (l.left == 0) break;
-        now = l;
+        if (moved || then.left == 0) break;   // one segment ahead, no further
+        now = then;
         pages = pages2;
-        ls = to;
+        loads = next;
+        moved = true;
       }
       issue();
     }
   };
 
-  for (;;) {
-    fill();
-    const Segment& seg = segs[cs];
-    if (tid == 32) s_walk.next(p, &segs[cs == 0 ? 2 : cs - 1]);
+  // Turn k computes segment k; meanwhile the warps load on into segment k + 1
+  // and one thread looks for segment k + 2.  Turns −2 and −1 have none yet.
+  bool first_segment = true;
+#pragma unroll 1
+  for (int turn = -2;; turn = turn < 0 ? turn + 1 : 0) {
+    if (tid == 32) next_segment<C>(p, &s_walk, &segs[find]);
+    if (turn >= -1) {
+      if (!moved) {
+        now = then;
+        pages = pages2;
+        loads = cur;
+      }
+      moved = false;
+      const Segment& s = segs[next];
+      then = {};
+      if (s.there) {
+        then.t0 = s.blk0 * BLOCK + warp * STEP;
+        const int end = min(s.n, s.blk1 * BLOCK) - 1;   // the last token
+        if (then.t0 <= end) {
+          then.left = (end - then.t0) / BLOCK + 1;
+          then.col = then.t0 / p.page;
+          then.off = then.t0 - then.col * p.page;
+          pages2.start(row_of(s), then.col, end / p.page + 1, lane);
+        }
+      }
+    }
+
+    const Segment& seg = segs[cur];   // not read in the first two turns
     const int row0 = seg.tile * C::ROWS, rows = p.per_seq * p.group;
     const int len = seg.len, n = seg.n;
     const int64_t qrow = (int64_t)seg.seq * p.per_seq;
-    if (len > n && tid == 0) record_error(p.status, kDevPage, 43);
-
+    const int last = turn < 0 ? 0 : min(n, seg.blk1 * BLOCK);
     // ---- Q: lane (g, t) holds elements of row 8·nt + g as the products take
     // them (over codes, four neighbours of a step instead of two and two)
     uint32_t q[C::QREG ? NT : 1][KS][2];
     float qf[C::QREG ? NT : 1][2];   // scale of rows 8·nt + 2·t4 (+ 1)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + 8 * nt + g;
-      const bool there = r < rows;
-      const int j = there ? r / p.group : 0;
-      const uint16_t* src =
-          static_cast<const uint16_t*>(p.a.q) + (qrow + j) * p.a.q_row +
-          (there ? (int64_t)(seg.kvh * p.group + r - j * p.group) * p.a.q_head
-                 : 0);
-      uint32_t u[KS][2];
-      float amax = 0.0f;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int e0 = 16 * s + (FP8 ? 4 : 2) * t4, e1 = e0 + (FP8 ? 2 : 8);
-        u[s][0] = there ? *reinterpret_cast<const uint32_t*>(src + e0) : 0u;
-        u[s][1] = there ? *reinterpret_cast<const uint32_t*>(src + e1) : 0u;
-      }
-      float f = 1.0f;
-      if (!BF) {
-        auto pair = [&](uint32_t x) {
-          return p.a.bf16 ? unpack_bf16x2(x) : unpack_f16x2(x);
-        };
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float2 x = pair(u[s][h]);
-            amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
-          }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^e ≤ amax < 2^(e + 1), and q·2^-e
-        const int e =
-            amax == 0.0f
-                ? 0
-                : min((int)(__float_as_uint(amax) >> 23) - 127, 126);
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        f = e >= -126 ? __uint_as_float((uint32_t)(127 + e) << 23)
-                      : 5.8774717541114375e-39f;   // 2^-127
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float2 x = pair(u[s][h]);
-            u[s][h] = pack_f16x2(x.x * down, x.y * down);
-          }
-      }
-      f *= scale;
-      if constexpr (C::QREG) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          q[nt][s][0] = u[s][0];
-          q[nt][s][1] = u[s][1];
-        }
-        qf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
-        qf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
-      } else if (nt % WARPS == warp) {   // [nt][s][lane] pairs of registers
-        if (t4 == 0) s_qf[8 * nt + g] = f;
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-          reinterpret_cast<uint2*>(join)[(nt * KS + s) * 32 + lane] =
-              make_uint2(u[s][0], u[s][1]);
-      }
-    }
-    if constexpr (!C::QREG) __syncthreads();
-
     float o[KS][NT][4];
     float m[NT][2], l[NT][2], over_codes[FP8 ? NT : 1][2];
     auto& top = pick<FP8>(over_codes, m);   // maxima that the weights refer to
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[s][nt][j] = 0.0f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        m[nt][h] = top[nt][h] = -INFINITY;
-        l[nt][h] = 0.0f;
-      }
-    }
-
     // tokens that row 8·nt + 2·t4 + h sees
     auto seen = [&](int nt, int h) {
       const int rr = row0 + 8 * nt + 2 * t4 + h;
@@ -594,20 +517,104 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
     };
 
     // ---- the warp's steps: 16·MT tokens from BLOCK·blk + STEP·warp on
-    const int last = min(n, seg.blk1 * BLOCK);
+    bool fresh = turn >= 0;
 #pragma unroll 1
-    for (int t0 = seg.blk0 * BLOCK + warp * STEP; t0 < last; t0 += BLOCK) {
+    for (int t0 = turn < 0 ? 0 : seg.blk0 * BLOCK + warp * STEP;;
+         t0 += BLOCK) {
+      if (turn >= -1) fill();
+      if (fresh) {
+        fresh = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = row0 + 8 * nt + g;
+          const bool there = r < rows;
+          const int j = there ? r / p.group : 0;
+          const uint16_t* src =
+              static_cast<const uint16_t*>(p.a.q) + (qrow + j) * p.a.q_row +
+              (there ? (int64_t)(seg.kvh * p.group + r - j * p.group) * p.a.q_head
+                     : 0);
+          uint32_t u[KS][2];
+          float amax = 0.0f;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const int e0 = 16 * s + (FP8 ? 4 : 2) * t4, e1 = e0 + (FP8 ? 2 : 8);
+            u[s][0] = there ? *reinterpret_cast<const uint32_t*>(src + e0) : 0u;
+            u[s][1] = there ? *reinterpret_cast<const uint32_t*>(src + e1) : 0u;
+          }
+          float f = 1.0f;
+          if (!BF) {
+            auto pair = [&](uint32_t x) {
+              return p.a.bf16 ? unpack_bf16x2(x) : unpack_f16x2(x);
+            };
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float2 x = pair(u[s][h]);
+                amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+              }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^e ≤ amax < 2^(e + 1), and q·2^-e
+            const int e =
+                amax == 0.0f
+                    ? 0
+                    : min((int)(__float_as_uint(amax) >> 23) - 127, 126);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            f = e >= -126 ? __uint_as_float((uint32_t)(127 + e) << 23)
+                          : 5.8774717541114375e-39f;   // 2^-127
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float2 x = pair(u[s][h]);
+                u[s][h] = pack_f16x2(x.x * down, x.y * down);
+              }
+          }
+          f *= scale;
+          if constexpr (C::QREG) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              q[nt][s][0] = u[s][0];
+              q[nt][s][1] = u[s][1];
+            }
+            qf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
+            qf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+          } else if (nt % WARPS == warp) {   // [nt][s][lane] pairs of registers
+            if (t4 == 0) s_qf[8 * nt + g] = f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+              reinterpret_cast<uint2*>(join)[(nt * KS + s) * 32 + lane] =
+                  make_uint2(u[s][0], u[s][1]);
+          }
+        }
+        if constexpr (!C::QREG) __syncthreads();
+
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[s][nt][j] = 0.0f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            m[nt][h] = top[nt][h] = -INFINITY;
+            l[nt][h] = 0.0f;
+          }
+        }
+
+      }
+      if (t0 >= last) break;
       // this step's copies are done when those issued after it may not be
       switch (issued - done - 1) {
         case 0: cp_async_wait<0>(); break;
         case 1: cp_async_wait<1>(); break;
         case 2: cp_async_wait<2>(); break;
-        default: cp_async_wait<3>();
+        case 3: cp_async_wait<3>(); break;
+        default: cp_async_wait<4>();
       }
       static_assert(STAGES <= 5, "waits for the ring's steps");
       __syncwarp();
-      fill();
-      ++done;
       const uint32_t kt = smem_u32(ring) + stage * C::STAGE, vt = kt + C::TILE;
       const uint32_t valid = valid_of[warp][stage];
 
@@ -883,6 +890,17 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
           }
       }
       if (++stage == STAGES) stage = 0;
+      ++done;
+      __syncwarp();   // its place in the ring is free
+    }
+    const int old = cur;
+    cur = next;
+    next = find;
+    find = old;
+    if (turn < 0) {
+      __syncthreads();   // the segment that was found
+      if (turn == -1 && !segs[cur].there) return;
+      continue;
     }
 
     // ---- the warps' results together
@@ -903,31 +921,56 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
     const bool part = seg.blk0 > 0 || seg.blk1 < seg.nb;
     const int64_t part_at = 2 * (int64_t)blockIdx.x + !first_segment;
     __syncthreads();   // and Q is read
-    if (seg.blk0 == 0 && seg.blk1 < seg.nb && tid == 0) {
-      // the CTA of slot x is the last one c with ⌊total·c / ctas⌋ ≤ x
-      const int64_t end = seg.first + seg.nb - 1;
-      Cut cut;
-      cut.seq = seg.seq;
-      cut.head = seg.kvh;
-      cut.tile = seg.tile;
-      cut.first_slot = (int)part_at;
-      cut.parts =
-          (int)(quotient((end + 1) * ctas - 1, total) - blockIdx.x + 1);
-      p.cuts[blockIdx.x] = cut;
+    if (tid < C::ROWS) {
+      const int r = tid;
+      float mm = s_m[0][r], tt = s_top[0][r], sum = 0.0f;
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) {
+        mm = fmaxf(mm, s_m[w][r]);
+        tt = fmaxf(tt, s_top[w][r]);
+      }
+      // a warp without a maximum has l = 0, or NaN of NaN scores
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w)
+        sum = s_m[w][r] == -INFINITY
+                  ? sum + s_l[w][r]
+                  : fmaf(s_l[w][r], ex2_approx(s_m[w][r] - mm), sum);
+      const bool none = sum == 0.0f;
+      s_ref[r] = tt;
+      s_out[r] = none ? 0.0f : (FP8 ? ex2_approx(tt - mm) : 1.0f) / sum;
+      const float lse2 = none ? -INFINITY : mm + log2f(sum);
+      const int rr = row0 + r, j = rr / p.group;
+      if (rr >= rows) {
+      } else if (part) {
+        p.part_lse[part_at * C::ROWS + r] = lse2;
+      } else if (p.a.lse != nullptr) {
+        p.a.lse[(qrow + j) * p.a.n_q + seg.kvh * p.group + rr -
+                j * p.group] = lse2 * LN2;
+      }
     }
-    // Halves of the warps take the other half's in, eight rows at a time, then
+    if (tid == THREADS - 1) {
+      if (len > n) record_error(p.status, kDevPage, 43);
+      if (seg.blk0 == 0 && seg.blk1 < seg.nb) {
+        Cut cut;
+        cut.seq = seg.seq;
+        cut.head = seg.kvh;
+        cut.tile = seg.tile;
+        cut.first_slot = (int)part_at;
+        cut.parts = pieces.cta_of(seg.first + seg.nb - 1) - blockIdx.x + 1;
+        p.cuts[blockIdx.x] = cut;
+      }
+    }
+    __syncthreads();
+    // Half of the warps take the other half's in, eight rows at a time, then
     // all threads add what is left.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float f[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 8 * nt + 2 * t4 + h;
-        float all = s_top[0][r];
-#pragma unroll
-        for (int w = 1; w < WARPS; ++w) all = fmaxf(all, s_top[w][r]);
-        f[h] = top[nt][h] == -INFINITY ? 0.0f : ex2_approx(top[nt][h] - all);
-      }
+      for (int h = 0; h < 2; ++h)
+        f[h] = top[nt][h] == -INFINITY
+                   ? 0.0f
+                   : ex2_approx(top[nt][h] - s_ref[8 * nt + 2 * t4 + h]);
       float* const mine =
           join + ((warp % (WARPS / 2)) * 8 + 2 * t4) * (D + 4) +
           (FP8 ? 2 * g : g);
@@ -954,23 +997,12 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       }
       __syncthreads();
       constexpr int QUADS = D / 4;
+#pragma unroll 1
       for (int i = tid; i < 8 * QUADS; i += THREADS) {
         const int r8 = i / QUADS, e = 4 * (i - r8 * QUADS);
         const int r = 8 * nt + r8, rr = row0 + r;
         if (rr >= rows) break;
-        float mm = s_m[0][r], tt = s_top[0][r];
-#pragma unroll
-        for (int w = 1; w < WARPS; ++w) {
-          mm = fmaxf(mm, s_m[w][r]);
-          tt = fmaxf(tt, s_top[w][r]);
-        }
-        float sum = 0.0f;
-        // a warp without a maximum has l = 0, or NaN of NaN scores
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w)
-          sum = s_m[w][r] == -INFINITY
-                    ? sum + s_l[w][r]
-                    : fmaf(s_l[w][r], ex2_approx(s_m[w][r] - mm), sum);
+        const float y = s_out[r];
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < WARPS / 2; ++w) {
@@ -981,37 +1013,22 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
           v.z += x.z;
           v.w += x.w;
         }
-        const bool none = sum == 0.0f;
-        const float y = none ? 0.0f : (FP8 ? ex2_approx(tt - mm) : 1.0f) / sum;
         v.x *= y;
         v.y *= y;
         v.z *= y;
         v.w *= y;
-        const float lse2 = none ? -INFINITY : mm + log2f(sum);
         if (part) {
           *reinterpret_cast<float4*>(p.part_o +
                                      (part_at * C::ROWS + r) * D + e) = v;
-          if (e == 0) p.part_lse[part_at * C::ROWS + r] = lse2;
         } else {
           const int j = rr / p.group;
-          const int head = seg.kvh * p.group + rr - j * p.group;
-          store4(p.a, qrow + j, head, e, v);
-          if (e == 0 && p.a.lse != nullptr)
-            p.a.lse[(qrow + j) * p.a.n_q + head] = lse2 * LN2;
+          store4(p.a, qrow + j, seg.kvh * p.group + rr - j * p.group, e, v);
         }
       }
       __syncthreads();   // the sums, and `seg`, are read
     }
+    if (!segs[cur].there) return;
     first_segment = false;
-    const int old = cs;
-    cs = cs == 2 ? 0 : cs + 1;
-    if (!segs[cs].there) return;
-    if (ls == old) {   // nothing of this one is loaded yet
-      ls = cs;
-      now = plan(segs[cs]);
-      pages = pages2;
-    }
-    read_pages(segs[cs == 2 ? 0 : cs + 1], pages2);
   }
 }
 
@@ -1171,6 +1188,14 @@ int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,
   const int tile_rows = tile_rows_of(unit);
   p.tiles = (int)((unit + tile_rows - 1) / tile_rows);
   p.status = status;
+  p.page = c.page;
+  p.pages = (int)c.pages;
+  p.page_s = (int)c.page_stride;
+  p.token_s = (int)c.token_stride;
+  p.head_s = (int)c.head_stride;
+  p.s_page_s = (int)c.s_page_stride;
+  p.s_token_s = (int)c.s_token_stride;
+  p.s_head_s = (int)c.s_head_stride;
   const int sms = device_sm_count();
   const Layout l = layout_of(MAX_CTAS * sms, tile_rows, c.d);
   char* ws = static_cast<char*>(a.ws);
