@@ -559,8 +559,8 @@ typedef struct {
 } tp_kv_cache;
 
 /* Write new tokens: rows of K and V ([rows, n_kv, d], TP_BF16 or TP_F16; a
- * row's and a head's element strides are multiples of 8, such as those of the
- * QKV projection's output), each value rounded once to the cache's type (an
+ * row's and a head's element strides are multiples of 8 below 2^31, such as
+ * those of the QKV projection's output), each value rounded once to the cache's type (an
  * fp16 cache reports TP_ERR_RANGE for what fp16 does not hold).  The new
  * tokens are their sequence's last ones: of m rows, row j belongs to position
  * lens[i] − m + j, and to no token where that is negative (an idle place;

@@ -298,8 +298,8 @@ def fp8_block_empty(rows, cols, group=FP8_ROW, device="cuda"):
     return q, s
 
 
-# The checks of a call run before every launch, which for a generated token is
-# most of its time.  csrc/pycall.cpp makes them for arguments in their ordinary
+# The checks of a call (these and those of the key-value cache below) run before
+# every launch, which for a generated token is most of its time.  csrc/pycall.cpp makes them for arguments in their ordinary
 # form and calls the C entry (2.7 to 4 µs a call); where it finds anything else
 # it answers None, and the functions below check again and say what is wrong.
 # Where it is not built for this Python and torch they make every call.
@@ -312,6 +312,7 @@ class _EveryCallInPython:
         return None
 
     swiglu = swiglu_bwd = norm = gemm = quantize
+    kv_write = kv_read = decode = quantize
 
 
 def _load():
@@ -327,7 +328,9 @@ def _load():
         fast.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in
                     ("tp_quantize_fp8_block", "tp_swiglu_fp8_fwd",
                      "tp_swiglu_fp8_bwd", "tp_add_rmsnorm_fp8_fwd",
-                     "tp_gemm_fp8_block")))
+                     "tp_gemm_fp8_block", "tp_kv_cache_write",
+                     "tp_kv_cache_read", "tp_attn_decode",
+                     "tp_attn_decode_workspace_bytes")))
     except ImportError as e:
         warnings.warn("the block-scaled calls' module is not built for this "
                       f"Python and torch, each call takes longer: {e}")
@@ -714,6 +717,9 @@ def kv_cache_write(k, v, cache, table, lens, start=None, stream=None):
     same number of each, or rows start[i] up to start[i + 1] (int32 [b + 1])
     those of sequence i.  Rows that would lie in front of a sequence, and rows
     outside [start[0], start[b]), are not read."""
+    if _done((_tpcall or _load()).kv_write(cache, table, lens, k, v, start,
+                                           stream), "tp_kv_cache_write"):
+        return
     _kv_move(lib().tp_kv_cache_write, "tp_kv_cache_write", cache, table, lens,
              k, v, start, stream)
 
@@ -722,6 +728,9 @@ def kv_cache_read(cache, table, lens, k, v, start=None, stream=None):
     """What kv_cache_write with the same arguments writes, read back into k and
     v: the last tokens of each sequence (with start, as many as it says: whole
     sequences where start adds up lens).  Other rows are left as they were."""
+    if _done((_tpcall or _load()).kv_read(cache, table, lens, k, v, start,
+                                          stream), "tp_kv_cache_read"):
+        return
     _kv_move(lib().tp_kv_cache_read, "tp_kv_cache_read", cache, table, lens,
              k, v, start, stream)
 
@@ -740,6 +749,10 @@ def attn_decode(q, cache, table, lens, out, lse=None, scale=None, ws=None,
     log of the sum of e^score, -inf of such a row.  scale: 1/√d.  ws: scratch
     of attn_decode_workspace_bytes, of this call alone while it runs; made
     anew where it is None."""
+    if _done((_tpcall or _load()).decode(q, cache, table, lens, out, lse,
+                                         scale, ws, stream),
+             "tp_attn_decode"):
+        return
     c, dev = _kv_cache(cache, table, lens)
     code = _kv_16bit(q, "q")
     if q.dim() != 3:

@@ -81,7 +81,8 @@ def _build_pycall():
         return "torch not found"
     src = os.path.join(CSRC, "pycall.cpp")
     if os.path.exists(path) and os.path.getmtime(path) >= max(
-            os.path.getmtime(src), os.path.getmtime(__file__)):
+            os.path.getmtime(src), os.path.getmtime(__file__),
+            os.path.getmtime(os.path.join(INCLUDE, "tp.h"))):
         return None
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:

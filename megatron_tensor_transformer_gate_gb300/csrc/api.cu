@@ -1431,7 +1431,7 @@ tp_status check_rows(int64_t rows, int64_t heads, int64_t d, const void* p,
   *row_used = used(row, rows);
   *head_used = used(head, heads);
   if (*row_used % 8 || *head_used % 8 || *row_used < 0 || *head_used < 0 ||
-      *row_used > kMaxStride / rows || *head_used > kMaxStride / heads)
+      *row_used > INT32_MAX || *head_used > INT32_MAX)
     return TP_ERR_SHAPE;
   if (written &&
       !apart(d, {{{*row_used, rows}, {*head_used, heads}, {0, 1}}}))

@@ -1,5 +1,5 @@
-// pycall.cpp — CPython module _tpcall: the block-scaled E4M3 calls of binding.py
-// for arguments in their ordinary form.
+// pycall.cpp — CPython module _tpcall: the block-scaled E4M3 calls and those of
+// the key-value cache of binding.py for arguments in their ordinary form.
 //
 // A generated token's calls are as long as what the host does before their
 // launch, and reading eight tensors' types, shapes, strides, devices and
@@ -11,11 +11,14 @@
 // function goes through its own checks and says what is wrong.  It returns the
 // tp_status else.
 #define PY_SSIZE_T_CLEAN
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+
+#include "../../include/tp.h"
 
 namespace {
 
@@ -47,6 +50,11 @@ swiglu_fn c_swiglu;
 swiglu_bwd_fn c_swiglu_bwd;
 norm_fn c_norm;
 gemm_fn c_gemm;
+// the key-value cache's entries, as tp.h declares them
+decltype(&tp_kv_cache_write) c_kv_write;
+decltype(&tp_kv_cache_read) c_kv_read;
+decltype(&tp_attn_decode) c_decode;
+decltype(&tp_attn_decode_workspace_bytes) c_decode_ws;
 
 struct view {
   int64_t rows, cols, ld;  // a vector: rows elements, cols = 1
@@ -247,14 +255,202 @@ PyObject* gemm(PyObject*, PyObject* const* x, Py_ssize_t n) {
               c.ld, st));
 }
 
-// bind(five addresses): the C entries
+// ------------------------------------------------------- key-value cache --
+// The tensor on device dev; null if it is none or elsewhere.
+const at::Tensor* on(PyObject* o, long dev, int64_t dims) {
+  if (!THPVariable_Check(o)) return nullptr;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() != dims ||
+      t.get_device() != dev)
+    return nullptr;
+  return &t;
+}
+
+int kv_type(const at::Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kBFloat16: return TP_BF16;
+    case at::kHalf: return TP_F16;
+    case at::kFloat8_e4m3fn:
+    case at::kByte: return TP_FP8;
+    default: return -1;
+  }
+}
+
+// (k, v, ks, vs), table and lens into the C descriptor.
+bool kv_cache(PyObject* cache, PyObject* table, PyObject* lens, tp_kv_cache* c,
+              long* dev) {
+  if (!PyTuple_Check(cache)) return false;
+  const Py_ssize_t n = PyTuple_GET_SIZE(cache);
+  if (n != 2 && n != 4) return false;
+  PyObject* const ko = PyTuple_GET_ITEM(cache, 0);
+  if (!THPVariable_Check(ko) || !THPVariable_Unpack(ko).is_cuda())
+    return false;
+  *dev = THPVariable_Unpack(ko).get_device();
+  const at::Tensor* k = on(ko, *dev, 4);
+  const at::Tensor* v = on(PyTuple_GET_ITEM(cache, 1), *dev, 4);
+  const at::Tensor* t = on(table, *dev, 2);
+  const at::Tensor* l = on(lens, *dev, 1);
+  if (!k || !v || !t || !l || k->scalar_type() != v->scalar_type() ||
+      k->sizes() != v->sizes() || k->strides() != v->strides() ||
+      k->stride(3) != 1 || t->scalar_type() != at::kInt ||
+      l->scalar_type() != at::kInt || l->size(0) != t->size(0) ||
+      (t->size(1) > 1 && t->stride(1) != 1) ||
+      (l->size(0) > 1 && l->stride(0) != 1))
+    return false;
+  c->dtype = kv_type(*k);
+  if (c->dtype < 0) return false;
+  for (int i = 1; i < 4; ++i)   // what the descriptor's fields hold
+    if (k->size(i) > INT32_MAX) return false;
+  if (t->size(0) > INT32_MAX || t->size(1) > INT32_MAX) return false;
+  c->b = (int32_t)t->size(0);
+  c->n_kv = (int32_t)k->size(2);
+  c->d = (int32_t)k->size(3);
+  c->page = (int32_t)k->size(1);
+  c->table_cols = (int32_t)t->size(1);
+  c->pages = k->size(0);
+  c->k = k->data_ptr();
+  c->v = v->data_ptr();
+  c->page_stride = k->stride(0);
+  c->token_stride = k->stride(1);
+  c->head_stride = k->stride(2);
+  c->ks = c->vs = nullptr;
+  c->s_page_stride = c->s_token_stride = c->s_head_stride = 0;
+  PyObject* const kso = n == 4 ? PyTuple_GET_ITEM(cache, 2) : Py_None;
+  PyObject* const vso = n == 4 ? PyTuple_GET_ITEM(cache, 3) : Py_None;
+  if (c->dtype == TP_FP8) {
+    const at::Tensor* ks = on(kso, *dev, 3);
+    const at::Tensor* vs = on(vso, *dev, 3);
+    if (!ks || !vs || ks->scalar_type() != at::kFloat ||
+        vs->scalar_type() != at::kFloat ||
+        ks->sizes() != k->sizes().slice(0, 3) || ks->sizes() != vs->sizes() ||
+        ks->strides() != vs->strides())
+      return false;
+    c->ks = (float*)ks->data_ptr();
+    c->vs = (float*)vs->data_ptr();
+    c->s_page_stride = ks->stride(0);
+    c->s_token_stride = ks->stride(1);
+    c->s_head_stride = ks->stride(2);
+  } else if (kso != Py_None || vso != Py_None) {
+    return false;
+  }
+  c->table = (const int32_t*)t->data_ptr();
+  c->table_stride = t->stride(0);
+  c->lens = (const int32_t*)l->data_ptr();
+  return true;
+}
+
+// Rows [rows, heads, d] with adjacent elements of a vector.
+const at::Tensor* kv_rows(PyObject* o, long dev, int64_t rows, int64_t heads,
+                          int64_t d, at::ScalarType type) {
+  const at::Tensor* t = on(o, dev, 3);
+  if (!t || t->scalar_type() != type || t->size(0) != rows ||
+      t->size(1) != heads || t->size(2) != d || t->stride(2) != 1)
+    return nullptr;
+  return t;
+}
+
+// cache, table, lens, k, v, start, stream
+template <bool WRITE>
+PyObject* kv_move(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  tp_kv_cache c;
+  long dev;
+  void* st;
+  if (n != 7 || !kv_cache(x[0], x[1], x[2], &c, &dev)) return not_handled();
+  const at::Tensor* k = on(x[3], dev, 3);
+  if (!k || (k->scalar_type() != at::kBFloat16 &&
+             k->scalar_type() != at::kHalf))
+    return not_handled();
+  const int64_t rows = k->size(0);
+  k = kv_rows(x[3], dev, rows, c.n_kv, c.d, k->scalar_type());
+  if (!k) return not_handled();
+  const at::Tensor* v =
+      kv_rows(x[4], dev, rows, c.n_kv, c.d, k->scalar_type());
+  if (!v) return not_handled();
+  const int32_t* start = nullptr;
+  if (x[5] != Py_None) {
+    const at::Tensor* s = on(x[5], dev, 1);
+    if (!s || s->scalar_type() != at::kInt || s->size(0) != c.b + 1 ||
+        s->stride(0) != 1)
+      return not_handled();
+    start = (const int32_t*)s->data_ptr();
+  } else if (c.b == 0 || rows % c.b) {
+    return not_handled();
+  }
+  if (!stream_of(x[6], dev, &st)) return not_handled();
+  const int type = kv_type(*k);
+  void *const pk = k->data_ptr(), *const pv = v->data_ptr();
+  const int64_t kr = k->stride(0), kh = k->stride(1), vr = v->stride(0),
+                vh = v->stride(1);
+  if (WRITE) {
+    CALL(c_kv_write(&c, type, rows, pk, kr, kh, pv, vr, vh, start, st));
+  }
+  CALL(c_kv_read(&c, type, rows, pk, kr, kh, pv, vr, vh, start, st));
+}
+
+// q, cache, table, lens, out, lse, scale, ws, stream
+PyObject* decode(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  tp_kv_cache c;
+  long dev;
+  void* st;
+  if (n != 9 || !kv_cache(x[1], x[2], x[3], &c, &dev)) return not_handled();
+  const at::Tensor* q = on(x[0], dev, 3);
+  if (!q || (q->scalar_type() != at::kBFloat16 &&
+             q->scalar_type() != at::kHalf))
+    return not_handled();
+  const int64_t rows = q->size(0), n_q = q->size(1);
+  q = kv_rows(x[0], dev, rows, n_q, c.d, q->scalar_type());
+  if (!q || c.b == 0 || c.n_kv == 0 || rows % c.b || n_q % c.n_kv ||
+      n_q > INT32_MAX || (c.dtype == TP_BF16 && kv_type(*q) == TP_F16))
+    return not_handled();
+  const at::Tensor* out =
+      kv_rows(x[4], dev, rows, n_q, c.d, q->scalar_type());
+  if (!out) return not_handled();
+  float* lse = nullptr;
+  if (x[5] != Py_None) {
+    const at::Tensor* l = on(x[5], dev, 2);
+    if (!l || l->scalar_type() != at::kFloat || l->size(0) != rows ||
+        l->size(1) != n_q || !l->is_contiguous())
+      return not_handled();
+    lse = (float*)l->data_ptr();
+  }
+  double scale = 0.0;
+  if (x[6] == Py_None) {
+    scale = c.d == 128 ? 0.088388347648318447 : c.d == 64 ? 0.125 : 0.0;
+    if (scale == 0.0) return not_handled();
+  } else {
+    scale = PyFloat_AsDouble(x[6]);
+    if (PyErr_Occurred()) return not_handled();
+  }
+  if (!stream_of(x[8], dev, &st)) return not_handled();
+  at::Tensor ws;
+  const size_t need = c_decode_ws(&c, rows, (int32_t)n_q);
+  if (x[7] == Py_None) {
+    // memory of the current stream's: for another one binding.py makes it
+    if (x[8] != Py_None) return not_handled();
+    ws = at::empty({(int64_t)need},
+                   at::TensorOptions(at::kByte).device(at::kCUDA, dev));
+  } else {
+    if (!THPVariable_Check(x[7])) return not_handled();
+    ws = THPVariable_Unpack(x[7]);
+    if (!ws.is_cuda() || ws.get_device() != dev || !ws.is_contiguous())
+      return not_handled();
+  }
+  const size_t size = ws.nbytes();
+  void *const pq = q->data_ptr(), *const po = out->data_ptr(),
+             *const pw = size ? ws.data_ptr() : nullptr;
+  CALL(c_decode(&c, kv_type(*q), rows, (int32_t)n_q, (float)scale, pq,
+                q->stride(0), q->stride(1), po, out->stride(0), out->stride(1),
+                lse, pw, size, st));
+}
+
+// bind(nine addresses): the C entries
 PyObject* bind(PyObject*, PyObject* const* x, Py_ssize_t n) {
-  void* fn[5];
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind takes 5 arguments");
+  void* fn[9];
+  if (n != 9) {
+    PyErr_SetString(PyExc_TypeError, "bind takes 9 arguments");
     return nullptr;
   }
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 9; ++i) {
     fn[i] = PyLong_AsVoidPtr(x[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -263,6 +459,10 @@ PyObject* bind(PyObject*, PyObject* const* x, Py_ssize_t n) {
   c_swiglu_bwd = (swiglu_bwd_fn)fn[2];
   c_norm = (norm_fn)fn[3];
   c_gemm = (gemm_fn)fn[4];
+  c_kv_write = (decltype(c_kv_write))fn[5];
+  c_kv_read = (decltype(c_kv_read))fn[6];
+  c_decode = (decltype(c_decode))fn[7];
+  c_decode_ws = (decltype(c_decode_ws))fn[8];
   Py_RETURN_NONE;
 }
 
@@ -288,6 +488,9 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<caught<swiglu_bwd>>("swiglu_bwd"),
                          method<caught<norm>>("norm"),
                          method<caught<gemm>>("gemm"),
+                         method<caught<kv_move<true>>>("kv_write"),
+                         method<caught<kv_move<false>>>("kv_read"),
+                         method<caught<decode>>("decode"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tpcall", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
