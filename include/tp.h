@@ -567,8 +567,7 @@ typedef struct {
  * padding in front of a short prompt).  start NULL: rows = b·m, m for each
  * sequence in turn; else device int32 [b + 1], not decreasing: sequence i's
  * are rows start[i] up to start[i + 1], and rows outside [start[0], start[b])
- * are no tokens.  Rows of no token are not read and nothing is written for
- * them.  Positions that two rows of one call share hold either's value. */
+ * are no tokens.  For rows of no token nothing is written.  Positions that two rows of one call share hold either's value. */
 tp_status tp_kv_cache_write(const tp_kv_cache* c, int32_t dtype, int64_t rows,
                             const void* K, int64_t k_row, int64_t k_head,
                             const void* V, int64_t v_row, int64_t v_head,

@@ -715,8 +715,8 @@ def kv_cache_write(k, v, cache, table, lens, start=None, stream=None):
     """New tokens' k and v rows ([rows, n_kv, d], bf16 or fp16) into the cache.
     lens counts them already: they are the last tokens of their sequences, the
     same number of each, or rows start[i] up to start[i + 1] (int32 [b + 1])
-    those of sequence i.  Rows that would lie in front of a sequence, and rows
-    outside [start[0], start[b]), are not read."""
+    those of sequence i.  For rows that would lie in front of a sequence, and
+    for rows outside [start[0], start[b]), nothing is written."""
     if _done((_tpcall or _load()).kv_write(cache, table, lens, k, v, start,
                                            stream), "tp_kv_cache_write"):
         return
