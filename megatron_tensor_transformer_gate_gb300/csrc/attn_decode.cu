@@ -29,8 +29,10 @@
 // rounded to fp16 (2^-11); over bf16 values, where bf16 (2^-8) would show in
 // the output, it is the sum of two bf16 parts, 2^-16, at the price of a second
 // product.  A code's scale is multiplied into its score, and into its weight in
-// front of the product with V: w = 2^(x + log₂ s_v − M) with a running maximum
-// M of its own, so that scales of any size keep the weights in fp16's range.
+// front of the product with V: t = x + log₂ s_v, w = 2^(t − M) with M the
+// running maximum of t, so that scales of any size keep the weights of the
+// sum in fp16's range; the denominator is Σ w / s_v, relative to the same M
+// (fp32's range leaves s_v a factor of 2^100 from token to token).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -81,7 +83,9 @@ struct Conf {
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int CTAS = 2;                   // on an SM
-  static constexpr int STEP = ROW == 256 || NT == 4 ? 16 : 32;   // tokens of a warp at a time
+  // tokens of a warp: that are loaded, and that are worked on at a time
+  static constexpr int STEP = ROW == 256 ? 16 : 32;
+  static constexpr int PART = ROW == 256 || NT == 4 ? 16 : 32;
   static constexpr int BLOCK = STEP * WARPS;       // of a CTA
   static constexpr int EXTRA = (UNIT_TOKENS + BLOCK - 1) / BLOCK;
   static constexpr int TILE = STEP * ROW;
@@ -233,14 +237,6 @@ struct Pages {
   }
 };
 
-template <bool FIRST, class A, class B>
-__device__ __forceinline__ auto& pick(A& a, B& b) {
-  if constexpr (FIRST)
-    return a;
-  else
-    return b;
-}
-
 // A segment: blocks [blk0, blk1) of a unit.  Units take nb + EXTRA slots of
 // the CTAs' pieces, so that many short ones weigh what they cost; the blocks
 // lie behind the extra ones.
@@ -297,7 +293,8 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
   using C = Conf<CACHE, D, NT>;
   constexpr bool FP8 = CACHE == TP_FP8, BF = CACHE == TP_BF16;
   constexpr int WARPS = C::WARPS, THREADS = C::THREADS, STAGES = C::STAGES;
-  constexpr int STEP = C::STEP, BLOCK = C::BLOCK, MT = STEP / 16;
+  constexpr int STEP = C::STEP, BLOCK = C::BLOCK;
+  constexpr int PART = C::PART, MT = PART / 16;
   constexpr int KS = D / 16;          // steps of 16 elements
   constexpr int ROW = C::ROW, CHUNKS = ROW / 16;
   extern __shared__ unsigned char smem_raw[];
@@ -305,8 +302,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
   __shared__ Segment segs[3];   // the one computed, the next, the one after it
   __shared__ uint32_t valid_of[WARPS][STAGES];
   __shared__ float s_qf[C::ROWS];
-  __shared__ float s_m[WARPS][C::ROWS], s_top[WARPS][C::ROWS],
-      s_l[WARPS][C::ROWS];
+  __shared__ float s_top[WARPS][C::ROWS], s_l[WARPS][C::ROWS];
   __shared__ float s_ref[C::ROWS], s_out[C::ROWS];
   const tp_kv_cache& c = p.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -508,8 +504,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
     uint32_t q[C::QREG ? NT : 1][KS][2];
     float qf[C::QREG ? NT : 1][2];   // scale of rows 8·nt + 2·t4 (+ 1)
     float o[KS][NT][4];
-    float m[NT][2], l[NT][2], over_codes[FP8 ? NT : 1][2];
-    auto& top = pick<FP8>(over_codes, m);   // maxima that the weights refer to
+    float top[NT][2], l[NT][2];   // running maxima of t, sums
     // tokens that row 8·nt + 2·t4 + h sees
     auto seen = [&](int nt, int h) {
       const int rr = row0 + 8 * nt + 2 * t4 + h;
@@ -598,7 +593,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
             for (int j = 0; j < 4; ++j) o[s][nt][j] = 0.0f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            m[nt][h] = top[nt][h] = -INFINITY;
+            top[nt][h] = -INFINITY;
             l[nt][h] = 0.0f;
           }
         }
@@ -615,8 +610,14 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       }
       static_assert(STAGES <= 5, "waits for the ring's steps");
       __syncwarp();
-      const uint32_t kt = smem_u32(ring) + stage * C::STAGE, vt = kt + C::TILE;
-      const uint32_t valid = valid_of[warp][stage];
+      const uint32_t valid_all = valid_of[warp][stage];
+#pragma unroll 1
+      for (int part = 0; part < STEP; part += PART) {
+      const int t1 = t0 + part;   // the part's first token
+      unsigned char* const rows_at = ring + stage * C::STAGE + part * ROW;
+      const uint32_t kt = smem_u32(rows_at), vt = kt + C::TILE;
+      constexpr uint32_t FULL = 0xffffffffu >> (32 - PART);
+      const uint32_t valid = valid_all >> part & FULL;
 
       // ---- Sᵀ = K·Qᵀ
       float sc[MT][NT][4];
@@ -671,17 +672,20 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       }
 
       // ---- softmax of the lane's rows 2·t4, 2·t4 + 1 at tokens 16·mt + g and
-      // 16·mt + g + 8
-      float sk[MT][2], lv[MT][2];
+      // 16·mt + g + 8: t into sc
+      float sk[MT][2], lv[MT][2], back[MT][2];   // s_k, log₂ s_v, 1 / s_v
       if (FP8) {
         const float* ss = reinterpret_cast<const float*>(
-            ring + stage * C::STAGE + 2 * C::TILE);
+                              ring + stage * C::STAGE + 2 * C::TILE) +
+                          part;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             sk[mt][h] = ss[16 * mt + g + 8 * h];
             lv[mt][h] = lg2_approx(ss[STEP + 16 * mt + g + 8 * h]);
+            // (0 where nothing was loaded)
+            back[mt][h] = lv[mt][h] == -INFINITY ? 0.0f : ex2_approx(-lv[mt][h]);
           }
       }
 #pragma unroll
@@ -695,15 +699,16 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
               f = qf[nt][j & 1];
             else
               f = s_qf[8 * nt + 2 * t4 + (j & 1)];
-            sc[mt][nt][j] *= FP8 ? f * sk[mt][j >> 1] : f;
+            float& x = sc[mt][nt][j];
+            x = FP8 ? fmaf(x * sk[mt][j >> 1], f, lv[mt][j >> 1]) : x * f;
           }
-      const bool mixed = p.per_seq > 1 && t0 > len - p.per_seq + 1 - STEP;
-      if (valid != 0xffffffffu >> (32 - STEP) || mixed) {
+      const bool mixed = p.per_seq > 1 && t1 > len - p.per_seq + 1 - PART;
+      if (valid != FULL || mixed) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int end = seen(nt, h) - t0;
+            const int end = seen(nt, h) - t1;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -714,43 +719,34 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
               }
           }
       }
-      float hi[NT][2], hi2[NT][2];
+      float high[NT][2];
       bool rise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float x = m[nt][h], y = top[nt][h];
+          float x = fmaxf(sc[0][nt][h], sc[0][nt][2 + h]);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int mt = 1; mt < MT; ++mt)
             x = fmaxf(x, fmaxf(sc[mt][nt][h], sc[mt][nt][2 + h]));
-            if (FP8)
-              y = fmaxf(y, fmaxf(sc[mt][nt][h] + lv[mt][0],
-                                 sc[mt][nt][2 + h] + lv[mt][1]));
-          }
-          hi[nt][h] = x;
-          hi2[nt][h] = FP8 ? y : x;
-          rise |= x > m[nt][h] || (FP8 && y > top[nt][h]);
+          high[nt][h] = x;
+          rise |= x > top[nt][h];
         }
       if (__any_sync(0xffffffffu, rise)) {   // new maxima
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float x = hi[nt][h], y = hi2[nt][h];
+            float x = fmaxf(high[nt][h], top[nt][h]);
 #pragma unroll
-            for (int z = 4; z < 32; z <<= 1) {
+            for (int z = 4; z < 32; z <<= 1)
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
-              if (FP8) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
-            }
-            if (!FP8) y = x;
             // 0 where there was nothing yet
-            l[nt][h] *= m[nt][h] == -INFINITY ? 0.0f : ex2_approx(m[nt][h] - x);
             const float f = top[nt][h] == -INFINITY
                                 ? 0.0f
-                                : ex2_approx(top[nt][h] - y);
-            top[nt][h] = y;
-            m[nt][h] = x;
+                                : ex2_approx(top[nt][h] - x);
+            top[nt][h] = x;
+            l[nt][h] *= f;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
               o[s][nt][h] *= f;
@@ -763,20 +759,14 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float ref = m[nt][h] == -INFINITY ? 0.0f : m[nt][h];
-          const float far = top[nt][h] == -INFINITY ? 0.0f : top[nt][h];
+          const float ref = top[nt][h] == -INFINITY ? 0.0f : top[nt][h];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               float& x = sc[mt][nt][2 * k + h];
-              const float w = ex2_approx(x - ref);
-              l[nt][h] += w;
-              // (an infinite scale must not make NaN of a token left out)
-              if (FP8)
-                x = x == -INFINITY ? 0.0f : ex2_approx(x + lv[mt][k] - far);
-              else
-                x = w;
+              x = ex2_approx(x - ref);
+              l[nt][h] = FP8 ? fmaf(x, back[mt][k], l[nt][h]) : l[nt][h] + x;
             }
         }
       if (mixed) {
@@ -784,16 +774,16 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
         // a later token's v holds (NaN, say) must not reach a row that does
         // not see it through a weight of 0: the last tokens' products are
         // added one by one, and their v then cleared.
-        const int k1 = min(STEP, n - t0);
+        const int k1 = min(PART, n - t1);
 #pragma unroll 1
-        for (int k = max(0, len - p.per_seq + 1 - t0); k < k1; ++k) {
+        for (int k = max(0, len - p.per_seq + 1 - t1); k < k1; ++k) {
           float w[NT][2];
           uint32_t sees = 0;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (t0 + k < seen(nt, h)) sees |= 1u << (2 * nt + h);
+              if (t1 + k < seen(nt, h)) sees |= 1u << (2 * nt + h);
               w[nt][h] = 0.0f;
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
@@ -804,7 +794,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
                   if (k >> 3 == 2 * mt + i) w[nt][h] = x;
                 }
             }
-          unsigned char* const vrow = ring + stage * C::STAGE + C::TILE;
+          unsigned char* const vrow = rows_at + C::TILE;
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
             float2 v;
@@ -889,6 +879,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
             add_values(a, s, mt);
           }
       }
+      }
       if (++stage == STAGES) stage = 0;
       ++done;
       __syncwarp();   // its place in the ring is free
@@ -913,7 +904,6 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
           l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], z);
         if (g == 0) {
           const int r = 8 * nt + 2 * t4 + h;
-          s_m[warp][r] = m[nt][h];
           s_top[warp][r] = top[nt][h];
           s_l[warp][r] = l[nt][h];
         }
@@ -923,22 +913,19 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
     __syncthreads();   // and Q is read
     if (tid < C::ROWS) {
       const int r = tid;
-      float mm = s_m[0][r], tt = s_top[0][r], sum = 0.0f;
+      float all = s_top[0][r], sum = 0.0f;
 #pragma unroll
-      for (int w = 1; w < WARPS; ++w) {
-        mm = fmaxf(mm, s_m[w][r]);
-        tt = fmaxf(tt, s_top[w][r]);
-      }
+      for (int w = 1; w < WARPS; ++w) all = fmaxf(all, s_top[w][r]);
       // a warp without a maximum has l = 0, or NaN of NaN scores
 #pragma unroll
       for (int w = 0; w < WARPS; ++w)
-        sum = s_m[w][r] == -INFINITY
+        sum = s_top[w][r] == -INFINITY
                   ? sum + s_l[w][r]
-                  : fmaf(s_l[w][r], ex2_approx(s_m[w][r] - mm), sum);
+                  : fmaf(s_l[w][r], ex2_approx(s_top[w][r] - all), sum);
       const bool none = sum == 0.0f;
-      s_ref[r] = tt;
-      s_out[r] = none ? 0.0f : (FP8 ? ex2_approx(tt - mm) : 1.0f) / sum;
-      const float lse2 = none ? -INFINITY : mm + log2f(sum);
+      s_ref[r] = all;
+      s_out[r] = none ? 0.0f : 1.0f / sum;
+      const float lse2 = none ? -INFINITY : all + log2f(sum);
       const int rr = row0 + r, j = rr / p.group;
       if (rr >= rows) {
       } else if (part) {
