@@ -47,9 +47,7 @@
 namespace tp {
 namespace {
 
-constexpr int UNIT_TOKENS = 256;   // a segment's fixed cost, in tokens of work
 constexpr int MAX_CTAS = 4;        // on an SM
-constexpr int MIN_SLOTS = 3;       // of a CTA, where there is little to do
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -72,6 +70,17 @@ struct Params {
   unsigned* status;
   // the cache's strides (elements; a product of two is formed in 64 bits)
   int page, pages, page_s, token_s, head_s, s_page_s, s_token_s, s_head_s;
+  int units;                 // of a sequence
+  int cap;                   // tokens that a row of the table can list (≤ 2^30)
+  int skip_cols, skip_off;   // a block's tokens in pages and the rest
+  // ⌊n / page⌋ = n·page_mul >> page_shift for n ≤ 2^30: page_mul =
+  // ⌈2^page_shift / page⌉ is off by less than page·2^-page_shift of itself,
+  // and page_shift = 30 + ⌈log₂ page⌉
+  uint32_t page_mul;
+  int page_shift;
+  __device__ __forceinline__ int col_of(int n) const {
+    return (int)((uint64_t)(uint32_t)n * page_mul >> page_shift);
+  }
 };
 __device__ __forceinline__ int64_t mul(int a, int b) { return (int64_t)a * b; }
 
@@ -87,7 +96,10 @@ struct Conf {
   static constexpr int STEP = ROW == 256 ? 16 : 32;
   static constexpr int PART = ROW == 256 || NT == 4 ? 16 : 32;
   static constexpr int BLOCK = STEP * WARPS;       // of a CTA
-  static constexpr int EXTRA = (UNIT_TOKENS + BLOCK - 1) / BLOCK;
+  // A segment's fixed cost in blocks of work (64x8192 in E4M3: 55, 49, 45 and
+  // 51 µs with 128, 256, 512 and 1024 tokens; 256x1000 in fp16 21.0, 22.3, 24.9
+  // and 28.3).
+  static constexpr int EXTRA = (ROW == 256 ? 128 : 512) / BLOCK;
   static constexpr int TILE = STEP * ROW;
   // K, V and the scales of a step
   static constexpr int STAGE = 2 * TILE + (CACHE == TP_FP8 ? 8 * STEP : 0);
@@ -174,10 +186,8 @@ __device__ __forceinline__ uint32_t spread(int r, int ch) {
 }
 
 // A sequence's tokens that are followed.
-__device__ __forceinline__ int tokens_of(const tp_kv_cache& c, int seq) {
-  const int64_t cap = (int64_t)c.table_cols * c.page;
-  const int n = c.lens[seq];
-  return n < 0 ? 0 : n > cap ? (int)cap : n;
+__device__ __forceinline__ int tokens_of(const Params& p, int seq) {
+  return min(max(p.c.lens[seq], 0), p.cap);
 }
 // The blocks they take (at least one, so that a sequence without any has its
 // rows written too).
@@ -258,11 +268,10 @@ __device__ __forceinline__ void next_segment(const Params& p, Walk* walk,
                                              Segment* out) {
   Walk w = *walk;
   Segment s = {};
-  const int units = p.c.n_kv * p.tiles;
 #pragma unroll 1
   while (w.at < w.stop && !s.there) {
     s.len = max(p.c.lens[w.seq], 0);
-    s.n = tokens_of(p.c, w.seq);
+    s.n = tokens_of(p, w.seq);
     s.nb = blocks_of<C::BLOCK>(s.n);
     s.seq = w.seq;
     const int weight = s.nb + C::EXTRA;
@@ -277,8 +286,8 @@ __device__ __forceinline__ void next_segment(const Params& p, Walk* walk,
     s.blk1 = max(0, x1 - C::EXTRA);
     s.there = s.blk1 > s.blk0;
     w.at += x1 - x0;
-    if (unit == units - 1 && x1 == weight) {
-      w.before += weight * units;
+    if (unit == p.units - 1 && x1 == weight) {
+      w.before += weight * p.units;
       ++w.seq;
     }
   }
@@ -313,14 +322,13 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
   // (each warp for itself: lane l has sequences [l·span, (l + 1)·span))
   Pieces pieces;
   {
-    const int units = c.n_kv * p.tiles;   // of a sequence
     const int span = (c.b + 31) / 32;
     const int i0 = lane * span, i1 = min(i0 + span, c.b);
     auto slots = [&](int i) {
-      return (blocks_of<BLOCK>(tokens_of(c, i)) + C::EXTRA) * units;
+      return (blocks_of<BLOCK>(tokens_of(p, i)) + C::EXTRA) * p.units;
     };
     int sum = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = i0; i < i1; ++i) sum += slots(i);
     int inc = sum;
 #pragma unroll
@@ -329,8 +337,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       if (lane >= o) inc += v;
     }
     pieces.total = __shfl_sync(0xffffffffu, inc, 31);
-    pieces.ctas =
-        min((pieces.total + MIN_SLOTS - 1) / MIN_SLOTS, (int)gridDim.x);
+    pieces.ctas = min(pieces.total, (int)gridDim.x);
     pieces.share = pieces.total / pieces.ctas;
     pieces.more = pieces.total - pieces.share * pieces.ctas;
     const int cta = blockIdx.x;
@@ -355,7 +362,6 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
   const char* const kpool = static_cast<const char*>(c.k);
   const int64_t to_v = static_cast<const char*>(c.v) - kpool;
   const bool whole_pages = p.page % STEP == 0;
-  const int skip_cols = BLOCK / p.page, skip_off = BLOCK % p.page;
   unsigned char* const smem =
       smem_raw + (-smem_u32(smem_raw) & (C::ALIGN - 1));
   float* const join = reinterpret_cast<float*>(smem + WARPS * C::RING);
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
     // the page and the offset of the lane's token
     bool in = tok < rest;
     int off = now.off + tok, ahead = 0;
-    if (!whole_pages && in) ahead = off / p.page;
+    if (!whole_pages && in) ahead = p.col_of(off);
     off -= ahead * p.page;
     const int page = pages.at(now.col + ahead);
     if (in && (page < 0 || page >= p.pages)) {
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
                                   mul(kvh, p.head_s)) *
                                      C::SIZE
                                : 0;
-#pragma unroll 1
+#pragma unroll 4
       for (int k = 0; k < STEP / PER; ++k) {
         const int r = k * PER + sub;
         const char* src = kpool + __shfl_sync(0xffffffffu, place, r) + 16 * ch;
@@ -442,8 +448,8 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
     ++issued;
     --now.left;
     now.t0 += BLOCK;
-    now.col += skip_cols;
-    now.off += skip_off;
+    now.col += p.skip_cols;
+    now.off += p.skip_off;
     if (now.off >= p.page) {
       now.off -= p.page;
       ++now.col;
@@ -487,9 +493,9 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
         const int end = min(s.n, s.blk1 * BLOCK) - 1;   // the last token
         if (then.t0 <= end) {
           then.left = (end - then.t0) / BLOCK + 1;
-          then.col = then.t0 / p.page;
+          then.col = p.col_of(then.t0);
           then.off = then.t0 - then.col * p.page;
-          pages2.start(row_of(s), then.col, end / p.page + 1, lane);
+          pages2.start(row_of(s), then.col, p.col_of(end) + 1, lane);
         }
       }
     }
@@ -1019,79 +1025,135 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
   }
 }
 
-// Joins the parts of the units that were cut: CTA (i, r) row r of the one that
-// CTA i of the first kernel begins, if there is one.
-constexpr int JOIN_THREADS = 256;
+// Joins the parts of the units that were cut: CTA (i, j) rows j·cta_rows up to
+// (j + 1)·cta_rows of the one that CTA i of the first kernel begins, if there is
+// one.  A warp has a row, D/4 lanes of it a part each time; with more than FEW
+// parts all eight warps share a row, one after the other.  What bounds it is its chain of three
+// loads (the cut, its parts, nothing else waits) and a launch.
+constexpr int JOIN_WARPS = 8;
+constexpr int FEW = 8;
 template <int D>
-__global__ void __launch_bounds__(JOIN_THREADS)
-    join_kernel(const Params p, int tile_rows) {
-  constexpr int TEAM = D / 4, TEAMS = JOIN_THREADS / TEAM;
-  __shared__ float s_max[JOIN_THREADS / 32];
-  __shared__ float s_sum[TEAMS];
-  __shared__ float4 s_o[TEAMS][TEAM];
+__global__ void __launch_bounds__(32 * JOIN_WARPS)
+    join_kernel(const Params p, int tile_rows, int cta_rows) {
+  constexpr int LANES = D / 4, SIDE = 32 / LANES;   // of a part, parts a load
+  constexpr int U = 4;
+  __shared__ float s_top[JOIN_WARPS], s_sum[JOIN_WARPS];
+  __shared__ float4 s_o[JOIN_WARPS][LANES];
   // launched while the first kernel runs: everything is read after this
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = p.cuts[blockIdx.x];
-  if (cut.tile < 0) return;
-  const int tid = threadIdx.x;
-  for (int r = blockIdx.y; r < tile_rows; r += gridDim.y) {
-  const int rr = cut.tile * tile_rows + r;
-  if (rr >= p.per_seq * p.group) return;
-  auto slot_of = [&](int i) -> int64_t {
-    return i == 0 ? cut.first_slot : 2 * ((int64_t)blockIdx.x + i);
+  const int r0 = cta_rows * blockIdx.y, warp = threadIdx.x >> 5;
+  const int r1 = min(min(tile_rows, r0 + cta_rows),
+                     p.per_seq * p.group - cut.tile * tile_rows);
+  if (cut.tile < 0 || r0 >= r1) return;
+  const int lane = threadIdx.x & 31, e = 4 * (lane % LANES);
+  const bool few = cut.parts <= FEW;
+  const int stride = SIDE * (few ? 1 : JOIN_WARPS);
+  // o and the sum of parts side, side + stride, … of row r, relative to top
+  float top, sum;
+  float4 v;
+  auto add_parts = [&](int r) {
+    top = -INFINITY;
+    sum = 0.0f;
+    v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = lane / LANES + (few ? 0 : SIDE * warp); i0 < cut.parts;
+         i0 += U * stride) {
+      float x[U];
+      float4 u[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k * stride;
+        x[k] = -INFINITY;
+        u[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < cut.parts) {
+          const int64_t slot =
+              i == 0 ? cut.first_slot : 2 * ((int64_t)blockIdx.x + i);
+          const int64_t at = slot * tile_rows + r;
+          x[k] = p.part_lse[at];
+          u[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + e);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        // a part that saw nothing is left out; NaN is not
+        if (x[k] == -INFINITY) continue;
+        const float high = fmaxf(top, x[k]);
+        const float f = top == -INFINITY ? 0.0f : ex2_approx(top - high);
+        const float w = ex2_approx(x[k] - high);
+        top = high;
+        sum = fmaf(sum, f, w);
+        v.x = fmaf(v.x, f, w * u[k].x);
+        v.y = fmaf(v.y, f, w * u[k].y);
+        v.z = fmaf(v.z, f, w * u[k].z);
+        v.w = fmaf(v.w, f, w * u[k].w);
+      }
+    }
   };
-  float top = -INFINITY;
-  for (int i = tid; i < cut.parts; i += JOIN_THREADS)
-    top = fmaxf(top, p.part_lse[slot_of(i) * tile_rows + r]);
-#pragma unroll
-  for (int z = 16; z > 0; z >>= 1)
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
-  if ((tid & 31) == 0) s_max[tid >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < JOIN_THREADS / 32; ++w) top = fmaxf(top, s_max[w]);
-  // parts i, i + TEAMS, …: each team its own, then the teams in order
-  const int team = tid / TEAM, e = tid % TEAM;
-  float sum = 0.0f;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int i = team; i < cut.parts; i += TEAMS) {
-    const int64_t at = slot_of(i) * tile_rows + r;
-    const float x = p.part_lse[at];
-    const float w = x == -INFINITY ? 0.0f : ex2_approx(x - top);
-    const float4 u = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * e);
-    sum += w;
-    v.x = fmaf(w, u.x, v.x);
-    v.y = fmaf(w, u.y, v.y);
-    v.z = fmaf(w, u.z, v.z);
-    v.w = fmaf(w, u.w, v.w);
+  // another set of parts: (top2, sum2, v2) joins (top, sum, v)
+  auto merge = [&](float top2, float sum2, float4 v2) {
+    const float high = fmaxf(top, top2);
+    const float f = top == -INFINITY ? (sum == 0.0f ? 0.0f : 1.0f)
+                                     : ex2_approx(top - high);
+    const float f2 = top2 == -INFINITY ? (sum2 == 0.0f ? 0.0f : 1.0f)
+                                       : ex2_approx(top2 - high);
+    top = high;
+    sum = sum * f + sum2 * f2;
+    v.x = v.x * f + v2.x * f2;
+    v.y = v.y * f + v2.y * f2;
+    v.z = v.z * f + v2.z * f2;
+    v.w = v.w * f + v2.w * f2;
+  };
+  auto sides = [&]() {   // D = 64: the half-warps' parts
+    if constexpr (SIDE == 2) {
+      float4 v2;
+      const float top2 = __shfl_xor_sync(0xffffffffu, top, 16);
+      const float sum2 = __shfl_xor_sync(0xffffffffu, sum, 16);
+      v2.x = __shfl_xor_sync(0xffffffffu, v.x, 16);
+      v2.y = __shfl_xor_sync(0xffffffffu, v.y, 16);
+      v2.z = __shfl_xor_sync(0xffffffffu, v.z, 16);
+      v2.w = __shfl_xor_sync(0xffffffffu, v.w, 16);
+      merge(top2, sum2, v2);
+    }
+  };
+  auto finish = [&](int r) {
+    const bool none = sum == 0.0f;
+    const float f = none ? 0.0f : 1.0f / sum;
+    const int rr = cut.tile * tile_rows + r, j = rr / p.group;
+    const int head = cut.head * p.group + rr - j * p.group;
+    const int64_t row = (int64_t)cut.seq * p.per_seq + j;
+    v.x *= f;
+    v.y *= f;
+    v.z *= f;
+    v.w *= f;
+    if (lane < LANES) store4(p.a, row, head, e, v);
+    if (lane == 0 && p.a.lse != nullptr)
+      p.a.lse[row * p.a.n_q + head] =
+          none ? -INFINITY : (top + log2f(sum)) * LN2;
+  };
+  if (few) {
+    const int r = r0 + warp;
+    if (r >= r1) return;
+    add_parts(r);
+    sides();
+    finish(r);
+    return;
   }
-  s_o[team][e] = v;
-  if (e == 0) s_sum[team] = sum;
-  __syncthreads();
-  if (team == 0) {
-  for (int k = 1; k < TEAMS; ++k) {
-    const float4 u = s_o[k][e];
-    sum += s_sum[k];
-    v.x += u.x;
-    v.y += u.y;
-    v.z += u.z;
-    v.w += u.w;
-  }
-  const bool none = sum == 0.0f;
-  const float f = none ? 0.0f : 1.0f / sum;
-  const int j = rr / p.group;
-  const int head = cut.head * p.group + rr - j * p.group;
-  const int64_t row = (int64_t)cut.seq * p.per_seq + j;
-  v.x *= f;
-  v.y *= f;
-  v.z *= f;
-  v.w *= f;
-  store4(p.a, row, head, 4 * e, v);
-  if (e == 0 && p.a.lse != nullptr)
-    p.a.lse[row * p.a.n_q + head] =
-        none ? -INFINITY : (top + log2f(sum)) * LN2;
-  }
-  __syncthreads();
+  for (int r = r0; r < r1; ++r) {
+    add_parts(r);
+    sides();
+    if (lane < LANES) s_o[warp][lane] = v;
+    if (lane == 0) {
+      s_top[warp] = top;
+      s_sum[warp] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll 1
+      for (int w = 1; w < JOIN_WARPS; ++w)
+        merge(s_top[w], s_sum[w], s_o[w][lane % LANES]);
+      finish(r);
+    }
+    __syncthreads();
   }
 }
 
@@ -1113,7 +1175,7 @@ Layout layout_of(int ctas, int tile_rows, int d) {
 
 // `sms` SMs' worth of CTAs.
 template <int CACHE, int D, int NT>
-int launch(const Params& p, int sms, cudaStream_t s) {
+int launch(Params& p, int sms, cudaStream_t s) {
   using C = Conf<CACHE, D, NT>;
   static_assert(C::CTAS <= MAX_CTAS, "the workspace has room for MAX_CTAS");
   static std::atomic<uint64_t> ready{0};   // devices whose attribute is set
@@ -1129,29 +1191,36 @@ int launch(const Params& p, int sms, cudaStream_t s) {
     ready.fetch_or(bit);
   }
   const int ctas = C::CTAS * sms;
+  p.skip_cols = C::BLOCK / p.page;
+  p.skip_off = C::BLOCK % p.page;
   decode_kernel<CACHE, D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
   err = cudaGetLastError();
   if (err) return err;
   const int64_t unit = (int64_t)p.per_seq * p.group;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (unsigned)std::min<int64_t>(unit, 8));
-  cfg.blockDim = dim3(JOIN_THREADS);
+  // With fewer units than CTAs / 4 a unit has more than FEW parts, whose rows
+  // go to CTAs of their own (1x131072 with 8 units: 88 µs a call, else 99).
+  const int64_t units = (int64_t)p.c.b * p.c.n_kv * p.tiles;
+  const int cta_rows = 4 * units < ctas ? 1 : 8;
+  const int rows = (int)std::min<int64_t>(unit, 8 * NT);
+  cfg.gridDim = dim3(ctas, (rows + cta_rows - 1) / cta_rows);
+  cfg.blockDim = dim3(32 * JOIN_WARPS);
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, 8 * NT);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, 8 * NT, cta_rows);
 }
 template <int CACHE, int D>
-int launch_rows(const Params& p, int tile_rows, int sms, cudaStream_t s) {
+int launch_rows(Params& p, int tile_rows, int sms, cudaStream_t s) {
   return tile_rows == 8    ? launch<CACHE, D, 1>(p, sms, s)
          : tile_rows == 16 ? launch<CACHE, D, 2>(p, sms, s)
                            : launch<CACHE, D, 4>(p, sms, s);
 }
 template <int CACHE>
-int launch_d(const Params& p, int tile_rows, int sms, cudaStream_t s) {
+int launch_d(Params& p, int tile_rows, int sms, cudaStream_t s) {
   return p.c.d == 128 ? launch_rows<CACHE, 128>(p, tile_rows, sms, s)
                       : launch_rows<CACHE, 64>(p, tile_rows, sms, s);
 }
@@ -1176,6 +1245,11 @@ int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,
   p.tiles = (int)((unit + tile_rows - 1) / tile_rows);
   p.status = status;
   p.page = c.page;
+  p.units = c.n_kv * p.tiles;
+  p.cap = c.table_cols * c.page;
+  p.page_shift = 30;
+  while (1 << (p.page_shift - 30) < c.page) ++p.page_shift;
+  p.page_mul = (uint32_t)((((uint64_t)1 << p.page_shift) + c.page - 1) / c.page);
   p.pages = (int)c.pages;
   p.page_s = (int)c.page_stride;
   p.token_s = (int)c.token_stride;
