@@ -322,3 +322,104 @@ class TPBlockFP8MLP:
                       g["dgamma"], self.norm_scratch, dres=dx1, eps=self.eps,
                       stream=stream)
         return g
+
+
+class TPBlockFP8Attention:
+    """Residual + RMSNorm + attention of generated tokens over a paged key-value
+    cache, both projections on block-scaled E4M3 operands: in front of a
+    TPBlockFP8MLP, the other half of a layer that generates.
+
+        x1 = x + r,  Y = RMSNorm(x1)·γ,  [Q | K | V] = Y·[Wq; Wk; Wv]ᵀ,
+        the cache takes K and V,
+        O = softmax(Q·Kᵀ/√d)·V over it,  Z = O·Woᵀ
+
+    for the ``new`` newest tokens of each of b sequences (more than one where
+    drafted tokens are checked, or a few of a prompt): row i·new + j is the j-th
+    of sequence i.  The cache (binding.kv_cache_empty), its page table and the
+    lengths, which count the new tokens already, belong to the caller; a place
+    of the batch whose length is 0 is idle (its rows' O is 0).  Z is handed on
+    without x1: the next norm adds it as its r.  Activations and γ are bf16; Q,
+    K, V and O are rounded to bf16, K and V once more to what the cache holds.
+
+    Wq [n_q·d, h], Wk and Wv [n_kv·d, h], Wo [h, n_q·d], bf16 or fp32,
+    unsharded.  Each of the n logical shards holds n_q/n query heads and n_kv/n
+    kv heads; a shard's heads take a multiple of 128 columns, so that no block
+    of 128 crosses a shard, and the g sum is taken in the product's accumulation
+    (the fused mode; no other)."""
+
+    def __init__(self, b, h, n_q, n_kv, d=128, n=1, *, new=1, eps=1e-5,
+                 device="cuda"):
+        if min(b, h, n_q, n_kv, n, new) < 1 or h % 8 or h > 16384:
+            raise ValueError("sizes: b, new, n ≥ 1, h a multiple of 8 up to "
+                             "16384")
+        if d not in (64, 128):
+            raise ValueError("d: 64 or 128")
+        if n_q % n_kv or n_q % n or n_kv % n:
+            raise ValueError("heads: n_kv divides n_q, n divides both")
+        if n_q // n * d % 128 or n_kv // n * d % 128:
+            raise ValueError("a shard's heads: a multiple of 128 columns")
+        self.b, self.new, self.T, self.h = b, new, b * new, h
+        self.n_q, self.n_kv, self.d, self.n = n_q, n_kv, d, n
+        self.eps, self.device = eps, device
+        T, nq, nkv = self.T, n_q * d, n_kv * d
+        self.rows = (nq, nkv, nkv)              # of Wq, Wk and Wv
+        bf16 = dict(dtype=torch.bfloat16, device=device)
+        self.rstd = torch.empty(T, dtype=torch.float32, device=device)
+        self.y = B.fp8_block_empty(T, h, device=device)
+        self.a = B.fp8_block_empty(T, nq, device=device)
+        self.qkv = torch.empty((T, nq + 2 * nkv), **bf16)
+        heads = self.qkv.view(T, n_q + 2 * n_kv, d)
+        self.q, self.k, self.v = heads.split((n_q, n_kv, n_kv), dim=1)
+        self.o = torch.empty((T, nq), **bf16)
+        self.weights = None
+
+    def load_weights(self, Wq, Wk, Wv, Wo, stream=None):
+        """Quantize the weights (after every update of them)."""
+        nq = self.rows[0]
+        for W, what, shape in ((Wq, "Wq", (nq, self.h)),
+                               (Wk, "Wk", (self.rows[1], self.h)),
+                               (Wv, "Wv", (self.rows[2], self.h)),
+                               (Wo, "Wo", (self.h, nq))):
+            if tuple(W.shape) != shape:
+                raise ValueError(f"{what} {shape}, got {tuple(W.shape)}")
+        weights, self.weights = self.weights, None   # none, should a call fail
+        if weights is None:
+            with _made_on(stream):
+                weights = [B.fp8_block_empty(r, c, B.FP8_BLOCK, self.device)
+                           for r, c in ((sum(self.rows), self.h),
+                                        (self.h, nq))]
+        (q, s), wo = weights
+        at = 0
+        for W, r in zip((Wq, Wk, Wv), self.rows):
+            B.quantize_fp8_block(W, q[at:at + r],
+                                 s[:, at // 128:(at + r) // 128],
+                                 stream=stream)
+            at += r
+        B.quantize_fp8_block(Wo, *wo, stream=stream)
+        self.weights = weights
+
+    def forward(self, x, gamma, cache, table, lens, r=None, out=None, x1=None,
+                stream=None):
+        """(x1, Z); K and V of the new tokens are in the cache after it.  x1
+        may be given (x or r among it); without r it is x."""
+        if self.weights is None:
+            raise RuntimeError("load_weights comes first")
+        with _made_on(stream):
+            if r is None:
+                x1 = x if x1 is None else x1
+            elif x1 is None:
+                x1 = torch.empty_like(x)
+            if out is None:
+                out = torch.empty((self.T, self.h), dtype=torch.bfloat16,
+                                  device=self.device)
+        wqkv, wo = self.weights
+        B.add_rmsnorm_fp8_fwd(x, r, gamma, None if x1 is x and r is None
+                              else x1, *self.y, self.rstd, eps=self.eps,
+                              stream=stream)
+        B.gemm_fp8_block(*self.y, *wqkv, self.qkv, stream=stream)
+        B.kv_cache_write(self.k, self.v, cache, table, lens, stream=stream)
+        B.attn_decode(self.q, cache, table, lens,
+                      self.o.view(self.T, self.n_q, self.d), stream=stream)
+        B.quantize_fp8_block(self.o, *self.a, stream=stream)
+        B.gemm_fp8_block(*self.a, *wo, out, stream=stream)
+        return x1, out

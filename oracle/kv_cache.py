@@ -63,3 +63,33 @@ def attend(q, k, v, table, lens, scale):
             out[row, h] = w @ vs[:, h // group] / w.sum()
             lse[row, h] = top + np.log(w.sum())
     return out, lse
+
+
+def step(x, r, gamma, W, pools, table, lens, n_q, d, eps):
+    """A generation step's attention block (residual + RMSNorm, block-scaled
+    projections, cache and attention), each step's stored tensor rounded as the
+    device stores it.  W: Wq, Wk, Wv, Wo; pools: k and v as values
+    [pages, page, n_kv, d], written in place, and whether the cache holds E4M3
+    codes."""
+    from .fp8 import round_bf16
+    from .norm import rmsnorm_forward
+    k_pool, v_pool, quantized = pools
+
+    def deq(v, group):
+        return fp8_block.dequantize(*fp8_block.quantize(v, group))
+
+    x1 = round_bf16(x if r is None else x + r)
+    y = deq(rmsnorm_forward(x1, gamma, eps)["y"], "row")
+    rows, n_kv = x.shape[0], k_pool.shape[2]
+    q, k, v = (round_bf16(y @ deq(W[w], "block").T).reshape(rows, -1, d)
+               for w in ("Wq", "Wk", "Wv"))
+    assert k.shape[1] == n_kv and q.shape[1] == n_q
+    page = k_pool.shape[1]
+    for row, i, p in tokens(lens, rows):
+        at = table[i][p // page], p % page
+        for pool, new in ((k_pool, k), (v_pool, v)):
+            pool[at] = dequantize(*quantize(new[row])) if quantized \
+                else new[row]
+    o, _ = attend(q, k_pool, v_pool, table, lens, d ** -0.5)
+    Z = deq(round_bf16(o.reshape(rows, -1)), "row") @ deq(W["Wo"], "block").T
+    return x1, Z

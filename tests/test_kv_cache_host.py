@@ -373,3 +373,63 @@ def test_binding_refuses(tp, make):
         tp.kv_cache_write(rows().t, rows().t, [t if t is None else t.t for t in
                                                cache()], base["table"].t,
                           base["lens"].t)
+
+
+def test_oracles_step_is_the_layers_attention(tp):
+    # operands that E4M3 holds exactly leave only the bf16 roundings: the
+    # step's output is the attention oracle's last row through Wo
+    rng = np.random.default_rng(6)
+    h, n_q, n_kv, d, page = 16, 4, 2, 64, 4
+    n = 5
+    x = rng.integers(-1, 2, (n, h)).astype(np.float64)
+    x[:, 0] = 1.0
+    W = {k: rng.integers(-1, 2, s).astype(np.float64) for k, s in
+         (("Wq", (n_q * d, h)), ("Wk", (n_kv * d, h)), ("Wv", (n_kv * d, h)),
+          ("Wo", (h, n_q * d)))}
+    pools = [np.full((3, page, n_kv, d), np.nan) for _ in range(2)]
+    table = np.array([[2, 0]])
+    ys = []
+    for t in range(n):
+        # eps and gamma that make the norm's factor a power of two
+        rms = np.mean(x[t] ** 2)
+        eps = 1.0 - rms
+        _, Z = okv.step(x[t:t + 1], None, np.ones(h), W, (*pools, False),
+                        table, [t + 1], n_q, d, eps)
+        ys.append(x[t])
+    f = oracle.attention_forward(np.stack(ys), W["Wq"], W["Wk"], W["Wv"],
+                                 np.eye(n_q * d), b=1, s=n, n_q=n_q,
+                                 n_kv=n_kv, d=d)
+    got = Z[0]
+    # O once to bf16 and once to codes: 2^-8 and 2^-4 of its elements at most
+    want = f["Out"][-1] @ W["Wo"].T
+    slack = (2.0 ** -4 + 2.0 ** -7) * np.abs(f["Out"][-1]) @ np.abs(W["Wo"]).T
+    assert (np.abs(got - want) <= slack + 1e-9).all()
+    # whole numbers but for the scales' fp32 rounding, 2·2^-24 of 16 terms
+    for t in range(n):
+        assert np.allclose(pools[0][table[0][t // page], t % page],
+                           (W["Wk"] @ x[t]).reshape(n_kv, d), rtol=0,
+                           atol=16 * 2.0 ** -23)
+
+
+@pytest.mark.parametrize("args", [
+    (0, 256, 2, 1), (1, 252, 2, 1), (1, 16392, 2, 1), (1, 256, 3, 2),
+    (1, 256, 2, 1, 96), (1, 256, 4, 2, 128, 4), (1, 256, 2, 2, 64, 2)])
+def test_attention_block_refuses_sizes(args):
+    from megatron_tensor_transformer_gate_gb300.blocks import \
+        TPBlockFP8Attention
+    with pytest.raises(ValueError):
+        TPBlockFP8Attention(*args, device="cpu")
+
+
+def test_attention_blocks_weights_that_failed_to_load_are_not_used(tp):
+    from megatron_tensor_transformer_gate_gb300.blocks import \
+        TPBlockFP8Attention
+    blk = TPBlockFP8Attention(2, 256, 2, 1, device="cpu")
+    W = [torch.zeros(256, 256), torch.zeros(128, 256), torch.zeros(128, 256),
+         torch.zeros(256, 256)]
+    with pytest.raises(ValueError, match="Wv"):
+        blk.load_weights(W[0], W[1], W[0], W[3])
+    with pytest.raises(ValueError, match="not on a GPU"):
+        blk.load_weights(*W)
+    with pytest.raises(RuntimeError, match="load_weights"):
+        blk.forward(torch.zeros(2, 256), torch.ones(256), None, None, None)
