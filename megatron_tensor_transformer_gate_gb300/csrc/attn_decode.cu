@@ -48,6 +48,10 @@ namespace tp {
 namespace {
 
 constexpr int MAX_CTAS = 4;        // on an SM
+// The reference M may lie up to 2^SLACK below a row's largest t before the sums
+// are rescaled: some row of 32 has a new maximum in nearly every step of a short
+// segment, one beyond 2^8 hardly ever.  Weights stay far from fp16's end.
+constexpr float SLACK = 8.0f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -736,9 +740,9 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
           for (int mt = 1; mt < MT; ++mt)
             x = fmaxf(x, fmaxf(sc[mt][nt][h], sc[mt][nt][2 + h]));
           high[nt][h] = x;
-          rise |= x > top[nt][h];
+          rise |= x > top[nt][h] + SLACK;
         }
-      if (__any_sync(0xffffffffu, rise)) {   // new maxima
+      if (__any_sync(0xffffffffu, rise)) {   // maxima of all rows anew
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
