@@ -1511,7 +1511,9 @@ extern "C" tp_status tp_kv_cache_read(const tp_kv_cache* d, int32_t dtype,
 
 extern "C" size_t tp_attn_decode_workspace_bytes(const tp_kv_cache* c,
                                                  int64_t rows, int32_t n_q) {
-  if (c == nullptr || c->b < 1 || c->n_kv < 1 || !decode_shape(c, rows, n_q))
+  if (c == nullptr || c->b < 1 || c->n_kv < 1 || c->page < 1 ||
+      c->table_cols < 1 || (c->d != 64 && c->d != 128) ||
+      !decode_shape(c, rows, n_q))
     return 0;
   return attn_decode_ws_bytes(*c, rows, n_q);
 }

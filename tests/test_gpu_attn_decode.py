@@ -321,3 +321,76 @@ def test_a_workspace_too_small_is_refused(tp):
     if need > 16:
         with pytest.raises(tp.TPError, match="TP_ERR_WORKSPACE"):
             attend(tp, c, q, ws=ws[:need - 16])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_thousands_of_places_in_the_batch(tp, kind):
+    lens = [(i * 7) % 5 for i in range(3000)]
+    lens[1700] = 700
+    c = Cache(lens, 4, 1, 64, kind, 94)
+    check(tp, c, 2, 1, BF16)
+
+
+def test_two_captured_graphs(tp):
+    # with a workspace each, replayed at once; with one of theirs, in turn
+    cs = [Cache([3000, 50, 0], 32, 2, 128, k, 95) for k in ("bf16", "e4m3")]
+    qs = [queries(c, 3, 8, BF16, 9)[1] for c in cs]
+    alone = [attend(tp, c, q) for c, q in zip(cs, qs)]
+    need = max(tp.attn_decode_workspace_bytes(*c.args, 3, 8) for c in cs)
+    for shared in (False, True):
+        ws = [torch.empty(need, dtype=torch.uint8, device="cuda")
+              for _ in range(2)]
+        outs, graphs = [], []
+        for i, (c, q) in enumerate(zip(cs, qs)):
+            out = torch.zeros_like(q)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                for _ in range(5):
+                    tp.attn_decode(q, *c.args, out,
+                                   ws=ws[0 if shared else i])
+            graphs.append(g)
+            outs.append(out)
+        side = torch.cuda.Stream()
+        for _ in range(5):
+            graphs[0].replay()
+            if shared:
+                graphs[1].replay()
+            else:
+                with torch.cuda.stream(side):
+                    graphs[1].replay()
+        torch.cuda.synchronize()
+        for (a, _), o in zip(alone, outs):
+            assert torch.equal(a, o)
+    tp.device_status()
+
+
+def test_a_call_between_others_is_ordered_after_them(tp):
+    # the second kernel may be launched early, but reads after the first; what
+    # follows on the stream reads after both
+    c = Cache([9000], 32, 1, 128, "bf16", 96)
+    _, q = queries(c, 1, 8, BF16, 9, strided=False)
+    q2 = q.clone().neg_()
+    want = [attend(tp, c, x)[0].clone() for x in (q, q2)]
+    out = torch.empty_like(q)
+    got = torch.empty(40, *q.shape, dtype=BF16, device="cuda")
+    x = q.clone()
+    for i in range(40):
+        x.copy_(q2 if i % 2 else q)
+        tp.attn_decode(x, *c.args, out)
+        got[i].copy_(out)
+    for i in range(40):
+        assert torch.equal(got[i], want[i % 2])
+    tp.device_status()
+
+
+def test_idle_places_queries_have_no_influence(tp):
+    c = Cache([0, 40, 0], 16, 2, 128, "f16", 97)
+    _, q = queries(c, 3, 4, BF16, 9)
+    a = attend(tp, c, q)
+    q[0] = float("nan")
+    q[2] = float("inf")
+    b = attend(tp, c, q)
+    tp.device_status()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert not b[0][0].any() and not b[0][2].any()

@@ -260,3 +260,131 @@ def test_round_trip_through_another_stream(tp):
             torch.from_numpy(t % 16)
         for a, b in zip(copy, c.cache):
             assert torch.equal(a.cpu()[at], b.cpu()[at])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("src,d,n_kv,page,ragged", [
+    (torch.bfloat16, 128, 8, 16, True), (torch.float16, 128, 3, 33, False),
+    (torch.bfloat16, 64, 1, 100, True), (torch.float16, 64, 5, 8, False)])
+def test_many_rows(tp, kind, src, d, n_kv, page, ragged):
+    # enough vectors for four a thread, on a device of any number of SMs
+    vecs = 9 * 256 * 16 // d * 160
+    b = 7
+    m = vecs // n_kv // b + 3
+    rng = np.random.default_rng(d + n_kv)
+    lens = [m + 5 * i if i % 3 else m - 11 * i for i in range(b)]
+    table, pages = page_table(lens, page, rng)
+    start, rows = None, b * m
+    if ragged:
+        start = 1 + np.concatenate(([0], np.cumsum(lens)))
+        start[3:] -= 40        # the third one's newest but for the first 40
+        rows = start[-1] + 2
+    k, v, dk, dv = source(rng, rows, n_kv, d, src, True)
+    cache = pools(pages, page, n_kv, d, kind, "heads")
+    dt = torch.from_numpy(table).cuda()
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ds = None if start is None else torch.tensor(start, dtype=torch.int32,
+                                                 device="cuda")
+    want = [None if t is None else t.contiguous().cpu() for t in cache]
+    at = np.array(list(okv.tokens(lens, rows, start)))
+    row, place = torch.from_numpy(at[:, 0]), \
+        (torch.from_numpy(table[at[:, 1], at[:, 2] // page]).long(),
+         torch.from_numpy(at[:, 2] % page))
+    values = []
+    for j, x in ((0, k), (1, v)):
+        if kind == "e4m3":
+            codes, s = okv.quantize(x.float().numpy())
+            want[j].view(torch.uint8)[place] = torch.from_numpy(codes)[row]
+            want[j + 2][place] = torch.from_numpy(s)[row]
+            values.append(torch.from_numpy(okv.dequantize(codes, s)
+                                           .astype(np.float32)))
+        else:
+            want[j][place] = x[row].to(TORCH[kind])
+            values.append(x.to(TORCH[kind]))
+    tp.kv_cache_write(dk, dv, cache, dt, dl, start=ds)
+    tp.device_status()
+    for t, w in zip(cache, want):
+        if t is not None:
+            assert (bits(t) == bits(w)).all()
+    got = [torch.full((rows, n_kv, d), 3.0, dtype=src, device="cuda")
+           for _ in range(2)]
+    tp.kv_cache_read(cache, dt, dl, *got, start=ds)
+    tp.device_status()
+    for g, x in zip(got, values):
+        w = torch.full((rows, n_kv, d), 3.0, dtype=src)
+        w[row] = x[row].to(src)
+        assert (bits(g) == bits(w)).all()
+
+
+def test_the_module_and_the_python_checks_make_the_same_calls(tp, monkeypatch):
+    # write, read and attention by way of csrc/pycall.cpp and without it
+    assert tp._load().__name__.endswith("._tpcall")
+    for kind in ("bf16", "f16", "e4m3"):
+        c = Cache([70, 0, 33], 16, 2, 128, kind, 6)
+        x = torch.randn(3, 12, 128, device="cuda").bfloat16()
+        k, v, q = x[:, :2], x[:, 2:4], x[:, 4:]
+        start = torch.tensor([0, 2, 2, 3], dtype=torch.int32, device="cuda")
+        results = []
+        for module in (tp._load(), tp._EveryCallInPython):
+            monkeypatch.setattr(tp, "_tpcall", module)
+            cache = tuple(None if t is None else t.clone() for t in c.cache)
+            args = cache, c.dev_table, c.dev_lens
+            for s in (None, start):
+                tp.kv_cache_write(k, v, *args, start=s)
+                back = torch.zeros_like(k), torch.zeros_like(v)
+                tp.kv_cache_read(*args, *back, start=s)
+                out, lse = torch.zeros_like(q), torch.zeros(3, 8, device="cuda")
+                tp.attn_decode(q, *args, out, lse=lse)
+                out2 = torch.zeros_like(q)
+                tp.attn_decode(q, *args, out2, scale=0.5,
+                               ws=torch.empty(tp.attn_decode_workspace_bytes(
+                                   *args, 3, 8), dtype=torch.uint8,
+                                   device="cuda"))
+                results.append((*cache, *back, out, lse, out2))
+        tp.device_status()
+        for a, w in zip(results[:2], results[2:]):
+            for x1, x2 in zip(a, w):
+                assert x1 is x2 is None or (bits(x1) == bits(x2)).all()
+        monkeypatch.undo()
+
+
+@pytest.mark.parametrize("module", [True, False])
+def test_both_refuse_on_the_gpu(tp, monkeypatch, module):
+    if not module:
+        monkeypatch.setattr(tp, "_tpcall", tp._EveryCallInPython)
+    c = Cache([5, 6], 4, 2, 64, "bf16", 7)
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    n = tp.launch_count()
+    for a, kind in (
+            ((x.float(), x.float(), *c.args), TypeError),
+            ((x, x.half(), *c.args), TypeError),
+            ((x[:1], x, *c.args), ValueError),
+            ((x[..., ::2], x[..., ::2], *c.args), ValueError),
+            ((x, x, c.cache[:1] + (c.cache[1].half(),), *c.args[1:]),
+             TypeError),
+            ((x, x, c.cache, c.dev_table.long(), c.dev_lens), TypeError),
+            ((x, x, c.cache, c.dev_table, c.dev_lens[:1]), ValueError),
+            ((x, x, c.cache, c.dev_table.cpu(), c.dev_lens), ValueError),
+            ((x[:, :, :40], x[:, :, :40], *c.args), ValueError)):
+        with pytest.raises(kind):
+            tp.kv_cache_write(*a)
+    odd = torch.zeros(2 * 2 * 64 + 4, dtype=torch.bfloat16,
+                      device="cuda")[4:].view(2, 2, 64)
+    with pytest.raises(tp.TPError, match="TP_ERR_ARG"):
+        tp.kv_cache_write(odd, x, *c.args)
+    with pytest.raises(tp.TPError, match="TP_ERR_SHAPE"):   # written rows twice
+        tp.kv_cache_read(*c.args, x[:1].expand(2, 2, 64), x)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    for kw, kind in ((dict(q=q.half(), out=q.half()), TypeError),
+                     (dict(out=q[:, :2]), ValueError),
+                     (dict(q=q[:, :3], out=q[:, :3]), ValueError),
+                     (dict(lse=torch.zeros(2, 4, device="cuda").t()),
+                      ValueError),
+                     (dict(ws=torch.zeros(8, dtype=torch.uint8)), ValueError),
+                     (dict(scale=float("nan")), tp.TPError)):
+        a = dict(q=q, out=torch.empty_like(q), lse=None, ws=None, scale=None)
+        a.update(kw)
+        with pytest.raises(kind):
+            tp.attn_decode(a["q"], *c.args, a["out"], lse=a["lse"],
+                           scale=a["scale"], ws=a["ws"])
+    assert tp.launch_count() == n

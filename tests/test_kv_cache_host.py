@@ -255,6 +255,18 @@ def test_decode_refuses(tp):
     c = good(tp)
     assert tp.lib().tp_attn_decode_workspace_bytes(None, 4, 8) == 0
     assert tp.lib().tp_attn_decode_workspace_bytes(ctypes.byref(c), 5, 8) == 0
+    for kw in (dict(b=0), dict(n_kv=0), dict(page=0), dict(page=-64),
+               dict(table_cols=-17), dict(table_cols=0), dict(d=80)):
+        bad = good(tp, **kw)
+        assert tp.lib().tp_attn_decode_workspace_bytes(ctypes.byref(bad), 4,
+                                                       8) == 0, kw
+    # more work than is counted in 31 bits, tokens beyond 2^30
+    assert decode(tp, good(tp, b=2, n_kv=1024, page=1 << 20, table_cols=512,
+                           token_stride=131072, page_stride=1 << 38,
+                           s_token_stride=1024, table_stride=512),
+                  n_q=1024, qr=1 << 17, orow=1 << 17) == SHAPE
+    assert decode(tp, good(tp, page=1 << 20, table_cols=1025,
+                           page_stride=512 << 20, table_stride=1025)) == SHAPE
     need = tp.lib().tp_attn_decode_workspace_bytes(ctypes.byref(c), 4, 8)
     if need:
         assert decode(tp, size=need - 1) == WORKSPACE
