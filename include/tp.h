@@ -540,7 +540,7 @@ tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
  * A call reads the table and the lengths on the device, when it runs.  An
  * entry outside [0, pages), or a length beyond table_cols·page, is not
  * followed: the tokens there are left out and tp_device_status returns
- * TP_ERR_PAGE. */
+ * TP_ERR_PAGE.  Outputs do not overlap inputs or each other. */
 typedef struct {
   int32_t dtype;         /* TP_BF16, TP_F16 or TP_FP8 */
   int32_t b;             /* sequences (1 to 65536) */
@@ -567,7 +567,8 @@ typedef struct {
  * padding in front of a short prompt).  start NULL: rows = b·m, m for each
  * sequence in turn; else device int32 [b + 1], not decreasing: sequence i's
  * are rows start[i] up to start[i + 1], and rows outside [start[0], start[b])
- * are no tokens.  For rows of no token nothing is written.  Positions that two rows of one call share hold either's value. */
+ * are no tokens.  For rows of no token nothing is written.  What a place of
+ * the pool holds that two rows of one call are written to is undefined. */
 tp_status tp_kv_cache_write(const tp_kv_cache* c, int32_t dtype, int64_t rows,
                             const void* K, int64_t k_row, int64_t k_head,
                             const void* V, int64_t v_row, int64_t v_head,

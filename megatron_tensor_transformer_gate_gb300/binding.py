@@ -663,6 +663,9 @@ def _kv_cache(cache, table, lens):
     _on_device(table, "table", 2, torch.int32, dev)
     _on_device(lens, "lens", 1, torch.int32, dev)
     b, cols = table.shape
+    if 0 in k.shape or b == 0 or cols == 0:
+        raise ValueError(f"an empty cache or batch: k {_shape(k)}, table "
+                         f"{_shape(table)}")
     if cols > 1 and table.stride(1) != 1:
         raise ValueError(f"table: columns must be adjacent, strides "
                          f"{table.stride()}")

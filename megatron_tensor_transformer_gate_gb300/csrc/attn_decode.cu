@@ -266,22 +266,24 @@ struct Segment {
 struct Walk {
   int at, stop, before, seq;   // before: slots in front of the sequence
 };
-// The next segment with blocks of the piece (one thread).
+// The next segment with blocks of the piece (one thread).  Whatever the lengths
+// are (they are read again here, and may have been changed under the call), it
+// names a sequence of the batch, a kv head and tokens that its table lists.
 template <class C>
 __device__ __forceinline__ void next_segment(const Params& p, Walk* walk,
                                              Segment* out) {
   Walk w = *walk;
   Segment s = {};
 #pragma unroll 1
-  while (w.at < w.stop && !s.there) {
+  while (w.at < w.stop && w.seq < p.c.b && !s.there) {
     s.len = max(p.c.lens[w.seq], 0);
     s.n = tokens_of(p, w.seq);
     s.nb = blocks_of<C::BLOCK>(s.n);
     s.seq = w.seq;
     const int weight = s.nb + C::EXTRA;
     const int in_seq = w.at - w.before;
-    const int unit = in_seq / weight;
-    const int x0 = in_seq - unit * weight;
+    const int unit = min(max(in_seq, 0) / weight, p.units - 1);
+    const int x0 = min(max(in_seq - unit * weight, 0), weight - 1);
     const int x1 = min(weight, x0 + (w.stop - w.at));
     s.kvh = p.tiles == 1 ? unit : unit / p.tiles;
     s.tile = unit - s.kvh * p.tiles;
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
     if (warp == 1 && before <= at && at < inc) {   // one lane
       int i = i0;
 #pragma unroll 1
-      for (;; ++i) {
+      for (; i + 1 < i1; ++i) {
         const int w = slots(i);
         if (at < before + w) break;
         before += w;
@@ -953,7 +955,8 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
         cut.head = seg.kvh;
         cut.tile = seg.tile;
         cut.first_slot = (int)part_at;
-        cut.parts = pieces.cta_of(seg.first + seg.nb - 1) - blockIdx.x + 1;
+        cut.parts = min(pieces.cta_of(seg.first + seg.nb - 1), pieces.ctas - 1) -
+                    (int)blockIdx.x + 1;
         p.cuts[blockIdx.x] = cut;
       }
     }

@@ -42,7 +42,8 @@ TP_HOST_DEVICE bool kv_token_of(const tp_kv_cache& c, const int32_t* start,
   const int64_t p = c.lens[i] - (end - row);   // < lens[i]
   *seq = i;
   *pos = (int)p;
-  return p >= 0;
+  // (what is read twice above may have been changed in between)
+  return p >= 0 && row < end;
 }
 
 // The page of position pos ≥ 0 of a sequence and the offset in it; −1 where

@@ -333,6 +333,10 @@ def test_binding_refuses(tp, make):
         (both, dict(cache=c8[:3] + [on(torch.zeros(6, 4, 2))]), ValueError,
          "same strides"),
         (both, dict(table=ints(b, 5, dtype=torch.int64)), TypeError, "table"),
+        (both, dict(table=ints(0, 5), lens=ints(0)), ValueError, "empty"),
+        (both, dict(table=ints(b, 0)), ValueError, "empty"),
+        (both, dict(cache=cache(pages=0)), ValueError, "empty"),
+        (both, dict(cache=cache(n_kv=0)), ValueError, "empty"),
         (both, dict(table=ints(b * 5)), ValueError, "table: 2 axes"),
         (both, dict(table=ints(b, 5, dev=1)), ValueError, "table: on"),
         (both, dict(table=on(torch.zeros(5, b, dtype=torch.int32).t())),
