@@ -6,7 +6,9 @@ and the backward scratch for one shape; ``TPLayer`` composes the pre-norm
 layer  x1 = x + Attn(RMSNorm₁(x)),  out = x1 + MLP(RMSNorm₂(x1))  out of the
 library's RMSNorm, attention and MLP entry points, which gives the layer's
 four TP reductions (attention g and MLP g in forward, MLP f and attention f
-in backward).
+in backward).  ``TPBlockFP8MLP`` and ``TPBlockFP8Attention`` run their products
+on block-scaled E4M3 operands: the first for training and for generated tokens,
+the second, over a paged key-value cache, for generated tokens.
 """
 
 import contextlib
