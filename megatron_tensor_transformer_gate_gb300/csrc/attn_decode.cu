@@ -59,6 +59,9 @@ constexpr int MAX_CTAS = 4;        // on an SM
 // are rescaled: some row of 32 has a new maximum in nearly every step of a short
 // segment, one beyond 2^8 hardly ever.  Weights stay far from fp16's end.
 constexpr float SLACK = 8.0f;
+// M of a row that has seen nothing: finite, so that nothing needs a case of its
+// own (2^(−∞ − M) = 0, 2^(M − t) = 0 of any t that a row sees).
+constexpr float NOTHING = -1e30f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -594,11 +597,12 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
             }
             qf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
             qf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
-          } else if (nt % WARPS == warp) {   // [nt][s][lane] pairs of registers
+          } else if (nt % WARPS == warp) {   // [nt][s / 2][lane] four registers
             if (t4 == 0) s_qf[8 * nt + g] = f;
 #pragma unroll
             for (int s = 0; s < KS; ++s)
-              reinterpret_cast<uint2*>(join)[(nt * KS + s) * 32 + lane] =
+              reinterpret_cast<uint2*>(
+                  join)[((nt * KS + s) / 2 * 32 + lane) * 2 + s % 2] =
                   make_uint2(u[s][0], u[s][1]);
           }
         }
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
             for (int j = 0; j < 4; ++j) o[s][nt][j] = 0.0f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            top[nt][h] = -INFINITY;
+            top[nt][h] = NOTHING;
             l[nt][h] = 0.0f;
           }
         }
@@ -646,48 +650,43 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 4; ++j) sc[mt][nt][j] = 0.0f;
-      auto q_of = [&](int nt, int s) {
-        if constexpr (C::QREG)
-          return make_uint2(q[nt][s][0], q[nt][s][1]);
-        else
-          return reinterpret_cast<const uint2*>(join)[(nt * KS + s) * 32 +
-                                                      lane];
-      };
-      if constexpr (FP8) {
-        // rows 0–7 and 8–15 of chunk s, then of chunk s + 1
+      {
+        // rows 0–7 and 8–15 of a chunk of 16 bytes, then of the next: over
+        // codes that is all of steps s and s + 1, else of one step
         const uint32_t at = kt + spread<ROW>(lane & 15, lane >> 4);
 #pragma unroll
-        for (int s = 0; s < KS; s += 2)
+        for (int s = 0; s < KS; s += 2) {
+          uint4 b[NT];   // both steps' operands
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (C::QREG)
+              b[nt] = make_uint4(q[nt][s][0], q[nt][s][1], q[nt][s + 1][0],
+                                 q[nt][s + 1][1]);
+            else
+              b[nt] = reinterpret_cast<const uint4*>(
+                  join)[(nt * KS + s) / 2 * 32 + lane];
+          }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t u[4];
-            ldmatrix((at ^ (s << 4)) + mt * 16 * ROW, u);
+            if constexpr (FP8)
+              ldmatrix((at ^ (s << 4)) + mt * 16 * ROW, u);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t a[4];
-              codes_f16(u[2 * h], a[0], a[2]);
-              codes_f16(u[2 * h + 1], a[1], a[3]);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint2 b = q_of(nt, s + h);
-                mma<BF>(sc[mt][nt], a, b.x, b.y);
+              if constexpr (FP8) {
+                codes_f16(u[2 * h], a[0], a[2]);
+                codes_f16(u[2 * h + 1], a[1], a[3]);
+              } else {
+                ldmatrix((at ^ ((s + h) << 5)) + mt * 16 * ROW, a);
               }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<BF>(sc[mt][nt], a, h ? b[nt].z : b[nt].x,
+                        h ? b[nt].w : b[nt].y);
             }
           }
-      } else {
-        const uint32_t at = kt + spread<ROW>(lane & 15, lane >> 4);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t a[4];
-            ldmatrix((at ^ (s << 5)) + mt * 16 * ROW, a);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 b = q_of(nt, s);
-              mma<BF>(sc[mt][nt], a, b.x, b.y);
-            }
-          }
+        }
       }
 
       // ---- softmax of the lane's rows 2·t4, 2·t4 + 1 at tokens 16·mt + g and
@@ -760,10 +759,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
 #pragma unroll
             for (int z = 4; z < 32; z <<= 1)
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
-            // 0 where there was nothing yet
-            const float f = top[nt][h] == -INFINITY
-                                ? 0.0f
-                                : ex2_approx(top[nt][h] - x);
+            const float f = ex2_approx(top[nt][h] - x);
             top[nt][h] = x;
             l[nt][h] *= f;
 #pragma unroll
@@ -773,21 +769,19 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
             }
           }
       }
-      // weights: 0 where a row has seen nothing yet
+      // weights
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float ref = top[nt][h] == -INFINITY ? 0.0f : top[nt][h];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               float& x = sc[mt][nt][2 * k + h];
-              x = ex2_approx(x - ref);
+              x = ex2_approx(x - top[nt][h]);
               l[nt][h] = FP8 ? fmaf(x, back[mt][k], l[nt][h]) : l[nt][h] + x;
             }
-        }
       if (mixed) {
         // Rows of several new tokens see different ends of this step.  What
         // a later token's v holds (NaN, say) must not reach a row that does
@@ -935,12 +929,9 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       float all = s_top[0][r], sum = 0.0f;
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) all = fmaxf(all, s_top[w][r]);
-      // a warp without a maximum has l = 0, or NaN of NaN scores
 #pragma unroll
       for (int w = 0; w < WARPS; ++w)
-        sum = s_top[w][r] == -INFINITY
-                  ? sum + s_l[w][r]
-                  : fmaf(s_l[w][r], ex2_approx(s_top[w][r] - all), sum);
+        sum = fmaf(s_l[w][r], ex2_approx(s_top[w][r] - all), sum);
       const bool none = sum == 0.0f;
       s_ref[r] = all;
       s_out[r] = none ? 0.0f : 1.0f / sum;
@@ -975,9 +966,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       float f[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        f[h] = top[nt][h] == -INFINITY
-                   ? 0.0f
-                   : ex2_approx(top[nt][h] - s_ref[8 * nt + 2 * t4 + h]);
+        f[h] = ex2_approx(top[nt][h] - s_ref[8 * nt + 2 * t4 + h]);
       float* const mine =
           join + ((warp % (WARPS / 2)) * 8 + 2 * t4) * (D + 4) +
           (FP8 ? 2 * g : g);
