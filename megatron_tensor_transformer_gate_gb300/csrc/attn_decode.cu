@@ -5,30 +5,33 @@
 // The cost is one read of the cached K and V, so every byte of them is read
 // once for all query rows of a kv head (a unit: up to 32 rows, 8·NT), and what
 // the SMs read is shared out evenly whatever the sequences' lengths: all units'
-// blocks of 64 tokens, laid end to end, are cut into as many equal pieces as
-// there are CTAs.  A CTA walks its piece segment by segment (a segment: the
-// part of one unit in it).  A unit that lies in one CTA is finished there;
-// one that is cut leaves partial results (o normalised, log₂ of its sum) in the
-// workspace, at most two a CTA, which a second kernel joins in CTA order:
-//   L = max lse_c, o = Σ 2^(lse_c − L)·o_c / Σ 2^(lse_c − L).
+// blocks of 64 or 128 tokens, laid end to end with a fixed extra for each unit,
+// are cut into as many equal pieces as there are CTAs, two an SM.  A CTA walks
+// its piece segment by segment (a segment: the part of one unit in it).  A unit
+// that lies in one CTA is finished there; one that is cut leaves partial
+// results (o normalised, M and the sum l relative to it) in the workspace, at
+// most two a CTA, which a second kernel joins in CTA order:
+//   L = max M_c, o = Σ l_c·2^(M_c − L)·o_c / Σ l_c·2^(M_c − L).
 //
-// In a CTA each of four warps takes every fourth step of 16 tokens and runs an
-// online softmax of its own, so that nothing waits on another warp before the
-// segment's end.  Its K and V rows come by asynchronous 16-byte copies into a
-// ring of the warp's own.  Both products are mma.sync m16n8k16 with the cache
-// on the 16 side: Sᵀ = K·Qᵀ (16 tokens × 8 rows) and Oᵀ += Vᵀ·Pᵀ (16 elements
-// × 8 rows), K by ldmatrix, Vᵀ by its transposing form; between them P is
-// transposed in registers (movmatrix).  At eight rows that takes 14 to 16 % of
-// the tensor pipe; the tensor cores' 128-row instructions cost the same for one
-// row as for 128 and read shared memory, where codes would have to be written
-// again as fp16.  E4M3 codes become fp16 operands in registers here.
+// In a CTA each of four warps takes every fourth step of 16 tokens (32 where
+// their rows are 128 bytes or less) and runs an online softmax of its own, so
+// that nothing waits on another warp before the segment's end.  Its K and V
+// rows come by asynchronous 16-byte copies into a ring of the warp's own, the
+// next segment's behind this one's.  Both products are mma.sync m16n8k16 with
+// the cache on the 16 side: Sᵀ = K·Qᵀ (16 tokens × 8 rows) and Oᵀ += Vᵀ·Pᵀ (16
+// elements × 8 rows), K by ldmatrix, Vᵀ by its transposing form; between them P
+// is transposed in registers (movmatrix).  At eight rows that takes 14 to 16 %
+// of the tensor pipe; the tensor cores' 128-row instructions cost the same for
+// one row as for 128 and read shared memory, where codes would have to be
+// written again as fp16.  E4M3 codes become fp16 operands in registers here.
 //
-// Measured (GB300, copy 6.8 TB/s): 32 sequences of 32768 in bf16 630 µs = 1.0 of
-// a copy, in E4M3 337 µs = 0.97; one of 131072 in bf16 89 µs (0.88: 4 µs until the
-// first copies are in flight, 4 for the join and its launch); 64 of 61 to 8192 in
-// E4M3 44 µs (0.69: the start, 512 segments' ends, latencies between a step's
-// dependent instructions); with 32 rows over codes 367 µs for 1.6 GB (0.64: those
-// latencies alone, eight warps an SM at 250 registers a thread).
+// Measured (GB300, copy 6.8 TB/s): 32 sequences of 32768 in bf16 630 µs = 1.0
+// of a copy, in E4M3 337 µs = 0.97; one of 131072 in bf16 89 µs (0.88: 4 µs
+// until the first copies are in flight, 4 for the join and its launch); 64 of
+// 61 to 8192 in E4M3 44 µs (0.69: the start, 512 segments' ends, latencies
+// between a step's dependent instructions); with 32 rows over codes 367 µs for
+// 1.6 GB (0.64: those latencies alone, eight warps an SM at 250 registers a
+// thread).
 //
 // Precision: scores, maxima, sums and o are fp32.  Over fp16 values and E4M3
 // codes the operands are fp16, q divided by a power of two that brings its
@@ -37,9 +40,10 @@
 // the output, it is the sum of two bf16 parts, 2^-16, at the price of a second
 // product.  A code's scale is multiplied into its score, and into its weight in
 // front of the product with V: t = x + log₂ s_v, w = 2^(t − M) with M the
-// running maximum of t, so that scales of any size keep the weights of the
-// sum in fp16's range; the denominator is Σ w / s_v, relative to the same M
-// (fp32's range leaves s_v a factor of 2^100 from token to token).
+// running maximum of t, so that scales of any size keep the weights of the sum
+// in fp16's range; the denominator is Σ w / s_v, relative to the same M (fp32's
+// range leaves s_v a factor of 2^100 from token to token).  Like x itself t is
+// rounded to 2^-24 of its size, so that scales count while |x| is below 2^20.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -54,14 +58,14 @@
 namespace tp {
 namespace {
 
-constexpr int MAX_CTAS = 4;        // on an SM
+constexpr int CTAS = 2;   // on an SM
 // The reference M may lie up to 2^SLACK below a row's largest t before the sums
-// are rescaled: some row of 32 has a new maximum in nearly every step of a short
-// segment, one beyond 2^8 hardly ever.  Weights stay far from fp16's end.
+// are rescaled: some row of 32 has a new maximum in nearly every step of a
+// short segment, one beyond 2^8 hardly ever.  Weights stay far from fp16's end.
 constexpr float SLACK = 8.0f;
-// M of a row that has seen nothing: finite, so that nothing needs a case of its
-// own (2^(−∞ − M) = 0, 2^(M − t) = 0 of any t that a row sees).
-constexpr float NOTHING = -1e30f;
+// M of a row that has seen nothing: below every t and finite, so that nothing
+// needs a case of its own (2^(−∞ − M) = 0, 2^(M − t) = 0).
+constexpr float NOTHING = -3e38f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -79,7 +83,7 @@ struct Params {
   int group;             // query heads of a kv head
   int tiles;             // row tiles of a kv head
   float* part_o;         // [2·CTAs][8·NT][D]
-  float* part_lse;       // [2·CTAs][8·NT], log₂
+  float2* part_l;        // [2·CTAs][8·NT]: M and l
   Cut* cuts;             // [CTAs]
   unsigned* status;
   // the cache's strides (elements; a product of two is formed in 64 bits)
@@ -105,7 +109,6 @@ struct Conf {
   static constexpr int ROWS = 8 * NT;
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int CTAS = 2;                   // on an SM
   // tokens of a warp: that are loaded, and that are worked on at a time
   static constexpr int STEP = ROW == 256 ? 16 : 32;
   static constexpr int PART = ROW == 256 || NT == 4 ? 16 : 32;
@@ -312,8 +315,7 @@ __device__ __forceinline__ void next_segment(const Params& p, Walk* walk,
 }
 
 template <int CACHE, int D, int NT>
-__global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
-                                  Conf<CACHE, D, NT>::CTAS)
+__global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
     decode_kernel(const Params p) {
   using C = Conf<CACHE, D, NT>;
   constexpr bool FP8 = CACHE == TP_FP8, BF = CACHE == TP_BF16;
@@ -419,17 +421,14 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       record_error(p.status, kDevPage, 44);
     }
     const uint32_t valid = __ballot_sync(0xffffffffu, in) & ALL;
-    if (FP8) {   // 16 tokens: scales of K in half of the lanes, V in the other
+    if constexpr (FP8) {
+      static_assert(STEP == 32, "a lane for each token's scales");
       const int64_t at = in ? mul(page, p.s_page_s) + mul(off, p.s_token_s) +
                                   mul(kvh, p.s_head_s)
                             : 0;
       float* d = reinterpret_cast<float*>(ring + slot * C::STAGE + 2 * C::TILE);
-      if (STEP == 16) {
-        cp_async4(d + lane, (lane < 16 ? c.ks : c.vs) + at, in);
-      } else {
-        cp_async4(d + lane, c.ks + at, in);
-        cp_async4(d + STEP + lane, c.vs + at, in);
-      }
+      cp_async4(d + lane, c.ks + at, in);
+      cp_async4(d + STEP + lane, c.vs + at, in);
     }
     if (whole_pages && valid == ALL) {   // one page
       const char* src = kpool +
@@ -548,8 +547,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
           const int j = there ? r / p.group : 0;
           const uint16_t* src =
               static_cast<const uint16_t*>(p.a.q) + (qrow + j) * p.a.q_row +
-              (there ? (int64_t)(seg.kvh * p.group + r - j * p.group) * p.a.q_head
-                     : 0);
+              (there ? (seg.kvh * p.group + r - j * p.group) * p.a.q_head : 0);
           uint32_t u[KS][2];
           float amax = 0.0f;
 #pragma unroll
@@ -620,7 +618,6 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
             l[nt][h] = 0.0f;
           }
         }
-
       }
       if (t0 >= last) break;
       // this step's copies are done when those issued after it may not be
@@ -636,262 +633,263 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       const uint32_t valid_all = valid_of[warp][stage];
 #pragma unroll 1
       for (int part = 0; part < STEP; part += PART) {
-      const int t1 = t0 + part;   // the part's first token
-      unsigned char* const rows_at = ring + stage * C::STAGE + part * ROW;
-      const uint32_t kt = smem_u32(rows_at), vt = kt + C::TILE;
-      constexpr uint32_t FULL = 0xffffffffu >> (32 - PART);
-      const uint32_t valid = valid_all >> part & FULL;
+        const int t1 = t0 + part;   // the part's first token
+        unsigned char* const rows_at = ring + stage * C::STAGE + part * ROW;
+        const uint32_t kt = smem_u32(rows_at), vt = kt + C::TILE;
+        constexpr uint32_t FULL = 0xffffffffu >> (32 - PART);
+        const uint32_t valid = valid_all >> part & FULL;
 
-      // ---- Sᵀ = K·Qᵀ
-      float sc[MT][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sc[mt][nt][j] = 0.0f;
-      {
-        // rows 0–7 and 8–15 of a chunk of 16 bytes, then of the next: over
-        // codes that is all of steps s and s + 1, else of one step
-        const uint32_t at = kt + spread<ROW>(lane & 15, lane >> 4);
-#pragma unroll
-        for (int s = 0; s < KS; s += 2) {
-          uint4 b[NT];   // both steps' operands
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (C::QREG)
-              b[nt] = make_uint4(q[nt][s][0], q[nt][s][1], q[nt][s + 1][0],
-                                 q[nt][s + 1][1]);
-            else
-              b[nt] = reinterpret_cast<const uint4*>(
-                  join)[(nt * KS + s) / 2 * 32 + lane];
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t u[4];
-            if constexpr (FP8)
-              ldmatrix((at ^ (s << 4)) + mt * 16 * ROW, u);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t a[4];
-              if constexpr (FP8) {
-                codes_f16(u[2 * h], a[0], a[2]);
-                codes_f16(u[2 * h + 1], a[1], a[3]);
-              } else {
-                ldmatrix((at ^ ((s + h) << 5)) + mt * 16 * ROW, a);
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma<BF>(sc[mt][nt], a, h ? b[nt].z : b[nt].x,
-                        h ? b[nt].w : b[nt].y);
-            }
-          }
-        }
-      }
-
-      // ---- softmax of the lane's rows 2·t4, 2·t4 + 1 at tokens 16·mt + g and
-      // 16·mt + g + 8: t into sc
-      float sk[MT][2], lv[MT][2], back[MT][2];   // s_k, log₂ s_v, 1 / s_v
-      if (FP8) {
-        const float* ss = reinterpret_cast<const float*>(
-                              ring + stage * C::STAGE + 2 * C::TILE) +
-                          part;
+        // ---- Sᵀ = K·Qᵀ
+        float sc[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            sk[mt][h] = ss[16 * mt + g + 8 * h];
-            lv[mt][h] = lg2_approx(ss[STEP + 16 * mt + g + 8 * h]);
-            // (0 where nothing was loaded)
-            back[mt][h] = lv[mt][h] == -INFINITY ? 0.0f : ex2_approx(-lv[mt][h]);
-          }
-      }
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+            for (int j = 0; j < 4; ++j) sc[mt][nt][j] = 0.0f;
+        {
+          // rows 0–7 and 8–15 of a chunk of 16 bytes, then of the next: over
+          // codes that is all of steps s and s + 1, else of one step
+          const uint32_t at = kt + spread<ROW>(lane & 15, lane >> 4);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int s = 0; s < KS; s += 2) {
+            uint4 b[NT];   // both steps' operands
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float f;
-            if constexpr (C::QREG)
-              f = qf[nt][j & 1];
-            else
-              f = s_qf[8 * nt + 2 * t4 + (j & 1)];
-            float& x = sc[mt][nt][j];
-            x = FP8 ? fmaf(x * sk[mt][j >> 1], f, lv[mt][j >> 1]) : x * f;
-          }
-      const bool mixed = p.per_seq > 1 && t1 > len - p.per_seq + 1 - PART;
-      if (valid != FULL || mixed) {
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (C::QREG)
+                b[nt] = make_uint4(q[nt][s][0], q[nt][s][1], q[nt][s + 1][0],
+                                   q[nt][s + 1][1]);
+              else
+                b[nt] = reinterpret_cast<const uint4*>(
+                    join)[(nt * KS + s) / 2 * 32 + lane];
+            }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t u[4];
+              if constexpr (FP8)
+                ldmatrix((at ^ (s << 4)) + mt * 16 * ROW, u);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int end = seen(nt, h) - t1;
+              for (int h = 0; h < 2; ++h) {
+                uint32_t a[4];
+                if constexpr (FP8) {
+                  codes_f16(u[2 * h], a[0], a[2]);
+                  codes_f16(u[2 * h + 1], a[1], a[3]);
+                } else {
+                  ldmatrix((at ^ ((s + h) << 5)) + mt * 16 * ROW, a);
+                }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int k = 16 * mt + g + 8 * i;
-                if (!((valid >> k) & 1) || k >= end)
-                  sc[mt][nt][2 * i + h] = -INFINITY;
+                for (int nt = 0; nt < NT; ++nt)
+                  mma<BF>(sc[mt][nt], a, h ? b[nt].z : b[nt].x,
+                          h ? b[nt].w : b[nt].y);
               }
-          }
-      }
-      float high[NT][2];
-      bool rise = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float x = fmaxf(sc[0][nt][h], sc[0][nt][2 + h]);
-#pragma unroll
-          for (int mt = 1; mt < MT; ++mt)
-            x = fmaxf(x, fmaxf(sc[mt][nt][h], sc[mt][nt][2 + h]));
-          high[nt][h] = x;
-          rise |= x > top[nt][h] + SLACK;
-        }
-      if (__any_sync(0xffffffffu, rise)) {   // maxima of all rows anew
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x = fmaxf(high[nt][h], top[nt][h]);
-#pragma unroll
-            for (int z = 4; z < 32; z <<= 1)
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
-            const float f = ex2_approx(top[nt][h] - x);
-            top[nt][h] = x;
-            l[nt][h] *= f;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-              o[s][nt][h] *= f;
-              o[s][nt][2 + h] *= f;
             }
           }
-      }
-      // weights
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        }
+
+        // ---- softmax of the lane's rows 2·t4, 2·t4 + 1 at tokens 16·mt + g
+        // and 16·mt + g + 8: t into sc
+        float sk[MT][2], lv[MT][2], back[MT][2];   // s_k, log₂ s_v, 1 / s_v
+        if (FP8) {
+          const float* ss = reinterpret_cast<const float*>(
+                                ring + stage * C::STAGE + 2 * C::TILE) +
+                            part;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float& x = sc[mt][nt][2 * k + h];
-              x = ex2_approx(x - top[nt][h]);
-              l[nt][h] = FP8 ? fmaf(x, back[mt][k], l[nt][h]) : l[nt][h] + x;
+            for (int h = 0; h < 2; ++h) {
+              sk[mt][h] = ss[16 * mt + g + 8 * h];
+              lv[mt][h] = lg2_approx(ss[STEP + 16 * mt + g + 8 * h]);
+              // (0 where nothing was loaded)
+              back[mt][h] =
+                  lv[mt][h] == -INFINITY ? 0.0f : ex2_approx(-lv[mt][h]);
             }
-      if (mixed) {
-        // Rows of several new tokens see different ends of this step.  What
-        // a later token's v holds (NaN, say) must not reach a row that does
-        // not see it through a weight of 0: the last tokens' products are
-        // added one by one, and their v then cleared.
-        const int k1 = min(PART, n - t1);
-#pragma unroll 1
-        for (int k = max(0, len - p.per_seq + 1 - t1); k < k1; ++k) {
-          float w[NT][2];
-          uint32_t sees = 0;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float f;
+              if constexpr (C::QREG)
+                f = qf[nt][j & 1];
+              else
+                f = s_qf[8 * nt + 2 * t4 + (j & 1)];
+              float& x = sc[mt][nt][j];
+              x = FP8 ? fmaf(x * sk[mt][j >> 1], f, lv[mt][j >> 1]) : x * f;
+            }
+        const bool mixed = p.per_seq > 1 && t1 > len - p.per_seq + 1 - PART;
+        if (valid != FULL || mixed) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (t1 + k < seen(nt, h)) sees |= 1u << (2 * nt + h);
-              w[nt][h] = 0.0f;
+              const int end = seen(nt, h) - t1;
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const float x = __shfl_sync(
-                      0xffffffffu, sc[mt][nt][2 * i + h], 4 * (k & 7) + t4);
-                  if (k >> 3 == 2 * mt + i) w[nt][h] = x;
+                  const int k = 16 * mt + g + 8 * i;
+                  if (!((valid >> k) & 1) || k >= end)
+                    sc[mt][nt][2 * i + h] = -INFINITY;
                 }
             }
-          unsigned char* const vrow = rows_at + C::TILE;
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            float2 v;
-            if constexpr (FP8) {
-              v = pair_to_f32<TP_FP8>(*reinterpret_cast<const uint16_t*>(
-                  vrow + spread<ROW>(k, s) + 2 * g));
-            } else {
-              const uint32_t a = *reinterpret_cast<const uint16_t*>(
-                  vrow + spread<ROW>(k, 2 * s) + 2 * g);
-              const uint32_t b = *reinterpret_cast<const uint16_t*>(
-                  vrow + spread<ROW>(k, 2 * s + 1) + 2 * g);
-              v = pair_to_f32<CACHE>(a | b << 16);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (sees >> (2 * nt + h) & 1) {
-                  o[s][nt][h] = fmaf(w[nt][h], v.x, o[s][nt][h]);
-                  o[s][nt][2 + h] = fmaf(w[nt][h], v.y, o[s][nt][2 + h]);
-                }
-          }
-          __syncwarp();
-          if (lane < CHUNKS)
-            *reinterpret_cast<uint4*>(vrow + spread<ROW>(k, lane)) =
-                make_uint4(0, 0, 0, 0);
         }
-        __syncwarp();
-      }
-      uint32_t b[MT][NT][2], b2[MT][NT][2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        float high[NT][2];
+        bool rise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float w0 = sc[mt][nt][2 * h], w1 = sc[mt][nt][2 * h + 1];
-            if (BF) {
-              const uint32_t x = pack_bf16x2(w0, w1);
-              const float2 f = unpack_bf16x2(x);
-              b[mt][nt][h] = movmatrix(x);
-              b2[mt][nt][h] = movmatrix(pack_bf16x2(w0 - f.x, w1 - f.y));
-            } else {
-              b[mt][nt][h] = movmatrix(pack_f16x2(w0, w1));
-            }
+            float x = fmaxf(sc[0][nt][h], sc[0][nt][2 + h]);
+#pragma unroll
+            for (int mt = 1; mt < MT; ++mt)
+              x = fmaxf(x, fmaxf(sc[mt][nt][h], sc[mt][nt][2 + h]));
+            high[nt][h] = x;
+            rise |= x > top[nt][h] + SLACK;
           }
-
-      // ---- Oᵀ += Vᵀ·Pᵀ
-      auto add_values = [&](const uint32_t(&a)[4], int s, int mt) {
+        if (__any_sync(0xffffffffu, rise)) {   // maxima of all rows anew
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma<BF>(o[s][nt], a, b[mt][nt][0], b[mt][nt][1]);
-          if (BF) mma<BF>(o[s][nt], a, b2[mt][nt][0], b2[mt][nt][1]);
-        }
-      };
-      if constexpr (FP8) {
-        const uint32_t at = vt + spread<ROW>(lane & 15, lane >> 4);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int s = 0; s < KS; s += 2) {
-            uint32_t u[4];
-            ldmatrix_trans((at ^ (s << 4)) + mt * 16 * ROW, u);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              // elements 2g, 2g + 1 of tokens 2t, 2t + 1 to pairs of tokens
-              uint32_t a[4];
-              codes_f16(__byte_perm(u[2 * h], 0, 0x3120), a[0], a[1]);
-              codes_f16(__byte_perm(u[2 * h + 1], 0, 0x3120), a[2], a[3]);
-              add_values(a, s + h, mt);
+              float x = fmaxf(high[nt][h], top[nt][h]);
+#pragma unroll
+              for (int z = 4; z < 32; z <<= 1)
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
+              const float f = ex2_approx(top[nt][h] - x);
+              top[nt][h] = x;
+              l[nt][h] *= f;
+#pragma unroll
+              for (int s = 0; s < KS; ++s) {
+                o[s][nt][h] *= f;
+                o[s][nt][2 + h] *= f;
+              }
             }
+        }
+        // weights
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float& x = sc[mt][nt][2 * k + h];
+                x = ex2_approx(x - top[nt][h]);
+                l[nt][h] = FP8 ? fmaf(x, back[mt][k], l[nt][h]) : l[nt][h] + x;
+              }
+        if (mixed) {
+          // Rows of several new tokens see different ends of this step.  What
+          // a later token's v holds (NaN, say) must not reach a row that does
+          // not see it through a weight of 0: the last tokens' products are
+          // added one by one, and their v then cleared.
+          const int k1 = min(PART, n - t1);
+#pragma unroll 1
+          for (int k = max(0, len - p.per_seq + 1 - t1); k < k1; ++k) {
+            float w[NT][2];
+            uint32_t sees = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (t1 + k < seen(nt, h)) sees |= 1u << (2 * nt + h);
+                w[nt][h] = 0.0f;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const float x = __shfl_sync(
+                        0xffffffffu, sc[mt][nt][2 * i + h], 4 * (k & 7) + t4);
+                    if (k >> 3 == 2 * mt + i) w[nt][h] = x;
+                  }
+              }
+            unsigned char* const vrow = rows_at + C::TILE;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              float2 v;
+              if constexpr (FP8) {
+                v = pair_to_f32<TP_FP8>(*reinterpret_cast<const uint16_t*>(
+                    vrow + spread<ROW>(k, s) + 2 * g));
+              } else {
+                const uint32_t a = *reinterpret_cast<const uint16_t*>(
+                    vrow + spread<ROW>(k, 2 * s) + 2 * g);
+                const uint32_t b = *reinterpret_cast<const uint16_t*>(
+                    vrow + spread<ROW>(k, 2 * s + 1) + 2 * g);
+                v = pair_to_f32<CACHE>(a | b << 16);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (sees >> (2 * nt + h) & 1) {
+                    o[s][nt][h] = fmaf(w[nt][h], v.x, o[s][nt][h]);
+                    o[s][nt][2 + h] = fmaf(w[nt][h], v.y, o[s][nt][2 + h]);
+                  }
+            }
+            __syncwarp();
+            if (lane < CHUNKS)
+              *reinterpret_cast<uint4*>(vrow + spread<ROW>(k, lane)) =
+                  make_uint4(0, 0, 0, 0);
           }
-      } else {
-        const uint32_t at =
-            vt + spread<ROW>((lane & 7) + ((lane >> 1) & 8), (lane >> 3) & 1);
+          __syncwarp();
+        }
+        uint32_t b[MT][NT][2], b2[MT][NT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            uint32_t a[4];
-            ldmatrix_trans((at ^ (s << 5)) + mt * 16 * ROW, a);
-            add_values(a, s, mt);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float w0 = sc[mt][nt][2 * h], w1 = sc[mt][nt][2 * h + 1];
+              if (BF) {
+                const uint32_t x = pack_bf16x2(w0, w1);
+                const float2 f = unpack_bf16x2(x);
+                b[mt][nt][h] = movmatrix(x);
+                b2[mt][nt][h] = movmatrix(pack_bf16x2(w0 - f.x, w1 - f.y));
+              } else {
+                b[mt][nt][h] = movmatrix(pack_f16x2(w0, w1));
+              }
+            }
+
+        // ---- Oᵀ += Vᵀ·Pᵀ
+        auto add_values = [&](const uint32_t(&a)[4], int s, int mt) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<BF>(o[s][nt], a, b[mt][nt][0], b[mt][nt][1]);
+            if (BF) mma<BF>(o[s][nt], a, b2[mt][nt][0], b2[mt][nt][1]);
           }
-      }
+        };
+        if constexpr (FP8) {
+          const uint32_t at = vt + spread<ROW>(lane & 15, lane >> 4);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int s = 0; s < KS; s += 2) {
+              uint32_t u[4];
+              ldmatrix_trans((at ^ (s << 4)) + mt * 16 * ROW, u);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                // elements 2g, 2g + 1 of tokens 2t, 2t + 1 to pairs of tokens
+                uint32_t a[4];
+                codes_f16(__byte_perm(u[2 * h], 0, 0x3120), a[0], a[1]);
+                codes_f16(__byte_perm(u[2 * h + 1], 0, 0x3120), a[2], a[3]);
+                add_values(a, s + h, mt);
+              }
+            }
+        } else {
+          const uint32_t at =
+              vt + spread<ROW>((lane & 7) + ((lane >> 1) & 8), (lane >> 3) & 1);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              uint32_t a[4];
+              ldmatrix_trans((at ^ (s << 5)) + mt * 16 * ROW, a);
+              add_values(a, s, mt);
+            }
+        }
       }
       if (++stage == STAGES) stage = 0;
       ++done;
@@ -935,14 +933,13 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
       const bool none = sum == 0.0f;
       s_ref[r] = all;
       s_out[r] = none ? 0.0f : 1.0f / sum;
-      const float lse2 = none ? -INFINITY : all + log2f(sum);
       const int rr = row0 + r, j = rr / p.group;
       if (rr >= rows) {
       } else if (part) {
-        p.part_lse[part_at * C::ROWS + r] = lse2;
+        p.part_l[part_at * C::ROWS + r] = make_float2(all, sum);
       } else if (p.a.lse != nullptr) {
         p.a.lse[(qrow + j) * p.a.n_q + seg.kvh * p.group + rr -
-                j * p.group] = lse2 * LN2;
+                j * p.group] = none ? -INFINITY : (all + log2f(sum)) * LN2;
       }
     }
     if (tid == THREADS - 1) {
@@ -953,8 +950,9 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
         cut.head = seg.kvh;
         cut.tile = seg.tile;
         cut.first_slot = (int)part_at;
-        cut.parts = min(pieces.cta_of(seg.first + seg.nb - 1), pieces.ctas - 1) -
-                    (int)blockIdx.x + 1;
+        const int end =
+            min(pieces.cta_of(seg.first + seg.nb - 1), pieces.ctas - 1);
+        cut.parts = end - (int)blockIdx.x + 1;
         p.cuts[blockIdx.x] = cut;
       }
     }
@@ -1029,10 +1027,11 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS,
 }
 
 // Joins the parts of the units that were cut: CTA (i, j) rows j·cta_rows up to
-// (j + 1)·cta_rows of the one that CTA i of the first kernel begins, if there is
-// one.  A warp has a row, D/4 lanes of it a part each time; with more than FEW
-// parts all eight warps share a row, one after the other.  What bounds it is its chain of three
-// loads (the cut, its parts, nothing else waits) and a launch.
+// (j + 1)·cta_rows of the one that CTA i of the first kernel begins, if there
+// is one.  A warp has a row, D/4 lanes of it a part each time; with more than
+// FEW parts all eight warps share a row, one after the other.  What bounds it
+// is a launch and a chain of two loads, the cut and then its parts (2.7 µs; 4
+// with 38 parts a row).
 constexpr int JOIN_WARPS = 8;
 constexpr int FEW = 8;
 template <int D>
@@ -1053,52 +1052,54 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS)
   const bool few = cut.parts <= FEW;
   const int stride = SIDE * (few ? 1 : JOIN_WARPS);
   // o and the sum of parts side, side + stride, … of row r, relative to top
-  float top, sum;
-  float4 v;
+  float top = NOTHING, sum = 0.0f;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   auto add_parts = [&](int r) {
-    top = -INFINITY;
+    top = NOTHING;
     sum = 0.0f;
     v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int i0 = lane / LANES + (few ? 0 : SIDE * warp); i0 < cut.parts;
          i0 += U * stride) {
-      float x[U];
+      float2 x[U];
       float4 u[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int i = i0 + k * stride;
-        x[k] = -INFINITY;
+        x[k] = make_float2(NOTHING, 0.0f);
         u[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (i < cut.parts) {
           const int64_t slot =
               i == 0 ? cut.first_slot : 2 * ((int64_t)blockIdx.x + i);
           const int64_t at = slot * tile_rows + r;
-          x[k] = p.part_lse[at];
+          x[k] = p.part_l[at];
           u[k] = *reinterpret_cast<const float4*>(p.part_o + at * D + e);
         }
       }
+      float high = top;
+#pragma unroll
+      for (int k = 0; k < U; ++k) high = fmaxf(high, x[k].x);
+      const float f = ex2_approx(top - high);
+      top = high;
+      sum *= f;
+      v.x *= f;
+      v.y *= f;
+      v.z *= f;
+      v.w *= f;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        // a part that saw nothing is left out; NaN is not
-        if (x[k] == -INFINITY) continue;
-        const float high = fmaxf(top, x[k]);
-        const float f = top == -INFINITY ? 0.0f : ex2_approx(top - high);
-        const float w = ex2_approx(x[k] - high);
-        top = high;
-        sum = fmaf(sum, f, w);
-        v.x = fmaf(v.x, f, w * u[k].x);
-        v.y = fmaf(v.y, f, w * u[k].y);
-        v.z = fmaf(v.z, f, w * u[k].z);
-        v.w = fmaf(v.w, f, w * u[k].w);
+        const float w = x[k].y * ex2_approx(x[k].x - high);
+        sum += w;
+        v.x = fmaf(w, u[k].x, v.x);
+        v.y = fmaf(w, u[k].y, v.y);
+        v.z = fmaf(w, u[k].z, v.z);
+        v.w = fmaf(w, u[k].w, v.w);
       }
     }
   };
-  // another set of parts: (top2, sum2, v2) joins (top, sum, v)
+  // another set of parts, with its top, sum and v, joins them
   auto merge = [&](float top2, float sum2, float4 v2) {
     const float high = fmaxf(top, top2);
-    const float f = top == -INFINITY ? (sum == 0.0f ? 0.0f : 1.0f)
-                                     : ex2_approx(top - high);
-    const float f2 = top2 == -INFINITY ? (sum2 == 0.0f ? 0.0f : 1.0f)
-                                       : ex2_approx(top2 - high);
+    const float f = ex2_approx(top - high), f2 = ex2_approx(top2 - high);
     top = high;
     sum = sum * f + sum2 * f2;
     v.x = v.x * f + v2.x * f2;
@@ -1164,14 +1165,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS)
 int tile_rows_of(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 struct Layout {
-  size_t o, lse, cuts, bytes;
+  size_t o, l, cuts, bytes;
 };
 Layout layout_of(int ctas, int tile_rows, int d) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   Layout l;
   l.o = 0;
-  l.lse = up((size_t)2 * ctas * tile_rows * d * 4);
-  l.cuts = l.lse + up((size_t)2 * ctas * tile_rows * 4);
+  l.l = up((size_t)2 * ctas * tile_rows * d * 4);
+  l.cuts = l.l + up((size_t)2 * ctas * tile_rows * 8);
   l.bytes = l.cuts + up((size_t)ctas * sizeof(Cut));
   return l;
 }
@@ -1180,7 +1181,6 @@ Layout layout_of(int ctas, int tile_rows, int d) {
 template <int CACHE, int D, int NT>
 int launch(Params& p, int sms, cudaStream_t s) {
   using C = Conf<CACHE, D, NT>;
-  static_assert(C::CTAS <= MAX_CTAS, "the workspace has room for MAX_CTAS");
   static std::atomic<uint64_t> ready{0};   // devices whose attribute is set
   int dev = 0;
   int err = cudaGetDevice(&dev);
@@ -1193,7 +1193,7 @@ int launch(Params& p, int sms, cudaStream_t s) {
     if (err) return err;
     ready.fetch_or(bit);
   }
-  const int ctas = C::CTAS * sms;
+  const int ctas = CTAS * sms;
   p.skip_cols = C::BLOCK / p.page;
   p.skip_off = C::BLOCK % p.page;
   decode_kernel<CACHE, D, NT><<<ctas, C::THREADS, C::SMEM, s>>>(p);
@@ -1232,7 +1232,7 @@ int launch_d(Params& p, int tile_rows, int sms, cudaStream_t s) {
 
 size_t attn_decode_ws_bytes(const tp_kv_cache& c, int64_t rows, int n_q) {
   const int64_t unit = rows / c.b * (n_q / c.n_kv);
-  return layout_of(MAX_CTAS * device_sm_count(), tile_rows_of(unit), c.d).bytes;
+  return layout_of(CTAS * device_sm_count(), tile_rows_of(unit), c.d).bytes;
 }
 
 int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,
@@ -1252,7 +1252,8 @@ int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,
   p.cap = c.table_cols * c.page;
   p.page_shift = 30;
   while (1 << (p.page_shift - 30) < c.page) ++p.page_shift;
-  p.page_mul = (uint32_t)((((uint64_t)1 << p.page_shift) + c.page - 1) / c.page);
+  p.page_mul =
+      (uint32_t)((((uint64_t)1 << p.page_shift) + c.page - 1) / c.page);
   p.pages = (int)c.pages;
   p.page_s = (int)c.page_stride;
   p.token_s = (int)c.token_stride;
@@ -1261,10 +1262,10 @@ int attn_decode(const tp_kv_cache& c, int dtype, const DecodeArgs& a,
   p.s_token_s = (int)c.s_token_stride;
   p.s_head_s = (int)c.s_head_stride;
   const int sms = device_sm_count();
-  const Layout l = layout_of(MAX_CTAS * sms, tile_rows, c.d);
+  const Layout l = layout_of(CTAS * sms, tile_rows, c.d);
   char* ws = static_cast<char*>(a.ws);
   p.part_o = reinterpret_cast<float*>(ws + l.o);
-  p.part_lse = reinterpret_cast<float*>(ws + l.lse);
+  p.part_l = reinterpret_cast<float2*>(ws + l.l);
   p.cuts = reinterpret_cast<Cut*>(ws + l.cuts);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // the lengths, and with them the work, are known on the device alone

@@ -394,3 +394,23 @@ def test_idle_places_queries_have_no_influence(tp):
     tp.device_status()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert not b[0][0].any() and not b[0][2].any()
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_scores_of_1e34(tp, sign):
+    # every score is the same far value: the values' mean
+    c = Cache([300, 17], 16, 1, 128, "bf16", 98)
+    c.cache[0].fill_(2.0 ** 53 * sign)
+    q = torch.full((2, 8, 128), 2.0 ** 53, dtype=BF16, device="cuda")
+    out, lse = attend(tp, c, q, scale=1.0)
+    tp.device_status()
+    for i, n in enumerate(c.lens):
+        t = np.arange(n)
+        x = c.values[1][c.table[i][t // 16], t % 16][:, 0]
+        # one weight of 1 each, the sum's n + 9 roundings, the output's
+        e = (n + 9) * 2.0 ** -22 * np.abs(x).mean(0) + \
+            2.0 ** -8 * np.abs(x.mean(0))
+        assert (np.abs(out[i].double().cpu().numpy() - x.mean(0)) <=
+                e * 1.01).all()
+        far = lse[i].double().cpu().numpy() / (sign * 2.0 ** 113)
+        assert (np.abs(far - 1) <= 2.0 ** -20).all()
