@@ -594,7 +594,8 @@ tp_status tp_kv_cache_read(const tp_kv_cache* c, int32_t dtype, int64_t rows,
  * what is added of v are fp32.  What a masked or unused place of a page holds
  * (infinities and NaN among it) has no influence.
  * The same call gives the same bits; how a sequence's tokens are split, and
- * with it a sum's order, depends on the lengths of the whole batch.
+ * with it a sum's order, depends on the lengths of the whole batch and on how
+ * many tokens a row of the table can list.
  * ws: scratch, not kept between calls; calls that overlap on the GPU (two
  * streams, two graphs) need one each. */
 size_t tp_attn_decode_workspace_bytes(const tp_kv_cache* c, int64_t rows,

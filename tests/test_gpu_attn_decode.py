@@ -414,3 +414,25 @@ def test_scores_of_1e34(tp, sign):
                 e * 1.01).all()
         far = lse[i].double().cpu().numpy() / (sign * 2.0 ** 113)
         assert (np.abs(far - 1) <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_the_same_sequences_under_a_wider_table(tp, kind):
+    # a narrow table leaves every sequence to one CTA and needs no join
+    c = Cache([100, 0, 64, 7], 16, 2, 128, kind, 99)
+    x, q = queries(c, 4, 8, BF16, 9)
+    n = tp.launch_count()
+    narrow = attend(tp, c, q)
+    assert tp.launch_count() - n == 1
+    c.dev_table = torch.nn.functional.pad(c.dev_table, (0, 500), value=-1)
+    n = tp.launch_count()
+    wide = attend(tp, c, q)
+    assert tp.launch_count() - n == 2
+    tp.device_status()
+    want, wl, eo, el = attend_bounds(c, x, c.d ** -0.5, BF16)
+    for out, lse in (narrow, wide):
+        got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        seen = np.isfinite(wl)
+        assert (np.isfinite(gl) == seen).all() and not got[~seen].any()
+        assert (np.abs(got - want) <= eo).all()
+        assert (np.abs(gl[seen] - wl[seen]) <= el[seen]).all()
