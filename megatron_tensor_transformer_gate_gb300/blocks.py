@@ -406,6 +406,9 @@ class TPBlockFP8Attention:
         may be given (x or r among it); without r it is x."""
         if self.weights is None:
             raise RuntimeError("load_weights comes first")
+        if table.shape[0] != self.b:   # (fewer sequences with more new tokens?)
+            raise ValueError(f"table: {self.b} sequences, got "
+                             f"{table.shape[0]}")
         with _made_on(stream):
             if r is None:
                 x1 = x if x1 is None else x1

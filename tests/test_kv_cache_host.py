@@ -449,3 +449,17 @@ def test_attention_blocks_weights_that_failed_to_load_are_not_used(tp):
         blk.load_weights(*W)
     with pytest.raises(RuntimeError, match="load_weights"):
         blk.forward(torch.zeros(2, 256), torch.ones(256), None, None, None)
+
+
+def test_attention_block_refuses_another_batch():
+    """A table of one sequence for two rows is not one with two new tokens."""
+    from megatron_tensor_transformer_gate_gb300.blocks import \
+        TPBlockFP8Attention
+    blk = TPBlockFP8Attention(2, 256, 2, 1, device="cpu")
+    blk.weights = ((None, None), (None, None))
+    lens = torch.ones(1, dtype=torch.int32)
+    for b in (1, 4):
+        with pytest.raises(ValueError, match="2 sequences"):
+            blk.forward(torch.zeros(2, 256), torch.ones(256),
+                        (None, None, None, None),
+                        torch.zeros(b, 3, dtype=torch.int32), lens)
