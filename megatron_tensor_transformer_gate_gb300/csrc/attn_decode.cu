@@ -26,12 +26,12 @@
 // written again as fp16.  E4M3 codes become fp16 operands in registers here.
 //
 // Measured (GB300, copy 6.8 TB/s): 32 sequences of 32768 in bf16 630 µs = 1.0
-// of a copy, in E4M3 337 µs = 0.97; one of 131072 in bf16 89 µs (0.88: 4 µs
-// until the first copies are in flight, 4 for the join and its launch); 64 of
-// 61 to 8192 in E4M3 44 µs (0.69: the start, 512 segments' ends, latencies
-// between a step's dependent instructions); with 32 rows over codes 367 µs for
-// 1.6 GB (0.64: those latencies alone, eight warps an SM at 250 registers a
-// thread).
+// of a copy, in E4M3 335 to 348 = 0.97 to 0.93; one of 131072 in bf16 89 µs
+// (0.88: 4 µs until the first copies are in flight, 4 for the join and its
+// launch); 64 of 61 to 8192 in E4M3 44 µs (0.69: the start, 512 segments' ends,
+// latencies between a step's dependent instructions); with 32 rows over codes
+// 361 µs for 1.6 GB (0.65: those latencies alone, eight warps an SM at 250
+// registers a thread).
 //
 // Precision: scores, maxima, sums and o are fp32.  Over fp16 values and E4M3
 // codes the operands are fp16, q divided by a power of two that brings its
@@ -364,6 +364,8 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
     pieces.more = pieces.total - pieces.share * pieces.ctas;
     const int cta = blockIdx.x;
     if (tid == 0) p.cuts[cta].tile = -1;
+    // (read if this warp leaves and, lengths having changed, others do not)
+    if (tid == 32) segs[0].there = segs[1].there = segs[2].there = 0;
     if (cta >= pieces.ctas) return;
     const int at = pieces.begin(cta);
     int before = inc - sum;
