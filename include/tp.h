@@ -531,7 +531,8 @@ tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
  * TP_FP8 vectors are E4M3 codes with one fp32 scale each in ks and vs
  * [pages, page, n_kv] (strides of their own, again shared): as in
  * tp_quantize_fp8_block's TP_FP8_ROW, s = amax / 448, code = E4M3(x·448/amax)
- * and the element's value is code·s.
+ * and the element's value is code·s.  Scales are above 0 (the attention takes
+ * their logarithm).
  * table[i·table_stride + c], device int32, is the page of sequence i's tokens
  * [c·page, (c + 1)·page); lens[i], device int32, how many tokens the sequence
  * has, the newest ones of a call among them.  Only the entries that a call's
@@ -560,9 +561,9 @@ typedef struct {
 
 /* Write new tokens: rows of K and V ([rows, n_kv, d], TP_BF16 or TP_F16; a
  * row's and a head's element strides are multiples of 8 below 2^31, such as
- * those of the QKV projection's output), each value rounded once to the cache's type (an
- * fp16 cache reports TP_ERR_RANGE for what fp16 does not hold).  The new
- * tokens are their sequence's last ones: of m rows, row j belongs to position
+ * those of the QKV projection's output), each value rounded once to the
+ * cache's type (an fp16 cache reports TP_ERR_RANGE for what fp16 does not
+ * hold).  The new tokens are their sequence's last ones: of m rows, row j belongs to position
  * lens[i] − m + j, and to no token where that is negative (an idle place;
  * padding in front of a short prompt).  start NULL: rows = b·m, m for each
  * sequence in turn; else device int32 [b + 1], not decreasing: sequence i's
@@ -586,8 +587,9 @@ tp_status tp_kv_cache_read(const tp_kv_cache* c, int32_t dtype, int64_t rows,
  * q, out: [rows, n_q, d] of `dtype` (TP_BF16 or TP_F16; TP_F16 not over a
  * TP_BF16 cache: TP_ERR_UNSUPPORTED), row and head strides multiples of 8;
  * rows = b·m, the last m tokens of each sequence (b·n_kv·⌈m·n_q/(32·n_kv)⌉·
- * (table_cols·page/64 + 17) below 2^31): row j of sequence i is the token at p = lens[i] − m + j and sees the tokens t ≤ p.  Query head j reads
- * kv head ⌊j·n_kv/n_q⌋.
+ * (table_cols·page/64 + 17) below 2^31): row j of sequence i is the token at
+ * p = lens[i] − m + j and sees the tokens t ≤ p.  Query head j reads kv head
+ * ⌊j·n_kv/n_q⌋.
  *   x_t = scale·q·k_t,  out = Σ_t e^(x_t)·v_t / Σ_t e^(x_t),
  *   lse = ln Σ_t e^(x_t)     (fp32 [rows, n_q] dense; NULL: not written).
  * A row that sees nothing (p < 0) has out = 0 and lse = −∞.  Scores, sums and

@@ -299,10 +299,11 @@ def fp8_block_empty(rows, cols, group=FP8_ROW, device="cuda"):
 
 
 # The checks of a call (these and those of the key-value cache below) run before
-# every launch, which for a generated token is most of its time.  csrc/pycall.cpp makes them for arguments in their ordinary
-# form and calls the C entry (2.7 to 4 µs a call); where it finds anything else
-# it answers None, and the functions below check again and say what is wrong.
-# Where it is not built for this Python and torch they make every call.
+# every launch, which for a generated token is most of its time.
+# csrc/pycall.cpp makes them for arguments in their ordinary form and calls the C
+# entry (2.7 to 4 µs a call); where it finds anything else it answers None, and
+# the functions below check again and say what is wrong.  Where it is not built
+# for this Python and torch they make every call.
 _tpcall = None   # that module, or its stand-in
 
 

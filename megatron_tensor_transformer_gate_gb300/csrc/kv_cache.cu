@@ -11,9 +11,9 @@
 // exchanges that leave one vector's in each lane (or two), which then divides
 // for it alone.
 //
-// Measured (GB300, copy 6.8 TB/s): 79970 tokens of fp16 to E4M3 85 µs (0.86 of a
+// Measured (GB300, copy 6.8 TB/s): 79970 tokens of fp16 to E4M3 84 µs (0.87 of a
 // copy, bound by DRAM and the look-ups in front of a CTA's loads), back to fp16
-// 71767 in 75 (0.87); 256 tokens 2.7 µs, one 2.2: a chain of three loads and a
+// 71767 in 75 (0.87); 256 tokens 2.6 µs, one 2.2: a chain of three loads and a
 // launch.
 #include <cuda_runtime.h>
 
