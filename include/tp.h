@@ -592,9 +592,12 @@ tp_status tp_kv_cache_read(const tp_kv_cache* c, int32_t dtype, int64_t rows,
  * ⌊j·n_kv/n_q⌋.
  *   x_t = scale·q·k_t,  out = Σ_t e^(x_t)·v_t / Σ_t e^(x_t),
  *   lse = ln Σ_t e^(x_t)     (fp32 [rows, n_q] dense; NULL: not written).
- * A row that sees nothing (p < 0) has out = 0 and lse = −∞.  Scores, sums and
- * what is added of v are fp32.  What a masked or unused place of a page holds
- * (infinities and NaN among it) has no influence.
+ * A row that sees nothing (p < 0) has out = 0 and lse = −∞.  Scores and sums
+ * are fp32; a weight is rounded in front of its product with v: over a TP_BF16
+ * cache to 2^-16 of itself, else to 2^-11 of itself, or where it is below 2^-25
+ * of its row's largest (scales of v counted in) to 2^-36 of that one.  What a
+ * masked or unused place of a page holds (infinities and NaN among it) has no
+ * influence.
  * The same call gives the same bits; how a sequence's tokens are split, and
  * with it a sum's order, depends on the lengths of the whole batch and on how
  * many tokens a row of the table can list.

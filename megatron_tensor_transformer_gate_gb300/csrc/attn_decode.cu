@@ -36,8 +36,11 @@
 // Precision: scores, maxima, sums and o are fp32.  Over fp16 values and E4M3
 // codes the operands are fp16, q divided by a power of two that brings its
 // largest element to [1, 2) (exact but for elements below 2^-14 of it).  P is
-// rounded to fp16 (2^-11); over bf16 values, where bf16 (2^-8) would show in
-// the output, it is the sum of two bf16 parts, 2^-16, at the price of a second
+// rounded to fp16 in front of the product with V: by 2^-11 of a weight, of those
+// below 2^-25 of the largest by 2^-36 of that one (weights lie between 2^11 and
+// 2^15 at a row's maximum); the denominator adds up the weights in fp32, in front
+// of that rounding.  Over bf16 values, where bf16 (2^-8) would show in the
+// output, P is the sum of two bf16 parts, 2^-16, at the price of a second
 // product.  A code's scale is multiplied into its score, and into its weight in
 // front of the product with V: t = x + log₂ s_v, w = 2^(t − M) with M the
 // running maximum of t, so that scales of any size keep the weights of the sum
@@ -59,10 +62,12 @@ namespace tp {
 namespace {
 
 constexpr int CTAS = 2;   // on an SM
-// The reference M may lie up to 2^SLACK below a row's largest t before the sums
-// are rescaled: some row of 32 has a new maximum in nearly every step of a
-// short segment, one beyond 2^8 hardly ever.  Weights stay far from fp16's end.
-constexpr float SLACK = 8.0f;
+// The reference M is set to 2^BELOW (Conf) below a row's largest t, and the sums
+// are rescaled when a t comes to lie more than 2^SLACK further above it: some
+// row of 32 has a new maximum in nearly every step of a short segment, one
+// beyond 2^4 seldom (32 rows over codes, 16x65536: 400 µs without slack, 364 with
+// 2^4, 362 with 2^8).  Weights are 2^15 at most, where fp16 ends at 2^16.
+constexpr float SLACK = 4.0f;
 // M of a row that has seen nothing: below every t and finite, so that nothing
 // needs a case of its own (2^(−∞ − M) = 0, 2^(M − t) = 0).
 constexpr float NOTHING = -3e38f;
@@ -108,6 +113,9 @@ struct Conf {
   static constexpr int SIZE = CACHE == TP_FP8 ? 1 : 2;
   static constexpr int ROW = D * SIZE;             // bytes
   static constexpr int ROWS = 8 * NT;
+  // fp16 weights are as large as they may be, so that small ones keep their
+  // bits; bf16 has as many exponents as fp32.
+  static constexpr float BELOW = CACHE == TP_BF16 ? 0.0f : 11.0f;
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * WARPS;
   // tokens of a warp: that are loaded, and that are worked on at a time
@@ -752,17 +760,19 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
             for (int mt = 1; mt < MT; ++mt)
               x = fmaxf(x, fmaxf(sc[mt][nt][h], sc[mt][nt][2 + h]));
             high[nt][h] = x;
-            rise |= x > top[nt][h] + SLACK;
+            // (the difference: of far scores M + 15 may be rounded to M + 16)
+            rise |= x - top[nt][h] > C::BELOW + SLACK;
           }
         if (__any_sync(0xffffffffu, rise)) {   // maxima of all rows anew
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float x = fmaxf(high[nt][h], top[nt][h]);
+              float x = high[nt][h];
 #pragma unroll
               for (int z = 4; z < 32; z <<= 1)
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
+              x = fmaxf(x - C::BELOW, top[nt][h]);
               const float f = ex2_approx(top[nt][h] - x);
               top[nt][h] = x;
               l[nt][h] *= f;

@@ -1,0 +1,74 @@
+"""Attention of new tokens over a paged cache where weights, scales or values
+are far apart, against the fp64 definition (_kv_range.bounds)."""
+
+import numpy as np
+import pytest
+import torch
+
+from _kv_cache import Cache
+from _kv_range import agree, bounds
+from oracle import kv_cache as okv
+from test_gpu_attn_decode import attend, queries
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+def first_element_alone(c, x, k):
+    """Keys whose product with the queries (1, 0, …) is k[t] for token t of the
+    one sequence; returns the queries."""
+    n, table = c.lens[0], c.table[0]
+    t = np.arange(n)
+    c.values[0][table[t // c.page], t % c.page] = 0.0
+    c.values[0][table[t // c.page], t % c.page, :, 0] = k[:, None]
+    at = torch.from_numpy(table[t // c.page]).long().cuda(), \
+        torch.from_numpy(t % c.page).cuda()
+    if c.kind == "e4m3":
+        codes, s = okv.quantize(c.values[0][table[t // c.page], t % c.page])
+        c.cache[0].view(torch.uint8)[at] = torch.from_numpy(codes).cuda()
+        c.cache[2][at] = torch.from_numpy(s).cuda()
+    else:
+        c.cache[0][at] = torch.from_numpy(
+            c.values[0][table[t // c.page], t % c.page]).to(
+                c.cache[0].dtype).cuda()
+    x[:] = 0.0
+    x[..., 0] = 1.0
+    return torch.from_numpy(x).to(BF16).cuda()
+
+
+def set_values(c, t, codes=None, scale=None):
+    """Codes (or 16-bit values, all of a vector the same) and scales of tokens t
+    of the one sequence."""
+    page, off = c.table[0][t // c.page], t % c.page
+    at = torch.from_numpy(page).long().cuda(), torch.from_numpy(off).cuda()
+    if c.kind != "e4m3":
+        c.cache[1][at] = codes
+        c.values[1][page, off] = codes
+        return
+    v, s = c.cache[1].view(torch.uint8), c.cache[3]
+    if codes is not None:
+        v[at] = codes
+    if scale is not None:
+        s[at] = scale
+    with np.errstate(invalid="ignore"):
+        c.values[1] = okv.dequantize(v.cpu().numpy(), s.cpu().numpy())
+
+
+# ------------------------------------------------------------- weights far apart
+@pytest.mark.parametrize("nats", [10.0, 17.5, 20.0])
+@pytest.mark.parametrize("n", [192, 5000])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
+def test_heavy_tokens_without_a_value(tp, kind, n, nats):
+    # in each step of a warp one token has nearly all the weight and no value:
+    # what is left is the others' part
+    c = Cache([n], 16, 1, 128, kind, 101)
+    x, _ = queries(c, 1, 8, BF16, 9)
+    t = np.arange(n)
+    if kind == "e4m3":
+        set_values(c, t, scale=2.0 ** -8)
+    set_values(c, t[t % 16 == 0], codes=0)
+    q = first_element_alone(c, x, np.where(t % 16 == 0, nats, 0.0))
+    out, lse = attend(tp, c, q, scale=1.0)
+    tp.device_status()
+    agree(out, lse, bounds(c, x, 1.0, BF16))
