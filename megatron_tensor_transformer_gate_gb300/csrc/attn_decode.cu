@@ -713,9 +713,9 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
             for (int h = 0; h < 2; ++h) {
               sk[mt][h] = ss[16 * mt + g + 8 * h];
               lv[mt][h] = lg2_approx(ss[STEP + 16 * mt + g + 8 * h]);
-              // (0 where nothing was loaded)
-              back[mt][h] =
-                  lv[mt][h] == -INFINITY ? 0.0f : ex2_approx(-lv[mt][h]);
+              // 0 where nothing was loaded, and for NaN: 0·back of a token that
+              // a row does not see must not be NaN
+              back[mt][h] = lv[mt][h] > -110.0f ? ex2_approx(-lv[mt][h]) : 0.0f;
             }
         }
 #pragma unroll

@@ -72,3 +72,22 @@ def test_heavy_tokens_without_a_value(tp, kind, n, nats):
     out, lse = attend(tp, c, q, scale=1.0)
     tp.device_status()
     agree(out, lse, bounds(c, x, 1.0, BF16))
+
+
+# --------------------------------------------------------------- scales of values
+@pytest.mark.parametrize("scale", ["nan", "inf", "1e-45", "0"])
+@pytest.mark.parametrize("n", [50, 700])
+def test_scales_of_a_token_that_a_row_does_not_see(tp, n, scale):
+    # the third of four new tokens; the first two rows do not see it
+    c = Cache([n, 6], 16, 1, 128, "e4m3", 102)
+    x, q = queries(c, 8, 8, BF16, 9)
+    for i, m in enumerate(c.lens):
+        at = int(c.table[i][(m - 2) // 16]), (m - 2) % 16
+        c.cache[2][at] = c.cache[3][at] = float(scale)
+        for k in c.values:
+            k[at] = np.nan
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    with np.errstate(invalid="ignore"):
+        want = bounds(c, x, c.d ** -0.5, BF16)
+    agree(out, lse, want, [0, 1, 4, 5])
