@@ -116,6 +116,10 @@ struct Conf {
   // fp16 weights are as large as they may be, so that small ones keep their
   // bits; bf16 has as many exponents as fp32.
   static constexpr float BELOW = CACHE == TP_BF16 ? 0.0f : 11.0f;
+  // Sums over codes are kept 2^-RAISE of their size, Σ w·2^-RAISE / s_v: w is up
+  // to 2^15 and s_v from 2^-109 to 2^119, between which 2^20 tokens' sum stays
+  // in fp32's range at the one end, and 2^-18 of a w / s_v at the other.
+  static constexpr float RAISE = CACHE == TP_FP8 ? 12.0f : 0.0f;
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * WARPS;
   // tokens of a warp: that are loaded, and that are worked on at a time
@@ -195,6 +199,12 @@ __device__ __forceinline__ void codes_f16(uint32_t u, uint32_t& lo,
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(u));
+}
+// 2^x, subnormal results too
+__device__ __forceinline__ float ex2_whole(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
@@ -702,7 +712,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
 
         // ---- softmax of the lane's rows 2·t4, 2·t4 + 1 at tokens 16·mt + g
         // and 16·mt + g + 8: t into sc
-        float sk[MT][2], lv[MT][2], back[MT][2];   // s_k, log₂ s_v, 1 / s_v
+        float sk[MT][2], lv[MT][2], back[MT][2];   // s_k, log₂ s_v, 2^-RAISE / s_v
         if (FP8) {
           const float* ss = reinterpret_cast<const float*>(
                                 ring + stage * C::STAGE + 2 * C::TILE) +
@@ -715,7 +725,8 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
               lv[mt][h] = lg2_approx(ss[STEP + 16 * mt + g + 8 * h]);
               // 0 where nothing was loaded, and for NaN: 0·back of a token that
               // a row does not see must not be NaN
-              back[mt][h] = lv[mt][h] > -110.0f ? ex2_approx(-lv[mt][h]) : 0.0f;
+              back[mt][h] =
+                  lv[mt][h] > -110.0f ? ex2_whole(-lv[mt][h] - C::RAISE) : 0.0f;
             }
         }
 #pragma unroll
@@ -952,10 +963,11 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
       const int rr = row0 + r, j = rr / p.group;
       if (rr >= rows) {
       } else if (part) {
-        p.part_l[part_at * C::ROWS + r] = make_float2(all, sum);
+        p.part_l[part_at * C::ROWS + r] = make_float2(all + C::RAISE, sum);
       } else if (p.a.lse != nullptr) {
         p.a.lse[(qrow + j) * p.a.n_q + seg.kvh * p.group + rr -
-                j * p.group] = none ? -INFINITY : (all + log2f(sum)) * LN2;
+                j * p.group] =
+            none ? -INFINITY : (all + C::RAISE + log2f(sum)) * LN2;
       }
     }
     if (tid == THREADS - 1) {
@@ -980,7 +992,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
       float f[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        f[h] = ex2_approx(top[nt][h] - s_ref[8 * nt + 2 * t4 + h]);
+        f[h] = ex2_approx(top[nt][h] - s_ref[8 * nt + 2 * t4 + h] - C::RAISE);
       float* const mine =
           join + ((warp % (WARPS / 2)) * 8 + 2 * t4) * (D + 4) +
           (FP8 ? 2 * g : g);

@@ -91,3 +91,18 @@ def test_scales_of_a_token_that_a_row_does_not_see(tp, n, scale):
     with np.errstate(invalid="ignore"):
         want = bounds(c, x, c.d ** -0.5, BF16)
     agree(out, lse, want, [0, 1, 4, 5])
+
+
+@pytest.mark.parametrize("size", [-108, -60, 0, 60, 110, 119])
+@pytest.mark.parametrize("n", [300, 20000])
+def test_values_of_any_size(tp, n, size):
+    # scales of 2^size: from the smallest that kv_cache_write makes to bf16's end
+    c = Cache([n, 40], 64, 1, 128, "e4m3", 103)
+    codes, vs = c.cache[1].view(torch.uint8), c.cache[3]
+    vs.copy_(torch.where(torch.isfinite(vs), 2.0 ** size, vs))
+    with np.errstate(invalid="ignore"):
+        c.values[1] = okv.dequantize(codes.cpu().numpy(), vs.cpu().numpy())
+    x, q = queries(c, 2, 8, BF16, 9, std=0.1)
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    agree(out, lse, bounds(c, x, c.d ** -0.5, BF16))
