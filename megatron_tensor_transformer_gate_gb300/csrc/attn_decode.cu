@@ -71,6 +71,11 @@ constexpr float SLACK = 4.0f;
 // M of a row that has seen nothing: below every t and finite, so that nothing
 // needs a case of its own (2^(−∞ − M) = 0, 2^(M − t) = 0).
 constexpr float NOTHING = -3e38f;
+// Over codes a value scale below SMALLEST (the cache's writer makes none but 0 as
+// small) means that the vector has no value: it counts in the denominator alone.
+// What stands for log₂ of its scale is far below others', so that M is not its.
+constexpr float SMALLEST = 1.5407439555097887e-33f;   // 2^-109
+constexpr float NO_VALUE = -80.0f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -713,21 +718,43 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
         // ---- softmax of the lane's rows 2·t4, 2·t4 + 1 at tokens 16·mt + g
         // and 16·mt + g + 8: t into sc
         float sk[MT][2], lv[MT][2], back[MT][2];   // s_k, log₂ s_v, 2^-RAISE / s_v
-        if (FP8) {
+        if constexpr (FP8) {
           const float* ss = reinterpret_cast<const float*>(
                                 ring + stage * C::STAGE + 2 * C::TILE) +
                             part;
+          bool odd = false;   // a scale of no value (or of none loaded), or NaN
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               sk[mt][h] = ss[16 * mt + g + 8 * h];
-              lv[mt][h] = lg2_approx(ss[STEP + 16 * mt + g + 8 * h]);
-              // 0 where nothing was loaded, and for NaN: 0·back of a token that
-              // a row does not see must not be NaN
-              back[mt][h] =
-                  lv[mt][h] > -110.0f ? ex2_whole(-lv[mt][h] - C::RAISE) : 0.0f;
+              const float sv = ss[STEP + 16 * mt + g + 8 * h];
+              lv[mt][h] = lg2_approx(sv);
+              back[mt][h] = ex2_whole(-lv[mt][h] - C::RAISE);
+              odd |= !(fabsf(sv) >= SMALLEST);
             }
+          if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int k = 16 * mt + g + 8 * h;
+                const float sv = ss[STEP + k];
+                if (fabsf(sv) < SMALLEST) {
+                  lv[mt][h] = NO_VALUE;
+                  back[mt][h] = exp2f(-NO_VALUE - C::RAISE);
+#pragma unroll
+                  for (int ch = t4; ch < CHUNKS; ch += 4)
+                    *reinterpret_cast<uint4*>(rows_at + C::TILE +
+                                              spread<ROW>(k, ch)) =
+                        make_uint4(0, 0, 0, 0);
+                } else if (isnan(sv)) {
+                  // 0·back where a row does not see it must not be NaN
+                  back[mt][h] = 0.0f;
+                }
+              }
+            __syncwarp();
+          }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)

@@ -106,3 +106,21 @@ def test_values_of_any_size(tp, n, size):
     out, lse = attend(tp, c, q)
     tp.device_status()
     agree(out, lse, bounds(c, x, c.d ** -0.5, BF16))
+
+
+@pytest.mark.parametrize("n", [3, 300, 20000])
+def test_scales_of_zero(tp, n):
+    # whatever the codes are, the value is 0, and its weight counts
+    c = Cache([n], 64, 1, 128, "e4m3", 104)
+    x, q = queries(c, 2, 8, BF16, 9)
+    t = np.arange(n)
+    set_values(c, t[t % 3 == 1], scale=0.0)
+    set_values(c, t[t % 12 == 5], scale=2.0 ** -130)
+    agree(*attend(tp, c, q), bounds(c, x, c.d ** -0.5, BF16))
+    # no token has a value
+    set_values(c, t, scale=0.0)
+    c.values[1][:] = 0.0
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    assert not out.any()
+    agree(out, lse, bounds(c, x, c.d ** -0.5, BF16))
