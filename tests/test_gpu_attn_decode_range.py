@@ -124,3 +124,37 @@ def test_scales_of_zero(tp, n):
     tp.device_status()
     assert not out.any()
     agree(out, lse, bounds(c, x, c.d ** -0.5, BF16))
+
+
+@pytest.mark.parametrize("size", [2.0 ** -26, 1.0])
+@pytest.mark.parametrize("n", [60, 5000])
+def test_values_of_zeros_among_others(tp, n, size):
+    # as kv_cache_write stores them: the scale of zeros is 1, far above others'
+    c = Cache([n], 16, 1, 128, "e4m3", 105, std=size)
+    x, _ = queries(c, 1, 8, BF16, 9)
+    t = np.arange(n)
+    zeros = t % 16 == 0
+    set_values(c, t[zeros], codes=0, scale=1.0)
+    # with as much weight as the others, and with nearly all of it
+    for nats in (0.0, 20.0):
+        q = first_element_alone(c, x, np.where(zeros, nats, 0.0))
+        out, lse = attend(tp, c, q, scale=1.0)
+        agree(out, lse, bounds(c, x, 1.0, BF16))
+    # codes of −0, and nothing but zeros
+    set_values(c, t, codes=0x80, scale=1.0)
+    out, lse = attend(tp, c, q, scale=1.0)
+    tp.device_status()
+    assert not out.any()
+    agree(out, lse, bounds(c, x, 1.0, BF16))
+
+
+def test_a_nan_beside_zeros(tp):
+    c = Cache([40], 16, 1, 128, "e4m3", 106)
+    x, q = queries(c, 1, 8, BF16, 9)
+    set_values(c, np.arange(40), codes=0, scale=1.0)
+    c.cache[1].view(torch.uint8)[int(c.table[0][1]), 3, 0, 77] = 0xff
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    assert torch.isnan(out[0, :, 77]).all() and torch.isfinite(lse).all()
+    out[0, :, 77] = 0.0
+    assert not out.any()
