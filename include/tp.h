@@ -596,9 +596,10 @@ tp_status tp_kv_cache_read(const tp_kv_cache* c, int32_t dtype, int64_t rows,
  * A row that sees nothing (p < 0) has out = 0 and lse = −∞.  Scores and sums
  * are fp32; a weight is rounded in front of its product with v: over a TP_BF16
  * cache to 2^-16 of itself, else to 2^-11 of itself, or where it is below 2^-25
- * of its row's largest (scales of v counted in) to 2^-36 of that one.  What a
- * masked or unused place of a page holds (infinities and NaN among it) has no
- * influence.
+ * of its row's largest (scales of v counted in) to 2^-36 of that one.  An fp16
+ * output that fp16 does not hold (values of a TP_FP8 cache) is infinite and
+ * reported: TP_ERR_RANGE.  What a masked or unused place of a page holds
+ * (infinities and NaN among it) has no influence.
  * The same call gives the same bits; how a sequence's tokens are split, and
  * with it a sum's order, depends on the lengths of the whole batch and on how
  * many tokens a row of the table can list.

@@ -250,11 +250,24 @@ struct Pieces {
   }
 };
 
+// A finite output that fp16 does not hold is recorded.
+__device__ __noinline__ float4 to_f16_range(float4 v, unsigned* status) {
+  auto held = [&](float x) {
+    if (!(fabsf(x) > kF16Max) || isinf(x)) return x;
+    record_error(status, kDevRange, 45);
+    return x;
+  };
+  return make_float4(held(v.x), held(v.y), held(v.z), held(v.w));
+}
 // Elements e … e + 3 of a row's head.
-__device__ __forceinline__ void store4(const DecodeArgs& a, int64_t row,
-                                       int head, int e, float4 v) {
+__device__ __forceinline__ void store4(const Params& p, int64_t row, int head,
+                                       int e, float4 v) {
+  const DecodeArgs& a = p.a;
   uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.o_row +
                   head * a.o_head + e;
+  if (!a.bf16 && fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)),
+                       fmaxf(fabsf(v.z), fabsf(v.w))) > kF16Max)
+    v = to_f16_range(v, p.status);
   *reinterpret_cast<uint2*>(dst) =
       a.bf16 ? make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w))
              : make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
@@ -1089,7 +1102,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
                                      (part_at * C::ROWS + r) * D + e) = v;
         } else {
           const int j = rr / p.group;
-          store4(p.a, qrow + j, seg.kvh * p.group + rr - j * p.group, e, v);
+          store4(p, qrow + j, seg.kvh * p.group + rr - j * p.group, e, v);
         }
       }
       __syncthreads();   // the sums, and `seg`, are read
@@ -1202,7 +1215,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS)
     v.y *= f;
     v.z *= f;
     v.w *= f;
-    if (lane < LANES) store4(p.a, row, head, e, v);
+    if (lane < LANES) store4(p, row, head, e, v);
     if (lane == 0 && p.a.lse != nullptr)
       p.a.lse[row * p.a.n_q + head] =
           none ? -INFINITY : (top + log2f(sum)) * LN2;

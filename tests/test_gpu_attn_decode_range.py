@@ -158,3 +158,32 @@ def test_a_nan_beside_zeros(tp):
     assert torch.isnan(out[0, :, 77]).all() and torch.isfinite(lse).all()
     out[0, :, 77] = 0.0
     assert not out.any()
+
+
+# ------------------------------------------------------------------- fp16's end
+@pytest.mark.parametrize("n", [40, 3000])
+def test_outputs_that_fp16_does_not_hold(tp, n):
+    c = Cache([n], 16, 2, 64, "e4m3", 107)
+    set_values(c, np.arange(n), codes=0x70, scale=1024.0)   # 128 · 1024
+    c.cache[1].view(torch.uint8)[:, :, 1] = 0x60            # 32 · 1024
+    c.values[1][:, :, 1] = 32.0 * 1024
+    x, q = queries(c, 1, 4, F16, 9)
+    out, lse = attend(tp, c, q)
+    with pytest.raises(tp.TPError, match="TP_ERR_RANGE"):
+        tp.device_status()
+    assert torch.isinf(out[0, :2]).all()
+    assert (out[0, 2:] == 32768.0).all() and torch.isfinite(lse).all()
+    out, _ = attend(tp, c, q.bfloat16())     # which holds them
+    tp.device_status()
+    assert (out[0, :2] == 131072.0).all() and (out[0, 2:] == 32768.0).all()
+
+
+def test_an_infinite_value_is_no_output_beyond_fp16(tp):
+    c = Cache([40], 16, 1, 128, "f16", 109)
+    x, q = queries(c, 1, 8, F16, 9)
+    c.cache[1][int(c.table[0][0]), 3, 0, 5] = float("inf")
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    assert not torch.isfinite(out[0, :, 5]).any() and torch.isfinite(lse).all()
+    out[0, :, 5] = 0.0
+    assert torch.isfinite(out).all()
