@@ -250,10 +250,13 @@ struct Pieces {
   }
 };
 
-// A finite output that fp16 does not hold is recorded.
+// A finite output that fp16 does not hold: recorded, unless it is beyond fp16's
+// end by what the weights' rounding to fp16 adds to a mean of such values (2^-11)
+// and the sums' to that.
 __device__ __noinline__ float4 to_f16_range(float4 v, unsigned* status) {
   auto held = [&](float x) {
     if (!(fabsf(x) > kF16Max) || isinf(x)) return x;
+    if (fabsf(x) < kF16Max * (1.0f + 0x1p-10f)) return copysignf(kF16Max, x);
     record_error(status, kDevRange, 45);
     return x;
   };

@@ -178,6 +178,23 @@ def test_outputs_that_fp16_does_not_hold(tp, n):
     assert (out[0, :2] == 131072.0).all() and (out[0, 2:] == 32768.0).all()
 
 
+@pytest.mark.parametrize("kind", ["f16", "e4m3"])
+def test_means_of_fp16s_largest_value(tp, kind):
+    # one token's weight is 1, the others' are just above 1/2, where each is
+    # rounded up by 0.4 of fp16's step: a mean that is 2^-11.5 too large
+    c = Cache([16], 16, 1, 128, kind, 108)
+    t = np.arange(16)
+    if kind == "e4m3":
+        set_values(c, t, codes=0x7e, scale=65504.0 / 448.0)
+    else:
+        set_values(c, t, codes=65504.0)
+    x, _ = queries(c, 1, 8, BF16, 9)
+    q = first_element_alone(c, x, np.where(t == 0, 0.0, 1.0)).half()
+    out, _ = attend(tp, c, q, scale=float(np.log(0.5 * (1 + 0.6 * 2.0 ** -10))))
+    tp.device_status()
+    assert (out == 65504.0).all()
+
+
 def test_an_infinite_value_is_no_output_beyond_fp16(tp):
     c = Cache([40], 16, 1, 128, "f16", 109)
     x, q = queries(c, 1, 8, F16, 9)
