@@ -62,12 +62,6 @@ namespace tp {
 namespace {
 
 constexpr int CTAS = 2;   // on an SM
-// The reference M is set to 2^BELOW (Conf) below a row's largest t, and the sums
-// are rescaled when a t comes to lie more than 2^SLACK further above it: some
-// row of 32 has a new maximum in nearly every step of a short segment, one
-// beyond 2^4 seldom (32 rows over codes, 16x65536: 400 µs without slack, 364 with
-// 2^4, 362 with 2^8).  Weights are 2^15 at most, where fp16 ends at 2^16.
-constexpr float SLACK = 4.0f;
 // M of a row that has seen nothing: below every t and finite, so that nothing
 // needs a case of its own (2^(−∞ − M) = 0, 2^(M − t) = 0).
 constexpr float NOTHING = -3e38f;
@@ -119,9 +113,15 @@ struct Conf {
   static constexpr int SIZE = CACHE == TP_FP8 ? 1 : 2;
   static constexpr int ROW = D * SIZE;             // bytes
   static constexpr int ROWS = 8 * NT;
-  // fp16 weights are as large as they may be, so that small ones keep their
-  // bits; bf16 has as many exponents as fp32.
+  // The reference M is set to 2^BELOW below a row's largest t, and the sums are
+  // rescaled when a t comes to lie more than 2^SLACK further above it: some row
+  // of 32 has a new maximum in nearly every step of a short segment, one beyond
+  // 2^4 seldom (over codes, 16x65536 with 32 rows: 400 µs without slack, 364 with
+  // 2^4, 362 with 2^8; over bf16 473 with 2^8, 486 with 2^4).  fp16 weights are
+  // as large as they may be, 2^15 where fp16 ends at 2^16, so that small ones
+  // keep their bits; bf16 has as many exponents as fp32.
   static constexpr float BELOW = CACHE == TP_BF16 ? 0.0f : 11.0f;
+  static constexpr float SLACK = CACHE == TP_BF16 ? 8.0f : 4.0f;
   // Sums over codes are kept 2^-RAISE of their size, Σ w·2^-RAISE / s_v: w is up
   // to 2^15 and s_v from 2^-109 to 2^119, between which 2^20 tokens' sum stays
   // in fp32's range at the one end, and 2^-18 of a w / s_v at the other.
@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
               x = fmaxf(x, fmaxf(sc[mt][nt][h], sc[mt][nt][2 + h]));
             high[nt][h] = x;
             // (the difference: of far scores M + 15 may be rounded to M + 16)
-            rise |= x - top[nt][h] > C::BELOW + SLACK;
+            rise |= x - top[nt][h] > C::BELOW + C::SLACK;
           }
         if (__any_sync(0xffffffffu, rise)) {   // maxima of all rows anew
 #pragma unroll

@@ -204,3 +204,34 @@ def test_an_infinite_value_is_no_output_beyond_fp16(tp):
     assert not torch.isfinite(out[0, :, 5]).any() and torch.isfinite(lse).all()
     out[0, :, 5] = 0.0
     assert torch.isfinite(out).all()
+
+
+# ------------------------------------------------------------ many new tokens
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("f16", 64), ("e4m3", 128),
+                                    ("e4m3", 64)])
+def test_many_new_tokens_of_which_late_ones_are_nan(tp, kind, d):
+    # 64 new tokens of 8 heads: 16 tiles of rows, each with another end
+    c = Cache([150, 70, 20], 16, 1, d, kind, 110)
+    x, q = queries(c, 3 * 64, 8, BF16, 9)
+    first_bad = 40           # of each sequence's rows
+    for i, n in enumerate(c.lens):
+        for t in range(max(0, n - 64 + first_bad), n):
+            at = int(c.table[i][t // 16]), t % 16
+            for pool, k in zip(c.cache[:2], c.values):
+                if kind == "e4m3":
+                    pool.view(torch.uint8)[at] = 0x7f
+                else:
+                    pool[at] = float("nan")
+                k[at] = np.nan
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    with np.errstate(invalid="ignore"):
+        want = bounds(c, x, c.d ** -0.5, BF16)
+    rows = np.array([64 * i + j for i in range(3) for j in range(first_bad)])
+    seen = np.isfinite(want[1][rows]).all(axis=1)
+    assert np.isneginf(lse[torch.from_numpy(rows[~seen])].cpu().numpy()).all()
+    assert not out[torch.from_numpy(rows[~seen]).cuda()].any()
+    agree(out, lse, want, rows[seen])
+    for i, n in enumerate(c.lens):   # and those that see one
+        late = out[64 * i + max(first_bad, 64 - n):64 * (i + 1)]
+        assert torch.isnan(late).all()
