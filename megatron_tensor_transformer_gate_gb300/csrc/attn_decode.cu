@@ -116,8 +116,8 @@ struct Conf {
   // The reference M is set to 2^BELOW below a row's largest t, and the sums are
   // rescaled when a t comes to lie more than 2^SLACK further above it: some row
   // of 32 has a new maximum in nearly every step of a short segment, one beyond
-  // 2^4 seldom (over codes, 16x65536 with 32 rows: 400 µs without slack, 364 with
-  // 2^4, 362 with 2^8; over bf16 473 with 2^8, 486 with 2^4).  fp16 weights are
+  // 2^4 seldom (16x65536 with 32 rows: over codes 401 µs without slack, 368 with
+  // 2^4; over bf16 513, 477 and with 2^8 475).  fp16 weights are
   // as large as they may be, 2^15 where fp16 ends at 2^16, so that small ones
   // keep their bits; bf16 has as many exponents as fp32.
   static constexpr float BELOW = CACHE == TP_BF16 ? 0.0f : 11.0f;
@@ -262,18 +262,22 @@ __device__ __noinline__ float4 to_f16_range(float4 v, unsigned* status) {
   };
   return make_float4(held(v.x), held(v.y), held(v.z), held(v.w));
 }
-// Elements e … e + 3 of a row's head.
+// Elements e … e + 3 of a row's head.  F16: the output may be fp16 (over bf16
+// values it is not; the question alone takes 2 % with 32 rows).
+template <bool F16>
 __device__ __forceinline__ void store4(const Params& p, int64_t row, int head,
                                        int e, float4 v) {
   const DecodeArgs& a = p.a;
   uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.o_row +
                   head * a.o_head + e;
-  if (!a.bf16 && fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)),
-                       fmaxf(fabsf(v.z), fabsf(v.w))) > kF16Max)
+  if (F16 && !a.bf16 &&
+      fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))) >
+          kF16Max)
     v = to_f16_range(v, p.status);
   *reinterpret_cast<uint2*>(dst) =
-      a.bf16 ? make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w))
-             : make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+      F16 && !a.bf16
+          ? make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w))
+          : make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 // The pages of a warp's next tokens: lane l holds entries base + l and
@@ -1105,7 +1109,8 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
                                      (part_at * C::ROWS + r) * D + e) = v;
         } else {
           const int j = rr / p.group;
-          store4(p, qrow + j, seg.kvh * p.group + rr - j * p.group, e, v);
+          store4<!BF>(p, qrow + j, seg.kvh * p.group + rr - j * p.group, e,
+                      v);
         }
       }
       __syncthreads();   // the sums, and `seg`, are read
@@ -1218,7 +1223,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS)
     v.y *= f;
     v.z *= f;
     v.w *= f;
-    if (lane < LANES) store4(p, row, head, e, v);
+    if (lane < LANES) store4<true>(p, row, head, e, v);
     if (lane == 0 && p.a.lse != nullptr)
       p.a.lse[row * p.a.n_q + head] =
           none ? -INFINITY : (top + log2f(sum)) * LN2;
