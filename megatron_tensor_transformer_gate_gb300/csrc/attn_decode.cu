@@ -126,6 +126,7 @@ struct Conf {
   // to 2^15 and s_v from 2^-109 to 2^119, between which 2^20 tokens' sum stays
   // in fp32's range at the one end, and 2^-18 of a w / s_v at the other.
   static constexpr float RAISE = CACHE == TP_FP8 ? 12.0f : 0.0f;
+  static constexpr float LOWER = CACHE == TP_FP8 ? 0x1p-12f : 1.0f;   // 2^-RAISE
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * WARPS;
   // tokens of a warp: that are loaded, and that are worked on at a time
@@ -133,8 +134,9 @@ struct Conf {
   static constexpr int PART = ROW == 256 || NT == 4 ? 16 : 32;
   static constexpr int BLOCK = STEP * WARPS;       // of a CTA
   // A segment's fixed cost in blocks of work (64x8192 in E4M3: 55, 49, 45 and
-  // 51 µs with 128, 256, 512 and 1024 tokens; 256x1000 in fp16 21.0, 22.3, 24.9
-  // and 28.3).
+  // 51 µs with 128, 256, 512 and 1024 tokens, in fp16 with heads of 64 48.8,
+  // 44.2, 39.8 and 42.2, 31x2047 28.2, 27.5, 26.3 and 28.2; 256x1000 in fp16 with
+  // heads of 128 21.0, 22.3, 24.9 and 28.3).
   static constexpr int EXTRA = (ROW == 256 ? 128 : 512) / BLOCK;
   static constexpr int TILE = STEP * ROW;
   // K, V and the scales of a step
@@ -206,10 +208,9 @@ __device__ __forceinline__ void codes_f16(uint32_t u, uint32_t& lo,
       : "=r"(lo), "=r"(hi)
       : "r"(u));
 }
-// 2^x, subnormal results too
-__device__ __forceinline__ float ex2_whole(float x) {
+__device__ __forceinline__ float rcp_approx(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -682,16 +683,19 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
       __syncwarp();
       const uint32_t valid_all = valid_of[warp][stage];
       // Over codes, a token a lane: makes the step's vectors without a value ones
-      // of zeros with the scale NO_VALUE; whether there are any.
-      auto clear_no_values = [&]() {
+      // of zeros with the scale NO_VALUE, and those whose scale is NaN or negative
+      // ones of NaN (the scale itself would reach rows that do not see it through
+      // the sums); whether there are any.
+      auto mend_scales = [&]() {
         unsigned char* const v = ring + stage * C::STAGE + C::TILE;
         float* const sv = reinterpret_cast<float*>(v + C::TILE) + STEP + lane;
         auto codes = [&](int ch) -> uint4& {
           return *reinterpret_cast<uint4*>(v + spread<ROW>(lane, ch));
         };
         bool none = fabsf(*sv) < SMALLEST;   // (0: nothing was loaded)
+        const bool bad = !none && !(*sv > 0.0f);
         const bool zeros = *sv == 1.0f && (codes(0).x & 0x7f7f7f7fu) == 0;
-        if (!__any_sync(0xffffffffu, none || zeros)) return false;
+        if (!__any_sync(0xffffffffu, none || bad || zeros)) return false;
         if (zeros) {   // the first four are
           uint32_t any = 0;
 #pragma unroll 1
@@ -701,18 +705,19 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
           }
           none = (any & 0x7f7f7f7fu) == 0;
         }
-        if (none) {
-          *sv = NO_VALUE;
+        if (none || bad) {
+          *sv = none ? NO_VALUE : 1.0f;
+          const uint32_t x = none ? 0u : 0x7f7f7f7fu;
 #pragma unroll 1
-          for (int ch = 0; ch < CHUNKS; ++ch) codes(ch) = make_uint4(0, 0, 0, 0);
+          for (int ch = 0; ch < CHUNKS; ++ch) codes(ch) = make_uint4(x, x, x, x);
         }
         __syncwarp();
         return true;
       };
       // Looked for in front of every step of two parts; else only where the
-      // scales, once they are read, give reason to (16x65536 with 4 new 366 and
-      // 376 µs, 64x8192 46.1 and 45.0).
-      if constexpr (FP8 && PART < STEP) clear_no_values();
+      // scales, once they are read, give reason to (16x65536 with 4 new 364 and
+      // 376 µs, 64x8192 46.1 and 44.3).
+      if constexpr (FP8 && PART < STEP) mend_scales();
 #pragma unroll 1
       for (int part = 0; part < STEP; part += PART) {
         const int t1 = t0 + part;   // the part's first token
@@ -784,15 +789,13 @@ __global__ void __launch_bounds__(Conf<CACHE, D, NT>::THREADS, CTAS)
                 const float sv = ss[STEP + 16 * mt + g + 8 * h];
                 sk[mt][h] = ss[16 * mt + g + 8 * h];
                 lv[mt][h] = lg2_approx(sv);
-                // (NaN: 0·back where a row does not see it must not be NaN)
-                back[mt][h] =
-                    isnan(sv) ? 0.0f : ex2_whole(-lv[mt][h] - C::RAISE);
-                odd |= fabsf(sv) < SMALLEST || sv == 1.0f;
+                back[mt][h] = rcp_approx(sv) * C::LOWER;
+                odd |= !(sv >= SMALLEST) || sv == 1.0f;
               }
           };
           scales();
           if constexpr (PART == STEP)
-            if (__any_sync(0xffffffffu, odd) && clear_no_values()) scales();
+            if (__any_sync(0xffffffffu, odd) && mend_scales()) scales();
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -1272,11 +1275,19 @@ Layout layout_of(int ctas, int tile_rows, int d) {
 }
 
 // Where no sequence can have more than a few blocks its units are left whole:
-// that spares the join and its launch, at the price of a block's 0.75 µs for
-// each that another CTA would have taken.  Measured whole / cut (µs, sequences
-// of that length, 8 kv heads): in bf16 1x128 6.3 / 7.2, 1x256 7.9 / 7.5, 8x256
-// 8.8 / 10.3, 8x512 12.0 / 12.4, 8x768 15.2 / 14.1, 64x512 29.0 / 31.1; in E4M3
-// 1x256 7.2 / 7.6, 1x512 8.8 / 7.9, 8x512 9.6 / 11.6, 64x512 21.2 / 23.8.
+// that spares the join and its launch, at the price of the blocks that idle CTAs
+// would have taken.  Measured whole / cut (µs, 8 kv heads, sequences of all the
+// blocks they can have; a block is 64 tokens of 256 bytes or 128 shorter ones):
+//   8 units of 3 and 4 blocks: bf16 7.0 / 7.2 and 7.8 / 7.4, with 32 rows 16.1 /
+//     15.6 and 17.3 / 15.9, E4M3 7.8 / 7.7 and 8.6 / 7.8
+//   32 units of 3, 4 and 6: bf16 7.2 / 8.3, 8.0 / 8.8, 10.0 / 9.5
+//   64 units of 8 and 12: bf16 11.9 / 12.0 and 14.9 / 13.4, E4M3 13.4 / 13.2 and
+//     16.9 / 15.1, with 32 rows 29.0 / 29.7 and 35.5 / 32.8, fp16 heads of 64
+//     11.4 / 11.7 and 14.1 / 13.2
+//   256 units of 8 and 16: bf16 15.6 / 19.1 and 24.9 / 29.4
+// Where lengths differ the border lies lower (64 units of up to 8: E4M3 12.7 /
+// 11.6).  Over 8 to 512 units of up to 16 blocks and 8, 16 and 32 rows in all of
+// these types the rule costs 1.3 % against the better of both in the mean.
 bool left_whole(int64_t units, int blocks) {
   return blocks <= (units < 64 ? 3 : 8);
 }

@@ -75,7 +75,7 @@ def test_heavy_tokens_without_a_value(tp, kind, n, nats):
 
 
 # --------------------------------------------------------------- scales of values
-@pytest.mark.parametrize("scale", ["nan", "inf", "1e-45", "0"])
+@pytest.mark.parametrize("scale", ["nan", "inf", "1e-45", "0", "-1", "-inf"])
 @pytest.mark.parametrize("n", [50, 700])
 def test_scales_of_a_token_that_a_row_does_not_see(tp, n, scale):
     # the third of four new tokens; the first two rows do not see it
@@ -91,6 +91,21 @@ def test_scales_of_a_token_that_a_row_does_not_see(tp, n, scale):
     with np.errstate(invalid="ignore"):
         want = bounds(c, x, c.d ** -0.5, BF16)
     agree(out, lse, want, [0, 1, 4, 5])
+    if scale in ("nan", "inf", "-inf"):   # of its key too: rows that see it
+        assert torch.isnan(out[[2, 3, 6, 7]]).all()
+
+
+@pytest.mark.parametrize("scale", ["nan", "-1"])
+def test_a_values_scale_that_is_none(tp, scale):
+    # where it is seen the output is NaN; its weight is known
+    c = Cache([90], 16, 1, 128, "e4m3", 111)
+    x, q = queries(c, 1, 8, BF16, 9)
+    _, want, _, bound = bounds(c, x, c.d ** -0.5, BF16)
+    set_values(c, np.array([50]), scale=float(scale))
+    out, lse = attend(tp, c, q)
+    tp.device_status()
+    assert torch.isnan(out).all()
+    assert (np.abs(lse.double().cpu().numpy() - want) <= bound).all()
 
 
 @pytest.mark.parametrize("size", [-108, -60, 0, 60, 110, 119])
