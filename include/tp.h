@@ -626,7 +626,8 @@ tp_status tp_attn_decode(const tp_kv_cache* c, int32_t dtype, int64_t rows,
  * GEMM, 2 attention forward, 3 attention backward dK/dV, 4 attention
  * backward dQ, 5 shard-partial reduce, 6 other elementwise, 7 RMSNorm,
  * 8 tcgen05 GEMM on E4M3 operands, 9 FP8 amax / quantize, 10 key-value cache
- * (written, read), 11 attention over it. */
+ * (written, read), 11 attention over it (whose FLOPs and bytes are 0: the
+ * lengths are on the device). */
 typedef struct {
   uint64_t launches;
   double ms;
