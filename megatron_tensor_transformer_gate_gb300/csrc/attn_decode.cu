@@ -28,7 +28,7 @@
 // Measured (GB300, copy 6.8 TB/s): 32 sequences of 32768 in bf16 630 µs = 1.0
 // of a copy, in E4M3 335 to 348 = 0.97 to 0.93; one of 131072 in bf16 89 µs
 // (0.88: 4 µs until the first copies are in flight, 4 for the join and its
-// launch); 64 of 61 to 8192 in E4M3 44 µs (0.68: the start, 512 segments' ends,
+// launch); 64 of 61 to 8192 in E4M3 44.5 µs (0.68: the start, 512 segments' ends,
 // latencies between a step's dependent instructions); with 32 rows over codes
 // 364 µs for 1.6 GB (0.65: those latencies alone, eight warps an SM at 250
 // registers a thread), over bf16 475 for 3.1 GB (0.96).
@@ -42,12 +42,12 @@
 // of that rounding.  Over bf16 values, where bf16 (2^-8) would show in the
 // output, P is the sum of two bf16 parts, 2^-16, at the price of a second
 // product.  A code's scale is multiplied into its score, and into its weight in
-// front of the product with V: t = x + log₂ s_v, w = 2^(t − M) with M near
-// the running maximum of t (BELOW), so that scales of any size keep the weights of the sum
-// in fp16's range; the denominator is Σ w / s_v, relative to the same M (fp32's
-// range leaves s_v a factor of 2^100 from token to token; a vector without a
-// value has a place of its own in it, see SMALLEST).  Like x itself t is
-// rounded to 2^-24 of its size, so that scales count while |x| is below 2^20.
+// front of the product with V: t = x + log₂ s_v, w = 2^(t − M) with M near the
+// running maximum of t (BELOW), so that scales of any size keep the weights of
+// the sum in fp16's range; the denominator is Σ w / s_v, relative to the same M
+// (fp32's range leaves s_v a factor of 2^100 from token to token; for vectors
+// without a value see SMALLEST).  Like x itself t is rounded to 2^-24 of its
+// size, so that scales count while |x| is below 2^20.
 #include <cuda_runtime.h>
 
 #include <algorithm>
