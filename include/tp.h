@@ -531,9 +531,9 @@ tp_status tp_gemm_fp8_block_form(int64_t M, int64_t N, int64_t K,
  * TP_FP8 vectors are E4M3 codes with one fp32 scale each in ks and vs
  * [pages, page, n_kv] (strides of their own, again shared): as in
  * tp_quantize_fp8_block's TP_FP8_ROW, s = amax / 448, code = E4M3(x·448/amax)
- * and the element's value is code·s.  Scales are finite and not negative; the
- * attention takes a value whose scale is below 2^-109 (tp_kv_cache_write makes
- * none) for 0.
+ * and the element's value is code·s.  Scales are not negative and below 2^120
+ * (bf16's largest value has 2^119.2); the attention takes a value whose scale is
+ * below 2^-109 (tp_kv_cache_write makes none) for 0.
  * table[i·table_stride + c], device int32, is the page of sequence i's tokens
  * [c·page, (c + 1)·page); lens[i], device int32, how many tokens the sequence
  * has, the newest ones of a call among them.  Only the entries that a call's
